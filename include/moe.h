@@ -71,15 +71,33 @@ typedef enum moe_status {
 typedef enum moe_weight_format {
   MOE_W_BF16 = 0,        /* routed expert weights in bf16 */
   MOE_W_INT4_G128 = 1,   /* W4A16: uint4 codes, bf16 scale per 128 along K */
-  MOE_W_NVFP4 = 2        /* NVFP4: E2M1 codes, E4M3 scale per 16 along K,
+  MOE_W_NVFP4 = 2,       /* NVFP4: E2M1 codes, E4M3 scale per 16 along K,
                             fp32 scale per expert weight tensor */
+  MOE_W_FP8_B128 = 4     /* FP8: E4M3 codes, fp32 scale per 128 x 128 block;
+                            the activations are quantised too (below) */
 } moe_weight_format;
+
+/* Router scores of the logits l: sigmoid(l_e), or the softmax over all E. */
+typedef enum moe_score_func { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score_func;
+
+/* Value of a group of experts under group-limited routing: the sum of its
+ * two largest biased scores (of its one, when the group has one expert), or
+ * the largest. */
+typedef enum moe_group_score { MOE_GROUP_SUM2 = 0, MOE_GROUP_MAX = 1 } moe_group_score;
+
+/* Element types of the calls that take more than one. */
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 
 /* Largest k the router kernel selects per token ([glm5next] constant
  * KERNEL_MAX_TOP_K: the per-token selection lives in 16-entry arrays). */
 #define MOE_MAX_TOP_K 16
 /* Largest routed expert count this build supports. */
 #define MOE_MAX_EXPERTS 1024
+/* Largest count of expert groups (group-limited routing). */
+#define MOE_MAX_GROUPS 32
+/* Bytes of the workspace header that moe_workspace_init zeroes; all the
+ * workspace that moe_fp8_gemm needs. */
+#define MOE_WS_HEADER_BYTES 256
 
 /* Geometry and numerics of one MoE layer. */
 typedef struct moe_config {
@@ -98,6 +116,16 @@ typedef struct moe_config {
   int32_t renormalize;           /* 1: divide the k unbiased scores by their
                                     sum before alpha; 0: no renormalisation */
   int32_t expert_format;         /* moe_weight_format */
+  /* Routing; all zero: sigmoid scores, no groups. */
+  int32_t score;                 /* moe_score_func */
+  int32_t num_groups;            /* 0 or 1: no groups; else the experts form
+                                    num_groups groups of E / num_groups
+                                    consecutive ids (<= MOE_MAX_GROUPS) and
+                                    the k experts come from the top_groups
+                                    groups of largest value, ties to the
+                                    lower group */
+  int32_t top_groups;            /* 1..num_groups, with k <= top_groups * E / num_groups */
+  int32_t group_score;           /* moe_group_score */
 } moe_config;
 
 /* Device weight handles of one layer.  Gate rows come first in every fused
@@ -105,7 +133,8 @@ typedef struct moe_config {
 typedef struct moe_weights {
   const float* router_w;         /* fp32 [E, H] */
   const float* correction_bias;  /* fp32 [E], or NULL for zero bias */
-  /*                                bf16            | W4A16                  | NVFP4 */
+  /*                                bf16            | W4A16                  | NVFP4
+   *                                (FP8 block: see "FP8 experts" below) */
   const void* w_gate_up;         /* bf16 [E, 2I, H] | uint8 [E, 2I, H/2]     | uint8 [E, 2I, H/2] */
   const void* s_gate_up;         /* NULL            | bf16  [E, 2I, H/128]   | E4M3 uint8 [E, 2I, H/16] */
   const void* w_down;            /* bf16 [E, H, I]  | uint8 [E, H, I/2]      | uint8 [E, H, I/2] */
@@ -145,6 +174,18 @@ typedef struct moe_weights {
  * the fp32 sums by g[e]; the activation limits of the W4A16 range note above
  * (fp16 x and h, swiglu_limit) hold as stated there. */
 
+/* FP8 experts (MOE_W_FP8_B128; FP8 E4M3 of the OCP 8-bit Floating Point
+ * specification, its 256 - 2 finite codes up to 448):
+ *   w_gate_up  E4M3 [E, 2I, H]     s_gate_up  fp32 [E, 2I/128, H/128]
+ *   w_down     E4M3 [E, H, I]      s_down     fp32 [E, H/128, I/128]
+ *   w[n, k] = e4m3(code) * s[n / 128, k / 128]; H and I multiples of 128.
+ * The routed tokens and the SwiGLU activations are quantised as
+ * moe_fp8_quantize does: along each row, 128 values share a power-of-two
+ * scale.  Products of codes are summed in fp32 over each block of 128, and
+ * each block's sum is multiplied by both scales and added in fp32.  h goes
+ * from its fp32 value straight to E4M3 (no bf16 rounding between).
+ * swiglu_limit may be +inf.  The shared expert stays bf16. */
+
 /* Human-readable name of a status.  Never NULL. */
 MOE_API const char* moe_status_string(moe_status status);
 
@@ -177,6 +218,34 @@ MOE_API moe_status moe_router_topk(const moe_config* cfg, const moe_weights* w,
                            const void* x, int32_t T,
                            int32_t* topk_ids, float* topk_w,
                            void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* With cfg->score = MOE_SCORE_SOFTMAX or cfg->num_groups > 1, moe_router_topk
+ * (and every call that routes) takes the same fp32 tensor-core logits and
+ * selects from them as moe_gate_topk does. */
+
+/* Expert selection from given router logits (any router in front: one with a
+ * linear bias, a quantised one, logits gathered from another rank):
+ *   s = score(logits[t])                  cfg->score, over all E experts
+ *   v_e = s_e + correction_bias[e]        selection only
+ *   groups: when cfg->num_groups > 1, only experts of the top_groups groups
+ *   of largest value stay eligible
+ *   ids = the k eligible experts of largest v, in descending order, ties to
+ *   the lower id;  w = alpha * s_id, renormalised over the k first if
+ *   cfg->renormalize (0 where that sum is 0).
+ * The order is that of the exact scores of the given logits: where fp32
+ * leaves a decision open it is taken from fp64 scores.  The weights are fp32.
+ * Logits may be infinite: an expert with -inf has score 0, a softmax row of
+ * -inf alone has scores 0; NaN counts as the largest value.  The ids of a
+ * token are distinct and in [0, E) whatever the logits hold.
+ *   logits           [T, E] of logits_type (moe_dtype), row t at
+ *                    logits + t * row_stride elements (row_stride >= E);
+ *                    aligned to its element
+ *   correction_bias  fp32 [E] or NULL
+ *   topk_ids         int32 [T, k] out     topk_w  fp32 [T, k] out
+ * Needs no workspace. */
+MOE_API moe_status moe_gate_topk(const moe_config* cfg, const void* logits, int32_t logits_type,
+                                 int64_t row_stride, const float* correction_bias, int32_t T,
+                                 int32_t* topk_ids, float* topk_w, moe_stream_t stream);
 
 /* Token sort / permute by expert ([glm5next] MOE_MODULE): a deterministic
  * stable counting sort of the slots i = t*k + j by expert id.
@@ -306,6 +375,53 @@ MOE_API moe_status moe_forward_ep(const moe_config* cfg, const moe_weights* w, i
                                   int32_t expert_end, const void* x, int32_t T, void* out_partial,
                                   int32_t* topk_ids_opt, float* topk_w_opt, void* ws, size_t ws_bytes,
                                   moe_stream_t stream);
+
+/* Rows to FP8 E4M3 with a scale per 128 values along the row:
+ *   xr = x[src[r] / src_div] (src given: the token of routed row r, with
+ *        moe_permute's src and src_div = top_k) or x[r] (src NULL)
+ *   scale[b, r] = 2^e, the smallest with max |xr[128 b ..]| <= 448 * 2^e
+ *                 (e >= -126; 1 for a block of zeros)
+ *   q[r, k] = e4m3(xr[k] / scale[k / 128, r]), nearest, ties to even
+ * The scale is a power of two so that the division is exact: a code differs
+ * from its value by its own rounding alone, at most 2^-4 relative in E4M3's
+ * normal range, as with any other scale.  A block that holds an infinity or
+ * a NaN becomes NaN codes with scale 1.
+ *   x       [*, K] of x_type, row i at x + i * row_stride elements; rows
+ *           16-byte aligned (base and row_stride * element size)
+ *   q       E4M3 [rows, K] out, 16-byte aligned;  K a multiple of 16
+ *   scale   fp32 [ceil(K / 128), rows] out (block-major)
+ *   src     int32 [rows] or NULL;  src_div >= 1 */
+MOE_API moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t row_stride, const int32_t* src,
+                                    int32_t src_div, int32_t rows, int32_t K, void* q, float* scale,
+                                    moe_stream_t stream);
+
+/* Weights to FP8 E4M3 with a scale per 128 x 128 block (the edge blocks of N
+ * and K smaller), scales and codes as above:
+ *   w      [groups, N, K] of w_type, contiguous, 16-byte aligned; K a multiple of 16
+ *   q      E4M3 [groups, N, K] out
+ *   scale  fp32 [groups, ceil(N / 128), ceil(K / 128)] out */
+MOE_API moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_t groups, int32_t N, int32_t K,
+                                           void* q, float* scale, moe_stream_t stream);
+
+/* Product of FP8 E4M3 rows and weights with a scale per block of 128, dense
+ * or grouped by expert:
+ *   out[r, n] = c_r * sum_b a_scale[b, r] * w_scale[g, n / 128, b]
+ *                     * sum_{k in block b} e4m3(a[r, k]) e4m3(w[g, n, k])
+ * for the rows r of group g, expert_offsets[g] <= r < expert_offsets[g + 1]
+ * (NULL: one group of all rows).  Inner sums and the sum over b are fp32; one
+ * rounding to out_type at the end.  Rows outside the groups are not written.
+ *   a               E4M3 [rows, K]        a_scale  fp32 [ceil(K/128), rows]
+ *   expert_offsets  int32 [groups + 1] ascending, within [0, rows], or NULL with groups == 1
+ *   w               E4M3 [groups, N, K]   w_scale  fp32 [groups, ceil(N/128), ceil(K/128)]
+ *   row_scale       fp32 [rows] (c) or NULL (1)
+ *   out             MOE_BF16 or MOE_F32 [rows, N]
+ * N a multiple of 8, K of 16; a, w and out 16-byte aligned.  The scales need
+ * not be powers of two.  ws: an initialised workspace of any size from
+ * MOE_WS_HEADER_BYTES up (it holds the tile queue and the error word). */
+MOE_API moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const int32_t* expert_offsets,
+                                int32_t groups, const void* w, const float* w_scale, int32_t N, int32_t K,
+                                const float* row_scale, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
 
 /* Permute without a workspace, for callers that may not allocate device
  * memory on their enqueue path (framework / inference-server plugins and

@@ -14,16 +14,20 @@ from typing import Optional
 
 from . import _abi
 from ._abi import (  # noqa: F401
-    EXPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
-    MOE_ERR_WORKSPACE, MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_OK, MOE_W_BF16, MOE_W_INT4_G128, MOE_W_NVFP4, MoEError,
+    EXPORTED, MOE_BF16, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
+    MOE_ERR_WORKSPACE, MOE_F16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_SUM2, MOE_MAX_EXPERTS, MOE_MAX_GROUPS, MOE_MAX_TOP_K,
+    MOE_OK, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_BF16, MOE_W_FP8_B128, MOE_W_INT4_G128, MOE_W_NVFP4,
+    MOE_WS_HEADER_BYTES, MoEError,
     load_library, make_config, make_weights, moe_combine, moe_config, moe_config_validate, moe_forward,
+    moe_fp8_gemm, moe_fp8_quantize, moe_fp8_quantize_weight, moe_gate_topk,
     moe_grouped_swiglu_ffn, moe_grouped_swiglu_ffn_gather, moe_permute, moe_read_device_error, moe_router_topk,
     moe_weights,
     moe_workspace_init, moe_workspace_size, status_name,
 )
 
 __all__ = ["MoELayer", "load_library", "moe_forward", "moe_router_topk", "moe_permute",
-           "moe_grouped_swiglu_ffn", "moe_grouped_swiglu_ffn_gather", "moe_combine", "moe_workspace_size", "MoEError"]
+           "moe_grouped_swiglu_ffn", "moe_grouped_swiglu_ffn_gather", "moe_combine", "moe_workspace_size", "MoEError",
+           "moe_gate_topk", "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_gemm"]
 
 
 class MoELayer:
@@ -36,15 +40,20 @@ class MoELayer:
     [2I_s, H] and shared_w_down bf16 [H, I_s] (None when I_s == 0).
     NVFP4 experts: uint8 E2M1 codes as above, s_gate_up / s_down uint8 E4M3
     scales [E, 2I, H/16] / [E, H, I/16], and g_gate_up / g_down fp32 [E]
-    tensor scales (their presence selects the format)."""
+    tensor scales (their presence selects the format).
+    FP8 experts: float8_e4m3fn w_gate_up [E, 2I, H] / w_down [E, H, I] with
+    fp32 s_gate_up [E, 2I/128, H/128] / s_down [E, H/128, I/128].
+    Routing: score (MOE_SCORE_*), num_groups, top_groups and group_score
+    (MOE_GROUP_*) as in moe_config; by default sigmoid scores, no groups."""
 
     def __init__(self, *, hidden, num_experts, top_k, expert_inter, shared_inter, swiglu_limit,
                  routed_scaling_factor, renormalize, router_w, correction_bias, w_gate_up, w_down,
                  s_gate_up=None, s_down=None, shared_w_gate_up=None, shared_w_down=None,
-                 g_gate_up=None, g_down=None, max_tokens: int = 0):
+                 g_gate_up=None, g_down=None, max_tokens: int = 0, score=MOE_SCORE_SIGMOID, num_groups: int = 0,
+                 top_groups: int = 0, group_score=MOE_GROUP_SUM2):
         fmt = _abi.weight_format(w_gate_up, g_gate_up)
         self.cfg = make_config(hidden, num_experts, top_k, expert_inter, shared_inter, swiglu_limit,
-                               routed_scaling_factor, renormalize, fmt)
+                               routed_scaling_factor, renormalize, fmt, score, num_groups, top_groups, group_score)
         st = moe_config_validate(self.cfg)
         if st != MOE_OK:
             raise MoEError(st, "moe_config_validate")

@@ -26,6 +26,16 @@ MOE_ERR_DEVICE_TIMEOUT = 5
 MOE_W_BF16 = 0
 MOE_W_INT4_G128 = 1
 MOE_W_NVFP4 = 2
+MOE_W_FP8_B128 = 4
+MOE_SCORE_SIGMOID = 0
+MOE_SCORE_SOFTMAX = 1
+MOE_GROUP_SUM2 = 0
+MOE_GROUP_MAX = 1
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_F16 = 2
+MOE_MAX_GROUPS = 32
+MOE_WS_HEADER_BYTES = 256
 MOE_MAX_TOP_K = 16
 MOE_MAX_EXPERTS = 1024
 MOE_INT4_MAX_SWIGLU_LIMIT = 255.0
@@ -33,7 +43,7 @@ MOE_INT4_MAX_SWIGLU_LIMIT = 255.0
 EXPORTED = (
     "moe_status_string", "moe_config_validate", "moe_workspace_size", "moe_workspace_init",
     "moe_router_topk", "moe_permute", "moe_grouped_swiglu_ffn", "moe_grouped_swiglu_ffn_gather", "moe_combine",
-    "moe_forward", "moe_forward_ep",
+    "moe_forward", "moe_forward_ep", "moe_gate_topk", "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_gemm",
     "moe_read_device_error", "moe_permute_no_alloc", "moe_selftest_device_timeout", "moe_selftest_pair_timeout",
 )
 MOE_NO_ALLOC_MAX_ROWS = 131072
@@ -59,6 +69,10 @@ class moe_config(ctypes.Structure):
         ("routed_scaling_factor", ctypes.c_float),
         ("renormalize", ctypes.c_int32),
         ("expert_format", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
     ]
 
 
@@ -90,7 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             f"CUDA library not found at {path}; build it with "
             "`python -m routed_swiglu_experts_b200.build` (there is no CPU fallback)")
     lib = ctypes.CDLL(path)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     CFG, W = ctypes.POINTER(moe_config), ctypes.POINTER(moe_weights)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -104,6 +118,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_combine": (ctypes.c_int, [CFG, P, P, P, P, I32, P, P]),
         "moe_forward": (ctypes.c_int, [CFG, W, P, I32, P, P, P, P, SZ, P]),
         "moe_forward_ep": (ctypes.c_int, [CFG, W, I32, I32, P, I32, P, P, P, P, SZ, P]),
+        "moe_gate_topk": (ctypes.c_int, [CFG, P, I32, I64, P, I32, P, P, P]),
+        "moe_fp8_quantize": (ctypes.c_int, [P, I32, I64, P, I32, I32, I32, P, P, P]),
+        "moe_fp8_quantize_weight": (ctypes.c_int, [P, I32, I32, I32, I32, P, P, P]),
+        "moe_fp8_gemm": (ctypes.c_int, [P, P, I32, P, I32, P, P, I32, I32, P, P, I32, P, SZ, P]),
         "moe_read_device_error": (ctypes.c_int, [P, P, ctypes.POINTER(I32)]),
         "moe_selftest_device_timeout": (ctypes.c_int, [P, SZ, P]),
         "moe_selftest_pair_timeout": (ctypes.c_int, [P, SZ, I32, P]),
@@ -147,10 +165,11 @@ def _check(status: int, where: str):
 
 
 def make_config(hidden, num_experts, top_k, expert_inter, shared_inter, swiglu_limit,
-                routed_scaling_factor=1.0, renormalize=False, expert_format=MOE_W_BF16) -> moe_config:
+                routed_scaling_factor=1.0, renormalize=False, expert_format=MOE_W_BF16, score=MOE_SCORE_SIGMOID,
+                num_groups=0, top_groups=0, group_score=MOE_GROUP_SUM2) -> moe_config:
     return moe_config(int(hidden), int(num_experts), int(top_k), int(expert_inter), int(shared_inter),
                       float(swiglu_limit), float(routed_scaling_factor), int(bool(renormalize)),
-                      int(expert_format))
+                      int(expert_format), int(score), int(num_groups), int(top_groups), int(group_score))
 
 
 def make_weights(router_w=None, correction_bias=None, w_gate_up=None, s_gate_up=None, w_down=None,
@@ -162,9 +181,11 @@ def make_weights(router_w=None, correction_bias=None, w_gate_up=None, s_gate_up=
 
 
 def weight_format(w_gate_up, g_gate_up=None) -> int:
-    """The moe_weight_format of a layer's routed tensors: bf16 weights, or
-    uint8 codes -- NVFP4 when the per-expert fp32 tensor scales are given,
-    else W4A16."""
+    """The moe_weight_format of a layer's routed tensors: bf16 weights, E4M3
+    weights (torch.float8_e4m3fn, block scales), or uint8 codes -- NVFP4 when
+    the per-expert fp32 tensor scales are given, else W4A16."""
+    if str(w_gate_up.dtype) == "torch.float8_e4m3fn":
+        return MOE_W_FP8_B128
     if g_gate_up is not None:
         return MOE_W_NVFP4
     return MOE_W_INT4_G128 if str(w_gate_up.dtype) == "torch.uint8" else MOE_W_BF16
@@ -231,6 +252,112 @@ def moe_forward_ep(cfg, w, expert_begin, expert_end, x, T, out_partial, topk_ids
     _check(load_library().moe_forward_ep(ctypes.byref(cfg), ctypes.byref(w), int(expert_begin), int(expert_end),
                                          _ptr(x), int(T), _ptr(out_partial), _ptr(topk_ids_opt), _ptr(topk_w_opt),
                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_forward_ep")
+
+
+def _want(t, name, dtypes, shape, where, contiguous=True):
+    """A tensor argument's element type, shape, layout and device, checked
+    before its pointer is passed: the C call sees none of them.  The stream
+    and the kernel belong to the current device, so the tensor must too."""
+    import torch
+    if t is None:
+        raise ValueError(f"{where}: {name} is missing")
+    if str(t.dtype).replace("torch.", "") not in dtypes:
+        raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(dtypes)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{where}: {name} is not contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is on {t.device}, expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+
+
+_DTYPE = {"float32": MOE_F32, "bfloat16": MOE_BF16, "float16": MOE_F16}
+_CODES = ("float8_e4m3fn", "uint8")
+
+
+def _dtype(t) -> int:
+    return _DTYPE[str(t.dtype).replace("torch.", "")]
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _rows_of(t, name, where):
+    """A 2-D tensor whose rows are contiguous (any row stride)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def moe_gate_topk(cfg, logits, correction_bias, topk_ids, topk_w, stream=None):
+    """Expert selection from logits [T, E] (fp32, bf16 or fp16; rows may be strided)."""
+    where = "moe_gate_topk"
+    _want(logits, "logits", tuple(_DTYPE), None, where, contiguous=False)
+    stride = _rows_of(logits, "logits", where)
+    T = logits.shape[0]
+    if logits.shape[1] != cfg.num_experts:
+        raise ValueError(f"{where}: logits has {logits.shape[1]} columns for {cfg.num_experts} experts")
+    if correction_bias is not None:
+        _want(correction_bias, "correction_bias", ("float32",), (cfg.num_experts,), where)
+    _want(topk_ids, "topk_ids", ("int32",), (T, cfg.top_k), where)
+    _want(topk_w, "topk_w", ("float32",), (T, cfg.top_k), where)
+    _check(load_library().moe_gate_topk(ctypes.byref(cfg), _ptr(logits), _dtype(logits), stride, _ptr(correction_bias),
+                                        T, _ptr(topk_ids), _ptr(topk_w), _stream(stream)), where)
+
+
+def moe_fp8_quantize(x, q, scale, src=None, src_div=1, stream=None):
+    """Rows x [*, K] to E4M3 codes q [rows, K] and scales [ceil(K/128), rows];
+    src int32 [rows]: row r is x[src[r] // src_div]."""
+    where = "moe_fp8_quantize"
+    _want(x, "x", tuple(_DTYPE), None, where, contiguous=False)
+    stride = _rows_of(x, "x", where)
+    K = x.shape[1]
+    rows = x.shape[0] if src is None else src.shape[0]
+    if src is not None:
+        _want(src, "src", ("int32",), (rows,), where)
+    _want(q, "q", _CODES, (rows, K), where)
+    _want(scale, "scale", ("float32",), (_blocks(K), rows), where)
+    _check(load_library().moe_fp8_quantize(_ptr(x), _dtype(x), stride, _ptr(src), int(src_div), rows, K, _ptr(q),
+                                           _ptr(scale), _stream(stream)), where)
+
+
+def moe_fp8_quantize_weight(w, q, scale, stream=None):
+    """Weights w [groups, N, K] to E4M3 codes and scales [groups, ceil(N/128), ceil(K/128)]."""
+    where = "moe_fp8_quantize_weight"
+    _want(w, "w", tuple(_DTYPE), None, where)
+    if w.dim() != 3:
+        raise ValueError(f"{where}: w must be [groups, N, K]")
+    G, N, K = w.shape
+    _want(q, "q", _CODES, (G, N, K), where)
+    _want(scale, "scale", ("float32",), (G, _blocks(N), _blocks(K)), where)
+    _check(load_library().moe_fp8_quantize_weight(_ptr(w), _dtype(w), G, N, K, _ptr(q), _ptr(scale), _stream(stream)),
+           where)
+
+
+def moe_fp8_gemm(a, a_scale, w, w_scale, expert_offsets, row_scale, out, ws, stream=None):
+    """out [rows, N] = a [rows, K] times w [groups, N, K] by row groups, E4M3
+    codes with block scales (expert_offsets None: one group)."""
+    where = "moe_fp8_gemm"
+    _want(a, "a", _CODES, None, where)
+    _want(w, "w", _CODES, None, where)
+    if a.dim() != 2 or w.dim() != 3 or a.shape[1] != w.shape[2]:
+        raise ValueError(f"{where}: a must be [rows, K] and w [groups, N, K]")
+    rows, K = a.shape
+    G, N = w.shape[0], w.shape[1]
+    _want(a_scale, "a_scale", ("float32",), (_blocks(K), rows), where)
+    _want(w_scale, "w_scale", ("float32",), (G, _blocks(N), _blocks(K)), where)
+    if expert_offsets is not None:
+        _want(expert_offsets, "expert_offsets", ("int32",), (G + 1,), where)
+    if row_scale is not None:
+        _want(row_scale, "row_scale", ("float32",), (rows,), where)
+    _want(out, "out", ("bfloat16", "float32"), (rows, N), where)
+    _want(ws, "ws", ("uint8",), None, where)
+    _check(load_library().moe_fp8_gemm(_ptr(a), _ptr(a_scale), rows, _ptr(expert_offsets), G, _ptr(w), _ptr(w_scale),
+                                       N, K, _ptr(row_scale), _ptr(out), _dtype(out), _ptr(ws),
+                                       ws.numel() * ws.element_size(), _stream(stream)), where)
 
 
 def moe_permute_no_alloc(cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm, stream=None):

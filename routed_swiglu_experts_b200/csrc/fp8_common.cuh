@@ -1,0 +1,42 @@
+// FP8 E4M3 helpers of the block-scaled kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Four fp32 values to E4M3 codes (nearest, ties to even, saturating; NaN to
+// NaN), the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Scale of a block whose largest |value| has the bits `amax`, and its inverse
+// (both powers of two, so multiplying by the inverse is exact):
+// 448 = 1.75 * 2^8, so for amax = f * 2^p the scale is 2^(p - 8), or
+// 2^(p - 7) when f > 1.75; at least 2^-126.  A block of zeros has scale 1; one
+// with an infinity or a NaN scale 1 and a NaN inverse (all its codes NaN).
+__device__ __forceinline__ void e4m3_block_scale(uint32_t amax, float& scale, float& inv) {
+  int e = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = e < 1 ? 1 : e;
+  if (amax == 0u) e = 127;
+  scale = __uint_as_float(static_cast<uint32_t>(e) << 23);
+  inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  if (amax >= 0x7F800000u) {
+    scale = 1.f;
+    inv = __uint_as_float(0x7FC00000u);
+  }
+}
+
+// silu(min(g, L)) * clamp(u, -L, L); comparisons that keep a NaN.
+__device__ __forceinline__ float swiglu_clamped(float g, float u, float L) {
+  g = g > L ? L : g;
+  u = u > L ? L : (u < -L ? -L : u);
+  return __fdividef(g, 1.f + __expf(-g)) * u;
+}
+
+}  // namespace moe

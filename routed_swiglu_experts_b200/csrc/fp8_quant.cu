@@ -1,0 +1,198 @@
+// FP8 E4M3 quantisation with a power-of-two scale per block of 128 values:
+//   scale = smallest 2^e with amax <= 448 * 2^e,  q = e4m3(x / scale)
+// Rows: 1 x 128 blocks along a row (activations); weights: 128 x 128 blocks.
+// Both read every value once and keep it in registers between the maximum
+// and the conversion; memory bandwidth bounds them.
+#include <cuda_fp16.h>
+
+#include "fp8_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+template <typename T>
+struct Vec16;  // 16 values of a row as loaded
+template <>
+struct Vec16<__nv_bfloat16> {
+  uint4 v[2];
+  __device__ __forceinline__ void get(float (&f)[16]) const {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[2 * i] = bf16lo(w[i]);
+      f[2 * i + 1] = bf16hi(w[i]);
+    }
+  }
+};
+template <>
+struct Vec16<__half> {
+  uint4 v[2];
+  __device__ __forceinline__ void get(float (&f)[16]) const {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+};
+template <>
+struct Vec16<float> {
+  uint4 v[4];
+  __device__ __forceinline__ void get(float (&f)[16]) const {
+    const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                            v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ Vec16<T> load16(const T* p) {
+  Vec16<T> r;
+  const uint4* s = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.v[i] = __ldg(s + i);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t amax_bits16(const float (&f)[16]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&f)[16], float inv) {
+  uint4 o;
+  o.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+  o.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+  o.z = e4m3x4(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
+  o.w = e4m3x4(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
+  return o;
+}
+
+// One warp per row: 8 lanes per 128-block, 16 values (one 16-byte store of
+// codes) per lane.  Eight rows per block, so that the scales of neighbouring
+// rows, neighbours in the block-major layout, are written together.
+// Rows outside [range[0], range[range_len]) are skipped (range given).
+constexpr int kRowWarps = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32)
+    fp8_rows_kernel(const T* __restrict__ x, int64_t stride, const int32_t* __restrict__ src, int src_div, int rows,
+                    int K, unsigned char* __restrict__ q, float* __restrict__ scale,
+                    const int32_t* __restrict__ range, int range_len) {
+  const int r = blockIdx.x * kRowWarps + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (r >= rows) return;
+  if (range != nullptr && (r < __ldg(range) || r >= __ldg(range + range_len))) return;
+  const int64_t from = src != nullptr ? __ldg(src + r) / src_div : r;
+  const T* xr = x + from * stride;
+  unsigned char* qr = q + static_cast<size_t>(r) * K;
+  for (int k0 = 0; k0 < K; k0 += 512) {
+    const int k = k0 + lane * 16;
+    float f[16];
+    if (k < K) {
+      load16(xr + k).get(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = 0.f;
+    }
+    uint32_t m = amax_bits16(f);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float sc, inv;
+    e4m3_block_scale(m, sc, inv);
+    if (k < K) {
+      *reinterpret_cast<uint4*>(qr + k) = codes16(f, inv);
+      if ((lane & 7) == 0) scale[static_cast<size_t>(k / 128) * rows + r] = sc;
+    }
+  }
+}
+
+// One block per 128 x 128 weight block: 256 threads, a thread holds 16 values
+// of four rows.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    fp8_weight_kernel(const T* __restrict__ w, int N, int K, unsigned char* __restrict__ q, float* __restrict__ scale) {
+  __shared__ uint32_t s_max[8];
+  const int nb = (N + 127) / 128, kb = (K + 127) / 128;
+  const int bk = blockIdx.x % kb;
+  const int64_t rest = blockIdx.x / kb;
+  const int bn = static_cast<int>(rest % nb);
+  const int64_t g = rest / nb;
+  const int k = bk * 128 + (threadIdx.x & 7) * 16;
+  const int n0 = bn * 128 + threadIdx.x / 8;
+  Vec16<T> v[4];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + 32 * i;
+    if (n < N && k < K) v[i] = load16(w + (g * N + n) * K + k);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n0 + 32 * i < N && k < K) {
+      float f[16];
+      v[i].get(f);
+      m = max(m, amax_bits16(f));
+    }
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
+  float sc, inv;
+  e4m3_block_scale(m, sc, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + 32 * i;
+    if (n < N && k < K) {
+      float f[16];
+      v[i].get(f);
+      *reinterpret_cast<uint4*>(q + (g * N + n) * K + k) = codes16(f, inv);
+    }
+  }
+  if (threadIdx.x == 0) scale[blockIdx.x] = sc;
+}
+
+template <typename T>
+cudaError_t rows_typed(const void* x, int64_t stride, const int32_t* src, int src_div, int rows, int K, void* q,
+                       float* scale, const int32_t* range, int range_len, cudaStream_t stream) {
+  return launch_kernel(fp8_rows_kernel<T>, dim3(static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps)),
+                       dim3(kRowWarps * 32), 0, stream, static_cast<const T*>(x), stride, src, src_div, rows, K,
+                       static_cast<unsigned char*>(q), scale, range, range_len);
+}
+
+template <typename T>
+cudaError_t weight_typed(const void* w, int groups, int N, int K, void* q, float* scale, cudaStream_t stream) {
+  const int64_t blocks = static_cast<int64_t>(groups) * ((N + 127) / 128) * ((K + 127) / 128);
+  return launch_kernel(fp8_weight_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                       static_cast<const T*>(w), N, K, static_cast<unsigned char*>(q), scale);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const void* x, int dtype, int64_t stride, const int32_t* src, int src_div, int rows,
+                                int K, void* q, float* scale, const int32_t* range, int range_len,
+                                cudaStream_t stream) {
+  if (dtype == MOE_F32)
+    return rows_typed<float>(x, stride, src, src_div, rows, K, q, scale, range, range_len, stream);
+  if (dtype == MOE_BF16)
+    return rows_typed<__nv_bfloat16>(x, stride, src, src_div, rows, K, q, scale, range, range_len, stream);
+  return rows_typed<__half>(x, stride, src, src_div, rows, K, q, scale, range, range_len, stream);
+}
+
+cudaError_t launch_fp8_quantize_weight(const void* w, int dtype, int groups, int N, int K, void* q, float* scale,
+                                       cudaStream_t stream) {
+  if (dtype == MOE_F32) return weight_typed<float>(w, groups, N, K, q, scale, stream);
+  if (dtype == MOE_BF16) return weight_typed<__nv_bfloat16>(w, groups, N, K, q, scale, stream);
+  return weight_typed<__half>(w, groups, N, K, q, scale, stream);
+}
+
+}  // namespace moe

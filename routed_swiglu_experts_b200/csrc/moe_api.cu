@@ -59,6 +59,10 @@ bool is_int4(const moe_config& cfg) { return cfg.expert_format == MOE_W_INT4_G12
 bool is_nvfp4(const moe_config& cfg) { return cfg.expert_format == MOE_W_NVFP4; }
 // both 4-bit formats: fp16 activations, the 4-bit kernels gather the routed rows
 bool is_4bit(const moe_config& cfg) { return is_int4(cfg) || is_nvfp4(cfg); }
+bool is_fp8(const moe_config& cfg) { return cfg.expert_format == MOE_W_FP8_B128; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// rows of moe_fp8_quantize and moe_fp8_gemm: the routed rows of kMaxTokens tokens
+constexpr int64_t kMaxRows = kMaxTokens * MOE_MAX_TOP_K;
 
 moe_status check_expert_weights(const moe_config& cfg, const moe_weights* w) {
   if (w == nullptr) return MOE_ERR_INVALID_ARG;
@@ -67,6 +71,10 @@ moe_status check_expert_weights(const moe_config& cfg, const moe_weights* w) {
   if (is_4bit(cfg)) {
     if (w->s_gate_up == nullptr || w->s_down == nullptr) return MOE_ERR_INVALID_ARG;
     if (!aligned16(w->s_gate_up) || !aligned16(w->s_down)) return MOE_ERR_INVALID_ARG;
+  }
+  if (is_fp8(cfg)) {
+    if (w->s_gate_up == nullptr || w->s_down == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(w->s_gate_up) || !aligned4(w->s_down)) return MOE_ERR_INVALID_ARG;
   }
   if (is_nvfp4(cfg)) {
     if (w->g_gate_up == nullptr || w->g_down == nullptr) return MOE_ERR_INVALID_ARG;
@@ -140,7 +148,16 @@ moe_status run_ffn(const moe_config& cfg, const moe_weights& w, const void* x_ro
   if (shared_small)
     MOE_CUDA_TRY(launch_dense_small_ffn(x_shared, T, H, Is, w.shared_w_gate_up, w.shared_w_down, cfg.swiglu_limit,
                                         at<float>(ws, L.small_part), hs, shared_out, err, sms, stream));
-  if (!is_4bit(cfg)) {
+  if (is_fp8(cfg)) {
+    if (routed)
+      MOE_CUDA_TRY(launch_fp8_ffn(cfg, w, x_rows, gather_src, offsets, R, at<void>(ws, L.x_q), at<float>(ws, L.x_s),
+                                  at<float>(ws, L.h), at<void>(ws, L.h_q), at<float>(ws, L.h_s), w_perm, y_perm, err,
+                                  tile_queue(ws, kQueueFp8GateUp), sms, stream));
+    if (shared_tc) {
+      MOE_CUDA_TRY(launch_gemm_gateup(nullptr, &s_gu, cfg.swiglu_limit, err, qgu, sms, stream));
+      MOE_CUDA_TRY(launch_gemm_down(nullptr, &s_d, err, qd, sms, stream));
+    }
+  } else if (!is_4bit(cfg)) {
     FfnProblem r_gu{x_rows, R, offsets, E, w.w_gate_up, I, H, h, nullptr, gather_src, cfg.top_k, T};
     FfnProblem r_d{h, R, offsets, E, w.w_down, H, I, y_perm, w_perm};
     MOE_CUDA_TRY(launch_gemm_gateup(routed ? &r_gu : nullptr, shared_tc ? &s_gu : nullptr, cfg.swiglu_limit, err, qgu,
@@ -173,16 +190,16 @@ moe_status run_ffn(const moe_config& cfg, const moe_weights& w, const void* x_ro
 // copies them into the workspace's x_perm and the tensor-core kernel loads
 // contiguous token boxes (its per-row gather4 form, moe_grouped_swiglu_ffn_gather,
 // takes about twice as long: one TMA copy per four 128-byte rows is
-// latency-bound).  int4 and NVFP4 experts: the permute writes the maps only
-// and the activation conversion that every 4-bit kernel runs first gathers
-// the rows.
+// latency-bound).  int4, NVFP4 and FP8 experts: the permute writes the maps
+// only and the activation conversion that every such kernel runs first
+// gathers the rows.
 struct Rows {
   void* x_perm;                 // permute output, or nullptr (maps only)
   const void* x_rows;           // what run_ffn reads
   const int32_t* gather_src;    // nullptr, or the slot map of a gathered read
 };
 Rows routed_rows(const moe_config& cfg, void* ws, const WsLayout& L, const void* x, const int32_t* src) {
-  if (is_4bit(cfg)) return Rows{nullptr, x, src};
+  if (is_4bit(cfg) || is_fp8(cfg)) return Rows{nullptr, x, src};
   void* xp = at<void>(ws, L.x_perm);
   return Rows{xp, xp, nullptr};
 }
@@ -231,17 +248,22 @@ WsLayout ws_layout(const moe_config& cfg, int Tmax) {
   const bool four = cfg.expert_format == MOE_W_INT4_G128 || cfg.expert_format == MOE_W_NVFP4;
   // bf16 experts: the forward gathers the routed rows into x_perm (tiled TMA
   // copies then feed the tensor cores); 4-bit experts gather while converting
-  L.x_perm = take(four ? 0 : R * H * 2);
+  const bool fp8 = cfg.expert_format == MOE_W_FP8_B128;
+  L.x_perm = take(four || fp8 ? 0 : R * H * 2);
   // bf16 h, the 4-bit grouped GEMMs' fp16 h [R, I], or the 4-bit GEMVs' fp32
   // gate/up [R, 2I] (taken only below kInt4PrefillRowsPerExpert rows per expert)
   const size_t r_gemv = std::min(R, static_cast<size_t>(kInt4PrefillRowsPerExpert) * E);
-  L.h = take(four ? std::max(R * I * 2, r_gemv * 2 * I * 4) : R * I * 2);
+  L.h = take(four ? std::max(R * I * 2, r_gemv * 2 * I * 4) : fp8 ? R * 2 * I * 4 : R * I * 2);
   L.h_shared = take(T * Is * 2);
   L.y_perm = take(R * H * 2);
   L.shared_out = take(T * H * 2);
   const size_t kmax = std::max(H, I);
   L.act16 = take(four ? R * kmax * 2 : 0);
   L.small_part = take(Is > 0 ? dense_small_part_floats(static_cast<int>(H), static_cast<int>(Is)) * sizeof(float) : 0);
+  L.x_q = take(fp8 ? R * H : 0);
+  L.x_s = take(fp8 ? R * (H / 128) * sizeof(float) : 0);
+  L.h_q = take(fp8 ? R * I : 0);
+  L.h_s = take(fp8 ? R * (I / 128) * sizeof(float) : 0);
   L.total = off;
   return L;
 }
@@ -277,9 +299,20 @@ moe_status moe_config_validate(const moe_config* cfg) {
   if (std::isnan(c.swiglu_limit) || !(c.swiglu_limit > 0.f)) return MOE_ERR_INVALID_ARG;
   if (!std::isfinite(c.routed_scaling_factor)) return MOE_ERR_INVALID_ARG;
   if (c.renormalize != 0 && c.renormalize != 1) return MOE_ERR_INVALID_ARG;
-  if (c.expert_format != MOE_W_BF16 && c.expert_format != MOE_W_INT4_G128 && c.expert_format != MOE_W_NVFP4)
+  if (c.expert_format != MOE_W_BF16 && c.expert_format != MOE_W_INT4_G128 && c.expert_format != MOE_W_NVFP4 &&
+      c.expert_format != MOE_W_FP8_B128)
     return MOE_ERR_INVALID_ARG;
-  const bool four = c.expert_format != MOE_W_BF16;
+  if (c.score != MOE_SCORE_SIGMOID && c.score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID_ARG;
+  if (c.group_score != MOE_GROUP_SUM2 && c.group_score != MOE_GROUP_MAX) return MOE_ERR_INVALID_ARG;
+  if (c.num_groups < 0) return MOE_ERR_INVALID_ARG;
+  if (c.num_groups > 1) {
+    if (c.num_experts % c.num_groups != 0) return MOE_ERR_INVALID_ARG;
+    if (c.top_groups < 1 || c.top_groups > c.num_groups) return MOE_ERR_INVALID_ARG;
+    if (c.top_k > c.top_groups * (c.num_experts / c.num_groups)) return MOE_ERR_INVALID_ARG;
+    if (c.num_groups > MOE_MAX_GROUPS) return MOE_ERR_UNSUPPORTED;
+  }
+  const bool four = c.expert_format == MOE_W_INT4_G128 || c.expert_format == MOE_W_NVFP4;
+  if (is_fp8(c) && (c.hidden % 128 != 0 || c.expert_inter % 128 != 0)) return MOE_ERR_UNSUPPORTED;
   if (four && (c.hidden % 128 != 0 || c.expert_inter % 128 != 0)) return MOE_ERR_UNSUPPORTED;
   // the 4-bit paths feed h to fp16 tensor-core operands: |h| <= L^2 must stay finite in fp16
   if (four && !(c.swiglu_limit <= MOE_INT4_MAX_SWIGLU_LIMIT)) return MOE_ERR_UNSUPPORTED;
@@ -463,6 +496,66 @@ moe_status moe_forward_ep(const moe_config* cfg, const moe_weights* w, int32_t e
                   shared ? x : nullptr, shared_out, ws, L, stream, cfg->num_experts));
   return from_cuda(launch_combine(*cfg, y_perm, row_of, nullptr, shared_out, T, out_partial, offsets + expert_begin,
                                   El, stream));
+}
+
+moe_status moe_gate_topk(const moe_config* cfg, const void* logits, int32_t logits_type, int64_t row_stride,
+                         const float* correction_bias, int32_t T, int32_t* topk_ids, float* topk_w,
+                         moe_stream_t stream) {
+  MOE_TRY(moe_config_validate(cfg));
+  MOE_TRY(check_tokens(*cfg, T));
+  if (logits_type != MOE_F32 && logits_type != MOE_BF16 && logits_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (row_stride < cfg->num_experts) return MOE_ERR_INVALID_ARG;
+  if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == MOE_F32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(topk_ids) || !aligned4(topk_w) || !aligned4(correction_bias)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_gate(*cfg, logits, logits_type, row_stride, 1, 0, correction_bias, T, topk_ids, topk_w,
+                               stream));
+}
+
+moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t row_stride, const int32_t* src, int32_t src_div,
+                            int32_t rows, int32_t K, void* q, float* scale, moe_stream_t stream) {
+  if (x_type != MOE_F32 && x_type != MOE_BF16 && x_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || K < 16 || K % 16 != 0 || src_div < 1) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(rows) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  const int64_t size = x_type == MOE_F32 ? 4 : 2;
+  if (row_stride < K || (row_stride * size) % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale) || !aligned4(src)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_fp8_quantize(x, x_type, row_stride, src, src_div, rows, K, q, scale, nullptr, 0, stream));
+}
+
+moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_t groups, int32_t N, int32_t K, void* q,
+                                   float* scale, moe_stream_t stream) {
+  if (w_type != MOE_F32 && w_type != MOE_BF16 && w_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (groups < 0 || N < 1 || K < 16 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
+  const int64_t per = (static_cast<int64_t>(N) + 127) / 128 * ((static_cast<int64_t>(K) + 127) / 128);
+  if (per >= (int64_t(1) << 31) || per * groups >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;  // one block each
+  if (groups == 0) return MOE_OK;
+  if (w == nullptr || q == nullptr || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_fp8_quantize_weight(w, w_type, groups, N, K, q, scale, stream));
+}
+
+moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const int32_t* expert_offsets,
+                        int32_t groups, const void* w, const float* w_scale, int32_t N, int32_t K,
+                        const float* row_scale, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+  if (out_type != MOE_F32 && out_type != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || groups < 1 || N < 8 || N % 8 != 0 || K < 16 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (groups > 1 && expert_offsets == nullptr) return MOE_ERR_INVALID_ARG;
+  if (groups > MOE_MAX_EXPERTS || static_cast<int64_t>(rows) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(a_scale) || !aligned4(w_scale) || !aligned4(row_scale) || !aligned4(expert_offsets))
+    return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < MOE_WS_HEADER_BYTES) return MOE_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  const Fp8Problem p{a, a_scale, rows, expert_offsets, groups, w, w_scale, N, K, row_scale, out, out_type};
+  return from_cuda(launch_fp8_gemm(p, err_word(ws), tile_queue(ws, kQueueFp8GateUp), num_sms_current_device(), stream));
 }
 
 moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_bytes, moe_stream_t stream) {

@@ -26,7 +26,15 @@ struct WsHeader {
   int32_t pad[53];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
-enum TileQueueSlot { kQueueGateUp = 0, kQueueDown = 2, kQueueInt4GateUp = 4, kQueueInt4Down = 6 };
+// (a layer has 4-bit or FP8 experts, never both: their kernels share the slots)
+enum TileQueueSlot {
+  kQueueGateUp = 0,
+  kQueueDown = 2,
+  kQueueInt4GateUp = 4,
+  kQueueInt4Down = 6,
+  kQueueFp8GateUp = 4,
+  kQueueFp8Down = 6
+};
 
 __device__ __forceinline__ void report_error(int32_t* err, int32_t code, int32_t detail) {
   if (err != nullptr && atomicCAS(err, 0, code) == 0) err[1] = detail;

@@ -142,6 +142,44 @@ cudaError_t launch_int4_ffn_prefill(const moe_config& cfg, const moe_weights& w,
                                     void* h16, const float* w_perm, void* y_perm, int32_t* err, int32_t* queues,
                                     int num_sms, cudaStream_t stream);
 
+// Expert selection from logits (gate.cu): `slices` fp32 partial logits per
+// value are added in ascending order (1: the logits themselves).
+cudaError_t launch_gate(const moe_config& cfg, const void* logits, int dtype, int64_t stride, int slices,
+                        int64_t slice_stride, const float* bias, int T, int32_t* ids, float* w, cudaStream_t stream);
+// Routing choices beyond sigmoid scores over all experts go through launch_gate.
+inline bool plain_routing(const moe_config& cfg) { return cfg.score == MOE_SCORE_SIGMOID && cfg.num_groups <= 1; }
+
+// FP8 quantisation (fp8_quant.cu).  range: NULL, or expert offsets: only rows
+// in [range[0], range[range_len]) are written.
+cudaError_t launch_fp8_quantize(const void* x, int dtype, int64_t stride, const int32_t* src, int src_div, int rows,
+                                int K, void* q, float* scale, const int32_t* range, int range_len,
+                                cudaStream_t stream);
+cudaError_t launch_fp8_quantize_weight(const void* w, int dtype, int groups, int N, int K, void* q, float* scale,
+                                       cudaStream_t stream);
+
+// Block-scaled FP8 products (fp8_gemm.cu): see moe_fp8_gemm.
+struct Fp8Problem {
+  const void* a;           // E4M3 [rows, K]
+  const float* a_scale;    // [ceil(K / 128), rows]
+  int rows;
+  const int32_t* offsets;  // [groups + 1] device, or nullptr: one group of `rows`
+  int groups;
+  const void* w;           // E4M3 [groups, N, K]
+  const float* w_scale;    // [groups, ceil(N / 128), ceil(K / 128)]
+  int N, K;
+  const float* row_scale;  // [rows] or nullptr
+  void* out;               // [rows, N] of out_type
+  int out_type;            // MOE_BF16 or MOE_F32
+};
+// queue: the launch's two tile-queue words in the workspace header (zero).
+cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
+// The routed FFN on FP8 experts: quantised rows x_q / x_s, activations h_q /
+// h_s (scratch); queues: four tile-queue words (gate/up, then down).
+cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
+                           const int32_t* offsets, int rows, void* x_q, float* x_s, float* gu, void* h_q, float* h_s,
+                           const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms,
+                           cudaStream_t stream);
+
 // Shared expert for T <= 32 tokens: split-K tensor-core GEMMs streaming the
 // weights across all SMs, then an ordered sum of the K slices.
 constexpr int kDenseSmallMaxTokens = 32;
@@ -154,7 +192,8 @@ cudaError_t launch_dense_small_ffn(const void* x, int T, int H, int Is, const vo
 // Workspace layout (byte offsets from the workspace base; 256-aligned).
 struct WsLayout {
   size_t header, logits, w_split, ids, wts, offsets, row_of, src, w_perm, block_base, local_rank;
-  size_t x_perm, h, h_shared, y_perm, shared_out, act16, small_part, total;
+  size_t x_perm, h, h_shared, y_perm, shared_out, act16, small_part;
+  size_t x_q, x_s, h_q, h_s, total;  // FP8 experts: quantised rows and activations with their scales
 };
 WsLayout ws_layout(const moe_config& cfg, int Tmax);
 

@@ -475,6 +475,8 @@ cudaError_t launch_router(const moe_config& cfg, const moe_weights& w, const voi
   if (err_c != cudaSuccess) return err_c;
   err_c = launch_router_gemm(x, T, H, w_split, E, p.ks, part, err, num_sms, stream);
   if (err_c != cudaSuccess) return err_c;
+  if (!plain_routing(cfg))  // softmax scores or expert groups: select from the fp32 logits
+    return launch_gate(cfg, part, MOE_F32, E, p.ks, static_cast<int64_t>(T) * E, w.correction_bias, T, ids, wts, stream);
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   if (T < num_sms * kTopkWarps) {
     // few tokens: one token per block, so 256 threads read its partial sums

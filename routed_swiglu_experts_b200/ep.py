@@ -86,7 +86,8 @@ class ExpertParallelLayer:
                  routed_scaling_factor, renormalize, router_w, correction_bias, w_gate_up, w_down,
                  s_gate_up=None, s_down=None, shared_w_gate_up=None, shared_w_down=None,
                  g_gate_up=None, g_down=None, rank: int = 0, world: int = 1, max_tokens: int = 0,
-                 group=None):
+                 group=None, score=_abi.MOE_SCORE_SIGMOID, num_groups: int = 0, top_groups: int = 0,
+                 group_score=_abi.MOE_GROUP_SUM2):
         loc = local_tensors(rank, world, num_experts, shared_inter, w_gate_up=w_gate_up, w_down=w_down,
                             s_gate_up=s_gate_up, s_down=s_down, shared_w_gate_up=shared_w_gate_up,
                             shared_w_down=shared_w_down, g_gate_up=g_gate_up, g_down=g_down)
@@ -94,7 +95,8 @@ class ExpertParallelLayer:
         s0, s1 = loc["shared_slice"]
         fmt = _abi.weight_format(w_gate_up, g_gate_up)
         self.cfg = _abi.make_config(hidden, num_experts, top_k, expert_inter, s1 - s0, swiglu_limit,
-                                    routed_scaling_factor, renormalize, fmt)
+                                    routed_scaling_factor, renormalize, fmt, score, num_groups, top_groups,
+                                    group_score)
         st = _abi.moe_config_validate(self.cfg)
         if st != _abi.MOE_OK:
             raise _abi.MoEError(st, "moe_config_validate")
