@@ -1,8 +1,33 @@
-// Products of FP8 E4M3 rows and weights with a scale per block of 128:
+// Products of FP8 E4M3 rows and weights with a scale per block of 128, dense
+// or grouped by expert, on CTA pairs (tcgen05.mma.cta_group::2,
+// kind::f8f6f4):
 //   out[r, n] = c_r * sum_b sa[b, r] * sw[g, n / 128, b]
 //               * sum_{k in block b} a[r, k] * w[g, n, k]
-// dense or grouped by expert row offsets.  Plain form: a 64 x 64 tile per
-// block on the fp32 cores, one K block of 128 at a time in shared memory.
+// and the gate/up product of an FP8 expert, whose epilogue applies
+//   h = silu(min(G, L)) * clamp(U, -L, L)
+// and quantises h along the row, 128 features to a scale.
+//
+// The scales differ from K block to K block, so the tensor cores sum one
+// block of 128 (four MMAs) into one of several TMEM buffers and the epilogue
+// warps add scale * partial sum into fp32 registers while the next block is
+// multiplied.  The weights are the M operand and the rows ("tokens") N, as in
+// ffn_gemm.cu: a tile is 256 weight rows x up to TOK tokens of one expert,
+// rounded up to 16 tokens only.  A CTA's 128 weight rows lie in one scale
+// block, so a partial sum's scale is sa[token] times a number that is the same
+// for the whole CTA.  TMEM is read in the 16x256b shape: a thread holds 4
+// weight rows x 8 tokens of a 32-token chunk, so it needs 8 token scales for
+// 32 sums (with a row per thread it would need 32), and pairs of neighbouring
+// tokens go through fma.rn.f32x2.
+//
+// Roles per CTA (384 threads): warps 0-7 scale, add and write (two groups of
+// four warps; group w takes the 32-token chunks 2 i + w), warp 8 TMA
+// producer, warp 9 TMEM owner (+ MMA issuer in the first CTA), warp 10 copies
+// each K block's scales into a ring (warp 11 only fills its warpgroup).  Tile
+// queue and tile order as in ffn_gemm.cu.  Every mbarrier wait is bounded (MOE_ERR_DEVICE_TIMEOUT); a
+// scaling warp whose wait gave up goes on without waiting until the tile ends,
+// so that no warp is left alone at a named barrier.
+#include <cstring>
+
 #include "fp8_common.cuh"
 #include "moe_internal.h"
 
@@ -10,151 +35,843 @@ namespace moe {
 
 namespace {
 
-constexpr int kT = 64;
+constexpr int BK = 128;                       // one scale block, 128 bytes
+constexpr int ROWS = 128;                     // weight rows per CTA
+constexpr int A_BYTES = ROWS * BK;            // 16 KB
+constexpr int THREADS = 384;
+// Registers per thread after the split: the kernel starts with 168 x 384 =
+// 64512; the two warpgroups that hold sums take 208, the other one keeps 88
+// (256 x 208 + 128 x 88 = 64512).
+constexpr int kSumRegs = 208, kOtherRegs = 88;
+constexpr int QD = 8;                         // tile-id ring depth
+constexpr int SC = 4;                         // scale ring depth
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint64_t kTimeoutNs = 4000000000ull;
+constexpr int kStage = 2560;                  // output staging bytes per scaling warp
+// readers of a tile id: MMA issuer of the first CTA, producer of the second;
+// 8 scaling warps and the scale warp of both
+constexpr uint32_t kTileReaders = 1 + 1 + 2 * 9;
 
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t v, float* f) {
-  const uint32_t lo = e4m3x2_to_f16x2(static_cast<unsigned short>(v & 0xFFFFu));
-  const uint32_t hi = e4m3x2_to_f16x2(static_cast<unsigned short>(v >> 16));
-  const uint32_t h[2] = {lo, hi};
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
-        : "r"(h[i]));
+enum class Kind { GateUp, Plain };
+
+constexpr int kTokBoxes = 5;  // token boxes of TOK / 2 >> i rows, down to 8
+
+template <int TOK>
+struct Shape {
+  static constexpr int NBUF = 512 / TOK;               // TMEM buffers
+  static constexpr int NC = TOK / 64;                  // 32-token chunks per group of scaling warps
+  static constexpr int B_BYTES = TOK / 2 * BK;         // this CTA's half of the tokens
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = TOK == 256 ? 5 : 8;
+  static constexpr int BOXES = TOK == 256 ? 5 : 3;
+};
+
+struct alignas(64) Params {
+  CUtensorMap tma_w;             // GateUp {K, r 8, u 2, h 2, blocks of 16 rows}; Plain {K, N, G}
+  CUtensorMap tma_x[kTokBoxes];  // {K, rows}, box {128, TOK / 2 >> i}
+  const int32_t* offsets;        // [groups + 1], or nullptr: one group of `rows`
+  const float* a_scale;          // [k_blocks, rows]
+  const float* w_scale;          // [groups, n_blocks, k_blocks]
+  void* out;                     // Plain: [rows, N]; GateUp: E4M3 [rows, N]
+  float* out_scale;              // GateUp: [N / 128, rows]
+  const float* row_scale;        // Plain: per row, or nullptr
+  int32_t groups, rows, N;       // N: output columns (GateUp: features)
+  int32_t k_blocks, n_blocks;    // scale blocks of the weight
+  int32_t f_tiles;               // weight-row tiles per group
+  int32_t out_f32;
+  float limit;
+  int32_t* err;
+  int32_t* queue;                // {next tile, pairs retired}: zero at launch, left zero at exit
+  uint64_t wait_ns;
+  int32_t test_withhold;         // test hook: never signal the first partial sum
+};
+
+template <int TOK>
+struct Ctl {
+  uint64_t full[Shape<TOK>::STAGES];
+  uint64_t empty[Shape<TOK>::STAGES];
+  uint64_t tmem_full[Shape<TOK>::NBUF];
+  uint64_t tmem_empty[Shape<TOK>::NBUF];
+  uint64_t sc_full[SC];
+  uint64_t sc_empty[SC];
+  uint64_t amax_full[2];            // the other CTA's maxima of this group's tokens
+  uint64_t mma_done;
+  uint64_t tq_full[QD];
+  uint64_t tq_empty[QD];
+  int32_t tq[QD];
+  uint32_t tmem_base;
+  int32_t abort_flag;
+  int32_t tiles;
+  int32_t off[MOE_MAX_EXPERTS + 1];
+  int32_t tp[MOE_MAX_EXPERTS + 1];  // token-tile prefix per group
+  alignas(16) float sc[SC][TOK + 4];          // token scales of a K block, then the weight scales of gate and up
+  alignas(16) uint32_t amax[2][4][TOK / 2];   // per group and warp
+  uint32_t peer_amax[2][2][TOK / 2];          // written by the other CTA, double-buffered over tiles
+  alignas(16) float inv[2][TOK / 2];
+  alignas(16) unsigned char stage[8][kStage];
+};
+
+template <int TOK>
+constexpr size_t smem_bytes() {
+  return 1024 + static_cast<size_t>(Shape<TOK>::STAGES) * Shape<TOK>::STAGE + sizeof(Ctl<TOK>);
+}
+static_assert(smem_bytes<256>() <= 232448 && smem_bytes<64>() <= 232448, "fits the 227 KB opt-in shared memory");
+
+struct Tile {
+  int g, fidx, row0, ntok, nmma;
+};
+
+// Group by group; inside a group weight-row tile major, token tile minor.
+template <int TOK>
+__device__ __forceinline__ Tile decode(const Params& P, const Ctl<TOK>& c, int t) {
+  Tile ti;
+  int tm, tmi, r0, r1;
+  if (P.offsets != nullptr) {
+    const int u = t / P.f_tiles;
+    int lo = 0, hi = P.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (c.tp[mid] <= u) lo = mid; else hi = mid;
+    }
+    ti.g = lo;
+    tm = c.tp[lo + 1] - c.tp[lo];
+    t -= c.tp[lo] * P.f_tiles;
+    r0 = c.off[lo];
+    r1 = c.off[lo + 1];
+  } else {
+    tm = (P.rows + TOK - 1) / TOK;
+    ti.g = 0;
+    r0 = 0;
+    r1 = P.rows;
+  }
+  ti.fidx = t / tm;
+  tmi = t - ti.fidx * tm;
+  ti.row0 = r0 + tmi * TOK;
+  ti.ntok = min(TOK, r1 - ti.row0);
+  ti.nmma = (ti.ntok + 15) / 16 * 16;
+  return ti;
 }
 
-template <typename TOut>
-__global__ void __launch_bounds__(256)
-    fp8_gemm_kernel(const unsigned char* __restrict__ a, const float* __restrict__ sa, int rows,
-                    const int32_t* __restrict__ offsets, int groups, const unsigned char* __restrict__ w,
-                    const float* __restrict__ sw, int N, int K, const float* __restrict__ row_scale,
-                    TOut* __restrict__ out) {
-  __shared__ float s_a[32][kT + 1], s_w[32][kT + 1];
-  // the group and first row of this block's tile of rows
-  int g = 0, r0 = 0, r1 = rows, t = blockIdx.y;
-  if (offsets != nullptr) {
-    for (g = 0; g < groups; ++g) {
-      r0 = offsets[g];
-      r1 = offsets[g + 1];
-      const int n = (r1 - r0 + kT - 1) / kT;
-      if (t < n) break;
-      t -= n;
-    }
-    if (g == groups) return;
-  }
-  r0 += t * kT;
-  if (r0 >= r1) return;
-  const int n0 = blockIdx.x * kT;
-  const int nb = (N + 127) / 128, kb = (K + 127) / 128;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int b = 0; b < kb; ++b) {
-    float part[4][4] = {};
-    for (int k0 = b * 128; k0 < min(K, b * 128 + 128); k0 += 32) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kT * 8; i += 256) {
-        const int row = i / 8, k = k0 + (i % 8) * 4;
-        float f[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r0 + row < r1 && k < K)
-          e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(a + static_cast<size_t>(r0 + row) * K + k), f);
-        if (n0 + row < N && k < K)
-          e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(w + (static_cast<size_t>(g) * N + n0 + row) * K + k), h);
+// Sums of one thread: chunk, 16-row half, then pair (2 q + rh): tokens
+// 8 q + 2 (lane % 4) + {0, 1} of the chunk in weight row
+// 16 half + 8 rh + lane / 4 of the warp's 32.
+template <int NC>
+using Acc = uint64_t[NC][2][8];
+
+template <int TOK, Kind KIND>
+__device__ __forceinline__ void add_half(uint64_t (&acc)[8], const uint32_t (&v)[16], const uint64_t (&s0)[4],
+                                         const uint64_t (&s1)[4]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s_a[(i % 8) * 4 + j][row] = f[j];
-          s_w[(i % 8) * 4 + j][row] = h[j];
+  for (int q = 0; q < 4; ++q) {
+    acc[2 * q] = fma_f32x2(pack_b32x2(v[4 * q], v[4 * q + 1]), s0[q], acc[2 * q]);
+    acc[2 * q + 1] = fma_f32x2(pack_b32x2(v[4 * q + 2], v[4 * q + 3]), s1[q], acc[2 * q + 1]);
+  }
+}
+
+// Plain epilogue of a warp: 32 weight rows x the group's chunks, times the
+// row's weight, through the warp's staging to rows of out.
+template <int TOK>
+__device__ __forceinline__ void write_plain(const Params& P, const Tile& ti, unsigned char* stage, int n_warp, int grp,
+                                            int lane, Acc<Shape<TOK>::NC>& acc) {
+  const int N = P.N;
+#pragma unroll
+  for (int c = 0; c < Shape<TOK>::NC; ++c) {
+    const int col0 = 32 * (2 * c + grp);
+    if (col0 >= ti.ntok) continue;
+    if (P.row_scale != nullptr) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = col0 + 8 * q + 2 * (lane & 3);
+        const float w0 = col < ti.ntok ? __ldg(P.row_scale + ti.row0 + col) : 0.f;
+        const float w1 = col + 1 < ti.ntok ? __ldg(P.row_scale + ti.row0 + col + 1) : 0.f;
+        const uint64_t w = pack_f32x2(w0, w1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          acc[c][h][2 * q] = mul_f32x2(acc[c][h][2 * q], w);
+          acc[c][h][2 * q + 1] = mul_f32x2(acc[c][h][2 * q + 1], w);
         }
       }
-      __syncthreads();
-#pragma unroll 8
-      for (int k = 0; k < 32; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(s_a[k][ty * 4 + i], s_w[k][tx * 4 + j], part[i][j]);
     }
+    if (P.out_f32) {
+      // 16 tokens at a time: 32 fp32 per token, rows 144 bytes apart
+      float* st = reinterpret_cast<float*>(stage);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int part = 0; part < 2; ++part) {
+        __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = min(r0 + ty * 4 + i, rows - 1), n = min(n0 + tx * 4 + j, N - 1);
-        acc[i][j] += part[i][j] * (sa[static_cast<size_t>(b) * rows + r] *
-                                   sw[(static_cast<size_t>(g) * nb + n / 128) * kb + b]);
+        for (int qq = 0; qq < 2; ++qq)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+              const float2 v = unpack_f32x2(acc[c][h][2 * (2 * part + qq) + rh]);
+              const int n = 16 * h + 8 * rh + (lane >> 2), tok = 8 * qq + 2 * (lane & 3);
+              st[tok * 36 + n] = v.x;
+              st[(tok + 1) * 36 + n] = v.y;
+            }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int u = lane + 32 * i, tok = u >> 3, n = n_warp + (u & 7) * 4;
+          const int col = col0 + 16 * part + tok;
+          if (col < ti.ntok && n < N)
+            *reinterpret_cast<uint4*>(static_cast<float*>(P.out) + static_cast<size_t>(ti.row0 + col) * N + n) =
+                *reinterpret_cast<const uint4*>(st + tok * 36 + (u & 7) * 4);
+        }
       }
+    } else {
+      // 32 tokens x 32 bf16 (64 bytes), rows 80 bytes apart
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+          uint32_t r[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 v = unpack_f32x2(acc[c][h][2 * q + rh]);
+            r[q] = pack_bf16x2(v.x, v.y);
+          }
+          stmatrix_x4_trans(smem_u32(stage + lane * 80 + (2 * h + rh) * 16), r[0], r[1], r[2], r[3]);
+        }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = lane + 32 * i, tok = u >> 2, n = n_warp + (u & 3) * 8;
+        if (col0 + tok < ti.ntok && n < N)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + static_cast<size_t>(ti.row0 + col0 + tok) * N +
+                                    n) = *reinterpret_cast<const uint4*>(stage + tok * 80 + (u & 3) * 16);
+      }
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (r < r1 && n < N) {
-        const float v = acc[i][j] * (row_scale != nullptr ? row_scale[r] : 1.f);
-        if (sizeof(TOut) == 4)
-          reinterpret_cast<float*>(out)[static_cast<size_t>(r) * N + n] = v;
-        else
-          reinterpret_cast<__nv_bfloat16*>(out)[static_cast<size_t>(r) * N + n] = __float2bfloat16_rn(v);
-      }
-    }
 }
 
-// h = silu(min(G, L)) * clamp(U, -L, L) of the fp32 gate/up rows, quantised
-// along the row: one warp per 128 features of a row.
-__global__ void __launch_bounds__(256)
-    fp8_swiglu_kernel(const float* __restrict__ gu, const int32_t* __restrict__ range, int range_len, int rows, int I,
-                      float L, unsigned char* __restrict__ q, float* __restrict__ scale) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32, kb = I / 128;
-  const int r = static_cast<int>(i / kb), b = static_cast<int>(i % kb);
-  if (r >= rows || r < range[0] || r >= range[range_len]) return;
-  const float4 g = *reinterpret_cast<const float4*>(gu + static_cast<size_t>(r) * 2 * I + b * 128 + lane * 4);
-  const float4 u = *reinterpret_cast<const float4*>(gu + static_cast<size_t>(r) * 2 * I + I + b * 128 + lane * 4);
-  const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
-  float h[4];
-  uint32_t m = 0u;
+// Largest value bits of every token of the group over the warp's 16
+// features: halves of the tokens change hands until each lane has 4 (or, for
+// one chunk, a lane of every 8).  amax: the warp's row of the group's tokens.
+template <int NC>
+__device__ __forceinline__ void warp_amax(uint32_t (&m)[NC][8], uint32_t* amax, int lane) {
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  if constexpr (NC == 4) {
+    uint32_t x[2][8], y[8], z[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    h[j] = swiglu_clamped(gv[j], uv[j], L);
-    m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t give = b4 ? m[c][j] : m[c + 2][j], keep = b4 ? m[c + 2][j] : m[c][j];
+        x[c][j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t give = b3 ? x[0][j] : x[1][j], keep = b3 ? x[1][j] : x[0][j];
+      y[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t give = b2 ? y[j] : y[j + 4], keep = b2 ? y[j + 4] : y[j];
+      z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+    }
+    const int at = 32 * (2 * b4 + b3) + 16 * b2 + 2 * (lane & 3);
+    *reinterpret_cast<uint2*>(amax + at) = make_uint2(z[0], z[1]);
+    *reinterpret_cast<uint2*>(amax + at + 8) = make_uint2(z[2], z[3]);
+  } else {
+    uint32_t z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t give = b2 ? m[0][j] : m[0][j + 4], keep = b2 ? m[0][j + 4] : m[0][j];
+      z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+      z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 8));
+      z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 16));
+    }
+    if (!b4 && !b3) {
+      const int at = 16 * b2 + 2 * (lane & 3);
+      *reinterpret_cast<uint2*>(amax + at) = make_uint2(z[0], z[1]);
+      *reinterpret_cast<uint2*>(amax + at + 8) = make_uint2(z[2], z[3]);
+    }
   }
-  m = __reduce_max_sync(0xffffffffu, m);
-  float sc, inv;
-  e4m3_block_scale(m, sc, inv);
-  *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(r) * I + b * 128 + lane * 4) =
-      e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-  if (lane == 0) scale[static_cast<size_t>(b) * rows + r] = sc;
+}
+
+template <Kind KIND, int TOK>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    fp8_pair_kernel(const __grid_constant__ Params P) {
+  using S = Shape<TOK>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  unsigned char* smem_a = smem;
+  unsigned char* smem_b = smem + S::STAGES * A_BYTES;
+  Ctl<TOK>& c = *reinterpret_cast<Ctl<TOK>*>(smem + S::STAGES * S::STAGE);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&c.full[s], 1);
+      mbar_init(&c.empty[s], 1);
+    }
+    for (int b = 0; b < S::NBUF; ++b) {
+      mbar_init(&c.tmem_full[b], 1);
+      mbar_init(&c.tmem_empty[b], 2 * 8);
+    }
+    for (int s = 0; s < SC; ++s) {
+      mbar_init(&c.sc_full[s], 32);
+      mbar_init(&c.sc_empty[s], 8);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&c.amax_full[i], TOK / 2);
+    mbar_init(&c.mma_done, 1);
+    for (int i = 0; i < QD; ++i) {
+      mbar_init(&c.tq_full[i], 1);
+      mbar_init(&c.tq_empty[i], kTileReaders);
+    }
+    c.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&P.tma_w);
+    for (int b = 0; b < S::BOXES; ++b) tma_prefetch_desc(&P.tma_x[b]);
+  }
+  if (warp == 9) tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
+  if (warp == 0) {  // offsets + token-tile prefix, or the one group's tile count
+    int tiles;
+    if (P.offsets != nullptr) {
+      const int G = P.groups;
+      const int per = (G + 31) / 32;
+      int local = 0;
+      for (int j = 0; j < per; ++j) {
+        const int g = lane * per + j;
+        if (g < G) {
+          const int o0 = P.offsets[g], o1 = P.offsets[g + 1];
+          c.off[g] = o0;
+          local += (o1 - o0 + TOK - 1) / TOK;
+        }
+      }
+      int incl = local;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int run = incl - local;
+      for (int j = 0; j < per; ++j) {
+        const int g = lane * per + j;
+        if (g < G) {
+          c.tp[g] = run;
+          run += (P.offsets[g + 1] - P.offsets[g] + TOK - 1) / TOK;
+        }
+      }
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
+      if (lane == 0) {
+        c.off[G] = P.offsets[G];
+        c.tp[G] = total;
+      }
+      tiles = total * P.f_tiles;
+    } else {
+      tiles = ((P.rows + TOK - 1) / TOK) * P.f_tiles;
+    }
+    if (lane == 0) c.tiles = tiles;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // barriers of both CTAs initialised before any remote arrive
+  tc_fence_after();
+
+  const uint32_t tmem_base = c.tmem_base;
+  const int total_tiles = c.tiles;
+  const int nkb = P.k_blocks;
+  volatile int32_t* abort_flag = &c.abort_flag;
+  auto fail = [&](int detail) {
+    *abort_flag = 1;
+    report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, detail);
+  };
+
+  int q = 0;          // tile-id ring position of this role
+  uint32_t qph = 0;
+  auto next_q = [&] {
+    if (++q == QD) {
+      q = 0;
+      qph ^= 1u;
+    }
+  };
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == 8) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int t_next = -2;  // next queue position, once fetched
+      for (;;) {
+        int t = -1;
+        if (leader) {
+          if (!mbar_wait_bounded<true>(&c.tq_empty[q], qph ^ 1u, abort_flag, P.wait_ns)) {
+            fail(55);
+            break;
+          }
+          if (t_next == -2) t_next = atomicAdd(P.queue, 1);
+          t = t_next < total_tiles ? t_next : -1;
+          t_next = -2;
+          c.tq[q] = t;
+          st_cluster_u32(map_to_rank(smem_u32(&c.tq[q]), 1), static_cast<uint32_t>(t));
+          mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
+          mbar_arrive(&c.tq_full[q]);
+        } else {
+          if (!mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
+            fail(56);
+            break;
+          }
+          t = c.tq[q];
+          mbar_arrive_cluster(leader_bar(&c.tq_empty[q]));
+        }
+        next_q();
+        if (t < 0) break;
+        const Tile ti = decode<TOK>(P, c, t);
+        const int half = ti.nmma / 2;  // token rows of this CTA (a multiple of 8)
+        const int xrow = ti.row0 + static_cast<int>(rank) * half;
+        int xb = 0;
+        while (xb + 1 < S::BOXES && half <= (TOK / 2 >> (xb + 1))) ++xb;
+        const uint32_t b_bytes = static_cast<uint32_t>(TOK / 2 >> xb) * BK;
+        const int kpre = nkb > 4 ? nkb - 4 : 0;  // fetch the next id while the last copies run
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_bounded(&c.empty[stage], phase ^ 1u, abort_flag, P.wait_ns)) {
+            fail(51);
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&c.full[stage], 2u * (A_BYTES + b_bytes));
+          const uint32_t bar = leader_bar(&c.full[stage]);
+          unsigned char* sa = smem_a + stage * A_BYTES;
+          if (KIND == Kind::GateUp)
+            tma_load_5d_pair(sa, &P.tma_w, kb * BK, 0, 0, 0,
+                             (ti.g * 2 * P.N + ti.fidx * 128 + static_cast<int>(rank) * 64) / 16, bar);
+          else
+            tma_load_3d_pair(sa, &P.tma_w, kb * BK, ti.fidx * 256 + static_cast<int>(rank) * 128, ti.g, bar);
+          tma_load_2d_pair(smem_b + stage * S::B_BYTES, &P.tma_x[xb], kb * BK, xrow, bar);
+          if (leader && kb == kpre) t_next = atomicAdd(P.queue, 1);
+          ++issued;
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (leader) {
+        // retire from the queue; the last pair of the launch resets it
+        __threadfence();
+        if (atomicAdd(P.queue + 1, 1) == npairs - 1) {
+          __threadfence();
+          atomicExch(P.queue, 0);
+          atomicExch(P.queue + 1, 0);
+        }
+        // drain: the last copy of each stage (both CTAs' bytes land here)
+        const int nst = issued < S::STAGES ? issued : S::STAGES;
+        for (int j = 0; j < nst; ++j) {
+          const int i = issued - 1 - j;
+          volatile int32_t never = 0;
+          if (!mbar_wait_bounded(&c.full[i % S::STAGES], static_cast<uint32_t>((i / S::STAGES) & 1), &never,
+                                 kTimeoutNs))
+            report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 59);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // -------------------------------------------- MMA issuer (first CTA) --
+    if (leader && lane == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true, first = true;
+      for (;;) {
+        if (!mbar_wait_bounded(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
+          fail(57);
+          break;
+        }
+        const int t = c.tq[q];
+        mbar_arrive(&c.tq_empty[q]);
+        next_q();
+        if (t < 0) break;
+        const Tile ti = decode<TOK>(P, c, t);
+        const uint32_t idesc = umma_idesc_f16(2 * ROWS, ti.nmma);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_bounded(&c.tmem_empty[buf], buf_phase ^ 1u, abort_flag, P.wait_ns)) {
+            fail(52);
+            ok = false;
+            break;
+          }
+          if (!mbar_wait_bounded(&c.full[stage], phase, abort_flag, P.wait_ns)) {
+            fail(53);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem_a + stage * A_BYTES);
+          const uint32_t b_addr = smem_u32(smem_b + stage * S::B_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            umma_e4m3_pair(tmem_base + static_cast<uint32_t>(buf * TOK), sw128_kmajor_desc(a_addr + kk * 32),
+                           sw128_kmajor_desc(b_addr + kk * 32), idesc, kk != 0 ? 1u : 0u);
+          umma_commit_pair(&c.empty[stage]);
+          if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
+          first = false;
+          if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == S::NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      umma_commit_pair_leader(&c.mma_done);
+      volatile int32_t never = 0;
+      if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 58);
+    }
+  } else if (warp == 10) {
+    // --------------------------------------------------- scales, a K block ahead
+    const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
+    int slot = 0;
+    uint32_t sph = 0;
+    for (;;) {
+      bool got = mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) fail(61);
+        break;
+      }
+      const int t = c.tq[q];
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+      next_q();
+      if (t < 0) break;
+      const Tile ti = decode<TOK>(P, c, t);
+      const float* sa = P.a_scale + ti.row0;
+      // the weight's block row: gate and up rows lie in two
+      int nb = KIND == Kind::GateUp ? ti.fidx : min(ti.fidx * 2 + static_cast<int>(rank), P.n_blocks - 1);
+      if (KIND == Kind::GateUp && lane == 1) nb += P.N / 128;
+      const float* sw = P.w_scale + (static_cast<size_t>(ti.g) * P.n_blocks + nb) * nkb;
+      const int n = ti.ntok;
+      for (int kb = 0; kb < nkb; ++kb) {
+        got = mbar_wait_bounded(&c.sc_empty[slot], sph ^ 1u, abort_flag, P.wait_ns);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) fail(62);
+          break;
+        }
+        const uint32_t dst = smem_u32(c.sc[slot]);
+        for (int i = lane; i < ti.nmma; i += 32)
+          cp_async4(dst + i * 4, sa + static_cast<size_t>(kb) * P.rows + min(i, n - 1), i < n);
+        if (lane < (KIND == Kind::GateUp ? 2 : 1)) cp_async4(dst + (TOK + lane) * 4, sw + kb, true);
+        cp_async_mbar_arrive(&c.sc_full[slot]);
+        if (++slot == SC) {
+          slot = 0;
+          sph ^= 1u;
+        }
+      }
+      if (!__all_sync(0xffffffffu, got)) break;
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    // ---------------------------------------- scale, add, write (warps 0-7) --
+    const int grp = warp >> 2, w4 = warp & 3;
+    const uint32_t lane_addr = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tmem_empty_leader = map_to_rank(smem_u32(&c.tmem_empty[0]), 0);
+    const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
+    unsigned char* stage = c.stage[warp];
+    int buf = 0, slot = 0;
+    uint32_t buf_phase = 0, sph = 0;
+    uint32_t tile_no = 0;
+    bool ok = true;
+    for (;;) {
+      const bool gotq = ok && mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
+      if (!named_barrier_and(1, 256, gotq)) {  // all eight warps go on or leave together
+        if (lane == 0 && ok && !gotq) fail(60);
+        break;
+      }
+      const int t = c.tq[q];
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+      next_q();
+      if (t < 0) break;
+      const Tile ti = decode<TOK>(P, c, t);
+      const int nch = (ti.nmma + 31) / 32;
+      const int mine = (nch - grp + 1) / 2;  // chunks of this group: 2 c + grp < nch
+      Acc<S::NC> acc;
+#pragma unroll
+      for (int i = 0; i < S::NC; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[i][h][j] = 0ull;
+
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (ok) {
+          ok = mbar_wait_bounded(&c.sc_full[slot], sph, abort_flag, P.wait_ns);
+          ok = ok && mbar_wait_bounded(&c.tmem_full[buf], buf_phase, abort_flag, P.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok && lane == 0) fail(54);
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t tb = tmem_base + lane_addr + static_cast<uint32_t>(buf * TOK + 32 * grp);
+        const float* sx = c.sc[slot] + 32 * grp + 2 * (lane & 3);
+        const float g0 = c.sc[slot][TOK], g1 = KIND == Kind::GateUp ? c.sc[slot][TOK + 1] : g0;
+        const uint64_t sg = pack_f32x2(g0, g0), su = pack_f32x2(g1, g1);
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+        };
+        uint32_t va[16], vb[16];
+        if (mine > 0) tmem_ld16x256b_x4(tb, va);
+        else release();
+#pragma unroll
+        for (int i = 0; i < S::NC; ++i) {
+          if (i < mine) {
+            uint64_t s0[4], s1[4];
+#pragma unroll
+            for (int qq = 0; qq < 4; ++qq) {
+              const float2 s = *reinterpret_cast<const float2*>(sx + 64 * i + 8 * qq);
+              const uint64_t p = pack_f32x2(s.x, s.y);
+              s0[qq] = mul_f32x2(p, sg);
+              s1[qq] = KIND == Kind::GateUp ? mul_f32x2(p, su) : s0[qq];
+            }
+            tmem_ld_wait_regs(va);
+            tmem_ld16x256b_x4(tb + (16u << 16) + 64 * i, vb);
+            add_half<TOK, KIND>(acc[i][0], va, s0, s1);
+            tmem_ld_wait_regs(vb);
+            if (i + 1 < mine) tmem_ld16x256b_x4(tb + 64 * (i + 1), va);
+            else release();
+            add_half<TOK, KIND>(acc[i][1], vb, s0, s1);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.sc_empty[slot]);
+        if (++slot == SC) {
+          slot = 0;
+          sph ^= 1u;
+        }
+        if (++buf == S::NBUF) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+
+      if (KIND == Kind::Plain) {
+        const int n_warp = ti.fidx * 256 + static_cast<int>(rank) * 128 + w4 * 32;
+        write_plain<TOK>(P, ti, stage, n_warp, grp, lane, acc);
+      } else {
+        // h of 2 features (halves) per token, in place of the gate's sums
+        const float L = P.limit;
+        uint32_t m[S::NC][8];
+#pragma unroll
+        for (int i = 0; i < S::NC; ++i)
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) {
+            m[i][2 * qq] = m[i][2 * qq + 1] = 0u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 g = unpack_f32x2(acc[i][h][2 * qq]), u = unpack_f32x2(acc[i][h][2 * qq + 1]);
+              const float h0 = swiglu_clamped(g.x, u.x, L), h1 = swiglu_clamped(g.y, u.y, L);
+              acc[i][h][2 * qq] = pack_f32x2(h0, h1);
+              m[i][2 * qq] = max(m[i][2 * qq], __float_as_uint(h0) & 0x7FFFFFFFu);
+              m[i][2 * qq + 1] = max(m[i][2 * qq + 1], __float_as_uint(h1) & 0x7FFFFFFFu);
+            }
+          }
+        warp_amax<S::NC>(m, c.amax[grp][w4], lane);
+        named_barrier_sync(2 + grp, 128);
+        // one thread per token of the group: maximum over the CTA's 64
+        // features, then over the pair's 128
+        const int gt = threadIdx.x & 127;
+        if (gt < TOK / 2) {
+          const uint32_t mine_m = max(max(c.amax[grp][0][gt], c.amax[grp][1][gt]),
+                                      max(c.amax[grp][2][gt], c.amax[grp][3][gt]));
+          const uint32_t other = rank ^ 1u;
+          uint32_t* peer = &c.peer_amax[grp][tile_no & 1u][gt];
+          st_cluster_u32(map_to_rank(smem_u32(peer), other), mine_m);
+          mbar_arrive_cluster(map_to_rank(smem_u32(&c.amax_full[grp]), other));
+          if (ok && !mbar_wait_bounded<true>(&c.amax_full[grp], tile_no & 1u, abort_flag, P.wait_ns)) {
+            fail(63);
+            ok = false;
+          }
+          const uint32_t both = max(mine_m, *peer);
+          float sc, inv;
+          e4m3_block_scale(both, sc, inv);
+          c.inv[grp][gt] = inv;
+          const int col = 32 * (2 * (gt >> 5) + grp) + (gt & 31);
+          if (leader && col < ti.ntok) P.out_scale[static_cast<size_t>(ti.fidx) * P.rows + ti.row0 + col] = sc;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        named_barrier_sync(2 + grp, 128);
+        const int f0 = ti.fidx * 128 + static_cast<int>(rank) * 64 + w4 * 16;
+#pragma unroll
+        for (int i = 0; i < S::NC; ++i) {
+          const int col0 = 32 * (2 * i + grp);
+          if (col0 >= ti.ntok) continue;
+          uint32_t r[4];
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) {
+            const float2 iv = *reinterpret_cast<const float2*>(&c.inv[grp][32 * i + 8 * qq + 2 * (lane & 3)]);
+            const float2 a = unpack_f32x2(acc[i][0][2 * qq]), b = unpack_f32x2(acc[i][1][2 * qq]);
+            r[qq] = e4m3x4(a.x * iv.x, b.x * iv.x, a.y * iv.y, b.y * iv.y);
+          }
+          __syncwarp();
+          stmatrix_x4_trans(smem_u32(stage + lane * 16), r[0], r[1], r[2], r[3]);
+          __syncwarp();
+          if (col0 + lane < ti.ntok)
+            *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + static_cast<size_t>(ti.row0 + col0 + lane) * P.N +
+                                      f0) = *reinterpret_cast<const uint4*>(stage + lane * 16);
+        }
+      }
+      ++tile_no;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the pair's MMAs, remote arrives and copies are done
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+bool encode_w_plain(CUtensorMap* m, const void* base, int groups, int N, int K) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(groups)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(K) * N};
+  const uint32_t box[3] = {BK, ROWS, 1};
+  return encode_tma(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// gate/up weight [G, 2, I, K] seen as {K, r = 8, u = 2, h = 2, blocks of 16
+// rows}: the box {128, 8, 2, 2, 4} lands as 128 rows ordered (block, h, u, r),
+// row (b, h, u, r) the gate (u = 0) or up (u = 1) row of feature 16 b + 2 r + h:
+// a thread's two 16-row halves are neighbouring features, whose codes pack
+// into one 16-bit element.
+bool encode_w_gate_up(CUtensorMap* m, const void* base, int groups, int I, int K) {
+  const uint64_t row = static_cast<uint64_t>(K);
+  const uint64_t dims[5] = {row, 8, 2, 2, static_cast<uint64_t>(groups) * 2 * I / 16};
+  const uint64_t strides[4] = {2 * row, row * I, row, 16 * row};
+  const uint32_t box[5] = {BK, 8, 2, 2, 4};
+  return encode_tma(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int TOK>
+bool encode_x(CUtensorMap (&m)[kTokBoxes], const void* base, int rows, int K) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(K)};
+  for (int b = 0; b < Shape<TOK>::BOXES; ++b) {
+    const uint32_t box[2] = {BK, static_cast<uint32_t>(TOK / 2 >> b)};
+    if (!encode_tma(&m[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return false;
+  }
+  return true;
+}
+
+// CTA pairs that can be resident at once on the current device; 0 if unknown.
+template <Kind KIND, int TOK>
+int resident_pairs() {
+  static int cached[64];
+  static bool known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (!known[dev]) {
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(2);
+    lc.blockDim = dim3(THREADS);
+    lc.dynamicSmemBytes = smem_bytes<TOK>();
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel<KIND, TOK>, &lc) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    cached[dev] = n;
+    known[dev] = true;
+  }
+  return cached[dev];
+}
+
+template <Kind KIND, int TOK>
+cudaError_t start(Params& P, const void* a, int K, int num_sms, cudaStream_t stream) {
+  if (!encode_x<TOK>(P.tma_x, a, P.rows, K)) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fp8_pair_kernel<KIND, TOK>),
+                                   static_cast<int>(smem_bytes<TOK>()));
+  if (e != cudaSuccess) return e;
+  int grid = std::max(2, num_sms / 2 * 2);
+  const int pairs = resident_pairs<KIND, TOK>();
+  if (pairs > 0) grid = std::min(grid, 2 * pairs);
+  // no more pairs than there can be tiles
+  const int64_t most = (static_cast<int64_t>(P.rows) / TOK + std::min(P.groups, P.rows)) * P.f_tiles;
+  if (most < grid / 2) grid = static_cast<int>(2 * std::max<int64_t>(1, most));
+  return launch_kernel(fp8_pair_kernel<KIND, TOK>, dim3(grid), dim3(THREADS), smem_bytes<TOK>(), stream, P);
+}
+
+template <Kind KIND>
+cudaError_t start_for(Params& P, const void* a, int K, int num_sms, cudaStream_t stream) {
+  // 64-token tiles (8 TMEM buffers, 8 smaller stages) when the groups have 64
+  // rows or fewer on average
+  return static_cast<int64_t>(P.rows) <= 64ll * P.groups ? start<KIND, 64>(P, a, K, num_sms, stream)
+                                                         : start<KIND, 256>(P, a, K, num_sms, stream);
+}
+
+Params base_params(const float* a_scale, int rows, const int32_t* offsets, int groups, int K, int32_t* err,
+                   int32_t* queue) {
+  Params P;
+  memset(&P, 0, sizeof(P));
+  P.a_scale = a_scale;
+  P.rows = rows;
+  P.offsets = offsets;
+  P.groups = groups;
+  P.k_blocks = (K + BK - 1) / BK;
+  P.err = err;
+  P.queue = queue;
+  P.wait_ns = kTimeoutNs;
+  return P;
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
-  const dim3 grid((p.N + kT - 1) / kT, (p.rows + kT - 1) / kT + p.groups);
-  const unsigned char* a = static_cast<const unsigned char*>(p.a);
-  const unsigned char* w = static_cast<const unsigned char*>(p.w);
-  if (p.out_type == MOE_F32)
-    return launch_kernel(fp8_gemm_kernel<float>, grid, dim3(256), 0, stream, a, p.a_scale, p.rows, p.offsets, p.groups,
-                         w, p.w_scale, p.N, p.K, p.row_scale, static_cast<float*>(p.out));
-  return launch_kernel(fp8_gemm_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, a, p.a_scale, p.rows, p.offsets,
-                       p.groups, w, p.w_scale, p.N, p.K, p.row_scale, static_cast<__nv_bfloat16*>(p.out));
+  Params P = base_params(p.a_scale, p.rows, p.offsets, p.groups, p.K, err, queue);
+  P.w_scale = p.w_scale;
+  P.out = p.out;
+  P.out_f32 = p.out_type == MOE_F32;
+  P.row_scale = p.row_scale;
+  P.N = p.N;
+  P.n_blocks = (p.N + 127) / 128;
+  P.f_tiles = (p.N + 255) / 256;
+  if (!encode_w_plain(&P.tma_w, p.w, p.groups, p.N, p.K)) return cudaErrorInvalidValue;
+  return start_for<Kind::Plain>(P, p.a, p.K, num_sms, stream);
 }
 
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
-                           const int32_t* offsets, int rows, void* x_q, float* x_s, float* gu, void* h_q, float* h_s,
+                           const int32_t* offsets, int rows, void* x_q, float* x_s, void* h_q, float* h_s,
                            const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms,
                            cudaStream_t stream) {
   const int H = cfg.hidden, I = cfg.expert_inter, E = cfg.num_experts;
   cudaError_t e = launch_fp8_quantize(x_rows, MOE_BF16, H, gather_src, cfg.top_k, rows, H, x_q, x_s, offsets, E, stream);
   if (e != cudaSuccess) return e;
-  Fp8Problem gate_up{x_q, x_s, rows, offsets, E, w.w_gate_up, static_cast<const float*>(w.s_gate_up), 2 * I, H, nullptr,
-                     gu, MOE_F32};
-  e = launch_fp8_gemm(gate_up, err, queues, num_sms, stream);
+  Params P = base_params(x_s, rows, offsets, E, H, err, queues);
+  P.w_scale = static_cast<const float*>(w.s_gate_up);
+  P.out = h_q;
+  P.out_scale = h_s;
+  P.N = I;
+  P.n_blocks = 2 * I / 128;
+  P.f_tiles = I / 128;
+  P.limit = cfg.swiglu_limit;
+  if (!encode_w_gate_up(&P.tma_w, w.w_gate_up, E, I, H)) return cudaErrorInvalidValue;
+  e = start_for<Kind::GateUp>(P, x_q, H, num_sms, stream);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (static_cast<int64_t>(rows) * (I / 128) + 7) / 8;
-  e = launch_kernel(fp8_swiglu_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
-                    static_cast<const float*>(gu), offsets, E, rows, I, cfg.swiglu_limit,
-                    static_cast<unsigned char*>(h_q), h_s);
-  if (e != cudaSuccess) return e;
-  Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
-                  MOE_BF16};
+  const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
+                        MOE_BF16};
   return launch_fp8_gemm(down, err, queues + 2, num_sms, stream);
 }
 

@@ -151,7 +151,7 @@ moe_status run_ffn(const moe_config& cfg, const moe_weights& w, const void* x_ro
   if (is_fp8(cfg)) {
     if (routed)
       MOE_CUDA_TRY(launch_fp8_ffn(cfg, w, x_rows, gather_src, offsets, R, at<void>(ws, L.x_q), at<float>(ws, L.x_s),
-                                  at<float>(ws, L.h), at<void>(ws, L.h_q), at<float>(ws, L.h_s), w_perm, y_perm, err,
+                                  at<void>(ws, L.h_q), at<float>(ws, L.h_s), w_perm, y_perm, err,
                                   tile_queue(ws, kQueueFp8GateUp), sms, stream));
     if (shared_tc) {
       MOE_CUDA_TRY(launch_gemm_gateup(nullptr, &s_gu, cfg.swiglu_limit, err, qgu, sms, stream));
@@ -253,7 +253,7 @@ WsLayout ws_layout(const moe_config& cfg, int Tmax) {
   // bf16 h, the 4-bit grouped GEMMs' fp16 h [R, I], or the 4-bit GEMVs' fp32
   // gate/up [R, 2I] (taken only below kInt4PrefillRowsPerExpert rows per expert)
   const size_t r_gemv = std::min(R, static_cast<size_t>(kInt4PrefillRowsPerExpert) * E);
-  L.h = take(four ? std::max(R * I * 2, r_gemv * 2 * I * 4) : fp8 ? R * 2 * I * 4 : R * I * 2);
+  L.h = take(four ? std::max(R * I * 2, r_gemv * 2 * I * 4) : fp8 ? 0 : R * I * 2);
   L.h_shared = take(T * Is * 2);
   L.y_perm = take(R * H * 2);
   L.shared_out = take(T * H * 2);

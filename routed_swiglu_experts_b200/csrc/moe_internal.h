@@ -176,7 +176,7 @@ cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, i
 // The routed FFN on FP8 experts: quantised rows x_q / x_s, activations h_q /
 // h_s (scratch); queues: four tile-queue words (gate/up, then down).
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
-                           const int32_t* offsets, int rows, void* x_q, float* x_s, float* gu, void* h_q, float* h_s,
+                           const int32_t* offsets, int rows, void* x_q, float* x_s, void* h_q, float* h_s,
                            const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms,
                            cudaStream_t stream);
 
