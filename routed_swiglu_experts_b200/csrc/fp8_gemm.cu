@@ -623,10 +623,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const float* sx = c.sc[slot] + 32 * grp + 2 * (lane & 3);
         const float g0 = c.sc[slot][TOK], g1 = KIND == Kind::GateUp ? c.sc[slot][TOK + 1] : g0;
         const uint64_t sg = pack_f32x2(g0, g0), su = pack_f32x2(g1, g1);
+        // CTA-scope arrival: only TMEM, ordered by the tcgen05 fences, changes
+        // hands (a release at cluster scope is a memory barrier per K block)
         auto release = [&] {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+          if (lane == 0) mbar_arrive_peer(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
         };
         uint32_t va[16], vb[16];
         if (mine > 0) tmem_ld16x256b_x4(tb, va);
