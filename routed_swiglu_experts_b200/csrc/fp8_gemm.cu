@@ -14,10 +14,11 @@
 // ffn_gemm.cu: a tile is 256 weight rows x up to TOK tokens of one expert,
 // rounded up to 16 tokens only.  A CTA's 128 weight rows lie in one scale
 // block, so a partial sum's scale is sa[token] times a number that is the same
-// for the whole CTA.  TMEM is read in the 16x256b shape: a thread holds 4
+// for the whole CTA.  TMEM is read in the 16x128b shape: a thread holds 4
 // weight rows x 8 tokens of a 32-token chunk, so it needs 8 token scales for
-// 32 sums (with a row per thread it would need 32), and pairs of neighbouring
-// tokens go through fma.rn.f32x2.
+// 32 sums (with a row per thread, 32x32b, it would need 32, four times the
+// shared-memory bandwidth there is; 16x256b has the same 4 x 8 but reads at
+// about half the rate).
 //
 // Roles per CTA (384 threads): warps 0-7 scale, add and write (two groups of
 // four warps; group w takes the 32-token chunks 2 i + w), warp 8 TMA
@@ -27,6 +28,7 @@
 // scaling warp whose wait gave up goes on without waiting until the tile ends,
 // so that no warp is left alone at a named barrier.
 #include <cstring>
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "moe_internal.h"
@@ -152,19 +154,63 @@ __device__ __forceinline__ Tile decode(const Params& P, const Ctl<TOK>& c, int t
   return ti;
 }
 
-// Sums of one thread: chunk, 16-row half, then pair (2 q + rh): tokens
-// 8 q + 2 (lane % 4) + {0, 1} of the chunk in weight row
-// 16 half + 8 rh + lane / 4 of the warp's 32.
+// Sums of one thread: chunk, 16-row half, then 2 j + rh: token 4 j + lane % 4
+// of the chunk in weight row 16 half + 8 rh + lane / 4 of the warp's 32.
 template <int NC>
-using Acc = uint64_t[NC][2][8];
+using Acc = float[NC][2][16];
 
-template <int TOK, Kind KIND>
-__device__ __forceinline__ void add_half(uint64_t (&acc)[8], const uint32_t (&v)[16], const uint64_t (&s0)[4],
-                                         const uint64_t (&s1)[4]) {
+// Where the scale of a chunk's token lies in the chunk's 32: the 8 of a
+// thread side by side.
+__device__ __forceinline__ int scale_at(int tok) { return (tok & 3) * 8 + (tok >> 2); }
+
+// Staging row of a chunk's token block q: the thread's tokens 4 j + lane % 4,
+// j = 2 q and 2 q + 1, are columns 2 (lane % 4) and 2 (lane % 4) + 1 of the
+// 8 x 8 matrix that stmatrix takes.
+__device__ __forceinline__ int matrix_token(int lane) {
+  return (lane & ~7) + 4 * (lane & 1) + ((lane & 7) >> 1);
+}
+
+__device__ __forceinline__ void add_half(float (&acc)[16], const uint32_t (&v)[16], const float (&s0)[8],
+                                         const float (&s1)[8]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    acc[2 * q] = fma_f32x2(pack_b32x2(v[4 * q], v[4 * q + 1]), s0[q], acc[2 * q]);
-    acc[2 * q + 1] = fma_f32x2(pack_b32x2(v[4 * q + 2], v[4 * q + 3]), s1[q], acc[2 * q + 1]);
+  for (int j = 0; j < 8; ++j) {
+    acc[2 * j] = fmaf(__uint_as_float(v[2 * j]), s0[j], acc[2 * j]);
+    acc[2 * j + 1] = fmaf(__uint_as_float(v[2 * j + 1]), s1[j], acc[2 * j + 1]);
+  }
+}
+
+// One K block's partial sums of M chunks (64 columns apart from tb on) times
+// their scales into acc; va holds, or is about to hold, the first half chunk.
+// sx: the thread's token scales; sg, su: the weight scales of the two row
+// halves of 8 (GateUp: gate and up rows).  A load is in flight while the sums
+// of the one before are added; `turn` frees the TMEM buffer once it is read
+// and starts the next block's first load.
+template <int M, Kind KIND, int NC, typename Turn>
+__device__ __forceinline__ void add_block(Acc<NC>& acc, uint32_t (&va)[16], uint32_t tb, const float* sx, float sg,
+                                          float su, Turn turn) {
+  uint32_t vb[16];
+  const uint64_t sgg = pack_f32x2(sg, sg), suu = pack_f32x2(su, su);
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    float s0[8], s1[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 s = *reinterpret_cast<const float4*>(sx + 64 * i + 4 * h);
+      const uint64_t x = pack_f32x2(s.x, s.y), y = pack_f32x2(s.z, s.w);
+      const float2 gx = unpack_f32x2(mul_f32x2(x, sgg)), gy = unpack_f32x2(mul_f32x2(y, sgg));
+      s0[4 * h] = gx.x, s0[4 * h + 1] = gx.y, s0[4 * h + 2] = gy.x, s0[4 * h + 3] = gy.y;
+      if (KIND == Kind::GateUp) {
+        const float2 ux = unpack_f32x2(mul_f32x2(x, suu)), uy = unpack_f32x2(mul_f32x2(y, suu));
+        s1[4 * h] = ux.x, s1[4 * h + 1] = ux.y, s1[4 * h + 2] = uy.x, s1[4 * h + 3] = uy.y;
+      }
+    }
+    tmem_ld_wait_regs(va);
+    tmem_ld16x128b_x8(tb + (16u << 16) + 64 * i, vb);
+    add_half(acc[i][0], va, s0, KIND == Kind::GateUp ? s1 : s0);
+    tmem_ld_wait_regs(vb);
+    if (i + 1 < M) tmem_ld16x128b_x8(tb + 64 * (i + 1), va);
+    else turn();
+    add_half(acc[i][1], vb, s0, KIND == Kind::GateUp ? s1 : s0);
   }
 }
 
@@ -180,15 +226,13 @@ __device__ __forceinline__ void write_plain(const Params& P, const Tile& ti, uns
     if (col0 >= ti.ntok) continue;
     if (P.row_scale != nullptr) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = col0 + 8 * q + 2 * (lane & 3);
-        const float w0 = col < ti.ntok ? __ldg(P.row_scale + ti.row0 + col) : 0.f;
-        const float w1 = col + 1 < ti.ntok ? __ldg(P.row_scale + ti.row0 + col + 1) : 0.f;
-        const uint64_t w = pack_f32x2(w0, w1);
+      for (int j = 0; j < 8; ++j) {
+        const int col = col0 + 4 * j + (lane & 3);
+        const float w = col < ti.ntok ? __ldg(P.row_scale + ti.row0 + col) : 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          acc[c][h][2 * q] = mul_f32x2(acc[c][h][2 * q], w);
-          acc[c][h][2 * q + 1] = mul_f32x2(acc[c][h][2 * q + 1], w);
+          acc[c][h][2 * j] *= w;
+          acc[c][h][2 * j + 1] *= w;
         }
       }
     }
@@ -199,16 +243,12 @@ __device__ __forceinline__ void write_plain(const Params& P, const Tile& ti, uns
       for (int part = 0; part < 2; ++part) {
         __syncwarp();
 #pragma unroll
-        for (int qq = 0; qq < 2; ++qq)
+        for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
-              const float2 v = unpack_f32x2(acc[c][h][2 * (2 * part + qq) + rh]);
-              const int n = 16 * h + 8 * rh + (lane >> 2), tok = 8 * qq + 2 * (lane & 3);
-              st[tok * 36 + n] = v.x;
-              st[(tok + 1) * 36 + n] = v.y;
-            }
+            for (int rh = 0; rh < 2; ++rh)
+              st[(4 * jj + (lane & 3)) * 36 + 16 * h + 8 * rh + (lane >> 2)] = acc[c][h][2 * (4 * part + jj) + rh];
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -228,11 +268,8 @@ __device__ __forceinline__ void write_plain(const Params& P, const Tile& ti, uns
         for (int rh = 0; rh < 2; ++rh) {
           uint32_t r[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 v = unpack_f32x2(acc[c][h][2 * q + rh]);
-            r[q] = pack_bf16x2(v.x, v.y);
-          }
-          stmatrix_x4_trans(smem_u32(stage + lane * 80 + (2 * h + rh) * 16), r[0], r[1], r[2], r[3]);
+          for (int q = 0; q < 4; ++q) r[q] = pack_bf16x2(acc[c][h][4 * q + rh], acc[c][h][4 * q + 2 + rh]);
+          stmatrix_x4_trans(smem_u32(stage + matrix_token(lane) * 80 + (2 * h + rh) * 16), r[0], r[1], r[2], r[3]);
         }
       __syncwarp();
 #pragma unroll
@@ -271,9 +308,9 @@ __device__ __forceinline__ void warp_amax(uint32_t (&m)[NC][8], uint32_t* amax, 
       const uint32_t give = b2 ? y[j] : y[j + 4], keep = b2 ? y[j + 4] : y[j];
       z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
     }
-    const int at = 32 * (2 * b4 + b3) + 16 * b2 + 2 * (lane & 3);
-    *reinterpret_cast<uint2*>(amax + at) = make_uint2(z[0], z[1]);
-    *reinterpret_cast<uint2*>(amax + at + 8) = make_uint2(z[2], z[3]);
+    uint32_t* at = amax + 32 * (2 * b4 + b3) + 16 * b2 + (lane & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[4 * j] = z[j];
   } else {
     uint32_t z[4];
 #pragma unroll
@@ -284,9 +321,9 @@ __device__ __forceinline__ void warp_amax(uint32_t (&m)[NC][8], uint32_t* amax, 
       z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 16));
     }
     if (!b4 && !b3) {
-      const int at = 16 * b2 + 2 * (lane & 3);
-      *reinterpret_cast<uint2*>(amax + at) = make_uint2(z[0], z[1]);
-      *reinterpret_cast<uint2*>(amax + at + 8) = make_uint2(z[2], z[3]);
+      uint32_t* at = amax + 16 * b2 + (lane & 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at[4 * j] = z[j];
     }
   }
 }
@@ -481,41 +518,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 9) {
     // -------------------------------------------- MMA issuer (first CTA) --
-    if (leader && lane == 0) {
+    // The whole warp runs the loop and one elected thread issues: the operands
+    // of the MMAs then stay in uniform registers.
+    if (leader) {
+      const uint64_t a_desc = sw128_kmajor_desc(smem_u32(smem_a)), b_desc = sw128_kmajor_desc(smem_u32(smem_b));
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true, first = true;
       for (;;) {
-        if (!mbar_wait_bounded(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&c.tq_full[q], qph, abort_flag, P.wait_ns));
+        if (!ok) {
           fail(57);
           break;
         }
-        const int t = c.tq[q];
-        mbar_arrive(&c.tq_empty[q]);
+        const int t = __shfl_sync(0xffffffffu, c.tq[q], 0);
+        if (elect_one()) mbar_arrive(&c.tq_empty[q]);
         next_q();
         if (t < 0) break;
         const Tile ti = decode<TOK>(P, c, t);
-        const uint32_t idesc = umma_idesc_f16(2 * ROWS, ti.nmma);
+        const uint32_t idesc = umma_idesc_f16(2 * ROWS, __shfl_sync(0xffffffffu, ti.nmma, 0));
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_bounded(&c.tmem_empty[buf], buf_phase ^ 1u, abort_flag, P.wait_ns)) {
-            fail(52);
+          ok = mbar_wait_bounded(&c.tmem_empty[buf], buf_phase ^ 1u, abort_flag, P.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
+            fail(52);
             break;
           }
-          if (!mbar_wait_bounded(&c.full[stage], phase, abort_flag, P.wait_ns)) {
-            fail(53);
+          ok = mbar_wait_bounded(&c.full[stage], phase, abort_flag, P.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
+            fail(53);
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem_a + stage * A_BYTES);
-          const uint32_t b_addr = smem_u32(smem_b + stage * S::B_BYTES);
+          const uint64_t ad = a_desc + static_cast<uint64_t>(stage * (A_BYTES / 16));
+          const uint64_t bd = b_desc + static_cast<uint64_t>(stage * (S::B_BYTES / 16));
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * TOK);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            umma_e4m3_pair(tmem_base + static_cast<uint32_t>(buf * TOK), sw128_kmajor_desc(a_addr + kk * 32),
-                           sw128_kmajor_desc(b_addr + kk * 32), idesc, kk != 0 ? 1u : 0u);
-          umma_commit_pair(&c.empty[stage]);
-          if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
+            for (int kk = 0; kk < BK / 32; ++kk)  // 32 bytes of K each
+              umma_e4m3_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+            if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
+            umma_commit_pair(&c.empty[stage]);
+          }
+          __syncwarp();
           first = false;
           if (++stage == S::STAGES) {
             stage = 0;
@@ -528,9 +574,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         if (!ok) break;
       }
-      umma_commit_pair_leader(&c.mma_done);
-      volatile int32_t never = 0;
-      if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 58);
+      if (elect_one()) {
+        umma_commit_pair_leader(&c.mma_done);
+        volatile int32_t never = 0;
+        if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 58);
+      }
+      __syncwarp();
     }
   } else if (warp == 10) {
     // --------------------------------------------------- scales, a K block ahead
@@ -563,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const uint32_t dst = smem_u32(c.sc[slot]);
         for (int i = lane; i < ti.nmma; i += 32)
-          cp_async4(dst + i * 4, sa + static_cast<size_t>(kb) * P.rows + min(i, n - 1), i < n);
+          cp_async4(dst + ((i & ~31) + scale_at(i & 31)) * 4, sa + static_cast<size_t>(kb) * P.rows + min(i, n - 1), i < n);
         if (lane < (KIND == Kind::GateUp ? 2 : 1)) cp_async4(dst + (TOK + lane) * 4, sw + kb, true);
         cp_async_mbar_arrive(&c.sc_full[slot]);
         if (++slot == SC) {
@@ -608,61 +657,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][h][j] = 0ull;
+          for (int j = 0; j < 16; ++j) acc[i][h][j] = 0.f;
 
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (ok) {
-          ok = mbar_wait_bounded(&c.sc_full[slot], sph, abort_flag, P.wait_ns);
-          ok = ok && mbar_wait_bounded(&c.tmem_full[buf], buf_phase, abort_flag, P.wait_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok && lane == 0) fail(54);
-        }
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t tb = tmem_base + lane_addr + static_cast<uint32_t>(buf * TOK + 32 * grp);
-        const float* sx = c.sc[slot] + 32 * grp + 2 * (lane & 3);
-        const float g0 = c.sc[slot][TOK], g1 = KIND == Kind::GateUp ? c.sc[slot][TOK + 1] : g0;
-        const uint64_t sg = pack_f32x2(g0, g0), su = pack_f32x2(g1, g1);
-        // CTA-scope arrival: only TMEM, ordered by the tcgen05 fences, changes
-        // hands (a release at cluster scope is a memory barrier per K block)
-        auto release = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_peer(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
-        };
-        uint32_t va[16], vb[16];
-        if (mine > 0) tmem_ld16x256b_x4(tb, va);
-        else release();
-#pragma unroll
-        for (int i = 0; i < S::NC; ++i) {
-          if (i < mine) {
-            uint64_t s0[4], s1[4];
-#pragma unroll
-            for (int qq = 0; qq < 4; ++qq) {
-              const float2 s = *reinterpret_cast<const float2*>(sx + 64 * i + 8 * qq);
-              const uint64_t p = pack_f32x2(s.x, s.y);
-              s0[qq] = mul_f32x2(p, sg);
-              s1[qq] = KIND == Kind::GateUp ? mul_f32x2(p, su) : s0[qq];
-            }
-            tmem_ld_wait_regs(va);
-            tmem_ld16x256b_x4(tb + (16u << 16) + 64 * i, vb);
-            add_half<TOK, KIND>(acc[i][0], va, s0, s1);
-            tmem_ld_wait_regs(vb);
-            if (i + 1 < mine) tmem_ld16x256b_x4(tb + 64 * (i + 1), va);
-            else release();
-            add_half<TOK, KIND>(acc[i][1], vb, s0, s1);
+      // The K loop, with the chunk count a constant of its body.  Once a block
+      // is read its buffer is freed and the next block's first load started,
+      // before the last sums are added.
+      auto k_loop = [&](auto chunks) {
+        constexpr int M = decltype(chunks)::value;
+        uint32_t va[16];
+        const uint32_t tb0 = tmem_base + lane_addr + static_cast<uint32_t>(32 * grp);
+        auto wait_block = [&] {
+          if (ok) {
+            ok = mbar_wait_bounded(&c.tmem_full[buf], buf_phase, abort_flag, P.wait_ns);
+            ok = ok && mbar_wait_bounded(&c.sc_full[slot], sph, abort_flag, P.wait_ns);
+            if (!ok) fail(54);
           }
+          __syncwarp();
+          tc_fence_after();
+          if constexpr (M > 0) tmem_ld16x128b_x8(tb0 + static_cast<uint32_t>(buf * TOK), va);
+        };
+        wait_block();
+        for (int kb = 0; kb < nkb; ++kb) {
+          const float* sc = c.sc[slot];
+          const float g0 = sc[TOK], g1 = KIND == Kind::GateUp ? sc[TOK + 1] : g0;
+          const uint32_t tb = tb0 + static_cast<uint32_t>(buf * TOK);
+          auto turn = [&] {
+            // CTA-scope arrival: only TMEM, ordered by the tcgen05 fences, changes
+            // hands (a release at cluster scope is a memory barrier per K block)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_peer(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+              mbar_arrive(&c.sc_empty[slot]);  // every lane has read its scales
+            }
+            if (++slot == SC) {
+              slot = 0;
+              sph ^= 1u;
+            }
+            if (++buf == S::NBUF) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+            if (kb + 1 < nkb) wait_block();
+          };
+          if constexpr (M > 0) add_block<M, KIND, S::NC>(acc, va, tb, sc + 32 * grp + 8 * (lane & 3), g0, g1, turn);
+          else turn();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.sc_empty[slot]);
-        if (++slot == SC) {
-          slot = 0;
-          sph ^= 1u;
-        }
-        if (++buf == S::NBUF) {
-          buf = 0;
-          buf_phase ^= 1u;
-        }
+      };
+      if constexpr (S::NC == 4) {
+        if (mine == 4) k_loop(std::integral_constant<int, 4>{});
+        else if (mine == 3) k_loop(std::integral_constant<int, 3>{});
+        else if (mine == 2) k_loop(std::integral_constant<int, 2>{});
+        else if (mine == 1) k_loop(std::integral_constant<int, 1>{});
+        else k_loop(std::integral_constant<int, 0>{});
+      } else {
+        if (mine == 1) k_loop(std::integral_constant<int, 1>{});
+        else k_loop(std::integral_constant<int, 0>{});
       }
 
       if (KIND == Kind::Plain) {
@@ -675,15 +725,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < S::NC; ++i)
 #pragma unroll
-          for (int qq = 0; qq < 4; ++qq) {
-            m[i][2 * qq] = m[i][2 * qq + 1] = 0u;
+          for (int j = 0; j < 8; ++j) {
+            m[i][j] = 0u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float2 g = unpack_f32x2(acc[i][h][2 * qq]), u = unpack_f32x2(acc[i][h][2 * qq + 1]);
-              const float h0 = swiglu_clamped(g.x, u.x, L), h1 = swiglu_clamped(g.y, u.y, L);
-              acc[i][h][2 * qq] = pack_f32x2(h0, h1);
-              m[i][2 * qq] = max(m[i][2 * qq], __float_as_uint(h0) & 0x7FFFFFFFu);
-              m[i][2 * qq + 1] = max(m[i][2 * qq + 1], __float_as_uint(h1) & 0x7FFFFFFFu);
+              float* a = &acc[i][h][2 * j];
+              a[0] = swiglu_clamped(a[0], a[1], L);
+              m[i][j] = max(m[i][j], __float_as_uint(a[0]) & 0x7FFFFFFFu);
             }
           }
         warp_amax<S::NC>(m, c.amax[grp][w4], lane);
@@ -719,12 +767,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           uint32_t r[4];
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq) {
-            const float2 iv = *reinterpret_cast<const float2*>(&c.inv[grp][32 * i + 8 * qq + 2 * (lane & 3)]);
-            const float2 a = unpack_f32x2(acc[i][0][2 * qq]), b = unpack_f32x2(acc[i][1][2 * qq]);
-            r[qq] = e4m3x4(a.x * iv.x, b.x * iv.x, a.y * iv.y, b.y * iv.y);
+            // tokens 4 j + lane % 4, j = 2 qq and 2 qq + 1, of two neighbouring features
+            const float* iv = &c.inv[grp][32 * i + 8 * qq + (lane & 3)];
+            const float *a = &acc[i][0][4 * qq], *b = &acc[i][1][4 * qq];
+            r[qq] = e4m3x4(a[0] * iv[0], b[0] * iv[0], a[2] * iv[4], b[2] * iv[4]);
           }
           __syncwarp();
-          stmatrix_x4_trans(smem_u32(stage + lane * 16), r[0], r[1], r[2], r[3]);
+          stmatrix_x4_trans(smem_u32(stage + matrix_token(lane) * 16), r[0], r[1], r[2], r[3]);
           __syncwarp();
           if (col0 + lane < ti.ntok)
             *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + static_cast<size_t>(ti.row0 + col0 + lane) * P.N +
