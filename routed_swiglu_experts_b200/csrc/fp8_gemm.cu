@@ -204,10 +204,10 @@ __device__ __forceinline__ void add_block(Acc<NC>& acc, uint32_t (&va)[16], uint
         s1[4 * h] = ux.x, s1[4 * h + 1] = ux.y, s1[4 * h + 2] = uy.x, s1[4 * h + 3] = uy.y;
       }
     }
-    tmem_ld_wait_regs(va);
+    tmem_ld_wait();
     tmem_ld16x128b_x8(tb + (16u << 16) + 64 * i, vb);
     add_half(acc[i][0], va, s0, KIND == Kind::GateUp ? s1 : s0);
-    tmem_ld_wait_regs(vb);
+    tmem_ld_wait();
     if (i + 1 < M) tmem_ld16x128b_x8(tb + 64 * (i + 1), va);
     else turn();
     add_half(acc[i][1], vb, s0, KIND == Kind::GateUp ? s1 : s0);
@@ -873,6 +873,8 @@ cudaError_t start_for(Params& P, const void* a, int K, int num_sms, cudaStream_t
                                                          : start<KIND, 256>(P, a, K, num_sms, stream);
 }
 
+bool wide_preferred(int rows, int groups) { return static_cast<int64_t>(rows) > 64ll * groups; }
+
 Params base_params(const float* a_scale, int rows, const int32_t* offsets, int groups, int K, int32_t* err,
                    int32_t* queue) {
   Params P;
@@ -891,6 +893,7 @@ Params base_params(const float* a_scale, int rows, const int32_t* offsets, int g
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
+  if (wide_preferred(p.rows, p.groups)) return launch_fp8_wide_gemm(p, err, queue, num_sms, stream);
   Params P = base_params(p.a_scale, p.rows, p.offsets, p.groups, p.K, err, queue);
   P.w_scale = p.w_scale;
   P.out = p.out;
@@ -910,6 +913,15 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
   const int H = cfg.hidden, I = cfg.expert_inter, E = cfg.num_experts;
   cudaError_t e = launch_fp8_quantize(x_rows, MOE_BF16, H, gather_src, cfg.top_k, rows, H, x_q, x_s, offsets, E, stream);
   if (e != cudaSuccess) return e;
+  if (wide_preferred(rows, E)) {
+    const Fp8Problem gate_up{x_q, x_s, rows, offsets, E, w.w_gate_up, static_cast<const float*>(w.s_gate_up), I, H, nullptr,
+                             h_q, 0};
+    e = launch_fp8_wide_gateup(gate_up, h_s, cfg.swiglu_limit, err, queues, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
+                          MOE_BF16};
+    return launch_fp8_wide_gemm(down, err, queues + 2, num_sms, stream);
+  }
   Params P = base_params(x_s, rows, offsets, E, H, err, queues);
   P.w_scale = static_cast<const float*>(w.s_gate_up);
   P.out = h_q;

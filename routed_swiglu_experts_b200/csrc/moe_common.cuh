@@ -137,13 +137,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
-// Bounded wait on phase `parity` of `bar`.  Gives up when `abort` becomes
-// non-zero or after `limit_ns` nanoseconds; returns false in that case.
+// Bounded wait on phase `parity` of the barrier at shared address `a`.  Gives
+// up when `abort` becomes non-zero or after `limit_ns` nanoseconds; returns
+// false in that case.  The first tries do not look at the clock: reading the
+// global timer takes longer than most waits.
 template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
-                                                  volatile int32_t* abort, uint64_t limit_ns) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait<kCluster>(a, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_addr(uint32_t a, uint32_t parity, volatile int32_t* abort,
+                                               uint64_t limit_ns) {
+  for (uint32_t it = 0; it < 64u; ++it)
+    if (mbar_try_wait<kCluster>(a, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait<kCluster>(a, parity)) return true;
@@ -152,6 +154,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
       if (globaltimer_ns() - t0 > limit_ns) return false;
     }
   }
+}
+template <bool kCluster = false>
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
+                                                  volatile int32_t* abort, uint64_t limit_ns) {
+  return mbar_wait_addr<kCluster>(smem_u32(bar), parity, abort, limit_ns);
 }
 
 // ------------------------------------------------------------- cp.async ---
@@ -506,13 +513,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-// Wait for this thread's TMEM loads; the registers are operands so that no
-// use of them moves ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15])::"memory");
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

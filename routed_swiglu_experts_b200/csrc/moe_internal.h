@@ -173,6 +173,11 @@ struct Fp8Problem {
 };
 // queue: the launch's two tile-queue words in the workspace header (zero).
 cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
+// The forms for groups of many rows (fp8_wide.cu); gate/up: p.N features, p.out
+// the E4M3 activations [rows, N], out_scale theirs [N / 128, rows].
+cudaError_t launch_fp8_wide_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
+cudaError_t launch_fp8_wide_gateup(const Fp8Problem& p, float* out_scale, float limit, int32_t* err, int32_t* queue,
+                                   int num_sms, cudaStream_t stream);
 // The routed FFN on FP8 experts: quantised rows x_q / x_s, activations h_q /
 // h_s (scratch); queues: four tile-queue words (gate/up, then down).
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
