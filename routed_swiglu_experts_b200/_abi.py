@@ -153,7 +153,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch.cuda.Stream around it takes 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -254,39 +255,58 @@ def moe_forward_ep(cfg, w, expert_begin, expert_end, x, T, out_partial, topk_ids
                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_forward_ep")
 
 
-def _want(t, name, dtypes, shape, where, contiguous=True):
+class _Torch:
+    """What the checks below look up in torch, once."""
+
+    def __init__(self):
+        import torch
+        self.types = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+        self.floats = tuple(self.types)
+        self.f32 = (torch.float32,)
+        self.i32 = (torch.int32,)
+        self.u8 = (torch.uint8,)
+        self.codes = (torch.float8_e4m3fn, torch.uint8)
+        self.outs = (torch.bfloat16, torch.float32)
+        # without a GPU no tensor is on the current device (the CPU's number is -1)
+        self.device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2
+
+
+_torch = None
+
+
+def _tt() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _want(t, name, dtypes, shape, where, dev, contiguous=True):
     """A tensor argument's element type, shape, layout and device, checked
     before its pointer is passed: the C call sees none of them.  The stream
-    and the kernel belong to the current device, so the tensor must too."""
-    import torch
+    and the kernel belong to the current device `dev`, so the tensor must too."""
     if t is None:
         raise ValueError(f"{where}: {name} is missing")
-    if str(t.dtype).replace("torch.", "") not in dtypes:
-        raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(dtypes)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if (t.dtype in dtypes and (shape is None or t.shape == shape) and t.get_device() == dev
+            and (not contiguous or t.is_contiguous())):
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{where}: {name} is not contiguous")
     if not t.is_cuda:
         raise ValueError(f"{where}: {name} is on {t.device}, expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
-
-
-_DTYPE = {"float32": MOE_F32, "bfloat16": MOE_BF16, "float16": MOE_F16}
-_CODES = ("float8_e4m3fn", "uint8")
-
-
-def _dtype(t) -> int:
-    return _DTYPE[str(t.dtype).replace("torch.", "")]
+    if t.get_device() != dev:
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is {dev}")
+    raise ValueError(f"{where}: {name} is not contiguous")
 
 
 def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
-def _rows_of(t, name, where):
-    """A 2-D tensor whose rows are contiguous (any row stride)."""
+def _row_stride(t, name, where):
+    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -294,70 +314,76 @@ def _rows_of(t, name, where):
 
 def moe_gate_topk(cfg, logits, correction_bias, topk_ids, topk_w, stream=None):
     """Expert selection from logits [T, E] (fp32, bf16 or fp16; rows may be strided)."""
-    where = "moe_gate_topk"
-    _want(logits, "logits", tuple(_DTYPE), None, where, contiguous=False)
-    stride = _rows_of(logits, "logits", where)
-    T = logits.shape[0]
-    if logits.shape[1] != cfg.num_experts:
-        raise ValueError(f"{where}: logits has {logits.shape[1]} columns for {cfg.num_experts} experts")
+    where, tt = "moe_gate_topk", _tt()
+    dev = tt.device()
+    _want(logits, "logits", tt.floats, None, where, dev, contiguous=False)
+    stride = _row_stride(logits, "logits", where)
+    T, E = logits.shape
+    if E != cfg.num_experts:
+        raise ValueError(f"{where}: logits has {E} columns for {cfg.num_experts} experts")
     if correction_bias is not None:
-        _want(correction_bias, "correction_bias", ("float32",), (cfg.num_experts,), where)
-    _want(topk_ids, "topk_ids", ("int32",), (T, cfg.top_k), where)
-    _want(topk_w, "topk_w", ("float32",), (T, cfg.top_k), where)
-    _check(load_library().moe_gate_topk(ctypes.byref(cfg), _ptr(logits), _dtype(logits), stride, _ptr(correction_bias),
-                                        T, _ptr(topk_ids), _ptr(topk_w), _stream(stream)), where)
+        _want(correction_bias, "correction_bias", tt.f32, (E,), where, dev)
+    shape = (T, cfg.top_k)
+    _want(topk_ids, "topk_ids", tt.i32, shape, where, dev)
+    _want(topk_w, "topk_w", tt.f32, shape, where, dev)
+    _check(load_library().moe_gate_topk(ctypes.byref(cfg), logits.data_ptr(), tt.types[logits.dtype], stride,
+                                        _ptr(correction_bias), T, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                        _stream(stream)), where)
 
 
 def moe_fp8_quantize(x, q, scale, src=None, src_div=1, stream=None):
     """Rows x [*, K] to E4M3 codes q [rows, K] and scales [ceil(K/128), rows];
     src int32 [rows]: row r is x[src[r] // src_div]."""
-    where = "moe_fp8_quantize"
-    _want(x, "x", tuple(_DTYPE), None, where, contiguous=False)
-    stride = _rows_of(x, "x", where)
-    K = x.shape[1]
-    rows = x.shape[0] if src is None else src.shape[0]
+    where, tt = "moe_fp8_quantize", _tt()
+    dev = tt.device()
+    _want(x, "x", tt.floats, None, where, dev, contiguous=False)
+    stride = _row_stride(x, "x", where)
+    rows, K = x.shape
     if src is not None:
-        _want(src, "src", ("int32",), (rows,), where)
-    _want(q, "q", _CODES, (rows, K), where)
-    _want(scale, "scale", ("float32",), (_blocks(K), rows), where)
-    _check(load_library().moe_fp8_quantize(_ptr(x), _dtype(x), stride, _ptr(src), int(src_div), rows, K, _ptr(q),
-                                           _ptr(scale), _stream(stream)), where)
+        rows = src.shape[0]
+        _want(src, "src", tt.i32, (rows,), where, dev)
+    _want(q, "q", tt.codes, (rows, K), where, dev)
+    _want(scale, "scale", tt.f32, (_blocks(K), rows), where, dev)
+    _check(load_library().moe_fp8_quantize(x.data_ptr(), tt.types[x.dtype], stride, _ptr(src), int(src_div), rows, K,
+                                           q.data_ptr(), scale.data_ptr(), _stream(stream)), where)
 
 
 def moe_fp8_quantize_weight(w, q, scale, stream=None):
     """Weights w [groups, N, K] to E4M3 codes and scales [groups, ceil(N/128), ceil(K/128)]."""
-    where = "moe_fp8_quantize_weight"
-    _want(w, "w", tuple(_DTYPE), None, where)
+    where, tt = "moe_fp8_quantize_weight", _tt()
+    dev = tt.device()
+    _want(w, "w", tt.floats, None, where, dev)
     if w.dim() != 3:
         raise ValueError(f"{where}: w must be [groups, N, K]")
     G, N, K = w.shape
-    _want(q, "q", _CODES, (G, N, K), where)
-    _want(scale, "scale", ("float32",), (G, _blocks(N), _blocks(K)), where)
-    _check(load_library().moe_fp8_quantize_weight(_ptr(w), _dtype(w), G, N, K, _ptr(q), _ptr(scale), _stream(stream)),
-           where)
+    _want(q, "q", tt.codes, (G, N, K), where, dev)
+    _want(scale, "scale", tt.f32, (G, _blocks(N), _blocks(K)), where, dev)
+    _check(load_library().moe_fp8_quantize_weight(w.data_ptr(), tt.types[w.dtype], G, N, K, q.data_ptr(),
+                                                  scale.data_ptr(), _stream(stream)), where)
 
 
 def moe_fp8_gemm(a, a_scale, w, w_scale, expert_offsets, row_scale, out, ws, stream=None):
     """out [rows, N] = a [rows, K] times w [groups, N, K] by row groups, E4M3
     codes with block scales (expert_offsets None: one group)."""
-    where = "moe_fp8_gemm"
-    _want(a, "a", _CODES, None, where)
-    _want(w, "w", _CODES, None, where)
+    where, tt = "moe_fp8_gemm", _tt()
+    dev = tt.device()
+    _want(a, "a", tt.codes, None, where, dev)
+    _want(w, "w", tt.codes, None, where, dev)
     if a.dim() != 2 or w.dim() != 3 or a.shape[1] != w.shape[2]:
         raise ValueError(f"{where}: a must be [rows, K] and w [groups, N, K]")
     rows, K = a.shape
-    G, N = w.shape[0], w.shape[1]
-    _want(a_scale, "a_scale", ("float32",), (_blocks(K), rows), where)
-    _want(w_scale, "w_scale", ("float32",), (G, _blocks(N), _blocks(K)), where)
+    G, N, _ = w.shape
+    _want(a_scale, "a_scale", tt.f32, (_blocks(K), rows), where, dev)
+    _want(w_scale, "w_scale", tt.f32, (G, _blocks(N), _blocks(K)), where, dev)
     if expert_offsets is not None:
-        _want(expert_offsets, "expert_offsets", ("int32",), (G + 1,), where)
+        _want(expert_offsets, "expert_offsets", tt.i32, (G + 1,), where, dev)
     if row_scale is not None:
-        _want(row_scale, "row_scale", ("float32",), (rows,), where)
-    _want(out, "out", ("bfloat16", "float32"), (rows, N), where)
-    _want(ws, "ws", ("uint8",), None, where)
-    _check(load_library().moe_fp8_gemm(_ptr(a), _ptr(a_scale), rows, _ptr(expert_offsets), G, _ptr(w), _ptr(w_scale),
-                                       N, K, _ptr(row_scale), _ptr(out), _dtype(out), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream)), where)
+        _want(row_scale, "row_scale", tt.f32, (rows,), where, dev)
+    _want(out, "out", tt.outs, (rows, N), where, dev)
+    _want(ws, "ws", tt.u8, None, where, dev)
+    _check(load_library().moe_fp8_gemm(a.data_ptr(), a_scale.data_ptr(), rows, _ptr(expert_offsets), G, w.data_ptr(),
+                                       w_scale.data_ptr(), N, K, _ptr(row_scale), out.data_ptr(), tt.types[out.dtype],
+                                       ws.data_ptr(), ws.numel(), _stream(stream)), where)
 
 
 def moe_permute_no_alloc(cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm, stream=None):

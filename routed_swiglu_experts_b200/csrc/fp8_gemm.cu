@@ -1,34 +1,34 @@
-// Products of FP8 E4M3 rows and weights with a scale per block of 128, dense
-// or grouped by expert, on CTA pairs (tcgen05.mma.cta_group::2,
-// kind::f8f6f4):
+// Block-scaled FP8 products for groups of few rows, on CTA pairs
+// (tcgen05.mma.cta_group::2, kind::f8f6f4), and the choice between this form
+// and the one for many rows (fp8_wide.cu):
 //   out[r, n] = c_r * sum_b sa[b, r] * sw[g, n / 128, b]
 //               * sum_{k in block b} a[r, k] * w[g, n, k]
 // and the gate/up product of an FP8 expert, whose epilogue applies
 //   h = silu(min(G, L)) * clamp(U, -L, L)
 // and quantises h along the row, 128 features to a scale.
 //
-// The scales differ from K block to K block, so the tensor cores sum one
-// block of 128 (four MMAs) into one of several TMEM buffers and the epilogue
-// warps add scale * partial sum into fp32 registers while the next block is
-// multiplied.  The weights are the M operand and the rows ("tokens") N, as in
-// ffn_gemm.cu: a tile is 256 weight rows x up to TOK tokens of one expert,
-// rounded up to 16 tokens only.  A CTA's 128 weight rows lie in one scale
-// block, so a partial sum's scale is sa[token] times a number that is the same
+// With few rows the weights' bytes bound the product.  The weights are the M
+// operand and the rows N, as in ffn_gemm.cu: a tile is 256 weight rows x up to
+// 64 rows of one expert, rounded up to 16 only, so that an expert with one row
+// costs 16 columns of MMA.  The scales differ from K block to K block, so the
+// tensor cores sum one block of 128 (four MMAs) into one of eight TMEM
+// buffers, and eight warps add scale * partial sum into fp32 registers while
+// the next blocks are multiplied.  A CTA's 128 weight rows lie in one scale
+// block, so a partial sum's scale is sa[row] times a number that is the same
 // for the whole CTA.  TMEM is read in the 16x128b shape: a thread holds 4
-// weight rows x 8 tokens of a 32-token chunk, so it needs 8 token scales for
-// 32 sums (with a row per thread, 32x32b, it would need 32, four times the
-// shared-memory bandwidth there is; 16x256b has the same 4 x 8 but reads at
-// about half the rate).
+// weight rows x 8 rows of a chunk of 32, so it needs 8 row scales for 32 sums.
 //
-// Roles per CTA (384 threads): warps 0-7 scale, add and write (two groups of
-// four warps; group w takes the 32-token chunks 2 i + w), warp 8 TMA
-// producer, warp 9 TMEM owner (+ MMA issuer in the first CTA), warp 10 copies
-// each K block's scales into a ring (warp 11 only fills its warpgroup).  Tile
-// queue and tile order as in ffn_gemm.cu.  Every mbarrier wait is bounded (MOE_ERR_DEVICE_TIMEOUT); a
-// scaling warp whose wait gave up goes on without waiting until the tile ends,
-// so that no warp is left alone at a named barrier.
+// Roles per CTA (384 threads): warps 0-7 scale, add and write (warps 4 w ..
+// 4 w + 3 take the chunk 32 w ..), warp 8 TMA producer, warp 9 TMEM owner (+
+// MMA issuer in the first CTA), warp 10 copies the scales, SK K blocks at a
+// time, into a ring (one K block at a time, four ahead, left the scaling warps
+// waiting for memory: decode feed-forward 505 us, 466 us with 16 ahead); warp
+// 11 only fills its warpgroup.  A stage of the operand ring holds two K blocks.
+// Tile queue and tile order as in ffn_gemm.cu.  Every mbarrier wait is bounded
+// (MOE_ERR_DEVICE_TIMEOUT); a scaling warp whose wait gave up goes on without
+// waiting until the tile ends, so that no warp is left alone at a named
+// barrier.
 #include <cstring>
-#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "moe_internal.h"
@@ -41,12 +41,15 @@ constexpr int BK = 128;                       // one scale block, 128 bytes
 constexpr int ROWS = 128;                     // weight rows per CTA
 constexpr int A_BYTES = ROWS * BK;            // 16 KB
 constexpr int THREADS = 384;
-// Registers per thread after the split: the kernel starts with 168 x 384 =
-// 64512; the two warpgroups that hold sums take 208, the other one keeps 88
-// (256 x 208 + 128 x 88 = 64512).
-constexpr int kSumRegs = 208, kOtherRegs = 88;
 constexpr int QD = 8;                         // tile-id ring depth
-constexpr int SC = 4;                         // scale ring depth
+constexpr int SK = 4, SC = 4;                 // scale ring: SC slots of SK K blocks
+constexpr int TOK = 64;                       // rows per tile
+constexpr int NBUF = 512 / TOK;               // TMEM buffers
+constexpr int B_BYTES = TOK / 2 * BK;         // this CTA's half of the rows
+constexpr int KCH = 2;                        // K blocks per stage
+constexpr int STAGES = 4;
+constexpr int A_STAGE = KCH * A_BYTES, B_STAGE = KCH * B_BYTES;
+constexpr int kTokBoxes = 3;                  // row boxes of TOK / 2 >> i, down to 8
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int kStage = 2560;                  // output staging bytes per scaling warp
@@ -55,18 +58,6 @@ constexpr int kStage = 2560;                  // output staging bytes per scalin
 constexpr uint32_t kTileReaders = 1 + 1 + 2 * 9;
 
 enum class Kind { GateUp, Plain };
-
-constexpr int kTokBoxes = 5;  // token boxes of TOK / 2 >> i rows, down to 8
-
-template <int TOK>
-struct Shape {
-  static constexpr int NBUF = 512 / TOK;               // TMEM buffers
-  static constexpr int NC = TOK / 64;                  // 32-token chunks per group of scaling warps
-  static constexpr int B_BYTES = TOK / 2 * BK;         // this CTA's half of the tokens
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = TOK == 256 ? 5 : 8;
-  static constexpr int BOXES = TOK == 256 ? 5 : 3;
-};
 
 struct alignas(64) Params {
   CUtensorMap tma_w;             // GateUp {K, r 8, u 2, h 2, blocks of 16 rows}; Plain {K, N, G}
@@ -88,15 +79,14 @@ struct alignas(64) Params {
   int32_t test_withhold;         // test hook: never signal the first partial sum
 };
 
-template <int TOK>
 struct Ctl {
-  uint64_t full[Shape<TOK>::STAGES];
-  uint64_t empty[Shape<TOK>::STAGES];
-  uint64_t tmem_full[Shape<TOK>::NBUF];
-  uint64_t tmem_empty[Shape<TOK>::NBUF];
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tmem_full[NBUF];
+  uint64_t tmem_empty[NBUF];
   uint64_t sc_full[SC];
   uint64_t sc_empty[SC];
-  uint64_t amax_full[2];            // the other CTA's maxima of this group's tokens
+  uint64_t amax_full[2];            // the other CTA's maxima of this group's rows
   uint64_t mma_done;
   uint64_t tq_full[QD];
   uint64_t tq_empty[QD];
@@ -105,27 +95,24 @@ struct Ctl {
   int32_t abort_flag;
   int32_t tiles;
   int32_t off[MOE_MAX_EXPERTS + 1];
-  int32_t tp[MOE_MAX_EXPERTS + 1];  // token-tile prefix per group
-  alignas(16) float sc[SC][TOK + 4];          // token scales of a K block, then the weight scales of gate and up
+  int32_t tp[MOE_MAX_EXPERTS + 1];  // row-tile prefix per group
+  alignas(16) float sx[SC][SK][TOK];          // row scales, in scale_at order
+  float sw[SC][SK][2];                        // weight scales of gate and up
   alignas(16) uint32_t amax[2][4][TOK / 2];   // per group and warp
   uint32_t peer_amax[2][2][TOK / 2];          // written by the other CTA, double-buffered over tiles
   alignas(16) float inv[2][TOK / 2];
   alignas(16) unsigned char stage[8][kStage];
 };
 
-template <int TOK>
-constexpr size_t smem_bytes() {
-  return 1024 + static_cast<size_t>(Shape<TOK>::STAGES) * Shape<TOK>::STAGE + sizeof(Ctl<TOK>);
-}
-static_assert(smem_bytes<256>() <= 232448 && smem_bytes<64>() <= 232448, "fits the 227 KB opt-in shared memory");
+constexpr size_t kSmem = 1024 + static_cast<size_t>(STAGES) * (A_STAGE + B_STAGE) + sizeof(Ctl);
+static_assert(kSmem <= 232448, "fits the 227 KB opt-in shared memory");
 
 struct Tile {
   int g, fidx, row0, ntok, nmma;
 };
 
 // Group by group; inside a group weight-row tile major, token tile minor.
-template <int TOK>
-__device__ __forceinline__ Tile decode(const Params& P, const Ctl<TOK>& c, int t) {
+__device__ __forceinline__ Tile decode(const Params& P, const Ctl& c, int t) {
   Tile ti;
   int tm, tmi, r0, r1;
   if (P.offsets != nullptr) {
@@ -154,10 +141,9 @@ __device__ __forceinline__ Tile decode(const Params& P, const Ctl<TOK>& c, int t
   return ti;
 }
 
-// Sums of one thread: chunk, 16-row half, then 2 j + rh: token 4 j + lane % 4
+// Sums of one thread: 16-row half, then 2 j + rh: row ("token") 4 j + lane % 4
 // of the chunk in weight row 16 half + 8 rh + lane / 4 of the warp's 32.
-template <int NC>
-using Acc = float[NC][2][16];
+using Acc = float[2][16];
 
 // Where the scale of a chunk's token lies in the chunk's 32: the 8 of a
 // thread side by side.
@@ -179,165 +165,99 @@ __device__ __forceinline__ void add_half(float (&acc)[16], const uint32_t (&v)[1
   }
 }
 
-// One K block's partial sums of M chunks (64 columns apart from tb on) times
-// their scales into acc; va holds, or is about to hold, the first half chunk.
-// sx: the thread's token scales; sg, su: the weight scales of the two row
-// halves of 8 (GateUp: gate and up rows).  A load is in flight while the sums
-// of the one before are added; `turn` frees the TMEM buffer once it is read
-// and starts the next block's first load.
-template <int M, Kind KIND, int NC, typename Turn>
-__device__ __forceinline__ void add_block(Acc<NC>& acc, uint32_t (&va)[16], uint32_t tb, const float* sx, float sg,
-                                          float su, Turn turn) {
-  uint32_t vb[16];
-  const uint64_t sgg = pack_f32x2(sg, sg), suu = pack_f32x2(su, su);
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    float s0[8], s1[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 s = *reinterpret_cast<const float4*>(sx + 64 * i + 4 * h);
-      const uint64_t x = pack_f32x2(s.x, s.y), y = pack_f32x2(s.z, s.w);
-      const float2 gx = unpack_f32x2(mul_f32x2(x, sgg)), gy = unpack_f32x2(mul_f32x2(y, sgg));
-      s0[4 * h] = gx.x, s0[4 * h + 1] = gx.y, s0[4 * h + 2] = gy.x, s0[4 * h + 3] = gy.y;
-      if (KIND == Kind::GateUp) {
-        const float2 ux = unpack_f32x2(mul_f32x2(x, suu)), uy = unpack_f32x2(mul_f32x2(y, suu));
-        s1[4 * h] = ux.x, s1[4 * h + 1] = ux.y, s1[4 * h + 2] = uy.x, s1[4 * h + 3] = uy.y;
-      }
-    }
-    tmem_ld_wait();
-    tmem_ld16x128b_x8(tb + (16u << 16) + 64 * i, vb);
-    add_half(acc[i][0], va, s0, KIND == Kind::GateUp ? s1 : s0);
-    tmem_ld_wait();
-    if (i + 1 < M) tmem_ld16x128b_x8(tb + 64 * (i + 1), va);
-    else turn();
-    add_half(acc[i][1], vb, s0, KIND == Kind::GateUp ? s1 : s0);
-  }
-}
-
 // Plain epilogue of a warp: 32 weight rows x the group's chunks, times the
 // row's weight, through the warp's staging to rows of out.
-template <int TOK>
 __device__ __forceinline__ void write_plain(const Params& P, const Tile& ti, unsigned char* stage, int n_warp, int grp,
-                                            int lane, Acc<Shape<TOK>::NC>& acc) {
+                                            int lane, Acc& acc) {
   const int N = P.N;
+  const int col0 = 32 * grp;
+  if (col0 >= ti.ntok) return;
+  if (P.row_scale != nullptr) {
 #pragma unroll
-  for (int c = 0; c < Shape<TOK>::NC; ++c) {
-    const int col0 = 32 * (2 * c + grp);
-    if (col0 >= ti.ntok) continue;
-    if (P.row_scale != nullptr) {
+    for (int j = 0; j < 8; ++j) {
+      const int col = col0 + 4 * j + (lane & 3);
+      const float w = col < ti.ntok ? __ldg(P.row_scale + ti.row0 + col) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = col0 + 4 * j + (lane & 3);
-        const float w = col < ti.ntok ? __ldg(P.row_scale + ti.row0 + col) : 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          acc[c][h][2 * j] *= w;
-          acc[c][h][2 * j + 1] *= w;
-        }
+      for (int h = 0; h < 2; ++h) {
+        acc[h][2 * j] *= w;
+        acc[h][2 * j + 1] *= w;
       }
     }
-    if (P.out_f32) {
-      // 16 tokens at a time: 32 fp32 per token, rows 144 bytes apart
-      float* st = reinterpret_cast<float*>(stage);
+  }
+  if (P.out_f32) {
+    // 16 tokens at a time: 32 fp32 per token, rows 144 bytes apart
+    float* st = reinterpret_cast<float*>(stage);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        __syncwarp();
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int rh = 0; rh < 2; ++rh)
-              st[(4 * jj + (lane & 3)) * 36 + 16 * h + 8 * rh + (lane >> 2)] = acc[c][h][2 * (4 * part + jj) + rh];
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = lane + 32 * i, tok = u >> 3, n = n_warp + (u & 7) * 4;
-          const int col = col0 + 16 * part + tok;
-          if (col < ti.ntok && n < N)
-            *reinterpret_cast<uint4*>(static_cast<float*>(P.out) + static_cast<size_t>(ti.row0 + col) * N + n) =
-                *reinterpret_cast<const uint4*>(st + tok * 36 + (u & 7) * 4);
-        }
-      }
-    } else {
-      // 32 tokens x 32 bf16 (64 bytes), rows 80 bytes apart
+    for (int part = 0; part < 2; ++part) {
       __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-        for (int rh = 0; rh < 2; ++rh) {
-          uint32_t r[4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) r[q] = pack_bf16x2(acc[c][h][4 * q + rh], acc[c][h][4 * q + 2 + rh]);
-          stmatrix_x4_trans(smem_u32(stage + matrix_token(lane) * 80 + (2 * h + rh) * 16), r[0], r[1], r[2], r[3]);
-        }
+          for (int rh = 0; rh < 2; ++rh)
+            st[(4 * jj + (lane & 3)) * 36 + 16 * h + 8 * rh + (lane >> 2)] = acc[h][2 * (4 * part + jj) + rh];
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int u = lane + 32 * i, tok = u >> 2, n = n_warp + (u & 3) * 8;
-        if (col0 + tok < ti.ntok && n < N)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + static_cast<size_t>(ti.row0 + col0 + tok) * N +
-                                    n) = *reinterpret_cast<const uint4*>(stage + tok * 80 + (u & 3) * 16);
+        const int u = lane + 32 * i, tok = u >> 3, n = n_warp + (u & 7) * 4;
+        const int col = col0 + 16 * part + tok;
+        if (col < ti.ntok && n < N)
+          *reinterpret_cast<uint4*>(static_cast<float*>(P.out) + static_cast<size_t>(ti.row0 + col) * N + n) =
+              *reinterpret_cast<const uint4*>(st + tok * 36 + (u & 7) * 4);
       }
+    }
+  } else {
+    // 32 tokens x 32 bf16 (64 bytes), rows 80 bytes apart
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh) {
+        uint32_t r[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) r[q] = pack_bf16x2(acc[h][4 * q + rh], acc[h][4 * q + 2 + rh]);
+        stmatrix_x4_trans(smem_u32(stage + matrix_token(lane) * 80 + (2 * h + rh) * 16), r[0], r[1], r[2], r[3]);
+      }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = lane + 32 * i, tok = u >> 2, n = n_warp + (u & 3) * 8;
+      if (col0 + tok < ti.ntok && n < N)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + static_cast<size_t>(ti.row0 + col0 + tok) * N +
+                                  n) = *reinterpret_cast<const uint4*>(stage + tok * 80 + (u & 3) * 16);
     }
   }
 }
 
-// Largest value bits of every token of the group over the warp's 16
-// features: halves of the tokens change hands until each lane has 4 (or, for
-// one chunk, a lane of every 8).  amax: the warp's row of the group's tokens.
-template <int NC>
-__device__ __forceinline__ void warp_amax(uint32_t (&m)[NC][8], uint32_t* amax, int lane) {
-  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-  if constexpr (NC == 4) {
-    uint32_t x[2][8], y[8], z[4];
+// Largest value bits of every row of the chunk over the warp's 16 features,
+// into the warp's amax[32].
+__device__ __forceinline__ void warp_amax(const uint32_t (&m)[8], uint32_t* amax, int lane) {
+  const bool b2 = lane & 4;
+  uint32_t z[4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t give = b4 ? m[c][j] : m[c + 2][j], keep = b4 ? m[c + 2][j] : m[c][j];
-        x[c][j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-      }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t give = b3 ? x[0][j] : x[1][j], keep = b3 ? x[1][j] : x[0][j];
-      y[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 8));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t give = b2 ? y[j] : y[j + 4], keep = b2 ? y[j + 4] : y[j];
-      z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
-    }
-    uint32_t* at = amax + 32 * (2 * b4 + b3) + 16 * b2 + (lane & 3);
+  for (int j = 0; j < 4; ++j) {  // halves change hands: four rows per lane are left
+    const uint32_t give = b2 ? m[j] : m[j + 4], keep = b2 ? m[j + 4] : m[j];
+    z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+    z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 8));
+    z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 16));
+  }
+  if (lane < 8) {
+    uint32_t* at = amax + 16 * b2 + (lane & 3);
 #pragma unroll
     for (int j = 0; j < 4; ++j) at[4 * j] = z[j];
-  } else {
-    uint32_t z[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t give = b2 ? m[0][j] : m[0][j + 4], keep = b2 ? m[0][j + 4] : m[0][j];
-      z[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
-      z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 8));
-      z[j] = max(z[j], __shfl_xor_sync(0xffffffffu, z[j], 16));
-    }
-    if (!b4 && !b3) {
-      uint32_t* at = amax + 16 * b2 + (lane & 3);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) at[4 * j] = z[j];
-    }
   }
 }
 
-template <Kind KIND, int TOK>
+template <Kind KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    fp8_pair_kernel(const __grid_constant__ Params P) {
-  using S = Shape<TOK>;
+    fp8_few_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   unsigned char* smem_a = smem;
-  unsigned char* smem_b = smem + S::STAGES * A_BYTES;
-  Ctl<TOK>& c = *reinterpret_cast<Ctl<TOK>*>(smem + S::STAGES * S::STAGE);
+  unsigned char* smem_b = smem + STAGES * A_STAGE;
+  Ctl& c = *reinterpret_cast<Ctl*>(smem + STAGES * (A_STAGE + B_STAGE));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
@@ -345,11 +265,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int npairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
     }
-    for (int b = 0; b < S::NBUF; ++b) {
+    for (int b = 0; b < NBUF; ++b) {
       mbar_init(&c.tmem_full[b], 1);
       mbar_init(&c.tmem_empty[b], 2 * 8);
     }
@@ -368,10 +288,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&P.tma_w);
-    for (int b = 0; b < S::BOXES; ++b) tma_prefetch_desc(&P.tma_x[b]);
+    for (int b = 0; b < kTokBoxes; ++b) tma_prefetch_desc(&P.tma_x[b]);
   }
   if (warp == 9) tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
-  if (warp == 0) {  // offsets + token-tile prefix, or the one group's tile count
+  if (warp == 0) {  // offsets + row-tile prefix, or the one group's tile count
     int tiles;
     if (P.offsets != nullptr) {
       const int G = P.groups;
@@ -418,13 +338,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = c.tmem_base;
   const int total_tiles = c.tiles;
   const int nkb = P.k_blocks;
+  const int nstage = (nkb + KCH - 1) / KCH;  // the last stage of an odd count holds one K block
   volatile int32_t* abort_flag = &c.abort_flag;
   auto fail = [&](int detail) {
     *abort_flag = 1;
     report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, detail);
   };
+  // A wait by a whole warp; the lanes go on together.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, P.wait_ns)) != 0;
+  };
 
-  int q = 0;          // tile-id ring position of this role
+  int q = 0;  // tile-id ring position of this role
   uint32_t qph = 0;
   auto next_q = [&] {
     if (++q == QD) {
@@ -433,143 +358,155 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   };
 
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      int t_next = -2;  // next queue position, once fetched
-      for (;;) {
-        int t = -1;
+    // The whole warp runs the loop, one elected thread acts: loop state and
+    // operands stay in uniform registers.
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int t_next = -2;  // next queue position, once fetched (lane 0 of the first CTA)
+    for (;;) {
+      int t = -1, got = 1;
+      if (lane == 0) {
         if (leader) {
           if (!mbar_wait_bounded<true>(&c.tq_empty[q], qph ^ 1u, abort_flag, P.wait_ns)) {
-            fail(55);
-            break;
+            fail(75);
+            got = 0;
+          } else {
+            if (t_next == -2) t_next = atomicAdd(P.queue, 1);
+            t = t_next < total_tiles ? t_next : -1;
+            t_next = -2;
+            c.tq[q] = t;
+            st_cluster_u32(map_to_rank(smem_u32(&c.tq[q]), 1), static_cast<uint32_t>(t));
+            mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
+            mbar_arrive(&c.tq_full[q]);
           }
-          if (t_next == -2) t_next = atomicAdd(P.queue, 1);
-          t = t_next < total_tiles ? t_next : -1;
-          t_next = -2;
-          c.tq[q] = t;
-          st_cluster_u32(map_to_rank(smem_u32(&c.tq[q]), 1), static_cast<uint32_t>(t));
-          mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
-          mbar_arrive(&c.tq_full[q]);
+        } else if (!mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
+          fail(76);
+          got = 0;
         } else {
-          if (!mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
-            fail(56);
-            break;
-          }
           t = c.tq[q];
           mbar_arrive_cluster(leader_bar(&c.tq_empty[q]));
         }
-        next_q();
-        if (t < 0) break;
-        const Tile ti = decode<TOK>(P, c, t);
-        const int half = ti.nmma / 2;  // token rows of this CTA (a multiple of 8)
-        const int xrow = ti.row0 + static_cast<int>(rank) * half;
-        int xb = 0;
-        while (xb + 1 < S::BOXES && half <= (TOK / 2 >> (xb + 1))) ++xb;
-        const uint32_t b_bytes = static_cast<uint32_t>(TOK / 2 >> xb) * BK;
-        const int kpre = nkb > 4 ? nkb - 4 : 0;  // fetch the next id while the last copies run
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_bounded(&c.empty[stage], phase ^ 1u, abort_flag, P.wait_ns)) {
-            fail(51);
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(&c.full[stage], 2u * (A_BYTES + b_bytes));
-          const uint32_t bar = leader_bar(&c.full[stage]);
-          unsigned char* sa = smem_a + stage * A_BYTES;
-          if (KIND == Kind::GateUp)
-            tma_load_5d_pair(sa, &P.tma_w, kb * BK, 0, 0, 0,
-                             (ti.g * 2 * P.N + ti.fidx * 128 + static_cast<int>(rank) * 64) / 16, bar);
-          else
-            tma_load_3d_pair(sa, &P.tma_w, kb * BK, ti.fidx * 256 + static_cast<int>(rank) * 128, ti.g, bar);
-          tma_load_2d_pair(smem_b + stage * S::B_BYTES, &P.tma_x[xb], kb * BK, xrow, bar);
-          if (leader && kb == kpre) t_next = atomicAdd(P.queue, 1);
-          ++issued;
-          if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
       }
-      if (leader) {
-        // retire from the queue; the last pair of the launch resets it
+      got = __shfl_sync(0xffffffffu, got, 0);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      if (!got) break;
+      next_q();
+      if (t < 0) break;
+      const Tile ti = decode(P, c, t);
+      const int half = ti.nmma / 2;  // rows of this CTA (a multiple of 8)
+      const int xrow = ti.row0 + static_cast<int>(rank) * half;
+      int xb = 0;
+      while (xb + 1 < kTokBoxes && half <= (TOK / 2 >> (xb + 1))) ++xb;
+      const uint32_t b_bytes = static_cast<uint32_t>(TOK / 2 >> xb) * BK;
+      const CUtensorMap* xmap = &P.tma_x[xb];
+      const int wrow = KIND == Kind::GateUp ? (ti.g * 2 * P.N + ti.fidx * 128 + static_cast<int>(rank) * 64) / 16
+                                            : ti.fidx * 256 + static_cast<int>(rank) * 128;
+      const int kpre = nstage > 2 ? nstage - 2 : 0;  // fetch the next id while the last copies run
+      for (int st = 0; st < nstage; ++st) {
+        if (!warp_wait(&c.empty[stage], phase ^ 1u)) {
+          fail(71);
+          ok = false;
+          break;
+        }
+        const int nk = min(KCH, nkb - st * KCH);
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&c.full[stage], 2u * static_cast<uint32_t>(nk) * (A_BYTES + b_bytes));
+          const uint32_t bar = leader_bar(&c.full[stage]);
+#pragma unroll
+          for (int ch = 0; ch < KCH; ++ch) {
+            if (ch < nk) {
+              const int k = (st * KCH + ch) * BK;
+              unsigned char* sa = smem_a + stage * A_STAGE + ch * A_BYTES;
+              if (KIND == Kind::GateUp)
+                tma_load_5d_pair(sa, &P.tma_w, k, 0, 0, 0, wrow, bar);
+              else
+                tma_load_3d_pair(sa, &P.tma_w, k, wrow, ti.g, bar);
+              tma_load_2d_pair(smem_b + stage * B_STAGE + ch * B_BYTES, xmap, k, xrow, bar);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0 && leader && st == kpre) t_next = atomicAdd(P.queue, 1);
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+    if (leader && lane == 0) {
+      // retire from the queue; the last pair of the launch resets it
+      __threadfence();
+      if (atomicAdd(P.queue + 1, 1) == npairs - 1) {
         __threadfence();
-        if (atomicAdd(P.queue + 1, 1) == npairs - 1) {
-          __threadfence();
-          atomicExch(P.queue, 0);
-          atomicExch(P.queue + 1, 0);
-        }
-        // drain: the last copy of each stage (both CTAs' bytes land here)
-        const int nst = issued < S::STAGES ? issued : S::STAGES;
-        for (int j = 0; j < nst; ++j) {
-          const int i = issued - 1 - j;
-          volatile int32_t never = 0;
-          if (!mbar_wait_bounded(&c.full[i % S::STAGES], static_cast<uint32_t>((i / S::STAGES) & 1), &never,
-                                 kTimeoutNs))
-            report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 59);
-        }
+        atomicExch(P.queue, 0);
+        atomicExch(P.queue + 1, 0);
+      }
+      // drain: the last copy of each stage (both CTAs' bytes land here)
+      const int nst = issued < STAGES ? issued : STAGES;
+      for (int j = 0; j < nst; ++j) {
+        const int i = issued - 1 - j;
+        volatile int32_t never = 0;
+        if (!mbar_wait_bounded(&c.full[i % STAGES], static_cast<uint32_t>((i / STAGES) & 1), &never, kTimeoutNs))
+          report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 79);
       }
     }
   } else if (warp == 9) {
     // -------------------------------------------- MMA issuer (first CTA) --
-    // The whole warp runs the loop and one elected thread issues: the operands
-    // of the MMAs then stay in uniform registers.
     if (leader) {
       const uint64_t a_desc = sw128_kmajor_desc(smem_u32(smem_a)), b_desc = sw128_kmajor_desc(smem_u32(smem_b));
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true, first = true;
       for (;;) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&c.tq_full[q], qph, abort_flag, P.wait_ns));
-        if (!ok) {
-          fail(57);
+        if (!warp_wait(&c.tq_full[q], qph)) {
+          fail(77);
           break;
         }
         const int t = __shfl_sync(0xffffffffu, c.tq[q], 0);
         if (elect_one()) mbar_arrive(&c.tq_empty[q]);
         next_q();
         if (t < 0) break;
-        const Tile ti = decode<TOK>(P, c, t);
+        const Tile ti = decode(P, c, t);
         const uint32_t idesc = umma_idesc_f16(2 * ROWS, __shfl_sync(0xffffffffu, ti.nmma, 0));
-        for (int kb = 0; kb < nkb; ++kb) {
-          ok = mbar_wait_bounded(&c.tmem_empty[buf], buf_phase ^ 1u, abort_flag, P.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
+        for (int st = 0; st < nstage && ok; ++st) {
+          if (!warp_wait(&c.full[stage], phase)) {
+            fail(73);
             ok = false;
-            fail(52);
             break;
           }
-          ok = mbar_wait_bounded(&c.full[stage], phase, abort_flag, P.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            fail(53);
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = a_desc + static_cast<uint64_t>(stage * (A_BYTES / 16));
-          const uint64_t bd = b_desc + static_cast<uint64_t>(stage * (S::B_BYTES / 16));
-          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * TOK);
-          if (elect_one()) {
+          const int nk = min(KCH, nkb - st * KCH);
+          for (int ch = 0; ch < nk; ++ch) {
+            if (!warp_wait(&c.tmem_empty[buf], buf_phase ^ 1u)) {
+              fail(72);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = a_desc + static_cast<uint64_t>((stage * A_STAGE + ch * A_BYTES) / 16);
+            const uint64_t bd = b_desc + static_cast<uint64_t>((stage * B_STAGE + ch * B_BYTES) / 16);
+            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * TOK);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)  // 32 bytes of K each
-              umma_e4m3_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-            if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
-            umma_commit_pair(&c.empty[stage]);
+              for (int kk = 0; kk < BK / 32; ++kk)  // 32 bytes of K each
+                umma_e4m3_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+              if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
+              if (ch + 1 == nk) umma_commit_pair(&c.empty[stage]);
+            }
+            __syncwarp();
+            first = false;
+            if (++buf == NBUF) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
           }
-          __syncwarp();
-          first = false;
-          if (++stage == S::STAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
-          }
-          if (++buf == S::NBUF) {
-            buf = 0;
-            buf_phase ^= 1u;
           }
         }
         if (!ok) break;
@@ -577,19 +514,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (elect_one()) {
         umma_commit_pair_leader(&c.mma_done);
         volatile int32_t never = 0;
-        if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 58);
+        if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 78);
       }
       __syncwarp();
     }
   } else if (warp == 10) {
-    // --------------------------------------------------- scales, a K block ahead
+    // --------------------------------------- scales, SK K blocks to a slot --
     const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
     int slot = 0;
     uint32_t sph = 0;
-    for (;;) {
-      bool got = mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
-      if (!__all_sync(0xffffffffu, got)) {
-        if (lane == 0) fail(61);
+    bool ok = true;
+    while (ok) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns))) {
+        fail(81);
         break;
       }
       const int t = c.tq[q];
@@ -597,50 +534,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
       if (t < 0) break;
-      const Tile ti = decode<TOK>(P, c, t);
+      const Tile ti = decode(P, c, t);
       const float* sa = P.a_scale + ti.row0;
-      // the weight's block row: gate and up rows lie in two
-      int nb = KIND == Kind::GateUp ? ti.fidx : min(ti.fidx * 2 + static_cast<int>(rank), P.n_blocks - 1);
-      if (KIND == Kind::GateUp && lane == 1) nb += P.N / 128;
+      // the weight's block row: gate (lane 0) and up (lane 1) rows lie in two
+      const int nb = KIND == Kind::GateUp ? ti.fidx + (lane & 1) * (P.N / 128)
+                                          : min(ti.fidx * 2 + static_cast<int>(rank), P.n_blocks - 1);
       const float* sw = P.w_scale + (static_cast<size_t>(ti.g) * P.n_blocks + nb) * nkb;
-      const int n = ti.ntok;
-      for (int kb = 0; kb < nkb; ++kb) {
-        got = mbar_wait_bounded(&c.sc_empty[slot], sph ^ 1u, abort_flag, P.wait_ns);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0) fail(62);
+      for (int k0 = 0; k0 < nkb; k0 += SK) {
+        if (!warp_wait(&c.sc_empty[slot], sph ^ 1u)) {
+          fail(82);
+          ok = false;
           break;
         }
-        const uint32_t dst = smem_u32(c.sc[slot]);
-        for (int i = lane; i < ti.nmma; i += 32)
-          cp_async4(dst + ((i & ~31) + scale_at(i & 31)) * 4, sa + static_cast<size_t>(kb) * P.rows + min(i, n - 1), i < n);
-        if (lane < (KIND == Kind::GateUp ? 2 : 1)) cp_async4(dst + (TOK + lane) * 4, sw + kb, true);
+        const int nk = min(SK, nkb - k0);
+        for (int k = 0; k < nk; ++k) {
+          const float* row = sa + static_cast<size_t>(k0 + k) * P.rows;
+#pragma unroll
+          for (int i = 0; i < TOK; i += 32)
+            if (i + lane < ti.ntok)
+              cp_async4(smem_u32(&c.sx[slot][k][i + scale_at(lane)]), row + i + lane, true);
+          if (lane < 2) cp_async4(smem_u32(&c.sw[slot][k][lane]), sw + k0 + k, true);
+        }
         cp_async_mbar_arrive(&c.sc_full[slot]);
         if (++slot == SC) {
           slot = 0;
           sph ^= 1u;
         }
       }
-      if (!__all_sync(0xffffffffu, got)) break;
     }
     cp_async_commit();
     cp_async_wait<0>();
-  }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+  } else if (warp < 8) {
     // ---------------------------------------- scale, add, write (warps 0-7) --
     const int grp = warp >> 2, w4 = warp & 3;
-    const uint32_t lane_addr = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tb0 = tmem_base + (static_cast<uint32_t>(w4 * 32) << 16) + static_cast<uint32_t>(32 * grp);
+    // buffers are freed by CTA-scope arrivals: only TMEM, ordered by the tcgen05
+    // fences, changes hands (a release at cluster scope is a memory barrier of
+    // about 340 clocks per K block)
     const uint32_t tmem_empty_leader = map_to_rank(smem_u32(&c.tmem_empty[0]), 0);
     const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
+    const uint32_t tmem_full = smem_u32(&c.tmem_full[0]), sc_full = smem_u32(&c.sc_full[0]);
     unsigned char* stage = c.stage[warp];
-    int buf = 0, slot = 0;
-    uint32_t buf_phase = 0, sph = 0;
-    uint32_t tile_no = 0;
+    uint32_t buf = 0, buf_phase = 0, slot = 0, sph = 0, tile_no = 0;
     bool ok = true;
     for (;;) {
       const bool gotq = ok && mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
       if (!named_barrier_and(1, 256, gotq)) {  // all eight warps go on or leave together
-        if (lane == 0 && ok && !gotq) fail(60);
+        if (lane == 0 && ok && !gotq) fail(80);
         break;
       }
       const int t = c.tq[q];
@@ -648,136 +588,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
       if (t < 0) break;
-      const Tile ti = decode<TOK>(P, c, t);
-      const int nch = (ti.nmma + 31) / 32;
-      const int mine = (nch - grp + 1) / 2;  // chunks of this group: 2 c + grp < nch
-      Acc<S::NC> acc;
+      const Tile ti = decode(P, c, t);
+      const bool mine = 32 * grp < ti.ntok;  // the group's chunk has rows
+      Acc acc;
 #pragma unroll
-      for (int i = 0; i < S::NC; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[i][h][j] = 0.f;
+        for (int j = 0; j < 16; ++j) acc[h][j] = 0.f;
 
-      // The K loop, with the chunk count a constant of its body.  Once a block
-      // is read its buffer is freed and the next block's first load started,
-      // before the last sums are added.
-      auto k_loop = [&](auto chunks) {
-        constexpr int M = decltype(chunks)::value;
-        uint32_t va[16];
-        const uint32_t tb0 = tmem_base + lane_addr + static_cast<uint32_t>(32 * grp);
-        auto wait_block = [&] {
-          if (ok) {
-            ok = mbar_wait_bounded(&c.tmem_full[buf], buf_phase, abort_flag, P.wait_ns);
-            ok = ok && mbar_wait_bounded(&c.sc_full[slot], sph, abort_flag, P.wait_ns);
-            if (!ok) fail(54);
+      for (int k0 = 0; k0 < nkb; k0 += SK) {
+        const int nk = min(SK, nkb - k0);
+        if (!mbar_try_wait(sc_full + 8u * slot, sph) && ok &&
+            !mbar_wait_addr(sc_full + 8u * slot, sph, abort_flag, P.wait_ns)) {
+          ok = false;
+          fail(84);
+        }
+        __syncwarp();
+        const float* sx = &c.sx[slot][0][32 * grp + 8 * (lane & 3)];
+        const float* sw = &c.sw[slot][0][0];
+#pragma unroll 1
+        for (int k = 0; k < nk; ++k) {
+          if (!mbar_try_wait(tmem_full + 8u * buf, buf_phase) && ok &&
+              !mbar_wait_addr(tmem_full + 8u * buf, buf_phase, abort_flag, P.wait_ns)) {
+            ok = false;
+            fail(74);
           }
           __syncwarp();
           tc_fence_after();
-          if constexpr (M > 0) tmem_ld16x128b_x8(tb0 + static_cast<uint32_t>(buf * TOK), va);
-        };
-        wait_block();
-        for (int kb = 0; kb < nkb; ++kb) {
-          const float* sc = c.sc[slot];
-          const float g0 = sc[TOK], g1 = KIND == Kind::GateUp ? sc[TOK + 1] : g0;
-          const uint32_t tb = tb0 + static_cast<uint32_t>(buf * TOK);
-          auto turn = [&] {
-            // CTA-scope arrival: only TMEM, ordered by the tcgen05 fences, changes
-            // hands (a release at cluster scope is a memory barrier per K block)
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_peer(tmem_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
-              mbar_arrive(&c.sc_empty[slot]);  // every lane has read its scales
+          uint32_t va[16], vb[16];
+          if (mine) {
+            const uint32_t tb = tb0 + buf * TOK;
+            tmem_ld16x128b_x8(tb, va);
+            tmem_ld16x128b_x8(tb + (16u << 16), vb);
+            tmem_ld_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_peer(tmem_empty_leader + 8u * buf);
+          if (mine) {
+            const float g0 = sw[0], g1 = KIND == Kind::GateUp ? sw[1] : g0;
+            float s0[8], s1[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 s = *reinterpret_cast<const float4*>(sx + 4 * h);
+              const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                s0[4 * h + j] = v[j] * g0;
+                s1[4 * h + j] = KIND == Kind::GateUp ? v[j] * g1 : s0[4 * h + j];
+              }
             }
-            if (++slot == SC) {
-              slot = 0;
-              sph ^= 1u;
-            }
-            if (++buf == S::NBUF) {
-              buf = 0;
-              buf_phase ^= 1u;
-            }
-            if (kb + 1 < nkb) wait_block();
-          };
-          if constexpr (M > 0) add_block<M, KIND, S::NC>(acc, va, tb, sc + 32 * grp + 8 * (lane & 3), g0, g1, turn);
-          else turn();
+            add_half(acc[0], va, s0, s1);
+            add_half(acc[1], vb, s0, s1);
+          }
+          sx += TOK;
+          sw += 2;
+          if (++buf == NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
         }
-      };
-      if constexpr (S::NC == 4) {
-        if (mine == 4) k_loop(std::integral_constant<int, 4>{});
-        else if (mine == 3) k_loop(std::integral_constant<int, 3>{});
-        else if (mine == 2) k_loop(std::integral_constant<int, 2>{});
-        else if (mine == 1) k_loop(std::integral_constant<int, 1>{});
-        else k_loop(std::integral_constant<int, 0>{});
-      } else {
-        if (mine == 1) k_loop(std::integral_constant<int, 1>{});
-        else k_loop(std::integral_constant<int, 0>{});
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.sc_empty[slot]);
+        if (++slot == SC) {
+          slot = 0;
+          sph ^= 1u;
+        }
       }
 
       if (KIND == Kind::Plain) {
         const int n_warp = ti.fidx * 256 + static_cast<int>(rank) * 128 + w4 * 32;
-        write_plain<TOK>(P, ti, stage, n_warp, grp, lane, acc);
+        write_plain(P, ti, stage, n_warp, grp, lane, acc);
       } else {
-        // h of 2 features (halves) per token, in place of the gate's sums
+        // h of 2 features (halves) per row, in place of the gate's sums
         const float L = P.limit;
-        uint32_t m[S::NC][8];
+        uint32_t m[8];
 #pragma unroll
-        for (int i = 0; i < S::NC; ++i)
+        for (int j = 0; j < 8; ++j) {
+          m[j] = 0u;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            m[i][j] = 0u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float* a = &acc[i][h][2 * j];
-              a[0] = swiglu_clamped(a[0], a[1], L);
-              m[i][j] = max(m[i][j], __float_as_uint(a[0]) & 0x7FFFFFFFu);
-            }
+          for (int h = 0; h < 2; ++h) {
+            float* a = &acc[h][2 * j];
+            a[0] = swiglu_clamped(a[0], a[1], L);
+            m[j] = max(m[j], __float_as_uint(a[0]) & 0x7FFFFFFFu);
           }
-        warp_amax<S::NC>(m, c.amax[grp][w4], lane);
+        }
+        warp_amax(m, c.amax[grp][w4], lane);
         named_barrier_sync(2 + grp, 128);
-        // one thread per token of the group: maximum over the CTA's 64
+        // one warp of the group, a thread per row: maximum over the CTA's 64
         // features, then over the pair's 128
-        const int gt = threadIdx.x & 127;
-        if (gt < TOK / 2) {
-          const uint32_t mine_m = max(max(c.amax[grp][0][gt], c.amax[grp][1][gt]),
-                                      max(c.amax[grp][2][gt], c.amax[grp][3][gt]));
+        if (w4 == 0) {
+          const uint32_t mine_m = max(max(c.amax[grp][0][lane], c.amax[grp][1][lane]),
+                                      max(c.amax[grp][2][lane], c.amax[grp][3][lane]));
           const uint32_t other = rank ^ 1u;
-          uint32_t* peer = &c.peer_amax[grp][tile_no & 1u][gt];
+          uint32_t* peer = &c.peer_amax[grp][tile_no & 1u][lane];
           st_cluster_u32(map_to_rank(smem_u32(peer), other), mine_m);
           mbar_arrive_cluster(map_to_rank(smem_u32(&c.amax_full[grp]), other));
           if (ok && !mbar_wait_bounded<true>(&c.amax_full[grp], tile_no & 1u, abort_flag, P.wait_ns)) {
-            fail(63);
+            fail(83);
             ok = false;
           }
           const uint32_t both = max(mine_m, *peer);
           float sc, inv;
           e4m3_block_scale(both, sc, inv);
-          c.inv[grp][gt] = inv;
-          const int col = 32 * (2 * (gt >> 5) + grp) + (gt & 31);
+          c.inv[grp][lane] = inv;
+          const int col = 32 * grp + lane;
           if (leader && col < ti.ntok) P.out_scale[static_cast<size_t>(ti.fidx) * P.rows + ti.row0 + col] = sc;
         }
-        ok = __all_sync(0xffffffffu, ok);
         named_barrier_sync(2 + grp, 128);
         const int f0 = ti.fidx * 128 + static_cast<int>(rank) * 64 + w4 * 16;
-#pragma unroll
-        for (int i = 0; i < S::NC; ++i) {
-          const int col0 = 32 * (2 * i + grp);
-          if (col0 >= ti.ntok) continue;
+        if (mine) {
           uint32_t r[4];
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq) {
-            // tokens 4 j + lane % 4, j = 2 qq and 2 qq + 1, of two neighbouring features
-            const float* iv = &c.inv[grp][32 * i + 8 * qq + (lane & 3)];
-            const float *a = &acc[i][0][4 * qq], *b = &acc[i][1][4 * qq];
+            // rows 4 j + lane % 4, j = 2 qq and 2 qq + 1, of two neighbouring features
+            const float* iv = &c.inv[grp][8 * qq + (lane & 3)];
+            const float *a = &acc[0][4 * qq], *b = &acc[1][4 * qq];
             r[qq] = e4m3x4(a[0] * iv[0], b[0] * iv[0], a[2] * iv[4], b[2] * iv[4]);
           }
           __syncwarp();
           stmatrix_x4_trans(smem_u32(stage + matrix_token(lane) * 16), r[0], r[1], r[2], r[3]);
           __syncwarp();
-          if (col0 + lane < ti.ntok)
-            *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + static_cast<size_t>(ti.row0 + col0 + lane) * P.N +
-                                      f0) = *reinterpret_cast<const uint4*>(stage + lane * 16);
+          const int col = 32 * grp + lane;
+          if (col < ti.ntok)
+            *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + static_cast<size_t>(ti.row0 + col) * P.N + f0) =
+                *reinterpret_cast<const uint4*>(stage + lane * 16);
         }
       }
       ++tile_no;
@@ -814,11 +749,10 @@ bool encode_w_gate_up(CUtensorMap* m, const void* base, int groups, int I, int K
   return encode_tma(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int TOK>
 bool encode_x(CUtensorMap (&m)[kTokBoxes], const void* base, int rows, int K) {
   const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
   const uint64_t strides[1] = {static_cast<uint64_t>(K)};
-  for (int b = 0; b < Shape<TOK>::BOXES; ++b) {
+  for (int b = 0; b < kTokBoxes; ++b) {
     const uint32_t box[2] = {BK, static_cast<uint32_t>(TOK / 2 >> b)};
     if (!encode_tma(&m[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return false;
@@ -827,7 +761,7 @@ bool encode_x(CUtensorMap (&m)[kTokBoxes], const void* base, int rows, int K) {
 }
 
 // CTA pairs that can be resident at once on the current device; 0 if unknown.
-template <Kind KIND, int TOK>
+template <Kind KIND>
 int resident_pairs() {
   static int cached[64];
   static bool known[64];
@@ -838,9 +772,9 @@ int resident_pairs() {
     memset(&lc, 0, sizeof(lc));
     lc.gridDim = dim3(2);
     lc.blockDim = dim3(THREADS);
-    lc.dynamicSmemBytes = smem_bytes<TOK>();
+    lc.dynamicSmemBytes = kSmem;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel<KIND, TOK>, &lc) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_few_kernel<KIND>, &lc) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -850,29 +784,21 @@ int resident_pairs() {
   return cached[dev];
 }
 
-template <Kind KIND, int TOK>
+template <Kind KIND>
 cudaError_t start(Params& P, const void* a, int K, int num_sms, cudaStream_t stream) {
-  if (!encode_x<TOK>(P.tma_x, a, P.rows, K)) return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fp8_pair_kernel<KIND, TOK>),
-                                   static_cast<int>(smem_bytes<TOK>()));
+  if (!encode_x(P.tma_x, a, P.rows, K)) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fp8_few_kernel<KIND>), static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   int grid = std::max(2, num_sms / 2 * 2);
-  const int pairs = resident_pairs<KIND, TOK>();
+  const int pairs = resident_pairs<KIND>();
   if (pairs > 0) grid = std::min(grid, 2 * pairs);
   // no more pairs than there can be tiles
   const int64_t most = (static_cast<int64_t>(P.rows) / TOK + std::min(P.groups, P.rows)) * P.f_tiles;
   if (most < grid / 2) grid = static_cast<int>(2 * std::max<int64_t>(1, most));
-  return launch_kernel(fp8_pair_kernel<KIND, TOK>, dim3(grid), dim3(THREADS), smem_bytes<TOK>(), stream, P);
+  return launch_kernel(fp8_few_kernel<KIND>, dim3(grid), dim3(THREADS), kSmem, stream, P);
 }
 
-template <Kind KIND>
-cudaError_t start_for(Params& P, const void* a, int K, int num_sms, cudaStream_t stream) {
-  // 64-token tiles (8 TMEM buffers, 8 smaller stages) when the groups have 64
-  // rows or fewer on average
-  return static_cast<int64_t>(P.rows) <= 64ll * P.groups ? start<KIND, 64>(P, a, K, num_sms, stream)
-                                                         : start<KIND, 256>(P, a, K, num_sms, stream);
-}
-
+// Rows of many groups: the wide form multiplies whole tiles of 256 rows.
 bool wide_preferred(int rows, int groups) { return static_cast<int64_t>(rows) > 64ll * groups; }
 
 Params base_params(const float* a_scale, int rows, const int32_t* offsets, int groups, int K, int32_t* err,
@@ -903,7 +829,7 @@ cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, i
   P.n_blocks = (p.N + 127) / 128;
   P.f_tiles = (p.N + 255) / 256;
   if (!encode_w_plain(&P.tma_w, p.w, p.groups, p.N, p.K)) return cudaErrorInvalidValue;
-  return start_for<Kind::Plain>(P, p.a, p.K, num_sms, stream);
+  return start<Kind::Plain>(P, p.a, p.K, num_sms, stream);
 }
 
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
@@ -931,7 +857,7 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
   P.f_tiles = I / 128;
   P.limit = cfg.swiglu_limit;
   if (!encode_w_gate_up(&P.tma_w, w.w_gate_up, E, I, H)) return cudaErrorInvalidValue;
-  e = start_for<Kind::GateUp>(P, x_q, H, num_sms, stream);
+  e = start<Kind::GateUp>(P, x_q, H, num_sms, stream);
   if (e != cudaSuccess) return e;
   const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
                         MOE_BF16};

@@ -75,42 +75,60 @@ __device__ __forceinline__ uint4 codes16(const float (&f)[16], float inv) {
   return o;
 }
 
-// One warp per row: 8 lanes per 128-block, 16 values (one 16-byte store of
-// codes) per lane.  Eight rows per block, so that the scales of neighbouring
-// rows, neighbours in the block-major layout, are written together.
+// One warp per row and slab of 2048 columns: 8 lanes per 128-block, 16 values
+// (one 16-byte store of codes) per lane, the slab's four loads in flight at
+// once.  Eight rows per block: their scales, neighbours in the block-major
+// layout, go through shared memory and are written 32 bytes at a time.
 // Rows outside [range[0], range[range_len]) are skipped (range given).
 constexpr int kRowWarps = 8;
+constexpr int kSlab = 2048;
 
 template <typename T>
 __global__ void __launch_bounds__(kRowWarps * 32)
     fp8_rows_kernel(const T* __restrict__ x, int64_t stride, const int32_t* __restrict__ src, int src_div, int rows,
                     int K, unsigned char* __restrict__ q, float* __restrict__ scale,
                     const int32_t* __restrict__ range, int range_len) {
-  const int r = blockIdx.x * kRowWarps + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (r >= rows) return;
-  if (range != nullptr && (r < __ldg(range) || r >= __ldg(range + range_len))) return;
-  const int64_t from = src != nullptr ? __ldg(src + r) / src_div : r;
-  const T* xr = x + from * stride;
-  unsigned char* qr = q + static_cast<size_t>(r) * K;
-  for (int k0 = 0; k0 < K; k0 += 512) {
-    const int k = k0 + lane * 16;
-    float f[16];
-    if (k < K) {
-      load16(xr + k).get(f);
-    } else {
+  __shared__ float s_scale[kSlab / 128][kRowWarps];
+  const int r0 = blockIdx.x * kRowWarps, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = r0 + w;
+  int lo = 0, hi = rows;
+  if (range != nullptr) {
+    lo = __ldg(range);
+    hi = __ldg(range + range_len);
+  }
+  const int k0 = blockIdx.y * kSlab;
+  if (r >= lo && r < hi) {
+    const int64_t from = src != nullptr ? __ldg(src + r) / src_div : r;
+    const T* xr = x + from * stride;
+    unsigned char* qr = q + static_cast<size_t>(r) * K;
+    Vec16<T> v[kSlab / 512];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.f;
+    for (int i = 0; i < kSlab / 512; ++i) {
+      const int k = k0 + 512 * i + lane * 16;
+      if (k < K) v[i] = load16(xr + k);
     }
-    uint32_t m = amax_bits16(f);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sc, inv;
-    e4m3_block_scale(m, sc, inv);
-    if (k < K) {
-      *reinterpret_cast<uint4*>(qr + k) = codes16(f, inv);
-      if ((lane & 7) == 0) scale[static_cast<size_t>(k / 128) * rows + r] = sc;
+    for (int i = 0; i < kSlab / 512; ++i) {
+      const int k = k0 + 512 * i + lane * 16;
+      if (k0 + 512 * i >= K) break;
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = 0.f;
+      if (k < K) v[i].get(f);
+      uint32_t m = amax_bits16(f);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float sc, inv;
+      e4m3_block_scale(m, sc, inv);
+      if (k < K) *reinterpret_cast<uint4*>(qr + k) = codes16(f, inv);
+      if ((lane & 7) == 0) s_scale[4 * i + lane / 8][w] = sc;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSlab / 128 * kRowWarps; i += kRowWarps * 32) {
+    const int row = r0 + i % kRowWarps, b = i / kRowWarps;
+    if (row >= lo && row < hi && k0 + 128 * b < K)
+      scale[static_cast<size_t>(k0 / 128 + b) * rows + row] = s_scale[b][i % kRowWarps];
   }
 }
 
@@ -164,7 +182,8 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 cudaError_t rows_typed(const void* x, int64_t stride, const int32_t* src, int src_div, int rows, int K, void* q,
                        float* scale, const int32_t* range, int range_len, cudaStream_t stream) {
-  return launch_kernel(fp8_rows_kernel<T>, dim3(static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps)),
+  return launch_kernel(fp8_rows_kernel<T>,
+                       dim3(static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps), (K + kSlab - 1) / kSlab),
                        dim3(kRowWarps * 32), 0, stream, static_cast<const T*>(x), stride, src, src_div, rows, K,
                        static_cast<unsigned char*>(q), scale, range, range_len);
 }

@@ -10,17 +10,24 @@
 //
 // One warp takes one token and reads its logits once; lane i holds the chunk
 // of c consecutive experts from i * c on, in registers, and c divides the
-// group size, so that a group is a run of whole lanes.  Each of the k rounds
-// is one warp-wide max (redux.sync) over 32-bit order-preserving keys; a
-// ballot finds the lowest lane, hence the lowest id, among equals.
+// group size, so that a group is a run of whole lanes.  Every value becomes a
+// 32-bit key of the same order with its place in the lane's chunk in the low
+// bits; each lane sorts its keys once (Batcher's odd-even merge sort) and puts
+// them into shared memory, and each of the k rounds is one warp-wide max
+// (redux.sync) over the lanes' heads, after which the winner's head moves on.
+// Issue slots bound it on many tokens, latency on few.
 //
 // The order is exact.  Without a bias the scores rise with the logits, so the
-// keys are the logits' own bits.  With a bias (or group sums) the fp32 values
-// carry a bounded error (gate_tau), and a token whose decision gaps are all
-// wider than its bound allows is decided by fp32; any other token is decided
-// once more from fp64 scores in shared memory (warp_exact).  The same path
-// serves group sizes that no chunk of lanes divides.
+// keys are the logits' own bits (16-bit logits share the key with the id: no
+// ties are left).  With a bias (or group sums) the fp32 values carry a bounded
+// error (gate_tau), and a token whose decision gaps are all wider than its
+// bound allows is decided by fp32; any other token, one with equal keys among
+// its first k + 1 too, is decided once more from fp64 scores in shared memory
+// (warp_exact).  The same path serves group sizes that no chunk of lanes
+// divides.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "moe_internal.h"
 
@@ -31,19 +38,22 @@ namespace {
 constexpr int kGateWarps = 4;
 
 // Half the fp32 decision width: a bound on the error of one value v = s + b.
-// Sigmoid: expf (2 ulp), one addition and one division on s <= 1, below
-// 2^-21.  Softmax: the sum of positive terms (at most 32 + 5 additions in a
-// row) adds 37 * 2^-24, below 2^-18 in all.  The bias addition rounds by
-// 2^-24 |v|; twice that is allowed.  A sum of two values has twice the bound.
+// Sigmoid: __expf is off by 2 + 1.17 |l| ulp, which moves s by s (1 - s) times
+// that, at most 2^-23.7; the fast division adds 2 ulp of s <= 1 (2^-22) and the
+// sum 1 + e half an ulp: below 2^-21.  Softmax: the sum of positive terms (at
+// most 32 + 5 additions in a row) adds 37 * 2^-24, below 2^-18 in all.  The
+// bias addition rounds by 2^-24 |v|; twice that is allowed.  A sum of two
+// values has twice the bound.  (Keys that carry a place in their low bits are
+// off by up to C ulp more: key_width.)
 __device__ __forceinline__ float gate_tau(float v, int softmax) {
   return (softmax ? 3.8146973e-06f : 4.7683716e-07f) + 1.1920929e-07f * fabsf(v);
 }
 
-__device__ __forceinline__ uint32_t key32(float v) {  // > 0; NaN above +inf
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
-  const uint32_t z = u == 0x80000000u ? 0u : u;       // -0 and 0 are equal
-  return (z & 0x80000000u) ? ~z : (z | 0x80000000u);
+// Order-preserving bits, > 0.  Adding 0 makes -0 into 0 and every NaN the
+// canonical one, 0x7FFFFFFF, whose key (all ones) is above +inf's.
+__device__ __forceinline__ uint32_t key32(float v) {
+  const uint32_t u = __float_as_uint(__fadd_rn(v, 0.f));
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float unkey32(uint32_t k) {
@@ -74,20 +84,56 @@ struct GateArgs {
   int T, E, k;
   int groups, top, max_score;  // groups == 1: none; max_score: a group's value is its largest v
   int chunk;             // experts per lane; 0: no chunk divides the groups (exact path only)
+  int group_lanes;       // lanes of a group (groups > 1, chunk > 0), and its log2 or -1
+  int group_shift;
   int softmax, renorm;
   float alpha;
   int32_t* ids;
   float* w;
 };
 
+// One logit (fp32: the sum of its slices).
 template <typename TIn>
 __device__ __forceinline__ float load_logit(const GateArgs& a, const TIn* row, int e) {
-  if (sizeof(TIn) == 4) {
-    float l = 0.f;
-    for (int s = 0; s < a.slices; ++s) l += to_f32(row[s * a.slice_stride + e]);
-    return l;
+  float l = to_f32(row[e]);
+  if (sizeof(TIn) == 4)
+    for (int s = 1; s < a.slices; ++s) l += to_f32(row[s * a.slice_stride + e]);
+  return l;
+}
+
+// The lane's chunk, experts e0 .. e0 + c - 1 (-inf past the end): 16-byte
+// loads where the row and the chunk allow (VEC), slices added in ascending
+// order.
+template <typename TIn, int C, bool VEC>
+__device__ __forceinline__ void load_chunk(const GateArgs& a, const TIn* row, int e0, float (&l)[C]) {
+  constexpr int kPer = 16 / sizeof(TIn);
+  const int c = a.chunk, E = a.E;
+  if constexpr (VEC && C % kPer == 0) {  // chunk == C, E a multiple of C
+    const bool in = e0 < E;
+    for (int s = 0; s < a.slices; ++s) {
+      uint4 raw[C / kPer];
+#pragma unroll
+      for (int i = 0; i < C / kPer; ++i)
+        raw[i] = in ? __ldg(reinterpret_cast<const uint4*>(row + s * a.slice_stride + e0) + i) : make_uint4(0, 0, 0, 0);
+      const TIn* v = reinterpret_cast<const TIn*>(raw);
+#pragma unroll
+      for (int i = 0; i < C; ++i) l[i] = s == 0 ? to_f32(v[i]) : l[i] + to_f32(v[i]);
+    }
+    if (!in) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) l[i] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) l[i] = i < c && e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+    if (sizeof(TIn) == 4) {
+      for (int s = 1; s < a.slices; ++s) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if (i < c && e0 + i < E) l[i] += to_f32(row[s * a.slice_stride + e0 + i]);
+      }
+    }
   }
-  return to_f32(row[e]);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -99,6 +145,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Score for the ranking: fast functions, within gate_tau.
+__device__ __forceinline__ float rank_score(const GateArgs& a, float l, float m, float inv_z) {
+  if (a.softmax) return l == -INFINITY ? 0.f : __expf(l - m) * inv_z;
+  return __fdividef(1.f, 1.f + __expf(-l));  // (0 where the divisor is above 2^126: off by less than 2^-126)
 }
 
 // Unbiased fp32 score.  m, inv_z: the row's maximum and 1 / sum (softmax).
@@ -197,20 +249,80 @@ __device__ int warp_exact(const GateArgs& a, const TIn* row, double* v, int lane
   return mine;
 }
 
-// C: register entries per lane (the chunk a.chunk <= C).
-template <typename TIn, int C>
+// A 16-bit logit (given as the fp32 it was widened to) and expert id in one
+// key: order-preserving bits of the logit above 65535 - id.
+template <typename TIn>
+__device__ __forceinline__ uint32_t pack_key(float l, int id) {
+  uint32_t u = sizeof(TIn) == 4 ? 0u
+               : std::is_same<TIn, __half>::value ? __half_as_ushort(__float2half_rn(l)) : __float_as_uint(l) >> 16;
+  constexpr uint32_t kInf = std::is_same<TIn, __half>::value ? 0x7C00u : 0x7F80u;
+  u = u == 0x8000u ? 0u : u;
+  u = (u & 0x7FFFu) > kInf ? 0xFFFFu : (u & 0x8000u) ? 0xFFFFu - u : u | 0x8000u;
+  return (u << 16) | (0xFFFFu - static_cast<uint32_t>(id));
+}
+
+// The logit of a key (of a packed one, or of key32's).
+template <typename TIn, bool PACKED>
+__device__ __forceinline__ float logit_of_key(uint32_t key) {
+  if (!PACKED) return unkey32(key);
+  const uint32_t k = key >> 16;
+  const uint32_t u = (k & 0x8000u) ? k & 0x7FFFu : 0xFFFFu - k;
+  return std::is_same<TIn, __half>::value ? __half2float(__ushort_as_half(static_cast<unsigned short>(u)))
+                                          : __uint_as_float(u << 16);
+}
+
+// Descending sort of a lane's keys (Batcher's odd-even merge sort).
+template <int C>
+__device__ __forceinline__ void lane_sort(uint32_t (&key)[C]) {
+#pragma unroll
+  for (int p = 1; p < C; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < C; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k && i + j + k < C; ++i)
+          if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(key[i + j], key[i + j + k]), lo = min(key[i + j], key[i + j + k]);
+            key[i + j] = hi;
+            key[i + j + k] = lo;
+          }
+}
+
+// Shared memory of a warp: its lanes' sorted keys [C + 1][32], or the E fp64
+// values of warp_exact.
+__host__ __device__ constexpr size_t gate_smem(int E, int C) {
+  const size_t keys = static_cast<size_t>(C + 1) * 32 * 4, exact = static_cast<size_t>(E) * 8;
+  return ((keys > exact ? keys : exact) + 15) / 16 * 16;
+}
+
+// C: register entries per lane (the chunk a.chunk <= C); VEC: 16-byte loads;
+// PACKED: 16-bit logits without a bias, key = logit bits above 65535 - id;
+// otherwise the low bits of a key hold C - 1 - its place in the lane's chunk.
+template <typename TIn, int C, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a) {
-  extern __shared__ __align__(16) double exact_v[];
+  extern __shared__ __align__(16) unsigned char gate_smem_raw[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= a.T) return;
   const TIn* row = static_cast<const TIn*>(a.logits) + static_cast<size_t>(t) * a.stride;
   const int E = a.E, c = a.chunk;
   const int e0 = lane * c;
+  const bool biased = !PACKED && a.bias != nullptr;  // else the logits have the scores' order
 
-  float l[C];
+  float bias[C];
+  if (VEC && biased) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) l[i] = i < c && e0 + i < E ? load_logit(a, row, e0 + i) : -INFINITY;
+    for (int i = 0; i < C; i += 4) {
+      const float4 v = e0 < E ? __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      bias[i] = v.x, bias[i + 1] = v.y, bias[i + 2] = v.z, bias[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) bias[i] = biased && i < c && e0 + i < E ? __ldg(a.bias + e0 + i) : 0.f;
+  }
+  float l[C];
+  load_chunk<TIn, C, VEC>(a, row, e0, l);
   float m = 0.f, inv_z = 0.f;
   if (c > 0 && a.softmax) {
     m = -INFINITY;
@@ -225,100 +337,118 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
   }
 
   bool exact = c == 0;
-  int mine = 0;
+  int mine = 0;  // lane r < k: the r-th expert
   if (c > 0) {
-    const bool by_logit = a.bias == nullptr;  // the logits have the scores' order
     uint32_t key[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      key[i] = 0u;
-      if (i < c && e0 + i < E) {
-        const float x = by_logit ? l[i] : gate_score(a, l[i], m, inv_z) + __ldg(a.bias + e0 + i);
-        key[i] = key32(x);
-      }
+      key[i] = PACKED ? pack_key<TIn>(l[i], e0 + i)
+                      : (key32(biased ? rank_score(a, l[i], m, inv_z) + bias[i] : l[i]) & ~(C - 1u)) | (C - 1u - i);
+      if (VEC ? e0 >= E : !(i < c && e0 + i < E)) key[i] = 0u;
     }
+    lane_sort<C>(key);
+    // a value known by its key: rounded down by up to C - 1 ulp
+    constexpr float key_width = PACKED ? 0.f : C * 1.1920929e-07f;
+    bool alive = true;  // the lane's group is kept
     if (a.groups > 1) {
-      const int per = E / a.groups;
-      const int lanes = per / c;  // lanes of a group
-      const int g = lane / lanes;
-      // the two largest values of the lane, then of the group's run of lanes
-      uint32_t b1 = 0u, b2 = 0u;
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        uint32_t x = key[i];
-        if (by_logit && !a.max_score && x != 0u) x = key32(gate_score(a, l[i], m, inv_z));
-        b2 = max(b2, min(b1, x));
-        b1 = max(b1, x);
+      const int lanes = a.group_lanes;
+      const int g = a.group_shift >= 0 ? lane >> a.group_shift : lane / lanes;
+      const bool sums = !a.max_score && lanes * c > 1;
+      // the lane's two largest values (scores rise with the logits), then its group's
+      uint32_t g1 = key[0], g2 = C > 1 ? key[C > 1 ? 1 : 0] : 0u;
+      if (!biased && sums) {
+        const float l1 = logit_of_key<TIn, PACKED>(g1), l2 = logit_of_key<TIn, PACKED>(g2);
+        g1 = g1 > C ? key32(rank_score(a, l1, m, inv_z)) : 0u;
+        g2 = g2 > C ? key32(rank_score(a, l2, m, inv_z)) : 0u;
       }
-      const int first = g * lanes;
-      uint32_t g1 = 0u, g2 = 0u;
-      for (int j = 0; j < lanes; ++j) {
-        const uint32_t o1 = __shfl_sync(0xffffffffu, b1, (first + j) & 31);
-        const uint32_t o2 = __shfl_sync(0xffffffffu, b2, (first + j) & 31);
-        g2 = max(max(g2, o2), min(g1, o1));
-        g1 = max(g1, o1);
+      if (a.group_shift >= 0) {
+        for (int o = 1; o < lanes; o *= 2) {
+          const uint32_t o1 = __shfl_xor_sync(0xffffffffu, g1, o);
+          const uint32_t o2 = __shfl_xor_sync(0xffffffffu, g2, o);
+          g2 = max(max(g2, o2), min(g1, o1));
+          g1 = max(g1, o1);
+        }
+      } else {
+        const uint32_t b1 = g1, b2 = g2;
+        const int first = g * lanes;
+        g1 = g2 = 0u;
+        for (int j = 0; j < lanes; ++j) {
+          const uint32_t o1 = __shfl_sync(0xffffffffu, b1, (first + j) & 31);
+          const uint32_t o2 = __shfl_sync(0xffffffffu, b2, (first + j) & 31);
+          g2 = max(max(g2, o2), min(g1, o1));
+          g1 = max(g1, o1);
+        }
       }
-      // value of the lane's group; NaN (key of all ones) stays the largest
-      const float v1 = unkey32(g1), v2 = unkey32(g2);
-      const uint32_t gk = a.max_score || per == 1 || g1 == 0xFFFFFFFFu ? g1 : key32(v1 + v2);
+      // value of the lane's group; NaN stays the largest
+      const uint32_t gk = !sums || g1 > 0xFF800000u + C ? g1 : key32(unkey32(g1) + unkey32(g2));
       int rank = 0;
-      uint32_t below = 0u, above = 0xFFFFFFFFu;  // nearest values on the other side of the lane's
+      uint32_t below = 0u;  // nearest value behind the lane's
       for (int j = 0; j < a.groups; ++j) {
         const uint32_t o = __shfl_sync(0xffffffffu, gk, j * lanes);
         const bool ahead = o > gk || (o == gk && j < g);
         rank += ahead;
-        if (ahead) above = min(above, o);
-        else if (j != g) below = max(below, o);
+        if (!ahead && j != g) below = max(below, o);
       }
       const bool has = g < a.groups;
       // the border between the last group kept and the first left out
       bool open = false;
-      if (has && rank == a.top - 1 && a.top < a.groups && !(by_logit && a.max_score)) {
-        const float vg = unkey32(gk), vb = unkey32(below);
-        open = !(vg - vb >= 2.f * (gate_tau(vg, a.softmax) + gate_tau(vb, a.softmax)));
+      if (!PACKED || sums) {
+        if (has && rank == a.top - 1 && a.top < a.groups) {
+          const float vg = unkey32(gk), vb = unkey32(below);
+          open = !(vg - vb > 2.f * (gate_tau(vg, a.softmax) + gate_tau(vb, a.softmax)) +
+                                 2.f * key_width * (fabsf(vg) + fabsf(vb)));
+        }
+        exact = __any_sync(0xffffffffu, open);
       }
-      exact = __any_sync(0xffffffffu, open);
-      if (!has || rank >= a.top) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) key[i] = 0u;
-      }
+      alive = has && rank < a.top;
     }
-    // k rounds (one more when fp32 has to be wide apart from the next)
-    uint32_t best = 0u;
+    // sorted keys to shared memory: a lane's head moves down by one place when
+    // it wins a round
+    uint32_t* list = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)) + lane;
+    uint32_t head = alive ? key[0] : 0u;
 #pragma unroll
-    for (int i = 0; i < C; ++i) best = max(best, key[i]);
-    float prev = 0.f;
-    const int rounds = by_logit ? a.k : a.k + 1;
-    for (int r = 0; r < rounds; ++r) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      if (top == 0u) break;  // no expert left: round k + 1 of a token that takes all
-      if (!by_logit) {
-        const float v = unkey32(top);
-        if (r > 0 && !(prev - v >= gate_tau(prev, a.softmax) + gate_tau(v, a.softmax))) exact = true;
-        prev = v;
-      }
-      const uint32_t who = __ballot_sync(0xffffffffu, best == top);
-      const int owner = __ffs(who) - 1;
-      int at = 0;
-      if (lane == owner) {
-        bool done = false;
-        best = 0u;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const bool hit = !done && key[i] == top;
-          if (hit) {
-            key[i] = 0u;
-            at = i;
-            done = true;
-          }
-          best = max(best, key[i]);
+    for (int i = 1; i < C; ++i) list[32 * i] = key[i];
+    list[32 * C] = 0u;
+    if (PACKED) {
+      for (int r = 0; r < a.k; ++r) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, head);
+        if (lane == r) mine = static_cast<int>(0xFFFFu - (top & 0xFFFFu));
+        if (head == top) {
+          list += 32;
+          head = *list;
         }
       }
-      const int id = __shfl_sync(0xffffffffu, e0 + at, owner);
-      if (lane == r) mine = id;
+    } else {
+      uint32_t won = 0u;  // lane r: the key of round r; one round more than k: the k-th has to be apart from the next
+      for (int r = 0; r <= a.k; ++r) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, head);
+        if (top == 0u) break;  // no expert is left (round k + 1): no lane's list may move past its end
+        const uint32_t id = static_cast<uint32_t>(e0) + (~head & (C - 1u));
+        const uint32_t best = __reduce_min_sync(0xffffffffu, head == top ? id : 0xFFFFFFFFu);
+        if (lane == r) {
+          mine = static_cast<int>(best);
+          won = top;
+        }
+        if (head == top && id == best) {  // (an empty lane's id may be another's)
+          list += 32;
+          head = *list;
+        }
+      }
+      // neighbours in the order: equal keys, or values too close
+      const uint32_t next = __shfl_down_sync(0xffffffffu, won, 1);
+      bool open = false;
+      if (lane < a.k && next != 0u) {  // (0: no expert was left for round k + 1)
+        const float v0 = unkey32(won), v1 = unkey32(next);
+        open = !(v0 - v1 > (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
+                               key_width * (fabsf(v0) + fabsf(v1)));
+      }
+      exact = exact || __any_sync(0xffffffffu, open);
     }
+    __syncwarp();
   }
-  if (exact) mine = warp_exact(a, row, exact_v + static_cast<size_t>(warp) * E, lane);
+  if (exact) {
+    mine = warp_exact(a, row, reinterpret_cast<double*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
+  }
 
   if (c == 0 && a.softmax) {  // statistics for the weights: not taken above
     m = -INFINITY;
@@ -354,18 +484,28 @@ int gate_chunk(int E, int groups) {
   return 0;
 }
 
-template <typename TIn>
-cudaError_t launch_gate_typed(const GateArgs& a, cudaStream_t stream) {
-  void (*fn)(GateArgs) = a.chunk <= 1   ? gate_kernel<TIn, 1>
-                         : a.chunk <= 2 ? gate_kernel<TIn, 2>
-                         : a.chunk <= 4 ? gate_kernel<TIn, 4>
-                         : a.chunk <= 8 ? gate_kernel<TIn, 8>
-                         : a.chunk <= 16 ? gate_kernel<TIn, 16>
-                                         : gate_kernel<TIn, 32>;
-  const size_t smem = static_cast<size_t>(kGateWarps) * a.E * sizeof(double);
-  static_assert(kGateWarps * MOE_MAX_EXPERTS * sizeof(double) <= 48 * 1024, "no opt-in shared memory needed");
+template <typename TIn, int C, bool PACKED>
+cudaError_t launch_gate_chunk(const GateArgs& a, cudaStream_t stream) {
+  // 16-byte loads: the chunk fills whole ones, every row (and slice) 16-byte aligned
+  constexpr int kPer = 16 / sizeof(TIn);
+  constexpr bool kCan = C % kPer == 0 && C < 32;  // (more than 512 experts, or odd groups: element loads)
+  const bool vec = kCan && a.chunk == C && a.E % C == 0 && a.stride % kPer == 0 && a.slice_stride % kPer == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
+  void (*fn)(GateArgs) = vec ? gate_kernel<TIn, C, kCan, PACKED> : gate_kernel<TIn, C, false, PACKED>;
+  const size_t smem = kGateWarps * gate_smem(a.E, C);
+  static_assert(kGateWarps * gate_smem(MOE_MAX_EXPERTS, C) <= 48 * 1024, "no opt-in shared memory needed");
   return launch_kernel(fn, dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), dim3(kGateWarps * 32), smem,
                        stream, a);
+}
+
+template <typename TIn, bool PACKED>
+cudaError_t launch_gate_typed(const GateArgs& a, cudaStream_t stream) {
+  if (a.chunk <= 1) return launch_gate_chunk<TIn, 1, PACKED>(a, stream);
+  if (a.chunk <= 2) return launch_gate_chunk<TIn, 2, PACKED>(a, stream);
+  if (a.chunk <= 4) return launch_gate_chunk<TIn, 4, PACKED>(a, stream);
+  if (a.chunk <= 8) return launch_gate_chunk<TIn, 8, PACKED>(a, stream);
+  if (a.chunk <= 16) return launch_gate_chunk<TIn, 16, PACKED>(a, stream);
+  return launch_gate_chunk<TIn, 32, PACKED>(a, stream);
 }
 
 }  // namespace
@@ -385,14 +525,20 @@ cudaError_t launch_gate(const moe_config& cfg, const void* logits, int dtype, in
   a.top = a.groups > 1 ? cfg.top_groups : 1;
   a.max_score = cfg.group_score == MOE_GROUP_MAX;
   a.chunk = gate_chunk(a.E, a.groups);
+  a.group_lanes = a.groups > 1 && a.chunk > 0 ? a.E / a.groups / a.chunk : 32;
+  a.group_shift = -1;
+  for (int s = 0; s <= 5; ++s)
+    if (a.group_lanes == 1 << s) a.group_shift = s;
   a.softmax = cfg.score == MOE_SCORE_SOFTMAX;
   a.renorm = cfg.renormalize;
   a.alpha = cfg.routed_scaling_factor;
   a.ids = ids;
   a.w = w;
-  if (dtype == MOE_F32) return launch_gate_typed<float>(a, stream);
-  if (dtype == MOE_BF16) return launch_gate_typed<__nv_bfloat16>(a, stream);
-  return launch_gate_typed<__half>(a, stream);
+  if (dtype == MOE_F32) return launch_gate_typed<float, false>(a, stream);
+  const bool packed = bias == nullptr;
+  if (dtype == MOE_BF16)
+    return packed ? launch_gate_typed<__nv_bfloat16, true>(a, stream) : launch_gate_typed<__nv_bfloat16, false>(a, stream);
+  return packed ? launch_gate_typed<__half, true>(a, stream) : launch_gate_typed<__half, false>(a, stream);
 }
 
 }  // namespace moe

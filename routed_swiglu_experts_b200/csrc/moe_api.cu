@@ -517,7 +517,7 @@ moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t row_stride, c
                             int32_t rows, int32_t K, void* q, float* scale, moe_stream_t stream) {
   if (x_type != MOE_F32 && x_type != MOE_BF16 && x_type != MOE_F16) return MOE_ERR_INVALID_ARG;
   if (rows < 0 || K < 16 || K % 16 != 0 || src_div < 1) return MOE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(rows) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(rows) > kMaxRows || K > (1 << 26)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (x == nullptr || q == nullptr || scale == nullptr) return MOE_ERR_INVALID_ARG;
   const int64_t size = x_type == MOE_F32 ? 4 : 2;
