@@ -12,41 +12,76 @@ namespace moe {
 
 namespace {
 
+// 16 values of a row as loaded: their largest magnitude (as fp32 bits, a NaN
+// above infinity) and their codes.  16-bit values are compared two at a time,
+// by their bits; bf16 values are also scaled as pairs, exactly: the inverse
+// scale is a power of two, and what falls below bf16's range is code 0 anyway.
 template <typename T>
-struct Vec16;  // 16 values of a row as loaded
+struct Vec16;
+
+__device__ __forceinline__ uint32_t max_bits2(const uint4 (&v)[2]) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  const uint32_t a = __vmaxu2(v[0].x & kAbs, v[0].y & kAbs), b = __vmaxu2(v[0].z & kAbs, v[0].w & kAbs);
+  const uint32_t c = __vmaxu2(v[1].x & kAbs, v[1].y & kAbs), d = __vmaxu2(v[1].z & kAbs, v[1].w & kAbs);
+  const uint32_t m = __vmaxu2(__vmaxu2(a, b), __vmaxu2(c, d));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
 template <>
 struct Vec16<__nv_bfloat16> {
   uint4 v[2];
-  __device__ __forceinline__ void get(float (&f)[16]) const {
+  __device__ __forceinline__ uint32_t amax() const { return max_bits2(v) << 16; }
+  __device__ __forceinline__ uint4 codes(float inv) const {
+    const __nv_bfloat162 s = __float2bfloat162_rn(inv);
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[2 * i] = bf16lo(w[i]);
-      f[2 * i + 1] = bf16hi(w[i]);
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * i]), s);
+      const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * i + 1]), s);
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(&p), b = *reinterpret_cast<const uint32_t*>(&q);
+      o[i] = e4m3x4(bf16lo(a), bf16hi(a), bf16lo(b), bf16hi(b));
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
 };
+
 template <>
 struct Vec16<__half> {
   uint4 v[2];
-  __device__ __forceinline__ void get(float (&f)[16]) const {
+  __device__ __forceinline__ uint32_t amax() const {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(max_bits2(v)))));
+  }
+  __device__ __forceinline__ uint4 codes(float inv) const {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * i]));
+      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * i + 1]));
+      o[i] = e4m3x4(p.x * inv, p.y * inv, q.x * inv, q.y * inv);
     }
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
 };
+
 template <>
 struct Vec16<float> {
   uint4 v[4];
-  __device__ __forceinline__ void get(float (&f)[16]) const {
-    const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
-                            v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i)
+      m = max(max(max(m, v[i].x & 0x7FFFFFFFu), max(v[i].y & 0x7FFFFFFFu, v[i].z & 0x7FFFFFFFu)), v[i].w & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ uint4 codes(float inv) const {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = e4m3x4(__uint_as_float(v[i].x) * inv, __uint_as_float(v[i].y) * inv, __uint_as_float(v[i].z) * inv,
+                    __uint_as_float(v[i].w) * inv);
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
 };
 
@@ -57,22 +92,6 @@ __device__ __forceinline__ Vec16<T> load16(const T* p) {
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.v[i] = __ldg(s + i);
   return r;
-}
-
-__device__ __forceinline__ uint32_t amax_bits16(const float (&f)[16]) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  return m;
-}
-
-__device__ __forceinline__ uint4 codes16(const float (&f)[16], float inv) {
-  uint4 o;
-  o.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-  o.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-  o.z = e4m3x4(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
-  o.w = e4m3x4(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
-  return o;
 }
 
 // One warp per row and slab of 2048 columns: 8 lanes per 128-block, 16 values
@@ -111,16 +130,12 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     for (int i = 0; i < kSlab / 512; ++i) {
       const int k = k0 + 512 * i + lane * 16;
       if (k0 + 512 * i >= K) break;
-      float f[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] = 0.f;
-      if (k < K) v[i].get(f);
-      uint32_t m = amax_bits16(f);
+      uint32_t m = k < K ? v[i].amax() : 0u;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       float sc, inv;
       e4m3_block_scale(m, sc, inv);
-      if (k < K) *reinterpret_cast<uint4*>(qr + k) = codes16(f, inv);
+      if (k < K) *reinterpret_cast<uint4*>(qr + k) = v[i].codes(inv);
       if ((lane & 7) == 0) s_scale[4 * i + lane / 8][w] = sc;
     }
   }
@@ -154,11 +169,7 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (n0 + 32 * i < N && k < K) {
-      float f[16];
-      v[i].get(f);
-      m = max(m, amax_bits16(f));
-    }
+    if (n0 + 32 * i < N && k < K) m = max(m, v[i].amax());
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = m;
@@ -170,11 +181,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = n0 + 32 * i;
-    if (n < N && k < K) {
-      float f[16];
-      v[i].get(f);
-      *reinterpret_cast<uint4*>(q + (g * N + n) * K + k) = codes16(f, inv);
-    }
+    if (n < N && k < K) *reinterpret_cast<uint4*>(q + (g * N + n) * K + k) = v[i].codes(inv);
   }
   if (threadIdx.x == 0) scale[blockIdx.x] = sc;
 }
