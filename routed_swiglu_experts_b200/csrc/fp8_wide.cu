@@ -90,7 +90,7 @@ struct Ctl {
   uint64_t mma_done;
   uint64_t tq_full[QD];
   uint64_t tq_empty[QD];
-  int32_t tq[QD];
+  int4 tq[QD];                         // decoded tiles: group (-1: no more), weight-row tile, first row, rows
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t tiles;
@@ -108,6 +108,7 @@ static_assert(kSmem <= 232448, "fits the 227 KB opt-in shared memory");
 struct Tile {
   int g, fidx, row0, ntok;
 };
+__device__ __forceinline__ Tile tile_of(const int4& v) { return Tile{v.x, v.y, v.z, v.w}; }
 
 // Group by group; inside a group weight-row tile major, row tile minor.
 __device__ __forceinline__ Tile decode(const WideParams& P, const Ctl& c, int t) {
@@ -263,7 +264,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       int t_next = -2;  // next queue position, once fetched (lane 0 of the first CTA)
       for (;;) {
-        int t = -1, got = 1;
+        // The first CTA takes the next tile from the launch's queue, decodes it
+        // and publishes it to every role of both CTAs.
+        Tile ti{-1, 0, 0, 0};
+        int got = 1;
         if (lane == 0) {
           if (leader) {
             if (!mbar_wait_bounded<true>(&c.tq_empty[q], qph ^ 1u, abort_flag, P.wait_ns)) {
@@ -271,10 +275,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               got = 0;
             } else {
               if (t_next == -2) t_next = atomicAdd(P.queue, 1);
-              t = t_next < total_tiles ? t_next : -1;
+              if (t_next < total_tiles) ti = decode(P, c, t_next);
               t_next = -2;
-              c.tq[q] = t;
-              st_cluster_u32(map_to_rank(smem_u32(&c.tq[q]), 1), static_cast<uint32_t>(t));
+              c.tq[q] = make_int4(ti.g, ti.fidx, ti.row0, ti.ntok);
+              const uint32_t peer = map_to_rank(smem_u32(&c.tq[q]), 1);
+              st_cluster_u32(peer, static_cast<uint32_t>(ti.g));
+              st_cluster_u32(peer + 4, static_cast<uint32_t>(ti.fidx));
+              st_cluster_u32(peer + 8, static_cast<uint32_t>(ti.row0));
+              st_cluster_u32(peer + 12, static_cast<uint32_t>(ti.ntok));
               mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
               mbar_arrive(&c.tq_full[q]);
             }
@@ -282,16 +290,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             fail(56);
             got = 0;
           } else {
-            t = c.tq[q];
-            mbar_arrive_cluster(leader_bar(&c.tq_empty[q]));
+            ti = tile_of(c.tq[q]);
+            mbar_arrive_peer(leader_bar(&c.tq_empty[q]));
           }
         }
         got = __shfl_sync(0xffffffffu, got, 0);
-        t = __shfl_sync(0xffffffffu, t, 0);
+        ti.g = __shfl_sync(0xffffffffu, ti.g, 0);
+        ti.fidx = __shfl_sync(0xffffffffu, ti.fidx, 0);
+        ti.row0 = __shfl_sync(0xffffffffu, ti.row0, 0);
+        ti.ntok = __shfl_sync(0xffffffffu, ti.ntok, 0);
         if (!got) break;
         next_q();
-        if (t < 0) break;
-        const Tile ti = decode(P, c, t);
+        if (ti.g < 0) break;
         // rows of each CTA; a CTA without rows copies none (its partial sums are never read)
         const int mine = max(0, min(ROWS, ti.ntok - static_cast<int>(rank) * ROWS));
         auto box_of = [](int n) {
@@ -364,10 +374,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             fail(57);
             break;
           }
-          const int t = __shfl_sync(0xffffffffu, c.tq[q], 0);
+          const int g = __shfl_sync(0xffffffffu, c.tq[q].x, 0);
           if (elect_one()) mbar_arrive(&c.tq_empty[q]);
           next_q();
-          if (t < 0) break;
+          if (g < 0) break;
           for (int kb = 0; kb < nkb; ++kb) {
             // the operands first: they are there long before the buffer is free
             ok = mbar_wait_bounded(&c.full[stage], phase, abort_flag, P.wait_ns);
@@ -419,12 +429,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           fail(61);
           break;
         }
-        const int t = c.tq[q];
+        const Tile ti = tile_of(c.tq[q]);
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+        if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
         next_q();
-        if (t < 0) break;
-        const Tile ti = decode(P, c, t);
+        if (ti.g < 0) break;
         const int mine = min(ROWS, ti.ntok - static_cast<int>(rank) * ROWS);
         const float* sa = P.a_scale + ti.row0 + static_cast<int>(rank) * ROWS;
         // block row of the weight scale that lane 0 (columns 0-127, gate) or 1 (128-255, up) copies
@@ -471,16 +480,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (;;) {
       const bool gotq = ok && mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
-      if (!named_barrier_and(1, 256, gotq)) {  // all eight warps go on or leave together
+      // GateUp meets at named barriers: all eight warps go on or leave together
+      if (KIND == Kind::GateUp ? !named_barrier_and(1, 256, gotq) : !__all_sync(0xffffffffu, gotq)) {
         if (lane == 0 && ok && !gotq) fail(60);
         break;
       }
-      const int t = c.tq[q];
+      // The tile is in registers before the slot is given back (the arrival
+      // depends on it), so no cluster-scope release is needed; that would wait
+      // for the last tile's stores (3200 clocks a tile between two K loops).
+      const Tile ti = tile_of(c.tq[q]);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+      if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
-      if (t < 0) break;
-      const Tile ti = decode(P, c, t);
+      if (ti.g < 0) break;
       // rows of this warp: 32 w4 .. of the CTA's
       const int row_in_cta = w4 * 32;
       const int nrows = ti.ntok - static_cast<int>(rank) * ROWS - row_in_cta;
@@ -561,19 +573,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         // 128 bytes of each row at a time through the warp's staging, so that
         // eight lanes write 128 bytes of a row
-        auto flush = [&](int n, int n_per16, size_t esize) {
+        uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPitch);
+        const unsigned char* from = stage + (lane >> 3) * kPitch + (lane & 7) * 16;
+        const int esize = P.out_f32 ? 4 : 2;
+        const size_t step = static_cast<size_t>(P.N) * esize * 4;  // four rows on
+        unsigned char* to = static_cast<unsigned char*>(P.out) + ((row + (lane >> 3)) * P.N + n0) * esize + (lane & 7) * 16;
+        const int left = nrows - (lane >> 3);
+        auto flush = [&](int part) {  // the part's 128 bytes of the 128 columns
           __syncwarp();
+          const bool in = n0 + part * (128 / esize) + (lane & 7) * (16 / esize) < P.N;
+          unsigned char* d = to + part * 128;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int u = lane + 32 * i, r = u >> 3;
-            const int col = n + (u & 7) * n_per16;
-            if (r < nrows && col < P.N)
-              *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + ((row + r) * P.N + col) * esize) =
-                  *reinterpret_cast<const uint4*>(stage + r * kPitch + (u & 7) * 16);
+            if (in && 4 * i < left) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(from + i * 4 * kPitch);
+            d += step;
           }
           __syncwarp();
         };
-        uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPitch);
         if (nrows > 0 && P.out_f32) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -583,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               mine[j] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
                                    __float_as_uint(a[3]));
             }
-            flush(n0 + 32 * h, 4, 4);
+            flush(h);
           }
         } else if (nrows > 0) {
 #pragma unroll
@@ -594,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               mine[j] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
                                    pack_bf16x2(a[6], a[7]));
             }
-            flush(n0 + 64 * h, 8, 2);
+            flush(h);
           }
         }
       } else {
