@@ -51,7 +51,6 @@ constexpr int QD = 8;                  // tile-id ring depth
 constexpr int SK = 4, SC = 3;          // scale ring: SC slots of SK K blocks
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
-constexpr int kPitch = 144;            // staged row: 128 bytes, and 16 against bank conflicts
 // readers of a tile id: MMA issuer of the first CTA, producer of the second;
 // 8 scaling warps and the scale warp of both
 constexpr uint32_t kTileReaders = 1 + 1 + 2 * 9;
@@ -63,6 +62,7 @@ constexpr int kRowBoxes = 5;  // row boxes of 128 >> i
 struct alignas(64) WideParams {
   CUtensorMap tma_w;              // {K, weight rows, G}, box {128, 64 (GateUp) or 128, 1}
   CUtensorMap tma_x[kRowBoxes];   // {K, rows}, box {128, 128 >> i}
+  CUtensorMap tma_out;            // Plain: {N, rows}, box {128 bytes, 32}
   const int32_t* offsets;         // [groups + 1], or nullptr: one group of `rows`
   const float* a_scale;           // [k_blocks, rows]
   const float* w_scale;           // [groups, n_blocks, k_blocks]
@@ -81,6 +81,7 @@ struct alignas(64) WideParams {
 };
 
 struct Ctl {
+  alignas(1024) unsigned char stage[8][32 * 128];  // output staging per warp, 128-byte rows (Plain: swizzled)
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
   uint64_t tmem_full[2];
@@ -99,7 +100,6 @@ struct Ctl {
   float sx[SC][SK][ROWS];              // row scales
   float sw[SC][SK][2];                 // weight scales: of the two column halves, or of gate and up
   uint32_t amax[2][2][ROWS];           // GateUp: per tile parity and column half
-  alignas(16) unsigned char stage[8][32 * kPitch];
 };
 
 constexpr size_t kSmem = 1024 + static_cast<size_t>(STAGES) * (A_BYTES + B_BYTES) + sizeof(Ctl);
@@ -184,6 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&P.tma_w);
+    if (KIND == Kind::Plain) tma_prefetch_desc(&P.tma_out);
     for (int b = 0; b < kRowBoxes; ++b) tma_prefetch_desc(&P.tma_x[b]);
   }
   if (warp == 9) tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
@@ -571,46 +572,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 128; ++j) acc[j] *= w;
         }
-        // 128 bytes of each row at a time through the warp's staging, so that
-        // eight lanes write 128 bytes of a row
-        uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPitch);
-        const unsigned char* from = stage + (lane >> 3) * kPitch + (lane & 7) * 16;
+        // 128 bytes of each row at a time through the warp's staging (128-byte
+        // swizzle).  A warp with all its 32 rows sends the box off by TMA and
+        // goes on; at a group's end it writes the rows it has, eight lanes to a row.
+        uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
         const int esize = P.out_f32 ? 4 : 2;
-        const size_t step = static_cast<size_t>(P.N) * esize * 4;  // four rows on
-        unsigned char* to = static_cast<unsigned char*>(P.out) + ((row + (lane >> 3)) * P.N + n0) * esize + (lane & 7) * 16;
-        const int left = nrows - (lane >> 3);
-        auto flush = [&](int part) {  // the part's 128 bytes of the 128 columns
-          __syncwarp();
-          const bool in = n0 + part * (128 / esize) + (lane & 7) * (16 / esize) < P.N;
-          unsigned char* d = to + part * 128;
+        auto flush = [&](int n) {  // staged: columns n .. n + 128 / esize
+          if (nrows >= 32) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n < P.N) tma_store_2d(&P.tma_out, stage, n, static_cast<int>(row));
+          } else {
+            __syncwarp();
+            const bool in = n + (lane & 7) * (16 / esize) < P.N;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (in && 4 * i < left) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(from + i * 4 * kPitch);
-            d += step;
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              if (in && r < nrows)
+                *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) +
+                                          ((row + r) * P.N + n) * esize + (lane & 7) * 16) =
+                    *reinterpret_cast<const uint4*>(stage + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+            }
           }
+        };
+        auto reuse = [&] {  // the staging's last contents have been read
+          if (lane == 0) tma_store_wait_read();
           __syncwarp();
         };
         if (nrows > 0 && P.out_f32) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
+            reuse();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float* a = acc + 32 * h + 4 * j;
-              mine[j] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
-                                   __float_as_uint(a[3]));
+              mine[j ^ (lane & 7)] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                                                __float_as_uint(a[3]));
             }
-            flush(h);
+            flush(n0 + 32 * h);
           }
         } else if (nrows > 0) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            reuse();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float* a = acc + 64 * h + 8 * j;
-              mine[j] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                                   pack_bf16x2(a[6], a[7]));
+              mine[j ^ (lane & 7)] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
             }
-            flush(h);
+            flush(n0 + 64 * h);
           }
         }
       } else {
@@ -655,6 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       ++tile_no;
     }
+    if (KIND == Kind::Plain && lane == 0) tma_store_wait();
   }
 
   tc_fence_before();
@@ -725,6 +737,15 @@ cudaError_t start(const Fp8Problem& p, float* out_scale, float limit, int32_t* e
   for (int b = 0; b < kRowBoxes; ++b) {
     const uint32_t xb[2] = {BK, static_cast<uint32_t>(ROWS >> b)};
     if (!encode_tma(&P.tma_x[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  if (KIND == Kind::Plain) {
+    const uint64_t esize = P.out_f32 ? 4 : 2;
+    const uint64_t od[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.rows)};
+    const uint64_t os[1] = {static_cast<uint64_t>(p.N) * esize};
+    const uint32_t ob[2] = {static_cast<uint32_t>(128 / esize), 32};
+    if (!encode_tma(&P.tma_out, P.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,
+                    od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fp8_wide_kernel<KIND>), static_cast<int>(kSmem));
