@@ -798,8 +798,17 @@ cudaError_t start(Params& P, const void* a, int K, int num_sms, cudaStream_t str
   return launch_kernel(fp8_few_kernel<KIND>, dim3(grid), dim3(THREADS), kSmem, stream, P);
 }
 
-// Rows of many groups: the wide form multiplies whole tiles of 256 rows.
-bool wide_preferred(int rows, int groups) { return static_cast<int64_t>(rows) > 64ll * groups; }
+// Which form: this one up to 56 rows a group on average, or as long as all its
+// tiles run at once; above, its tiles of 64 rows read the weights again for
+// each (through L2), and the wide form's 256-row tiles are worth their padding.
+// Both measured, feed-forward of 64 experts (H 2048, I 1408), rows per expert:
+// 16: 144 us here, 188 wide; 48: 159, 192; 64: 204, 193; 127: 315, 202.  One
+// group (N 6144, K 2048): 192 rows (72 tiles) 12.7 us here, 15.5 wide; 256 rows
+// (96 tiles) 18.8, 16.0.
+bool wide_preferred(int rows, int groups, int f_tiles, int num_sms) {
+  if (static_cast<int64_t>(rows) <= 56ll * groups) return false;
+  return (static_cast<int64_t>(rows) / TOK + groups) * f_tiles > num_sms / 2;
+}
 
 Params base_params(const float* a_scale, int rows, const int32_t* offsets, int groups, int K, int32_t* err,
                    int32_t* queue) {
@@ -819,7 +828,7 @@ Params base_params(const float* a_scale, int rows, const int32_t* offsets, int g
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
-  if (wide_preferred(p.rows, p.groups)) return launch_fp8_wide_gemm(p, err, queue, num_sms, stream);
+  if (wide_preferred(p.rows, p.groups, (p.N + 255) / 256, num_sms)) return launch_fp8_wide_gemm(p, err, queue, num_sms, stream);
   Params P = base_params(p.a_scale, p.rows, p.offsets, p.groups, p.K, err, queue);
   P.w_scale = p.w_scale;
   P.out = p.out;
@@ -839,14 +848,14 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
   const int H = cfg.hidden, I = cfg.expert_inter, E = cfg.num_experts;
   cudaError_t e = launch_fp8_quantize(x_rows, MOE_BF16, H, gather_src, cfg.top_k, rows, H, x_q, x_s, offsets, E, stream);
   if (e != cudaSuccess) return e;
-  if (wide_preferred(rows, E)) {
+  const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
+                        MOE_BF16};
+  if (wide_preferred(rows, E, I / 128, num_sms)) {
     const Fp8Problem gate_up{x_q, x_s, rows, offsets, E, w.w_gate_up, static_cast<const float*>(w.s_gate_up), I, H, nullptr,
                              h_q, 0};
     e = launch_fp8_wide_gateup(gate_up, h_s, cfg.swiglu_limit, err, queues, num_sms, stream);
     if (e != cudaSuccess) return e;
-    const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
-                          MOE_BF16};
-    return launch_fp8_wide_gemm(down, err, queues + 2, num_sms, stream);
+    return launch_fp8_gemm(down, err, queues + 2, num_sms, stream);
   }
   Params P = base_params(x_s, rows, offsets, E, H, err, queues);
   P.w_scale = static_cast<const float*>(w.s_gate_up);
@@ -859,8 +868,6 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
   if (!encode_w_gate_up(&P.tma_w, w.w_gate_up, E, I, H)) return cudaErrorInvalidValue;
   e = start<Kind::GateUp>(P, x_q, H, num_sms, stream);
   if (e != cudaSuccess) return e;
-  const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
-                        MOE_BF16};
   return launch_fp8_gemm(down, err, queues + 2, num_sms, stream);
 }
 
