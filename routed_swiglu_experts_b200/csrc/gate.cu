@@ -15,7 +15,11 @@
 // bits; each lane sorts its keys once (Batcher's odd-even merge sort) and puts
 // them into shared memory, and each of the k rounds is one warp-wide max
 // (redux.sync) over the lanes' heads, after which the winner's head moves on.
-// Issue slots bound it on many tokens, latency on few.
+// Measured (graph replay): one token of 256 experts in 8 groups 3.5 us, 512
+// tokens 4.9, 16384 tokens 24 us (0.7 TB/s of logits): issue slots bound it on
+// many tokens (about 850 instructions a token), latency on few.  Four tokens
+// per warp, eight lanes each, halve the instructions and came to 22.9 us there,
+// slower below 8192 tokens: the chain of one token stays as long.
 //
 // The order is exact.  Without a bias the scores rise with the logits, so the
 // keys are the logits' own bits (16-bit logits share the key with the id: no
@@ -176,6 +180,7 @@ __device__ int warp_exact(const GateArgs& a, const TIn* row, double* v, int lane
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
+#pragma unroll 4
   for (int e = lane; e < E; e += 32) {
     const float l = load_logit(a, row, e);
     double s;
@@ -195,6 +200,7 @@ __device__ int warp_exact(const GateArgs& a, const TIn* row, double* v, int lane
     if (lane < a.groups) {
       double b1 = -INFINITY, b2 = -INFINITY;
       bool nan = false;
+#pragma unroll 4
       for (int i = 0; i < per; ++i) {
         const double x = v[lane * per + i];
         nan |= x != x;
@@ -225,25 +231,34 @@ __device__ int warp_exact(const GateArgs& a, const TIn* row, double* v, int lane
     keys[e] = ((keep >> (a.groups > 1 ? e / per : 0)) & 1u) ? key64(x) : 0ull;
   }
   __syncwarp();
-  for (int r = 0; r < a.k; ++r) {
-    unsigned long long best = 0;
-    int id = 0x7fffffff;
-    for (int e = lane; e < E; e += 32)
-      if (keys[e] > best) {
-        best = keys[e];
-        id = e;
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oid = __shfl_xor_sync(0xffffffffu, id, o);
-      if (ob > best || (ob == best && oid < id)) {
-        best = ob;
-        id = oid;
+  // each lane keeps its best key (of e = lane, lane + 32, ...; the lowest e
+  // among equals); the winner's lane looks for its next
+  unsigned long long best;
+  int at;
+  auto scan = [&] {
+    best = 0ull;
+    at = 0x7fffffff;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) {
+      const unsigned long long x = keys[e];
+      if (x > best) {
+        best = x;
+        at = e;
       }
     }
+  };
+  scan();
+  for (int r = 0; r < a.k; ++r) {
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+    const uint32_t top_hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t top_lo = __reduce_max_sync(0xffffffffu, hi == top_hi ? lo : 0u);
+    const bool top = hi == top_hi && lo == top_lo;
+    const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
     if (lane == r) mine = id;
-    if ((id & 31) == lane) keys[id] = 0ull;
+    if (top && at == id) {
+      keys[id] = 0ull;
+      scan();
+    }
     __syncwarp();
   }
   return mine;
@@ -271,22 +286,47 @@ __device__ __forceinline__ float logit_of_key(uint32_t key) {
                                           : __uint_as_float(u << 16);
 }
 
-// Descending sort of a lane's keys (Batcher's odd-even merge sort).
+// The order of k experts whose set is certain (lane r < k holds one of them):
+// by fp64 biased sigmoid scores, or by the logits themselves, ties to the lower
+// id.  Lane r gets the r-th.  s: k words of shared memory.
+template <typename TIn>
+__device__ int warp_order(const GateArgs& a, const TIn* row, int id, uint32_t* s, int lane) {
+  double v = 0.0;
+  if (lane < a.k) {
+    const double l = static_cast<double>(load_logit(a, row, id));
+    v = a.bias != nullptr ? 1.0 / (1.0 + exp(-l)) + static_cast<double>(a.bias[id]) : l;
+  }
+  const unsigned long long key = key64(v);
+  int rank = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
+    const int oid = __shfl_sync(0xffffffffu, id, j);
+    rank += o > key || (o == key && oid < id);
+  }
+  __syncwarp();
+  if (lane < a.k) s[rank] = static_cast<uint32_t>(id);
+  __syncwarp();
+  return lane < a.k ? static_cast<int>(s[lane]) : 0;
+}
+
+// Descending sort of a lane's keys (Batcher's odd-even merge sort): all steps
+// (P, K) in order, each one flat loop, so that every index is a constant.
+template <int C, int P, int K>
+__device__ __forceinline__ void sort_step(uint32_t (&key)[C]) {
+#pragma unroll
+  for (int x = K % P; x + K < C; ++x) {
+    if (((x - K % P) / K) % 2 == 0 && x / (2 * P) == (x + K) / (2 * P)) {
+      const uint32_t hi = max(key[x], key[x + K]), lo = min(key[x], key[x + K]);
+      key[x] = hi;
+      key[x + K] = lo;
+    }
+  }
+  if constexpr (K > 1) sort_step<C, P, K / 2>(key);
+  else if constexpr (2 * P < C) sort_step<C, 2 * P, 2 * P>(key);
+}
 template <int C>
 __device__ __forceinline__ void lane_sort(uint32_t (&key)[C]) {
-#pragma unroll
-  for (int p = 1; p < C; p *= 2)
-#pragma unroll
-    for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-      for (int j = k % p; j + k < C; j += 2 * k)
-#pragma unroll
-        for (int i = 0; i < k && i + j + k < C; ++i)
-          if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-            const uint32_t hi = max(key[i + j], key[i + j + k]), lo = min(key[i + j], key[i + j + k]);
-            key[i + j] = hi;
-            key[i + j + k] = lo;
-          }
+  if constexpr (C > 1) sort_step<C, 1, 1>(key);
 }
 
 // Shared memory of a warp: its lanes' sorted keys [C + 1][32], or the E fp64
@@ -434,7 +474,8 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
           head = *list;
         }
       }
-      // neighbours in the order: equal keys, or values too close
+      // neighbours in the order: equal keys, or values too close.  Apart from the
+      // last pair that is a question of order alone.
       const uint32_t next = __shfl_down_sync(0xffffffffu, won, 1);
       bool open = false;
       if (lane < a.k && next != 0u) {  // (0: no expert was left for round k + 1)
@@ -442,7 +483,10 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
         open = !(v0 - v1 > (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
                                key_width * (fabsf(v0) + fabsf(v1)));
       }
-      exact = exact || __any_sync(0xffffffffu, open);
+      const uint32_t opens = __ballot_sync(0xffffffffu, open);
+      exact = exact || ((opens >> (a.k - 1)) & 1u) || (opens != 0u && biased && a.softmax);
+      if (opens != 0u && !exact)
+        mine = warp_order(a, row, mine, reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
     }
     __syncwarp();
   }
@@ -473,8 +517,8 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
   }
 }
 
-// Experts per lane: E experts on 32 lanes; with groups a divisor of the
-// group size, so that a lane holds experts of one group only.
+// Experts per lane: E experts on 32 lanes; with groups a divisor of the group
+// size, so that a lane holds experts of one group only.  0: there is none.
 int gate_chunk(int E, int groups) {
   const int least = (E + 31) / 32;
   if (groups <= 1) return least;
@@ -484,14 +528,18 @@ int gate_chunk(int E, int groups) {
   return 0;
 }
 
+// 16-byte loads: the chunk fills whole ones, every row (and slice) 16-byte aligned.
+template <typename TIn>
+bool gate_vec(const GateArgs& a, int C) {
+  const int per = 16 / static_cast<int>(sizeof(TIn));
+  return C % per == 0 && C % 4 == 0 && a.chunk == C && a.E % C == 0 && a.stride % per == 0 && a.slice_stride % per == 0 &&
+         (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
+}
+
 template <typename TIn, int C, bool PACKED>
 cudaError_t launch_gate_chunk(const GateArgs& a, cudaStream_t stream) {
-  // 16-byte loads: the chunk fills whole ones, every row (and slice) 16-byte aligned
-  constexpr int kPer = 16 / sizeof(TIn);
-  constexpr bool kCan = C % kPer == 0 && C < 32;  // (more than 512 experts, or odd groups: element loads)
-  const bool vec = kCan && a.chunk == C && a.E % C == 0 && a.stride % kPer == 0 && a.slice_stride % kPer == 0 &&
-                   (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
-  void (*fn)(GateArgs) = vec ? gate_kernel<TIn, C, kCan, PACKED> : gate_kernel<TIn, C, false, PACKED>;
+  constexpr bool kCan = C % (16 / sizeof(TIn)) == 0 && C < 32;  // (more than 512 experts, or odd groups: element loads)
+  void (*fn)(GateArgs) = kCan && gate_vec<TIn>(a, C) ? gate_kernel<TIn, C, kCan, PACKED> : gate_kernel<TIn, C, false, PACKED>;
   const size_t smem = kGateWarps * gate_smem(a.E, C);
   static_assert(kGateWarps * gate_smem(MOE_MAX_EXPERTS, C) <= 48 * 1024, "no opt-in shared memory needed");
   return launch_kernel(fn, dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), dim3(kGateWarps * 32), smem,
