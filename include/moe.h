@@ -390,7 +390,8 @@ MOE_API moe_status moe_forward_ep(const moe_config* cfg, const moe_weights* w, i
  *           16-byte aligned (base and row_stride * element size)
  *   q       E4M3 [rows, K] out, 16-byte aligned;  K a multiple of 16
  *   scale   fp32 [ceil(K / 128), rows] out (block-major)
- *   src     int32 [rows] or NULL;  src_div >= 1 */
+ *   src     int32 [rows] or NULL;  src_div >= 1;  src[r] / src_div has to be a
+ *           row of x (not checked: the values live on the device) */
 MOE_API moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t row_stride, const int32_t* src,
                                     int32_t src_div, int32_t rows, int32_t K, void* q, float* scale,
                                     moe_stream_t stream);
@@ -478,8 +479,10 @@ MOE_API moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_byt
  * pairs; the pages have no counterpart.  Zeroes `scratch` (as above; its
  * first 256 bytes are laid out like a workspace header) and launches one
  * pair (two CTAs on two SMs) of
- *   MOE_SELFTEST_PAIR_BF16: the bf16 grouped gate/up kernel, or
- *   MOE_SELFTEST_PAIR_INT4: the int4 (W4A16 prefill) grouped gate/up kernel,
+ *   MOE_SELFTEST_PAIR_BF16: the bf16 grouped gate/up kernel,
+ *   MOE_SELFTEST_PAIR_INT4: the int4 (W4A16 prefill) grouped gate/up kernel, or
+ *   MOE_SELFTEST_PAIR_FP8_FEW, MOE_SELFTEST_PAIR_FP8_WIDE: the FP8 product's
+ *   kernels for groups of few and of many rows,
  * on one tiny tile of zero operands held in scratch, with the signal that
  * the tile's accumulator is complete never sent to the epilogue and every
  * wait on another role limited to 20 ms.  Both CTAs' epilogue waits run
@@ -491,6 +494,8 @@ MOE_API moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_byt
  * enqueued; MOE_ERR_INVALID_ARG for another `kernel`. */
 #define MOE_SELFTEST_PAIR_BF16 0
 #define MOE_SELFTEST_PAIR_INT4 1
+#define MOE_SELFTEST_PAIR_FP8_FEW 3
+#define MOE_SELFTEST_PAIR_FP8_WIDE 4
 MOE_API moe_status moe_selftest_pair_timeout(void* scratch, size_t scratch_bytes, int32_t kernel,
                                              moe_stream_t stream);
 

@@ -827,9 +827,15 @@ Params base_params(const float* a_scale, int rows, const int32_t* offsets, int g
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
-  if (wide_preferred(p.rows, p.groups, (p.N + 255) / 256, num_sms)) return launch_fp8_wide_gemm(p, err, queue, num_sms, stream);
+namespace {
+
+cudaError_t few_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream,
+                     bool selftest = false) {
   Params P = base_params(p.a_scale, p.rows, p.offsets, p.groups, p.K, err, queue);
+  if (selftest) {
+    P.wait_ns = 20000000ull;
+    P.test_withhold = 1;
+  }
   P.w_scale = p.w_scale;
   P.out = p.out;
   P.out_f32 = p.out_type == MOE_F32;
@@ -839,6 +845,18 @@ cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, i
   P.f_tiles = (p.N + 255) / 256;
   if (!encode_w_plain(&P.tma_w, p.w, p.groups, p.N, p.K)) return cudaErrorInvalidValue;
   return start<Kind::Plain>(P, p.a, p.K, num_sms, stream);
+}
+
+}  // namespace
+
+// Test hook: as launch_fp8_wide_timeout_selftest, on this form (detail 74).
+cudaError_t launch_fp8_few_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream) {
+  return few_gemm(fp8_selftest_problem(scratch), err, queue, 2, stream, true);
+}
+
+cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
+  return wide_preferred(p.rows, p.groups, (p.N + 255) / 256, num_sms) ? launch_fp8_wide_gemm(p, err, queue, num_sms, stream)
+                                                                      : few_gemm(p, err, queue, num_sms, stream);
 }
 
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,

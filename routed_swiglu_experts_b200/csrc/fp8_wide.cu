@@ -705,7 +705,7 @@ int resident_pairs() {
 
 template <Kind KIND>
 cudaError_t start(const Fp8Problem& p, float* out_scale, float limit, int32_t* err, int32_t* queue, int num_sms,
-                  cudaStream_t stream) {
+                  cudaStream_t stream, bool selftest = false) {
   WideParams P;
   memset(&P, 0, sizeof(P));
   P.offsets = p.offsets;
@@ -725,7 +725,8 @@ cudaError_t start(const Fp8Problem& p, float* out_scale, float limit, int32_t* e
   P.limit = limit;
   P.err = err;
   P.queue = queue;
-  P.wait_ns = kTimeoutNs;
+  P.wait_ns = selftest ? 20000000ull : kTimeoutNs;
+  P.test_withhold = selftest;
   const uint64_t K = static_cast<uint64_t>(p.K);
   const uint64_t wd[3] = {K, static_cast<uint64_t>(w_rows), static_cast<uint64_t>(p.groups)};
   const uint64_t ws[2] = {K, K * w_rows};
@@ -763,6 +764,15 @@ cudaError_t start(const Fp8Problem& p, float* out_scale, float limit, int32_t* e
 
 cudaError_t launch_fp8_wide_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
   return start<Kind::Plain>(p, nullptr, 0.f, err, queue, num_sms, stream);
+}
+
+// Test hook: one tile (16 rows, 128 columns, K = 128; zero operands in
+// `scratch`) on one CTA pair whose first (only) partial sum is never signalled
+// to the scaling warps, with every wait on another role limited to 20 ms.  The
+// scaling warps of both CTAs record MOE_ERR_DEVICE_TIMEOUT (detail 54) and
+// finish the tile without waiting; the other roles finish on their normal paths.
+cudaError_t launch_fp8_wide_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream) {
+  return start<Kind::Plain>(fp8_selftest_problem(scratch), nullptr, 0.f, err, queue, 2, stream, true);
 }
 
 cudaError_t launch_fp8_wide_gateup(const Fp8Problem& p, float* out_scale, float limit, int32_t* err, int32_t* queue,

@@ -568,10 +568,18 @@ moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_bytes, moe_
 moe_status moe_selftest_pair_timeout(void* scratch, size_t scratch_bytes, int32_t kernel, moe_stream_t stream) {
   if (scratch == nullptr || scratch_bytes < MOE_SELFTEST_SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(scratch) & 255u) != 0) return MOE_ERR_INVALID_ARG;
-  if (kernel != MOE_SELFTEST_PAIR_BF16 && kernel != MOE_SELFTEST_PAIR_INT4) return MOE_ERR_INVALID_ARG;
+  if (kernel != MOE_SELFTEST_PAIR_BF16 && kernel != MOE_SELFTEST_PAIR_INT4 && kernel != MOE_SELFTEST_PAIR_FP8_FEW &&
+      kernel != MOE_SELFTEST_PAIR_FP8_WIDE)
+    return MOE_ERR_INVALID_ARG;
   MOE_CUDA_TRY(cudaMemsetAsync(scratch, 0, MOE_SELFTEST_SCRATCH_BYTES, stream));
   if (kernel == MOE_SELFTEST_PAIR_BF16)
     return from_cuda(launch_pair_timeout_selftest(scratch, err_word(scratch), tile_queue(scratch, kQueueGateUp), stream));
+  if (kernel == MOE_SELFTEST_PAIR_FP8_FEW)
+    return from_cuda(
+        launch_fp8_few_timeout_selftest(scratch, err_word(scratch), tile_queue(scratch, kQueueFp8GateUp), stream));
+  if (kernel == MOE_SELFTEST_PAIR_FP8_WIDE)
+    return from_cuda(
+        launch_fp8_wide_timeout_selftest(scratch, err_word(scratch), tile_queue(scratch, kQueueFp8GateUp), stream));
   return from_cuda(
       launch_int4_pair_timeout_selftest(scratch, err_word(scratch), tile_queue(scratch, kQueueInt4GateUp), stream));
 }

@@ -60,6 +60,8 @@ cudaError_t launch_splitk_timeout_selftest(void* scratch, int32_t* err, cudaStre
 // Test hooks of the CTA-pair kernels' timeout paths (see moe_selftest_pair_timeout).
 cudaError_t launch_pair_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream);
 cudaError_t launch_int4_pair_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream);
+cudaError_t launch_fp8_few_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream);
+cudaError_t launch_fp8_wide_timeout_selftest(void* scratch, int32_t* err, int32_t* queue, cudaStream_t stream);
 int router_actual_splits(int T, int E, int H, int k_splits);
 cudaError_t launch_router_gemm(const void* x, int T, int H, const void* w_split, int E, int k_splits, float* part,
                                int32_t* err, int num_sms, cudaStream_t stream);
@@ -171,6 +173,12 @@ struct Fp8Problem {
   void* out;               // [rows, N] of out_type
   int out_type;            // MOE_BF16 or MOE_F32
 };
+// The tile of the kernels' timeout hooks: 16 rows x 128 columns, K = 128, in scratch.
+inline Fp8Problem fp8_selftest_problem(void* scratch) {
+  unsigned char* base = static_cast<unsigned char*>(scratch);
+  return Fp8Problem{base + 1024, reinterpret_cast<float*>(base + 512), 16, nullptr, 1, base + 4096,
+                    reinterpret_cast<float*>(base + 768), 128, 128, nullptr, base + 20480, MOE_BF16};
+}
 // queue: the launch's two tile-queue words in the workspace header (zero).
 cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
 // The forms for groups of many rows (fp8_wide.cu); gate/up: p.N features, p.out

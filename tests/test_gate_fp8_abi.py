@@ -143,3 +143,32 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError, match="missing"):
         rse.moe_fp8_gemm(None, None, None, None, None, None, None, None)
     assert _abi.weight_format(torch.zeros(1, dtype=torch.float8_e4m3fn)) == _abi.MOE_W_FP8_B128
+
+
+def test_fp8_selftest_argument_checks(lib):
+    n = _abi.MOE_SELFTEST_SCRATCH_BYTES
+    for kernel in (_abi.MOE_SELFTEST_PAIR_FP8_FEW, _abi.MOE_SELFTEST_PAIR_FP8_WIDE):
+        assert lib.moe_selftest_pair_timeout(None, n, kernel, None) == WS
+        assert lib.moe_selftest_pair_timeout(FAKE, n - 1, kernel, None) == WS
+        assert lib.moe_selftest_pair_timeout(FAKE + 16, n, kernel, None) == BAD
+    assert lib.moe_selftest_pair_timeout(FAKE, n, 5, None) == BAD
+
+
+def test_new_constants_match_the_header(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    names = ["MOE_W_FP8_B128", "MOE_SCORE_SIGMOID", "MOE_SCORE_SOFTMAX", "MOE_GROUP_SUM2", "MOE_GROUP_MAX", "MOE_F32",
+             "MOE_BF16", "MOE_F16", "MOE_MAX_GROUPS", "MOE_WS_HEADER_BYTES", "MOE_SELFTEST_PAIR_FP8_FEW",
+             "MOE_SELFTEST_PAIR_FP8_WIDE"]
+    src = tmp_path / "c.c"
+    src.write_text('#include <stdio.h>\n#include "moe.h"\nint main(void) {\n' +
+                   "".join(f'  printf("%d\\n", (int)({n}));\n' for n in names) + "  return 0;\n}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o",
+                    str(tmp_path / "c")], check=True)
+    out = subprocess.run([str(tmp_path / "c")], check=True, capture_output=True, text=True).stdout.split()
+    assert [int(v) for v in out] == [getattr(_abi, n) for n in names]

@@ -12,6 +12,7 @@ whose fp32 value falls on the other side of an E4M3 border than the fp64 one
 (one in 2000 of them, off by a step of 2^-3 at most: sqrt(1/2000) / 8 = 2^-8.5)."""
 
 import math
+import time
 from types import SimpleNamespace
 
 import pytest
@@ -134,7 +135,9 @@ def check_gemm(out, want, mag, K, out_dtype):
 
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,N,K", [(1, 8, 16), (1, 256, 128), (3, 136, 144), (16, 512, 256), (17, 264, 400), (64, 128, 2000),
-                                      (65, 1000, 640), (255, 392, 1024), (257, 256, 384), (600, 520, 272)])
+                                      (65, 1000, 640), (255, 392, 1024), (257, 256, 384), (600, 520, 272),
+                                      # more tiles of 64 rows than run at once: the form for many rows
+                                      (1300, 1032, 400), (1153, 2056, 144), (2100, 1000, 1152), (4900, 136, 128)])
 def test_dense_product(rows, N, K, out_dtype):
     a, sa, w, sw, _ = gemm_inputs(rows, N, K, 1, rows + N + K)
     out = torch.full((rows, N), 7.0, dtype=out_dtype, device="cuda")
@@ -152,6 +155,9 @@ GROUPS = {
     "ragged": ([0, 31, 95, 96, 223, 480, 1009], 392, 528),
     "many": ([3 * i + (i % 2) for i in range(129)], 128, 128),
     "not_all_rows": ([4, 20, 20, 97], 264, 400),
+    # the form for many rows: whole and ragged tiles, a CTA without rows, an empty and a hot group
+    "wide": ([0, 256, 300, 300, 1500, 1628, 1629, 2300], 1032, 272),
+    "wide_not_all_rows": ([7, 200, 2200], 776, 640),
 }
 
 
@@ -257,6 +263,10 @@ LAYERS = {
     "clamped": dict(T=200, H=256, E=4, k=2, I=128, limit=0.5),
     "unclamped": dict(T=200, H=256, E=4, k=2, I=128, limit=math.inf),
     "many_experts": dict(T=40, H=128, E=128, k=16, I=128),
+    # the form for many rows on both products
+    "wide": dict(T=1500, H=1280, E=3, k=2, I=640, I_s=64),
+    "wide_hot": dict(T=1700, H=1024, E=8, k=1, I=512, hot=3),
+    "wide_clamped": dict(T=1600, H=1152, E=4, k=2, I=512, limit=0.5),
 }
 
 
@@ -324,12 +334,50 @@ def _error_free(part):
     return rse.moe_read_device_error(part.ws) == 0
 
 
-def test_nan_token_stays_in_its_rows():
-    c = fp8_layer(T=64, H=256, E=4, k=2, I=128)
+@pytest.mark.parametrize("T,H,I", [(64, 256, 128), (1500, 1280, 640)])
+def test_nan_token_stays_in_its_rows(T, H, I):
+    c = fp8_layer(T=T, H=H, E=4, k=2, I=I)
     clean = c.layer.forward(c.x.cuda())
     x = c.x.clone()
     x[9, 40] = math.nan
-    ids = torch.empty(64, 2, dtype=torch.int32, device="cuda")
-    out = c.layer.forward(x.cuda(), topk_ids=ids)
-    rest = [t for t in range(64) if t != 9]
+    out = c.layer.forward(x.cuda())
+    rest = [t for t in range(T) if t != 9]
     assert bool(torch.isnan(out[9]).all()) and torch.equal(out[rest], clean[rest])
+
+
+def test_two_streams_with_a_workspace_each():
+    """Two layers' calls in flight at once give the bits they give alone."""
+    a, b = fp8_layer(T=700, H=512, E=8, k=2, I=256, seed=1), fp8_layer(T=40, H=512, E=8, k=4, I=256, seed=2)
+    xs = [a.x.cuda(), b.x.cuda()]
+    alone = [a.layer.forward(xs[0]), b.layer.forward(xs[1])]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(alone[i]) for _ in range(10)] for i in range(2)]
+    for n in range(10):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                c.layer.forward(xs[i], out=outs[i][n])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("kernel", [rse._abi.MOE_SELFTEST_PAIR_FP8_FEW, rse._abi.MOE_SELFTEST_PAIR_FP8_WIDE])
+def test_forced_timeout_is_reported_and_context_survives(kernel):
+    abi = rse._abi
+    scratch = torch.zeros(abi.MOE_SELFTEST_SCRATCH_BYTES, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    abi.moe_selftest_pair_timeout(scratch, kernel)
+    code = abi.moe_read_device_error(scratch)
+    assert code == abi.MOE_ERR_DEVICE_TIMEOUT
+    assert time.perf_counter() - t0 < 2.0
+    assert torch.count_nonzero(scratch[:256].view(torch.int32)[2:10]).item() == 0   # the tile queue is ready again
+    assert abi.moe_read_device_error(scratch) == 0
+    # the same kernel goes on computing
+    rows, N, K = (40, 256, 256) if kernel == abi.MOE_SELFTEST_PAIR_FP8_FEW else (1300, 1032, 256)
+    a, sa, w, sw, _ = gemm_inputs(rows, N, K, 1, 5)
+    out = torch.empty(rows, N, device="cuda")
+    rse.moe_fp8_gemm(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), None, None, out, header())
+    want, mag = go.gemm(a.double(), sa, w.double(), sw)
+    check_gemm(out, want, mag, K, torch.float32)
