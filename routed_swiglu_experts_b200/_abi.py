@@ -154,9 +154,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        # the handle alone: building a torch.cuda.Stream around it takes 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        tt = _tt()
+        return tt.stream(tt.device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -271,6 +270,8 @@ class _Torch:
         self.outs = (torch.bfloat16, torch.float32)
         # without a GPU no tensor is on the current device (the CPU's number is -1)
         self.device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2
+        # the handle alone: building a torch.cuda.Stream around it takes 3 us
+        self.stream = torch._C._cuda_getCurrentRawStream
 
 
 _torch = None
