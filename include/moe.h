@@ -412,7 +412,8 @@ MOE_API moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_
  * (NULL: one group of all rows).  Inner sums and the sum over b are fp32; one
  * rounding to out_type at the end.  Rows outside the groups are not written.
  *   a               E4M3 [rows, K]        a_scale  fp32 [ceil(K/128), rows]
- *   expert_offsets  int32 [groups + 1] ascending, within [0, rows], or NULL with groups == 1
+ *   expert_offsets  int32 [groups + 1] ascending, within [0, rows] (values outside count as
+ *                   the nearer end), or NULL with groups == 1
  *   w               E4M3 [groups, N, K]   w_scale  fp32 [groups, ceil(N/128), ceil(K/128)]
  *   row_scale       fp32 [rows] (c) or NULL (1)
  *   out             MOE_BF16 or MOE_F32 [rows, N]

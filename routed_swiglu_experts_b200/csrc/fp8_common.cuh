@@ -43,4 +43,44 @@ __device__ __forceinline__ float swiglu_clamped(float g, float u, float L) {
   return __fdividef(g, 1.f + __expf(-g)) * u;
 }
 
+// Group offsets and row-tile prefix, by one warp: off and tp [groups + 1];
+// returns the launch's row tiles.  Offsets are held to 0 .. rows and to their
+// order, so that no value they may have leads out of the operands.
+__device__ __forceinline__ int scan_groups(const int32_t* offsets, int groups, int rows, int tok, int32_t* off,
+                                           int32_t* tp, int lane) {
+  const int per = (groups + 31) / 32;
+  auto tiles = [&](int g, int& begin) {
+    begin = min(max(offsets[g], 0), rows);
+    return (max(min(offsets[g + 1], rows) - begin, 0) + tok - 1) / tok;
+  };
+  int local = 0;
+  for (int j = 0; j < per; ++j) {
+    const int g = lane * per + j;
+    int begin;
+    if (g < groups) local += tiles(g, begin);
+  }
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int run = incl - local;
+  for (int j = 0; j < per; ++j) {
+    const int g = lane * per + j;
+    if (g < groups) {
+      int begin;
+      tp[g] = run;
+      run += tiles(g, begin);
+      off[g] = begin;
+    }
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (lane == 0) {
+    off[groups] = min(max(offsets[groups], 0), rows);
+    tp[groups] = total;
+  }
+  return total;
+}
+
 }  // namespace moe

@@ -90,7 +90,7 @@ struct Ctl {
   uint64_t mma_done;
   uint64_t tq_full[QD];
   uint64_t tq_empty[QD];
-  int32_t tq[QD];
+  int4 tq[QD];                      // decoded tiles: group (-1: no more), weight-row tile, first row, rows
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t tiles;
@@ -108,13 +108,17 @@ constexpr size_t kSmem = 1024 + static_cast<size_t>(STAGES) * (A_STAGE + B_STAGE
 static_assert(kSmem <= 232448, "fits the 227 KB opt-in shared memory");
 
 struct Tile {
-  int g, fidx, row0, ntok, nmma;
+  int g, fidx, row0, ntok;
 };
+__device__ __forceinline__ Tile tile_of(const int4& v) { return Tile{v.x, v.y, v.z, v.w}; }
+
+// Rows that are multiplied: whole 16s.
+__device__ __forceinline__ int mma_rows(int ntok) { return (ntok + 15) & ~15; }
 
 // Group by group; inside a group weight-row tile major, token tile minor.
 __device__ __forceinline__ Tile decode(const Params& P, const Ctl& c, int t) {
   Tile ti;
-  int tm, tmi, r0, r1;
+  int tm, r0, r1;
   if (P.offsets != nullptr) {
     const int u = t / P.f_tiles;
     int lo = 0, hi = P.groups;
@@ -134,10 +138,8 @@ __device__ __forceinline__ Tile decode(const Params& P, const Ctl& c, int t) {
     r1 = P.rows;
   }
   ti.fidx = t / tm;
-  tmi = t - ti.fidx * tm;
-  ti.row0 = r0 + tmi * TOK;
+  ti.row0 = r0 + (t - ti.fidx * tm) * TOK;
   ti.ntok = min(TOK, r1 - ti.row0);
-  ti.nmma = (ti.ntok + 15) / 16 * 16;
   return ti;
 }
 
@@ -292,42 +294,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (warp == 9) tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
   if (warp == 0) {  // offsets + row-tile prefix, or the one group's tile count
-    int tiles;
-    if (P.offsets != nullptr) {
-      const int G = P.groups;
-      const int per = (G + 31) / 32;
-      int local = 0;
-      for (int j = 0; j < per; ++j) {
-        const int g = lane * per + j;
-        if (g < G) {
-          const int o0 = P.offsets[g], o1 = P.offsets[g + 1];
-          c.off[g] = o0;
-          local += (o1 - o0 + TOK - 1) / TOK;
-        }
-      }
-      int incl = local;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      int run = incl - local;
-      for (int j = 0; j < per; ++j) {
-        const int g = lane * per + j;
-        if (g < G) {
-          c.tp[g] = run;
-          run += (P.offsets[g + 1] - P.offsets[g] + TOK - 1) / TOK;
-        }
-      }
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (lane == 0) {
-        c.off[G] = P.offsets[G];
-        c.tp[G] = total;
-      }
-      tiles = total * P.f_tiles;
-    } else {
-      tiles = ((P.rows + TOK - 1) / TOK) * P.f_tiles;
-    }
+    const int row_tiles = P.offsets != nullptr ? scan_groups(P.offsets, P.groups, P.rows, TOK, c.off, c.tp, lane)
+                                               : (P.rows + TOK - 1) / TOK;
+    const int tiles = row_tiles * P.f_tiles;
     if (lane == 0) c.tiles = tiles;
   }
   tc_fence_before();
@@ -367,7 +336,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true;
     int t_next = -2;  // next queue position, once fetched (lane 0 of the first CTA)
     for (;;) {
-      int t = -1, got = 1;
+      // The first CTA takes the next tile from the launch's queue, decodes it
+      // and publishes it to every role of both CTAs.
+      Tile ti{-1, 0, 0, 0};
+      int got = 1;
       if (lane == 0) {
         if (leader) {
           if (!mbar_wait_bounded<true>(&c.tq_empty[q], qph ^ 1u, abort_flag, P.wait_ns)) {
@@ -375,10 +347,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             got = 0;
           } else {
             if (t_next == -2) t_next = atomicAdd(P.queue, 1);
-            t = t_next < total_tiles ? t_next : -1;
+            if (t_next < total_tiles) ti = decode(P, c, t_next);
             t_next = -2;
-            c.tq[q] = t;
-            st_cluster_u32(map_to_rank(smem_u32(&c.tq[q]), 1), static_cast<uint32_t>(t));
+            c.tq[q] = make_int4(ti.g, ti.fidx, ti.row0, ti.ntok);
+            const uint32_t peer = map_to_rank(smem_u32(&c.tq[q]), 1);
+            st_cluster_u32(peer, static_cast<uint32_t>(ti.g));
+            st_cluster_u32(peer + 4, static_cast<uint32_t>(ti.fidx));
+            st_cluster_u32(peer + 8, static_cast<uint32_t>(ti.row0));
+            st_cluster_u32(peer + 12, static_cast<uint32_t>(ti.ntok));
             mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
             mbar_arrive(&c.tq_full[q]);
           }
@@ -386,17 +362,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           fail(76);
           got = 0;
         } else {
-          t = c.tq[q];
-          mbar_arrive_cluster(leader_bar(&c.tq_empty[q]));
+          ti = tile_of(c.tq[q]);
+          mbar_arrive_peer(leader_bar(&c.tq_empty[q]));
         }
       }
       got = __shfl_sync(0xffffffffu, got, 0);
-      t = __shfl_sync(0xffffffffu, t, 0);
+      ti.g = __shfl_sync(0xffffffffu, ti.g, 0);
+      ti.fidx = __shfl_sync(0xffffffffu, ti.fidx, 0);
+      ti.row0 = __shfl_sync(0xffffffffu, ti.row0, 0);
+      ti.ntok = __shfl_sync(0xffffffffu, ti.ntok, 0);
       if (!got) break;
       next_q();
-      if (t < 0) break;
-      const Tile ti = decode(P, c, t);
-      const int half = ti.nmma / 2;  // rows of this CTA (a multiple of 8)
+      if (ti.g < 0) break;
+      const int half = mma_rows(ti.ntok) / 2;  // rows of this CTA (a multiple of 8)
       const int xrow = ti.row0 + static_cast<int>(rank) * half;
       int xb = 0;
       while (xb + 1 < kTokBoxes && half <= (TOK / 2 >> (xb + 1))) ++xb;
@@ -467,12 +445,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           fail(77);
           break;
         }
-        const int t = __shfl_sync(0xffffffffu, c.tq[q], 0);
+        const int g = __shfl_sync(0xffffffffu, c.tq[q].x, 0);
+        const uint32_t idesc = umma_idesc_f16(2 * ROWS, mma_rows(__shfl_sync(0xffffffffu, c.tq[q].w, 0)));
         if (elect_one()) mbar_arrive(&c.tq_empty[q]);
         next_q();
-        if (t < 0) break;
-        const Tile ti = decode(P, c, t);
-        const uint32_t idesc = umma_idesc_f16(2 * ROWS, __shfl_sync(0xffffffffu, ti.nmma, 0));
+        if (g < 0) break;
         for (int st = 0; st < nstage && ok; ++st) {
           if (!warp_wait(&c.full[stage], phase)) {
             fail(73);
@@ -529,12 +506,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         fail(81);
         break;
       }
-      const int t = c.tq[q];
+      const Tile ti = tile_of(c.tq[q]);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+      if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
-      if (t < 0) break;
-      const Tile ti = decode(P, c, t);
+      if (ti.g < 0) break;
       const float* sa = P.a_scale + ti.row0;
       // the weight's block row: gate (lane 0) and up (lane 1) rows lie in two
       const int nb = KIND == Kind::GateUp ? ti.fidx + (lane & 1) * (P.N / 128)
@@ -583,12 +559,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0 && ok && !gotq) fail(80);
         break;
       }
-      const int t = c.tq[q];
+      // The tile is in registers before the slot is given back (the arrival
+      // depends on it): no cluster-scope release, which would wait for the last
+      // tile's stores.
+      const Tile ti = tile_of(c.tq[q]);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
+      if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
-      if (t < 0) break;
-      const Tile ti = decode(P, c, t);
+      if (ti.g < 0) break;
       const bool mine = 32 * grp < ti.ntok;  // the group's chunk has rows
       Acc acc;
 #pragma unroll

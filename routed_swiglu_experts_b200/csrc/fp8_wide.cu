@@ -189,42 +189,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (warp == 9) tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
   if (warp == 0) {  // offsets + row-tile prefix, or the one group's tile count
-    int tiles;
-    if (P.offsets != nullptr) {
-      const int G = P.groups;
-      const int per = (G + 31) / 32;
-      int local = 0;
-      for (int j = 0; j < per; ++j) {
-        const int g = lane * per + j;
-        if (g < G) {
-          const int o0 = P.offsets[g], o1 = P.offsets[g + 1];
-          c.off[g] = o0;
-          local += (o1 - o0 + TOK - 1) / TOK;
-        }
-      }
-      int incl = local;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      int run = incl - local;
-      for (int j = 0; j < per; ++j) {
-        const int g = lane * per + j;
-        if (g < G) {
-          c.tp[g] = run;
-          run += (P.offsets[g + 1] - P.offsets[g] + TOK - 1) / TOK;
-        }
-      }
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (lane == 0) {
-        c.off[G] = P.offsets[G];
-        c.tp[G] = total;
-      }
-      tiles = total * P.f_tiles;
-    } else {
-      tiles = ((P.rows + TOK - 1) / TOK) * P.f_tiles;
-    }
+    const int row_tiles = P.offsets != nullptr ? scan_groups(P.offsets, P.groups, P.rows, TOK, c.off, c.tp, lane)
+                                               : (P.rows + TOK - 1) / TOK;
+    const int tiles = row_tiles * P.f_tiles;
     if (lane == 0) c.tiles = tiles;
   }
   tc_fence_before();

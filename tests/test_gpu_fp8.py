@@ -182,6 +182,24 @@ def test_grouped_product(name, scaled):
     assert torch.count_nonzero(ws.view(torch.int32)).item() == 0
 
 
+@pytest.mark.parametrize("rows,N,K,given,held", [
+    (60, 264, 400, [-5, 20, 20, 70], [0, 20, 20, 60]),
+    (60, 264, 400, [10, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1], [10, 60, 60, 60]),
+    (60, 264, 400, [-2 ** 31, -7, 3, 50], [0, 0, 3, 50]),
+    (1500, 776, 272, [-40, 900, 900, 5000], [0, 900, 900, 1500]),
+])
+def test_offsets_are_held_to_the_rows(rows, N, K, given, held):
+    a, sa, w, sw, _ = gemm_inputs(rows + 300, N, K, 3, rows)
+    a, sa = a[:rows], sa[:, :rows].contiguous()
+    outs = []
+    for ends in (given, held):
+        out = torch.full((rows, N), 7.0, device="cuda")
+        off = torch.tensor(ends, dtype=torch.int64).to(torch.int32).cuda()
+        rse.moe_fp8_gemm(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), off, None, out, header())
+        outs.append(out.cpu())
+    assert torch.equal(*outs)
+
+
 def test_nan_stays_in_its_row():
     a, sa, w, sw, _ = gemm_inputs(40, 256, 256, 1, 3)
     a = a.double()
