@@ -779,10 +779,10 @@ cudaError_t start(Params& P, const void* a, int K, int num_sms, cudaStream_t str
 // Which form: this one up to 56 rows a group on average, or as long as all its
 // tiles run at once; above, its tiles of 64 rows read the weights again for
 // each (through L2), and the wide form's 256-row tiles are worth their padding.
-// Both measured, feed-forward of 64 experts (H 2048, I 1408), rows per expert:
-// 16: 144 us here, 188 wide; 48: 159, 192; 64: 204, 193; 127: 315, 202.  One
-// group (N 6144, K 2048): 192 rows (72 tiles) 12.7 us here, 15.5 wide; 256 rows
-// (96 tiles) 18.8, 16.0.
+// Both measured, 64 groups whose sizes vary by a quarter (N 2816, K 2048), rows
+// per group: 16: 73 us here, 87 wide; 48: 76, 88; 56: 81, 88; 64: 93, 89; 128:
+// 145, 100.  One group (N 6144, K 2048): 192 rows (72 tiles) 15.8 us here, 20.0
+// wide; 256 rows (96 tiles) 20.6, 20.1.
 bool wide_preferred(int rows, int groups, int f_tiles, int num_sms) {
   if (static_cast<int64_t>(rows) <= 56ll * groups) return false;
   return (static_cast<int64_t>(rows) / TOK + groups) * f_tiles > num_sms / 2;

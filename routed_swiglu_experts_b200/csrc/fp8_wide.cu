@@ -12,11 +12,19 @@
 // That addition, not the MMAs, is what a tile is built around: the rows are
 // the M operand, so a thread owns one row and 128 output columns, all of one
 // weight scale (gate/up: 64 gate and 64 up columns, two), and each K block
-// costs it four 32x32b TMEM loads and 128 FMAs with one or two scale
-// registers.  (With the weights as M, as in ffn_gemm.cu, every column has a
-// scale of its own to fetch: that form took 1385 clocks a K block, this one
-// see below.)  A tile is 256 rows x 256 weight rows; the price is that the last
-// tile of a group is multiplied as a whole one.
+// costs it TMEM loads of 32 lanes x 128 columns and 128 FMAs with one or two
+// scale registers.  (With the weights as M, as in ffn_gemm.cu, every column
+// has a scale of its own to fetch: 1385 clocks a K block; here about 935.)
+//
+// A tile is 256 rows x 256 weight rows, the largest whose sums fit the scaling
+// warps' registers.  What bounds it: each CTA copies 32 KB a K block through
+// L2 (721 clocks with nothing else running; the four MMAs take 517), the K
+// loop 935, and the epilogue about 3000 clocks a tile, 15% at K = 2048.  A
+// group's last tile, when it has at most 128 rows, is multiplied as 128 (64 a
+// CTA): the weights' copies stay, so it costs four fifths of a whole one.
+// Measured, 64 groups, N 2816, K 2048, rows per group: 128: 94 us (1.00
+// PFLOP/s; 115 with one row more), 256: 122 us (1.55), 384: 194 us (1.46; 220
+// with one row more), 512: 227 us (1.66).
 //
 // Roles per CTA (384 threads): warps 0-7 scale, add and write (warps 4 g ..
 // 4 g + 3: columns 128 g .. of the CTA's 128 rows), warp 8 TMA producer, warp
@@ -27,6 +35,7 @@
 // waiting until the tile ends, so that no warp is left alone at a named
 // barrier.
 #include <cstring>
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "moe_internal.h"
@@ -44,9 +53,9 @@ constexpr int B_BYTES = COLS / 2 * BK; // 16 KB
 constexpr int STAGES = 5;
 constexpr int THREADS = 384;
 // Registers per thread after the split: the kernel starts with 168 x 384 =
-// 64512; the two warpgroups that hold sums take 208, the other one keeps 88
-// (256 x 208 + 128 x 88 = 64512).
-constexpr int kSumRegs = 208, kOtherRegs = 88;
+// 64512; the two warpgroups that hold sums take 216, the other one keeps 72
+// (256 x 216 + 128 x 72 = 64512).
+constexpr int kSumRegs = 216, kOtherRegs = 72;
 constexpr int QD = 8;                  // tile-id ring depth
 constexpr int SK = 4, SC = 3;          // scale ring: SC slots of SK K blocks
 constexpr uint32_t TMEM_COLS = 512;
@@ -99,7 +108,7 @@ struct Ctl {
   int32_t tp[MOE_MAX_EXPERTS + 1];     // token-tile prefix per group
   float sx[SC][SK][ROWS];              // row scales
   float sw[SC][SK][2];                 // weight scales: of the two column halves, or of gate and up
-  uint32_t amax[2][2][ROWS];           // GateUp: per tile parity and column half
+  uint32_t amax[2][2 * ROWS];          // GateUp: per tile parity, the rows' maxima over each part of the features
 };
 
 constexpr size_t kSmem = 1024 + static_cast<size_t>(STAGES) * (A_BYTES + B_BYTES) + sizeof(Ctl);
@@ -109,6 +118,10 @@ struct Tile {
   int g, fidx, row0, ntok;
 };
 __device__ __forceinline__ Tile tile_of(const int4& v) { return Tile{v.x, v.y, v.z, v.w}; }
+
+// A tile of up to 128 rows is multiplied as one of 128: 64 rows per CTA.
+__device__ __forceinline__ bool is_half(int ntok) { return ntok <= ROWS; }
+__device__ __forceinline__ int cta_rows(int ntok) { return is_half(ntok) ? ROWS / 2 : ROWS; }
 
 // Group by group; inside a group weight-row tile major, row tile minor.
 __device__ __forceinline__ Tile decode(const WideParams& P, const Ctl& c, int t) {
@@ -271,16 +284,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         next_q();
         if (ti.g < 0) break;
         // rows of each CTA; a CTA without rows copies none (its partial sums are never read)
-        const int mine = max(0, min(ROWS, ti.ntok - static_cast<int>(rank) * ROWS));
+        const int per = cta_rows(ti.ntok);
+        const int mine = max(0, min(per, ti.ntok - static_cast<int>(rank) * per));
         auto box_of = [](int n) {
           int b = 0;
           while (b + 1 < kRowBoxes && n <= (ROWS >> (b + 1))) ++b;
           return b;
         };
         auto box_bytes = [&](int n) { return n > 0 ? static_cast<uint32_t>(ROWS >> box_of(n)) * BK : 0u; };
-        const uint32_t tx = 2u * B_BYTES + box_bytes(min(ROWS, ti.ntok)) + box_bytes(max(0, ti.ntok - ROWS));
+        const uint32_t tx = 2u * B_BYTES + box_bytes(min(per, ti.ntok)) + box_bytes(max(0, ti.ntok - per));
         const CUtensorMap* xmap = &P.tma_x[box_of(mine)];
-        const int xrow = ti.row0 + static_cast<int>(rank) * ROWS;
+        const int xrow = ti.row0 + static_cast<int>(rank) * per;
         const int kpre = nkb > 4 ? nkb - 4 : 0;  // fetch the next id while the last copies run
         for (int kb = 0; kb < nkb; ++kb) {
           if (!warp_wait(&c.empty[stage], phase ^ 1u)) {
@@ -333,7 +347,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------ MMA issuer (first CTA) --
       if (leader) {
         const uint64_t a_desc = sw128_kmajor_desc(smem_u32(smem_a)), b_desc = sw128_kmajor_desc(smem_u32(smem_b));
-        constexpr uint32_t idesc = umma_idesc_f16(TOK, COLS);
         int stage = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 0;
         bool ok = true, first = true;
@@ -343,6 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             break;
           }
           const int g = __shfl_sync(0xffffffffu, c.tq[q].x, 0);
+          const uint32_t idesc = umma_idesc_f16(2 * cta_rows(__shfl_sync(0xffffffffu, c.tq[q].w, 0)), COLS);
           if (elect_one()) mbar_arrive(&c.tq_empty[q]);
           next_q();
           if (g < 0) break;
@@ -402,8 +416,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
         next_q();
         if (ti.g < 0) break;
-        const int mine = min(ROWS, ti.ntok - static_cast<int>(rank) * ROWS);
-        const float* sa = P.a_scale + ti.row0 + static_cast<int>(rank) * ROWS;
+        const int per = cta_rows(ti.ntok);
+        const int mine = min(per, ti.ntok - static_cast<int>(rank) * per);
+        const float* sa = P.a_scale + ti.row0 + static_cast<int>(rank) * per;
         // block row of the weight scale that lane 0 (columns 0-127, gate) or 1 (128-255, up) copies
         const int nb = KIND == Kind::GateUp ? ti.fidx + (lane & 1) * (P.N / 128)
                                             : min(ti.fidx * 2 + (lane & 1), P.n_blocks - 1);
@@ -442,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t tmem_empty_leader = map_to_rank(smem_u32(&c.tmem_empty[0]), 0);
     const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
     unsigned char* stage = c.stage[warp];
-    const uint32_t tb0 = tmem_base + (static_cast<uint32_t>(w4 * 32) << 16) + static_cast<uint32_t>(128 * grp);
+    const uint32_t tb_lanes = tmem_base + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t tmem_full = smem_u32(&c.tmem_full[0]), sc_full = smem_u32(&c.sc_full[0]);
     uint32_t buf = 0, buf_phase = 0, slot = 0, sph = 0, tile_no = 0;
     bool ok = true;
@@ -461,79 +476,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0 && ti.g >= -1) mbar_arrive_peer(tq_empty_leader + static_cast<uint32_t>(q * sizeof(uint64_t)));
       next_q();
       if (ti.g < 0) break;
-      // rows of this warp: 32 w4 .. of the CTA's
-      const int row_in_cta = w4 * 32;
-      const int nrows = ti.ntok - static_cast<int>(rank) * ROWS - row_in_cta;
+      // A whole tile: TMEM lane = row, the warp's rows are 32 w4 .. of the CTA's
+      // and its columns 128 grp ...  A half one: lanes 0-63 are the CTA's 64 rows
+      // in columns 0-127, lanes 64-127 the same rows in columns 128-255; of its
+      // 128 columns a warp takes 64 (gate/up: 32 gate and 32 up ones).
+      const bool half = is_half(ti.ntok);
+      const int row_in_cta = 32 * (half ? w4 & 1 : w4);
+      const int nrows = ti.ntok - static_cast<int>(rank) * cta_rows(ti.ntok) - row_in_cta;
       float acc[128];
-#pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
 
-      for (int k0 = 0; k0 < nkb; k0 += SK) {
-        const int nk = min(SK, nkb - k0);
-        if (!mbar_try_wait(sc_full + 8u * slot, sph) && ok &&
-            !mbar_wait_addr(sc_full + 8u * slot, sph, abort_flag, P.wait_ns)) {
-          ok = false;
-          fail(64);
-        }
-        __syncwarp();
-        const float* sx = &c.sx[slot][0][row_in_cta + lane];
-        const float* sw = &c.sw[slot][0][KIND == Kind::GateUp ? 0 : grp];
-#pragma unroll 1
-        for (int k = 0; k < nk; ++k) {
-          if (!mbar_try_wait(tmem_full + 8u * buf, buf_phase) && ok &&
-              !mbar_wait_addr(tmem_full + 8u * buf, buf_phase, abort_flag, P.wait_ns)) {
+      // Every K block of the tile: add(tmem buffer, row scale x weight scales,
+      // free) adds the warp's columns and calls free() once they are read.
+      auto k_loop = [&](int sw_at, auto&& add) {
+        for (int k0 = 0; k0 < nkb; k0 += SK) {
+          const int nk = min(SK, nkb - k0);
+          if (!mbar_try_wait(sc_full + 8u * slot, sph) && ok &&
+              !mbar_wait_addr(sc_full + 8u * slot, sph, abort_flag, P.wait_ns)) {
             ok = false;
-            fail(54);
+            fail(64);
           }
           __syncwarp();
-          tc_fence_after();
-          if (nrows > 0) {  // whole warps without rows read nothing
-            const uint32_t tb = tb0 + buf * COLS;
-            // pieces of 32 and 16 columns in turn, one load in flight while the
-            // piece before is added (32 and 32 spilled registers: 6% slower, and
-            // 15% in the gate/up form)
-            uint32_t va[32], vb[16];
-            tmem_ld32(tb, va);
-            const float s0 = *sx * sw[0];
-            const float s1 = KIND == Kind::GateUp ? *sx * sw[1] : s0;
-            tmem_ld_wait();
-            tmem_ld16(tb + 32, vb);
-            add_columns<0>(acc, va, s0, s1);
-            tmem_ld_wait();
-            tmem_ld32(tb + 48, va);
-            add_columns<32>(acc, vb, s0, s1);
-            tmem_ld_wait();
-            tmem_ld16(tb + 80, vb);
-            add_columns<48>(acc, va, s0, s1);
-            tmem_ld_wait();
-            tmem_ld32(tb + 96, va);
-            add_columns<80>(acc, vb, s0, s1);
-            tmem_ld_wait();
-            tc_fence_before();
+          const float* sx = &c.sx[slot][0][row_in_cta + lane];
+          const float* sw = &c.sw[slot][0][sw_at];
+#pragma unroll 1
+          for (int k = 0; k < nk; ++k) {
+            if (!mbar_try_wait(tmem_full + 8u * buf, buf_phase) && ok &&
+                !mbar_wait_addr(tmem_full + 8u * buf, buf_phase, abort_flag, P.wait_ns)) {
+              ok = false;
+              fail(54);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive_peer(tmem_empty_leader + 8u * buf);
-            add_columns<96>(acc, va, s0, s1);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_peer(tmem_empty_leader + 8u * buf);
+            tc_fence_after();
+            auto free = [&] {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_peer(tmem_empty_leader + 8u * buf);
+            };
+            if (nrows > 0)  // whole warps without rows read nothing
+              add(tb_lanes + buf * COLS, sx, sw, free);
+            else
+              free();
+            sx += ROWS;
+            sw += 2;
+            buf_phase ^= buf;
+            buf ^= 1u;
           }
-          sx += ROWS;
-          sw += 2;
-          buf_phase ^= buf;
-          buf ^= 1u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.sc_empty[slot]);
+          if (++slot == SC) {
+            slot = 0;
+            sph ^= 1u;
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.sc_empty[slot]);
-        if (++slot == SC) {
-          slot = 0;
-          sph ^= 1u;
-        }
+      };
+      if (!half) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+        k_loop(KIND == Kind::GateUp ? 0 : grp, [&](uint32_t tb, const float* sx, const float* sw, auto&& free) {
+          // pieces of 32 and 16 columns in turn, one load in flight while the
+          // piece before is added (32 and 32 spilled registers: 6% slower, and
+          // 15% in the gate/up form)
+          uint32_t va[32], vb[16];
+          tb += 128 * grp;
+          tmem_ld32(tb, va);
+          const float s0 = *sx * sw[0];
+          const float s1 = KIND == Kind::GateUp ? *sx * sw[1] : s0;
+          tmem_ld_wait();
+          tmem_ld16(tb + 32, vb);
+          add_columns<0>(acc, va, s0, s1);
+          tmem_ld_wait();
+          tmem_ld32(tb + 48, va);
+          add_columns<32>(acc, vb, s0, s1);
+          tmem_ld_wait();
+          tmem_ld16(tb + 80, vb);
+          add_columns<48>(acc, va, s0, s1);
+          tmem_ld_wait();
+          tmem_ld32(tb + 96, va);
+          add_columns<80>(acc, vb, s0, s1);
+          tmem_ld_wait();
+          free();
+          add_columns<96>(acc, va, s0, s1);
+        });
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+        k_loop(KIND == Kind::GateUp ? 0 : w4 >> 1, [&](uint32_t tb, const float* sx, const float* sw, auto&& free) {
+          uint32_t va[32], vb[32];
+          tmem_ld32(tb + (KIND == Kind::GateUp ? 32 * grp : 64 * grp), va);
+          const float s0 = *sx * sw[0];
+          const float s1 = KIND == Kind::GateUp ? *sx * sw[1] : s0;
+          tmem_ld_wait();
+          tmem_ld32(tb + (KIND == Kind::GateUp ? 64 + 32 * grp : 64 * grp + 32), vb);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(va[j]), s0, acc[j]);
+          tmem_ld_wait();
+          free();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[32 + j] = fmaf(__uint_as_float(vb[j]), s1, acc[32 + j]);
+        });
       }
 
-      const size_t row = static_cast<size_t>(ti.row0) + rank * ROWS + row_in_cta;  // the warp's first
+      const size_t row = static_cast<size_t>(ti.row0) + rank * cta_rows(ti.ntok) + row_in_cta;  // the warp's first
       if (KIND == Kind::Plain) {
-        const int n0 = ti.fidx * COLS + 128 * grp;
+        const int n0 = ti.fidx * COLS + (half ? 128 * (w4 >> 1) + 64 * grp : 128 * grp);
         if (P.row_scale != nullptr) {
           const float w = lane < nrows ? __ldg(P.row_scale + row + lane) : 0.f;
 #pragma unroll
@@ -569,6 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (nrows > 0 && P.out_f32) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
+            if (half && h == 2) break;
             reuse();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -581,6 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         } else if (nrows > 0) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            if (half && h == 1) break;
             reuse();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -592,41 +639,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
       } else {
-        // h of the row's 64 features (columns 0-63 gate, 64-127 up) in acc[0 .. 63]
+        // h of the row's features in acc: a whole tile's 64 (columns 0-63 gate,
+        // 64-127 up), a half one's 32 (columns 0-31 gate, 32-63 up)
         const float L = P.limit;
         uint32_t m = 0u;
+        auto activate = [&](auto up) {
+          constexpr int n = decltype(up)::value;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          acc[j] = swiglu_clamped(acc[j], acc[64 + j], L);
-          m = max(m, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
-        }
-        // the other 64 features of the scale block are the other warpgroup's
-        uint32_t(*am)[ROWS] = c.amax[tile_no & 1u];
-        am[grp][row_in_cta + lane] = m;
+          for (int j = 0; j < n; ++j) {
+            acc[j] = swiglu_clamped(acc[j], acc[n + j], L);
+            m = max(m, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
+          }
+        };
+        if (half) activate(std::integral_constant<int, 32>()); else activate(std::integral_constant<int, 64>());
+        // the scale block's other features are other warps'
+        const int parts = half ? 4 : 2, part = half ? 2 * (w4 >> 1) + grp : grp, per = cta_rows(ti.ntok);
+        uint32_t* am = c.amax[tile_no & 1u] + row_in_cta + lane;
+        am[part * per] = m;
         named_barrier_sync(1, 256);
-        m = max(m, am[grp ^ 1][row_in_cta + lane]);
+        for (int i = 0; i < parts; ++i) m = max(m, am[i * per]);
         float sc, inv;
         e4m3_block_scale(m, sc, inv);
-        if (grp == 0 && lane < nrows) P.out_scale[static_cast<size_t>(ti.fidx) * P.rows + row + lane] = sc;
-        if (nrows > 0) {
+        if (part == 0 && lane < nrows) P.out_scale[static_cast<size_t>(ti.fidx) * P.rows + row + lane] = sc;
+        unsigned char* out = static_cast<unsigned char*>(P.out) + row * P.N + ti.fidx * 128;
+        auto codes = [&](int j) {  // of features 16 j .. (j constant)
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* a = acc + 16 * j + 4 * i;
+            v[i] = e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+          }
+          return make_uint4(v[0], v[1], v[2], v[3]);
+        };
+        if (half) {
+          if (lane < nrows) {
+            uint4* to = reinterpret_cast<uint4*>(out + static_cast<size_t>(lane) * P.N + 32 * part);
+            to[0] = codes(0);
+            to[1] = codes(1);
+          }
+        } else if (nrows > 0) {
           uint4* mine = reinterpret_cast<uint4*>(stage + lane * 80);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* a = acc + 16 * j + 4 * i;
-              v[i] = e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-            }
-            mine[j] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+          for (int j = 0; j < 4; ++j) mine[j] = codes(j);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int u = lane + 32 * i, r = u >> 2;
             if (r < nrows)
-              *reinterpret_cast<uint4*>(static_cast<unsigned char*>(P.out) + (row + r) * P.N + ti.fidx * 128 + 64 * grp +
-                                        (u & 3) * 16) = *reinterpret_cast<const uint4*>(stage + r * 80 + (u & 3) * 16);
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * P.N + 64 * grp + (u & 3) * 16) =
+                  *reinterpret_cast<const uint4*>(stage + r * 80 + (u & 3) * 16);
           }
           __syncwarp();
         }

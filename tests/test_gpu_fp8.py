@@ -158,6 +158,8 @@ GROUPS = {
     # the form for many rows: whole and ragged tiles, a CTA without rows, an empty and a hot group
     "wide": ([0, 256, 300, 300, 1500, 1628, 1629, 2300], 1032, 272),
     "wide_not_all_rows": ([7, 200, 2200], 776, 640),
+    # ... and tiles of at most 128 rows: 1 to 128, alone and behind whole ones
+    "wide_half": ([0, 64, 129, 257, 289, 290, 418, 738, 1122, 1507, 1600], 1032, 400),
 }
 
 
@@ -285,6 +287,7 @@ LAYERS = {
     "wide": dict(T=1500, H=1280, E=3, k=2, I=640, I_s=64),
     "wide_hot": dict(T=1700, H=1024, E=8, k=1, I=512, hot=3),
     "wide_clamped": dict(T=1600, H=1152, E=4, k=2, I=512, limit=0.5),
+    "wide_half": dict(T=1500, H=512, E=24, k=2, I=512),
 }
 
 
