@@ -312,7 +312,7 @@ def _row_stride(t, name, where):
     """Elements between the rows of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def moe_gate_topk(cfg, logits, correction_bias, topk_ids, topk_w, stream=None):

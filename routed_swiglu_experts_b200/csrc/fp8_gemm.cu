@@ -832,26 +832,30 @@ cudaError_t launch_fp8_few_timeout_selftest(void* scratch, int32_t* err, int32_t
   return few_gemm(fp8_selftest_problem(scratch), err, queue, 2, stream, true);
 }
 
-cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream) {
-  return wide_preferred(p.rows, p.groups, (p.N + 255) / 256, num_sms) ? launch_fp8_wide_gemm(p, err, queue, num_sms, stream)
-                                                                      : few_gemm(p, err, queue, num_sms, stream);
+cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream,
+                            int likely_rows) {
+  return wide_preferred(likely_rows, p.groups, (p.N + 255) / 256, num_sms)
+             ? launch_fp8_wide_gemm(p, err, queue, num_sms, stream)
+             : few_gemm(p, err, queue, num_sms, stream);
 }
 
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
                            const int32_t* offsets, int rows, void* x_q, float* x_s, void* h_q, float* h_s,
-                           const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms,
+                           const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms, int e_total,
                            cudaStream_t stream) {
   const int H = cfg.hidden, I = cfg.expert_inter, E = cfg.num_experts;
   cudaError_t e = launch_fp8_quantize(x_rows, MOE_BF16, H, gather_src, cfg.top_k, rows, H, x_q, x_s, offsets, E, stream);
   if (e != cudaSuccess) return e;
+  // this call's share of the routed rows, when it has part of the experts
+  const int likely = static_cast<int>(static_cast<int64_t>(rows) * E / e_total);
   const Fp8Problem down{h_q, h_s, rows, offsets, E, w.w_down, static_cast<const float*>(w.s_down), H, I, w_perm, y_perm,
                         MOE_BF16};
-  if (wide_preferred(rows, E, I / 128, num_sms)) {
+  if (wide_preferred(likely, E, I / 128, num_sms)) {
     const Fp8Problem gate_up{x_q, x_s, rows, offsets, E, w.w_gate_up, static_cast<const float*>(w.s_gate_up), I, H, nullptr,
                              h_q, 0};
     e = launch_fp8_wide_gateup(gate_up, h_s, cfg.swiglu_limit, err, queues, num_sms, stream);
     if (e != cudaSuccess) return e;
-    return launch_fp8_gemm(down, err, queues + 2, num_sms, stream);
+    return launch_fp8_gemm(down, err, queues + 2, num_sms, stream, likely);
   }
   Params P = base_params(x_s, rows, offsets, E, H, err, queues);
   P.w_scale = static_cast<const float*>(w.s_gate_up);
@@ -864,7 +868,7 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
   if (!encode_w_gate_up(&P.tma_w, w.w_gate_up, E, I, H)) return cudaErrorInvalidValue;
   e = start<Kind::GateUp>(P, x_q, H, num_sms, stream);
   if (e != cudaSuccess) return e;
-  return launch_fp8_gemm(down, err, queues + 2, num_sms, stream);
+  return launch_fp8_gemm(down, err, queues + 2, num_sms, stream, likely);
 }
 
 }  // namespace moe

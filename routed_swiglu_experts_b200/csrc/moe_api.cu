@@ -116,8 +116,8 @@ moe_status check_router_weights(const moe_weights* w) {
 // kernels' own loads.  cfg.num_experts is the number of experts this call
 // computes (0 allowed: shared expert only), `offsets` their [E + 1] row
 // offsets (absolute permuted rows), and w's routed weights hold exactly those
-// experts; e_total is the router's expert count (the 4-bit paths pick their
-// kernel by the average routed rows per expert, R / e_total).
+// experts; e_total is the router's expert count (the 4-bit and FP8 paths pick
+// their kernel by the average routed rows per expert, R / e_total).
 moe_status run_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
                    const int32_t* offsets, const float* w_perm, int32_t T, void* y_perm, const void* x_shared,
                    void* shared_out, void* ws, const WsLayout& L, cudaStream_t stream, int e_total) {
@@ -152,7 +152,7 @@ moe_status run_ffn(const moe_config& cfg, const moe_weights& w, const void* x_ro
     if (routed)
       MOE_CUDA_TRY(launch_fp8_ffn(cfg, w, x_rows, gather_src, offsets, R, at<void>(ws, L.x_q), at<float>(ws, L.x_s),
                                   at<void>(ws, L.h_q), at<float>(ws, L.h_s), w_perm, y_perm, err,
-                                  tile_queue(ws, kQueueFp8GateUp), sms, stream));
+                                  tile_queue(ws, kQueueFp8GateUp), sms, e_total, stream));
     if (shared_tc) {
       MOE_CUDA_TRY(launch_gemm_gateup(nullptr, &s_gu, cfg.swiglu_limit, err, qgu, sms, stream));
       MOE_CUDA_TRY(launch_gemm_down(nullptr, &s_d, err, qd, sms, stream));
@@ -555,7 +555,8 @@ moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const
   if (ws == nullptr || ws_bytes < MOE_WS_HEADER_BYTES) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
   const Fp8Problem p{a, a_scale, rows, expert_offsets, groups, w, w_scale, N, K, row_scale, out, out_type};
-  return from_cuda(launch_fp8_gemm(p, err_word(ws), tile_queue(ws, kQueueFp8GateUp), num_sms_current_device(), stream));
+  return from_cuda(launch_fp8_gemm(p, err_word(ws), tile_queue(ws, kQueueFp8GateUp), num_sms_current_device(), stream,
+                                   rows));
 }
 
 moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_bytes, moe_stream_t stream) {

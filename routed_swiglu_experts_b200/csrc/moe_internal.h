@@ -180,17 +180,20 @@ inline Fp8Problem fp8_selftest_problem(void* scratch) {
                     reinterpret_cast<float*>(base + 768), 128, 128, nullptr, base + 20480, MOE_BF16};
 }
 // queue: the launch's two tile-queue words in the workspace header (zero).
-cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
+// likely_rows: about how many of the rows lie in the groups; it picks the form.
+cudaError_t launch_fp8_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream,
+                            int likely_rows);
 // The forms for groups of many rows (fp8_wide.cu); gate/up: p.N features, p.out
 // the E4M3 activations [rows, N], out_scale theirs [N / 128, rows].
 cudaError_t launch_fp8_wide_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream);
 cudaError_t launch_fp8_wide_gateup(const Fp8Problem& p, float* out_scale, float limit, int32_t* err, int32_t* queue,
                                    int num_sms, cudaStream_t stream);
 // The routed FFN on FP8 experts: quantised rows x_q / x_s, activations h_q /
-// h_s (scratch); queues: four tile-queue words (gate/up, then down).
+// h_s (scratch); queues: four tile-queue words (gate/up, then down); e_total:
+// the router's expert count, of which cfg.num_experts are this call's.
 cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const void* x_rows, const int32_t* gather_src,
                            const int32_t* offsets, int rows, void* x_q, float* x_s, void* h_q, float* h_s,
-                           const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms,
+                           const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms, int e_total,
                            cudaStream_t stream);
 
 // Shared expert for T <= 32 tokens: split-K tensor-core GEMMs streaming the

@@ -80,6 +80,36 @@ def test_rows_values_at_the_borders():
     assert torch.equal(s.cpu().double(), want_s) and torch.equal(codes(q), want_q)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_of_16_bit_values_at_the_borders(dtype):
+    """Every finite value of the type in blocks of its own exponent and below the largest one."""
+    every = torch.arange(2 ** 16, dtype=torch.int32).to(torch.int16).view(dtype)
+    every = every[torch.isfinite(every)]
+    x = torch.zeros((every.numel() + 125) // 126, 128, dtype=dtype)
+    flat = torch.zeros(x.shape[0] * 126, dtype=dtype)
+    flat[:every.numel()] = every
+    x[:, :126] = flat.view(-1, 126)
+    top = x.clone()
+    top[::2, 127] = torch.finfo(dtype).max
+    top[1::2, 127] = 1.0
+    x = torch.cat([x, top], dim=1)
+    q = torch.empty(x.shape[0], 256, dtype=F8, device="cuda")
+    s = torch.empty(2, x.shape[0], device="cuda")
+    rse.moe_fp8_quantize(x.cuda(), q, s)
+    want_q, want_s = go.quantize_rows(x)
+    assert torch.equal(s.cpu().double(), want_s) and torch.equal(codes(q), want_q)
+
+
+def test_one_row_of_any_stride():
+    wide = torch.randn(3, 77, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    x = wide.cuda()[:1, :64]
+    q = torch.empty(1, 64, dtype=F8, device="cuda")
+    s = torch.empty(1, 1, device="cuda")
+    rse.moe_fp8_quantize(x, q, s)
+    want_q, want_s = go.quantize_rows(wide[:1, :64])
+    assert torch.equal(s.cpu().double(), want_s) and torch.equal(codes(q), want_q)
+
+
 def test_rows_with_nan_and_infinity_poison_their_block_only():
     x = torch.randn(3, 384, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
     clean_q, clean_s = go.quantize_rows(x)
@@ -212,12 +242,13 @@ def test_nan_stays_in_its_row():
     assert int(torch.isnan(out).sum()) == 256
 
 
-def test_product_is_deterministic_and_graph_replays_it():
-    a, sa, w, sw, _ = gemm_inputs(300, 384, 512, 3, 4)
+@pytest.mark.parametrize("rows,N", [(300, 384), (2300, 1032)])     # both forms
+def test_product_is_deterministic_and_graph_replays_it(rows, N):
+    a, sa, w, sw, _ = gemm_inputs(rows, N, 512, 3, 4)
     dev = [t.cuda() for t in (a, sa, w, sw)]
-    off = torch.tensor([0, 100, 101, 300], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 100, 101, rows], dtype=torch.int32, device="cuda")
     ws = header()
-    first = torch.empty(300, 384, dtype=torch.bfloat16, device="cuda")
+    first = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
     rse.moe_fp8_gemm(*dev, off, None, first, ws)
     again = torch.empty_like(first)
     s = torch.cuda.Stream()
@@ -338,7 +369,7 @@ def test_layer_routes_with_groups_and_replays_in_a_graph():
         assert torch.equal(c.layer.forward(x), out)
 
 
-@pytest.mark.parametrize("T,world", [(20, 2), (300, 3), (150, 5)])
+@pytest.mark.parametrize("T,world", [(20, 2), (300, 3), (150, 5), (6000, 2)])
 def test_expert_parallel_partials_add_up(T, world):
     c = fp8_layer(T=T, H=256, E=4, k=2, I=128, I_s=64)
     full = c.layer.forward(c.x.cuda())
