@@ -243,7 +243,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int t_next = -2;  // next queue position, once fetched (lane 0 of the first CTA)
+      // next queue position, once fetched (lane 0 of the first CTA); the first is the
+      // pair's own number, so the queue counts from npairs on
+      int t_next = static_cast<int>(blockIdx.x >> 1);
       for (;;) {
         // The first CTA takes the next tile from the launch's queue, decodes it
         // and publishes it to every role of both CTAs.
@@ -255,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               fail(55);
               got = 0;
             } else {
-              if (t_next == -2) t_next = atomicAdd(P.queue, 1);
+              if (t_next == -2) t_next = npairs + atomicAdd(P.queue, 1);
               if (t_next < total_tiles) ti = decode(P, c, t_next);
               t_next = -2;
               c.tq[q] = make_int4(ti.g, ti.fidx, ti.row0, ti.ntok);
@@ -317,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (mine > 0) tma_load_2d_pair(smem_a + stage * A_BYTES, xmap, kb * BK, xrow, bar);
           }
           __syncwarp();
-          if (lane == 0 && leader && kb == kpre) t_next = atomicAdd(P.queue, 1);
+          if (lane == 0 && leader && kb == kpre) t_next = npairs + atomicAdd(P.queue, 1);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
