@@ -18,6 +18,18 @@
 // for the whole CTA.  TMEM is read in the 16x128b shape: a thread holds 4
 // weight rows x 8 rows of a chunk of 32, so it needs 8 row scales for 32 sums.
 //
+// One CTA streams its weights at about 65 GB/s (128 KB in flight), so a
+// product of few tiles leaves most of the memory's rate unused.  SPLIT > 1
+// gives a tile to a cluster of two to four pairs, each with its part of the K
+// blocks; the first pair adds the others' sums out of their shared memory, in
+// order, and writes.  Measured (graph replay, weights from memory), one row:
+// N 2048, K 8192: 24.9 us whole, 12.5 split in four; N 6144, K 2048: 10.3, 9.2
+// in three; 6.2 of these are the launch, its barriers and TMEM.
+//
+// Measured with many groups: feed-forward of 64 experts, 32 tokens, 8 experts
+// each (H 6144, I 2048), 2.4 GB of weights in 420 to 440 us = 5.5 to 5.7 TB/s;
+// its copies alone 403 us.
+//
 // Roles per CTA (384 threads): warps 0-7 scale, add and write (warps 4 w ..
 // 4 w + 3 take the chunk 32 w ..), warp 8 TMA producer, warp 9 TMEM owner (+
 // MMA issuer in the first CTA), warp 10 copies the scales, SK K blocks at a
@@ -251,8 +263,8 @@ __device__ __forceinline__ void warp_amax(const uint32_t (&m)[8], uint32_t* amax
   }
 }
 
-template <Kind KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <Kind KIND, int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(THREADS, 1)
     fp8_few_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -262,9 +274,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   Ctl& c = *reinterpret_cast<Ctl*>(smem + STAGES * (A_STAGE + B_STAGE));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
+  // the pair of the cluster, its first CTA and the CTA in the pair
+  const uint32_t pair = SPLIT > 1 ? cluster_ctarank() >> 1 : 0, lead = 2 * pair;
+  const uint32_t rank = cluster_ctarank() - lead;
   const bool leader = rank == 0;
   const int npairs = gridDim.x >> 1;
+  auto leader_addr = [&](const uint64_t* bar) { return map_to_rank(smem_u32(bar), lead); };
+  auto other_addr = [&](const void* at) { return map_to_rank(smem_u32(at), lead + (rank ^ 1u)); };
+  const uint16_t both = static_cast<uint16_t>(3u << lead);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -306,7 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   const uint32_t tmem_base = c.tmem_base;
   const int total_tiles = c.tiles;
-  const int nkb = P.k_blocks;
+  // K blocks of this pair
+  const int kb0 = static_cast<int>(pair) * P.k_blocks / SPLIT;
+  const int nkb = (static_cast<int>(pair) + 1) * P.k_blocks / SPLIT - kb0;
   const int nstage = (nkb + KCH - 1) / KCH;  // the last stage of an odd count holds one K block
   volatile int32_t* abort_flag = &c.abort_flag;
   auto fail = [&](int detail) {
@@ -335,8 +354,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     // next queue position, once fetched (lane 0 of the first CTA); the first is the
-    // pair's own number, so the queue counts from npairs on
-    int t_next = static_cast<int>(blockIdx.x >> 1);
+    // pair's own number, so the queue counts from npairs on.  A cluster that splits
+    // K has one tile and needs no queue.
+    int t_next = static_cast<int>(blockIdx.x / (2 * SPLIT));
     for (;;) {
       // The first CTA takes the next tile from the launch's queue, decodes it
       // and publishes it to every role of both CTAs.
@@ -348,16 +368,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             fail(75);
             got = 0;
           } else {
-            if (t_next == -2) t_next = npairs + atomicAdd(P.queue, 1);
+            if (t_next == -2) t_next = SPLIT > 1 ? total_tiles : npairs + atomicAdd(P.queue, 1);
             if (t_next < total_tiles) ti = decode(P, c, t_next);
             t_next = -2;
             c.tq[q] = make_int4(ti.g, ti.fidx, ti.row0, ti.ntok);
-            const uint32_t peer = map_to_rank(smem_u32(&c.tq[q]), 1);
+            const uint32_t peer = other_addr(&c.tq[q]);
             st_cluster_u32(peer, static_cast<uint32_t>(ti.g));
             st_cluster_u32(peer + 4, static_cast<uint32_t>(ti.fidx));
             st_cluster_u32(peer + 8, static_cast<uint32_t>(ti.row0));
             st_cluster_u32(peer + 12, static_cast<uint32_t>(ti.ntok));
-            mbar_arrive_cluster(map_to_rank(smem_u32(&c.tq_full[q]), 1));
+            mbar_arrive_cluster(other_addr(&c.tq_full[q]));
             mbar_arrive(&c.tq_full[q]);
           }
         } else if (!mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns)) {
@@ -365,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           got = 0;
         } else {
           ti = tile_of(c.tq[q]);
-          mbar_arrive_peer(leader_bar(&c.tq_empty[q]));
+          mbar_arrive_peer(leader_addr(&c.tq_empty[q]));
         }
       }
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -394,11 +414,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int nk = min(KCH, nkb - st * KCH);
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&c.full[stage], 2u * static_cast<uint32_t>(nk) * (A_BYTES + b_bytes));
-          const uint32_t bar = leader_bar(&c.full[stage]);
+          const uint32_t bar = leader_addr(&c.full[stage]);
 #pragma unroll
           for (int ch = 0; ch < KCH; ++ch) {
             if (ch < nk) {
-              const int k = (st * KCH + ch) * BK;
+              const int k = (kb0 + st * KCH + ch) * BK;
               unsigned char* sa = smem_a + stage * A_STAGE + ch * A_BYTES;
               if (KIND == Kind::GateUp)
                 tma_load_5d_pair(sa, &P.tma_w, k, 0, 0, 0, wrow, bar);
@@ -409,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0 && leader && st == kpre) t_next = npairs + atomicAdd(P.queue, 1);
+        if (SPLIT == 1 && lane == 0 && leader && st == kpre) t_next = npairs + atomicAdd(P.queue, 1);
         ++issued;
         if (++stage == STAGES) {
           stage = 0;
@@ -420,8 +440,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     if (leader && lane == 0) {
       // retire from the queue; the last pair of the launch resets it
-      __threadfence();
-      if (atomicAdd(P.queue + 1, 1) == npairs - 1) {
+      if (SPLIT == 1) __threadfence();
+      if (SPLIT == 1 && atomicAdd(P.queue + 1, 1) == npairs - 1) {
         __threadfence();
         atomicExch(P.queue, 0);
         atomicExch(P.queue + 1, 0);
@@ -473,8 +493,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int kk = 0; kk < BK / 32; ++kk)  // 32 bytes of K each
                 umma_e4m3_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-              if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf]);
-              if (ch + 1 == nk) umma_commit_pair(&c.empty[stage]);
+              if (!(P.test_withhold && first)) umma_commit_pair(&c.tmem_full[buf], both);
+              if (ch + 1 == nk) umma_commit_pair(&c.empty[stage], both);
             }
             __syncwarp();
             first = false;
@@ -491,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!ok) break;
       }
       if (elect_one()) {
-        umma_commit_pair_leader(&c.mma_done);
+        umma_commit_pair_leader(&c.mma_done, static_cast<uint16_t>(1u << lead));
         volatile int32_t never = 0;
         if (!mbar_wait_bounded(&c.mma_done, 0, &never, kTimeoutNs)) report_error(P.err, MOE_ERR_DEVICE_TIMEOUT, 78);
       }
@@ -499,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 10) {
     // --------------------------------------- scales, SK K blocks to a slot --
-    const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
+    const uint32_t tq_empty_leader = leader_addr(&c.tq_empty[0]);
     int slot = 0;
     uint32_t sph = 0;
     bool ok = true;
@@ -517,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // the weight's block row: gate (lane 0) and up (lane 1) rows lie in two
       const int nb = KIND == Kind::GateUp ? ti.fidx + (lane & 1) * (P.N / 128)
                                           : min(ti.fidx * 2 + static_cast<int>(rank), P.n_blocks - 1);
-      const float* sw = P.w_scale + (static_cast<size_t>(ti.g) * P.n_blocks + nb) * nkb;
+      const float* sw = P.w_scale + (static_cast<size_t>(ti.g) * P.n_blocks + nb) * P.k_blocks + kb0;
       for (int k0 = 0; k0 < nkb; k0 += SK) {
         if (!warp_wait(&c.sc_empty[slot], sph ^ 1u)) {
           fail(82);
@@ -526,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const int nk = min(SK, nkb - k0);
         for (int k = 0; k < nk; ++k) {
-          const float* row = sa + static_cast<size_t>(k0 + k) * P.rows;
+          const float* row = sa + static_cast<size_t>(kb0 + k0 + k) * P.rows;
 #pragma unroll
           for (int i = 0; i < TOK; i += 32)
             if (i + lane < ti.ntok)
@@ -549,12 +569,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // buffers are freed by CTA-scope arrivals: only TMEM, ordered by the tcgen05
     // fences, changes hands (a release at cluster scope is a memory barrier of
     // about 340 clocks per K block)
-    const uint32_t tmem_empty_leader = map_to_rank(smem_u32(&c.tmem_empty[0]), 0);
-    const uint32_t tq_empty_leader = map_to_rank(smem_u32(&c.tq_empty[0]), 0);
+    const uint32_t tmem_empty_leader = leader_addr(&c.tmem_empty[0]);
+    const uint32_t tq_empty_leader = leader_addr(&c.tq_empty[0]);
     const uint32_t tmem_full = smem_u32(&c.tmem_full[0]), sc_full = smem_u32(&c.sc_full[0]);
     unsigned char* stage = c.stage[warp];
     uint32_t buf = 0, buf_phase = 0, slot = 0, sph = 0, tile_no = 0;
-    bool ok = true;
+    bool ok = true, met = false;
     for (;;) {
       const bool gotq = ok && mbar_wait_bounded<true>(&c.tq_full[q], qph, abort_flag, P.wait_ns);
       if (!named_barrier_and(1, 256, gotq)) {  // all eight warps go on or leave together
@@ -636,6 +656,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
 
+      if (SPLIT > 1) {
+        // The pairs' sums of the tile, added by the first pair in order.  The
+        // others leave theirs where the operands were (all their MMAs are done).
+        float4* part = reinterpret_cast<float4*>(smem) + warp * 8 * 32 + lane;
+        float* a = &acc[0][0];
+        if (pair != 0 && mine) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) part[32 * i] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+        }
+        __syncwarp();
+        cluster_sync_all();
+        met = true;
+        if (pair == 0 && mine) {
+#pragma unroll
+          for (int p = 1; p < SPLIT; ++p) {
+            const uint32_t from = map_to_rank(smem_u32(part), 2 * p + rank);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = ld_cluster_f32x4(from + 32 * 16 * i);
+              a[4 * i] += v.x, a[4 * i + 1] += v.y, a[4 * i + 2] += v.z, a[4 * i + 3] += v.w;
+            }
+          }
+        }
+        if (pair != 0) continue;
+      }
       if (KIND == Kind::Plain) {
         const int n_warp = ti.fidx * 256 + static_cast<int>(rank) * 128 + w4 * 32;
         write_plain(P, ti, stage, n_warp, grp, lane, acc);
@@ -660,17 +705,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (w4 == 0) {
           const uint32_t mine_m = max(max(c.amax[grp][0][lane], c.amax[grp][1][lane]),
                                       max(c.amax[grp][2][lane], c.amax[grp][3][lane]));
-          const uint32_t other = rank ^ 1u;
           uint32_t* peer = &c.peer_amax[grp][tile_no & 1u][lane];
-          st_cluster_u32(map_to_rank(smem_u32(peer), other), mine_m);
-          mbar_arrive_cluster(map_to_rank(smem_u32(&c.amax_full[grp]), other));
+          st_cluster_u32(other_addr(peer), mine_m);
+          mbar_arrive_cluster(other_addr(&c.amax_full[grp]));
           if (ok && !mbar_wait_bounded<true>(&c.amax_full[grp], tile_no & 1u, abort_flag, P.wait_ns)) {
             fail(83);
             ok = false;
           }
-          const uint32_t both = max(mine_m, *peer);
           float sc, inv;
-          e4m3_block_scale(both, sc, inv);
+          e4m3_block_scale(max(mine_m, *peer), sc, inv);
           c.inv[grp][lane] = inv;
           const int col = 32 * grp + lane;
           if (leader && col < ti.ntok) P.out_scale[static_cast<size_t>(ti.fidx) * P.rows + ti.row0 + col] = sc;
@@ -697,6 +740,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       ++tile_no;
     }
+    __syncwarp();
+    if (SPLIT > 1 && !met) cluster_sync_all();
+  }
+  if (SPLIT > 1 && warp >= 8) {  // the scaling warps' meeting above: every thread of the cluster takes part
+    __syncwarp();
+    cluster_sync_all();
   }
 
   tc_fence_before();
@@ -740,9 +789,9 @@ bool encode_x(CUtensorMap (&m)[kTokBoxes], const void* base, int rows, int K) {
   return true;
 }
 
-// CTA pairs that can be resident at once on the current device; 0 if unknown.
-template <Kind KIND>
-int resident_pairs() {
+// Clusters that can be resident at once on the current device; 0 if unknown.
+template <Kind KIND, int SPLIT>
+int resident_clusters() {
   static int cached[64];
   static bool known[64];
   int dev = 0;
@@ -750,11 +799,11 @@ int resident_pairs() {
   if (!known[dev]) {
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(2);
+    lc.gridDim = dim3(2 * SPLIT);
     lc.blockDim = dim3(THREADS);
     lc.dynamicSmemBytes = kSmem;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_few_kernel<KIND>, &lc) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_few_kernel<KIND, SPLIT>, &lc) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -764,18 +813,43 @@ int resident_pairs() {
   return cached[dev];
 }
 
+template <Kind KIND, int SPLIT>
+cudaError_t smem_attr() {
+  return ensure_smem_attr(reinterpret_cast<const void*>(fp8_few_kernel<KIND, SPLIT>), static_cast<int>(kSmem));
+}
+
+// K split over SPLIT pairs of a cluster, one tile per cluster: when all the
+// tiles there can be fit the device that way and a pair keeps four K blocks.
+template <int SPLIT>
+cudaError_t start_split(const Params& P, int64_t most, cudaStream_t stream, bool& started) {
+  cudaError_t e = smem_attr<Kind::Plain, SPLIT>();
+  if (e != cudaSuccess) return e;
+  started = P.k_blocks >= 4 * SPLIT && most <= resident_clusters<Kind::Plain, SPLIT>();
+  if (!started) return cudaSuccess;
+  return launch_kernel(fp8_few_kernel<Kind::Plain, SPLIT>, dim3(static_cast<unsigned>(2 * SPLIT * most)), dim3(THREADS),
+                       kSmem, stream, P);
+}
+
 template <Kind KIND>
 cudaError_t start(Params& P, const void* a, int K, int num_sms, cudaStream_t stream) {
   if (!encode_x(P.tma_x, a, P.rows, K)) return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fp8_few_kernel<KIND>), static_cast<int>(kSmem));
+  // no more pairs than there can be tiles
+  const int64_t most =
+      std::max<int64_t>(1, (static_cast<int64_t>(P.rows) / TOK + std::min(P.groups, P.rows)) * P.f_tiles);
+  if (KIND == Kind::Plain && 4 * most <= num_sms) {
+    bool started = false;
+    cudaError_t e = start_split<4>(P, most, stream, started);
+    if (e == cudaSuccess && !started) e = start_split<3>(P, most, stream, started);
+    if (e == cudaSuccess && !started) e = start_split<2>(P, most, stream, started);
+    if (e != cudaSuccess || started) return e;
+  }
+  cudaError_t e = smem_attr<KIND, 1>();
   if (e != cudaSuccess) return e;
   int grid = std::max(2, num_sms / 2 * 2);
-  const int pairs = resident_pairs<KIND>();
+  const int pairs = resident_clusters<KIND, 1>();
   if (pairs > 0) grid = std::min(grid, 2 * pairs);
-  // no more pairs than there can be tiles
-  const int64_t most = (static_cast<int64_t>(P.rows) / TOK + std::min(P.groups, P.rows)) * P.f_tiles;
-  if (most < grid / 2) grid = static_cast<int>(2 * std::max<int64_t>(1, most));
-  return launch_kernel(fp8_few_kernel<KIND>, dim3(grid), dim3(THREADS), kSmem, stream, P);
+  if (most < grid / 2) grid = static_cast<int>(2 * most);
+  return launch_kernel(fp8_few_kernel<KIND, 1>, dim3(grid), dim3(THREADS), kSmem, stream, P);
 }
 
 // Which form: this one up to 56 rows a group on average, or as long as all its

@@ -268,6 +268,16 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+// Four floats from the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 // shared::cluster address of the mbarrier at the same offset as `bar` in the
 // pair's first CTA.
 __device__ __forceinline__ uint32_t leader_bar(const uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); }
@@ -416,8 +426,8 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
-  const uint16_t mask = 0x3;
+// (mask: the pair's CTAs among the cluster's.)
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask = 0x3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
@@ -426,8 +436,7 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 }
 
 // Commit of pair MMAs signalling only the first CTA's barrier.
-__device__ __forceinline__ void umma_commit_pair_leader(uint64_t* bar) {
-  const uint16_t mask = 0x1;
+__device__ __forceinline__ void umma_commit_pair_leader(uint64_t* bar, uint16_t mask = 0x1) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),

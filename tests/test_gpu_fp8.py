@@ -166,6 +166,8 @@ def check_gemm(out, want, mag, K, out_dtype):
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,N,K", [(1, 8, 16), (1, 256, 128), (3, 136, 144), (16, 512, 256), (17, 264, 400), (64, 128, 2000),
                                       (65, 1000, 640), (255, 392, 1024), (257, 256, 384), (600, 520, 272),
+                                      # few tiles: K split over two to four CTA pairs
+                                      (1, 6144, 2048), (33, 520, 1552), (16, 136, 1024), (48, 2048, 4096), (130, 264, 1040),
                                       # more tiles of 64 rows than run at once: the form for many rows
                                       (1300, 1032, 400), (1153, 2056, 144), (2100, 1000, 1152), (4900, 136, 128)])
 def test_dense_product(rows, N, K, out_dtype):
@@ -185,6 +187,8 @@ GROUPS = {
     "ragged": ([0, 31, 95, 96, 223, 480, 1009], 392, 528),
     "many": ([3 * i + (i % 2) for i in range(129)], 128, 128),
     "not_all_rows": ([4, 20, 20, 97], 264, 400),
+    "split": ([0, 0, 3, 40, 40, 105], 264, 2064),
+    "split_empty": ([0, 0, 0], 128, 2048),
     # the form for many rows: whole and ragged tiles, a CTA without rows, an empty and a hot group
     "wide": ([0, 256, 300, 300, 1500, 1628, 1629, 2300], 1032, 272),
     "wide_not_all_rows": ([7, 200, 2200], 776, 640),
@@ -198,7 +202,7 @@ GROUPS = {
 def test_grouped_product(name, scaled):
     ends, N, K = GROUPS[name]
     G = len(ends) - 1
-    rows = ends[-1] + (9 if name == "not_all_rows" else 0)
+    rows = ends[-1] + (9 if name in ("not_all_rows", "split_empty") else 0)
     a, sa, w, sw, g = gemm_inputs(rows, N, K, G, rows)
     c = torch.rand(rows, generator=g) * 2 - 1 if scaled else None
     ws = header()
@@ -242,9 +246,9 @@ def test_nan_stays_in_its_row():
     assert int(torch.isnan(out).sum()) == 256
 
 
-@pytest.mark.parametrize("rows,N", [(300, 384), (2300, 1032)])     # both forms
-def test_product_is_deterministic_and_graph_replays_it(rows, N):
-    a, sa, w, sw, _ = gemm_inputs(rows, N, 512, 3, 4)
+@pytest.mark.parametrize("rows,N,K", [(300, 384, 512), (2300, 1032, 512), (110, 384, 1536)])  # both forms, K split
+def test_product_is_deterministic_and_graph_replays_it(rows, N, K):
+    a, sa, w, sw, _ = gemm_inputs(rows, N, K, 3, 4)
     dev = [t.cuda() for t in (a, sa, w, sw)]
     off = torch.tensor([0, 100, 101, rows], dtype=torch.int32, device="cuda")
     ws = header()
