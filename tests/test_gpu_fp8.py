@@ -246,6 +246,42 @@ def test_nan_stays_in_its_row():
     assert int(torch.isnan(out).sum()) == 256
 
 
+def test_output_of_more_than_2_31_elements():
+    """The last rows of a product whose output's offsets pass 32 bits."""
+    rows, N, K = 1_050_001, 2056, 128
+    a, sa, w, sw, _ = gemm_inputs(300, N, K, 1, 8)
+    big = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+    scale = torch.ones(1, rows, device="cuda")
+    at = torch.cat([torch.arange(20), torch.arange(rows - 280, rows)])
+    big[at.cuda()] = a.view(torch.uint8).cuda()
+    scale[:, at.cuda()] = sa.cuda()
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    rse.moe_fp8_gemm(big, scale, w.cuda(), sw.cuda(), None, None, out, header())
+    want, mag = go.gemm(a.double(), sa, w.double(), sw)
+    check_gemm(out[at.cuda()], want, mag, K, torch.bfloat16)
+    assert int(torch.count_nonzero(out[1000:1040])) == 0
+
+
+def test_rows_and_weights_of_more_than_2_31_elements():
+    g = torch.Generator().manual_seed(3)
+    part = torch.randn(2, 256, generator=g).to(torch.bfloat16)
+    x = torch.empty(3, 1_200_000_000, dtype=torch.bfloat16, device="cuda")    # only what is compared is written
+    x[0, :256], x[2, :256] = part[0].cuda(), part[1].cuda()
+    q = torch.empty(4, 256, dtype=F8, device="cuda")
+    s = torch.empty(2, 4, device="cuda")
+    rse.moe_fp8_quantize(x[:, :256], q, s, src=torch.tensor([0, 4, 5, 1], dtype=torch.int32, device="cuda"), src_div=2)
+    want_q, want_s = go.quantize_rows(part[[0, 1, 1, 0]])
+    assert torch.equal(s.cpu().double(), want_s) and torch.equal(codes(q), want_q)
+    del x
+    w = torch.zeros(2, 8200, 131072, dtype=torch.bfloat16, device="cuda")
+    w[1, -200:, -400:] = torch.randn(200, 400, generator=g).to(torch.bfloat16).cuda()
+    q = torch.empty(w.shape, dtype=F8, device="cuda")
+    s = torch.empty(2, 65, 1024, device="cuda")
+    rse.moe_fp8_quantize_weight(w, q, s)
+    want_q, want_s = go.quantize_weight(w[1:, -136:, -512:].cpu())    # rows 8064 on: whole blocks
+    assert torch.equal(s[1:, -2:, -4:].cpu().double(), want_s) and torch.equal(codes(q[1:, -136:, -512:]), want_q)
+
+
 @pytest.mark.parametrize("rows,N,K", [(300, 384, 512), (2300, 1032, 512), (110, 384, 1536)])  # both forms, K split
 def test_product_is_deterministic_and_graph_replays_it(rows, N, K):
     a, sa, w, sw, _ = gemm_inputs(rows, N, K, 3, 4)

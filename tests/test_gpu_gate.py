@@ -221,3 +221,15 @@ def test_layer_routes_as_configured(name, T):
     part = one.forward_partial(x)
     torch.cuda.synchronize()
     assert torch.equal(ids, ids2) and torch.equal(w, w2) and torch.equal(part, out)
+
+
+def test_logits_far_apart():
+    """Rows whose offsets pass 32 bits."""
+    T, E, stride = 9, 64, 300_000_000
+    z = torch.randn(T, E, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    wide = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda").as_strided((T, E), (stride, 1))
+    wide.copy_(z.cuda())
+    ids, w = run(config(E, 6, softmax=True), wide, None)
+    want_ids, want_w = go.gate_select(z, None, 6, 2.5, True, True, 1, 1, False)
+    assert torch.equal(ids, want_ids)
+    assert torch.allclose(w, want_w, rtol=RTOL, atol=1e-37)
