@@ -15,20 +15,24 @@
 // bits; each lane sorts its keys once (Batcher's odd-even merge sort) and puts
 // them into shared memory, and each of the k rounds is one warp-wide max
 // (redux.sync) over the lanes' heads, after which the winner's head moves on.
-// Measured (graph replay): one token of 256 experts in 8 groups 3.5 us, 512
-// tokens 4.9, 16384 tokens 24 us (0.7 TB/s of logits): issue slots bound it on
+// Measured (graph replay): one token of 256 experts in 8 groups 3.7 us, 4096
+// tokens 6.8, 16384 tokens 18.8 us (0.9 TB/s of logits): issue slots bound it on
 // many tokens (about 850 instructions a token), latency on few.  Four tokens
-// per warp, eight lanes each, halve the instructions and came to 22.9 us there,
-// slower below 8192 tokens: the chain of one token stays as long.
+// per warp, eight lanes each, halve the instructions and came to 22.9 us there
+// (24.3 this form, both before the next paragraph's pruning), slower below 8192
+// tokens: the chain of one token stays as long.
 //
 // The order is exact.  Without a bias the scores rise with the logits, so the
 // keys are the logits' own bits (16-bit logits share the key with the id: no
 // ties are left).  With a bias (or group sums) the fp32 values carry a bounded
-// error (gate_tau), and a token whose decision gaps are all wider than its
-// bound allows is decided by fp32; any other token, one with equal keys among
-// its first k + 1 too, is decided once more from fp64 scores in shared memory
-// (warp_exact).  The same path serves group sizes that no chunk of lanes
-// divides.
+// error (gate_tau); where a decision gap is not wider than its bound, fp64
+// scores of the few experts in question decide: between groups those that can
+// be among a group's two largest (warp_groups), at the k-th place and in the
+// order those of the rounds that go on until a gap is wide enough (warp_order).
+// Only more than 32 experts that close, softmax scores with a bias (or in group
+// sums), infinities next to a border and groups that no chunk of lanes divides
+// take fp64 scores of all experts (warp_exact: 5 us longer; when it decided
+// every close token, 4096 tokens took 11.2 us and 16384 took 23.7).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -68,6 +72,10 @@ __device__ __forceinline__ unsigned long long key64(double v) {
   if (v != v) return ~0ull;
   const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v == 0.0 ? 0.0 : v));
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double unkey64(unsigned long long k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
 
 template <typename T>
@@ -286,27 +294,66 @@ __device__ __forceinline__ float logit_of_key(uint32_t key) {
                                           : __uint_as_float(u << 16);
 }
 
-// The order of k experts whose set is certain (lane r < k holds one of them):
-// by fp64 biased sigmoid scores, or by the logits themselves, ties to the lower
-// id.  Lane r gets the r-th.  s: k words of shared memory.
+// The order of n experts (lane r < n holds one of them) that are certain to
+// hold the first k: by fp64 biased sigmoid scores, or by the logits themselves,
+// ties to the lower id.  Lane r < k gets the r-th.  s: n words of shared memory.
 template <typename TIn>
-__device__ int warp_order(const GateArgs& a, const TIn* row, int id, uint32_t* s, int lane) {
+__device__ int warp_order(const GateArgs& a, const TIn* row, int id, int n, uint32_t* s, int lane) {
   double v = 0.0;
-  if (lane < a.k) {
+  if (lane < n) {
     const double l = static_cast<double>(load_logit(a, row, id));
     v = a.bias != nullptr ? 1.0 / (1.0 + exp(-l)) + static_cast<double>(a.bias[id]) : l;
   }
   const unsigned long long key = key64(v);
   int rank = 0;
-  for (int j = 0; j < a.k; ++j) {
+  for (int j = 0; j < n; ++j) {
     const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
     const int oid = __shfl_sync(0xffffffffu, id, j);
     rank += o > key || (o == key && oid < id);
   }
   __syncwarp();
-  if (lane < a.k) s[rank] = static_cast<uint32_t>(id);
+  if (lane < n) s[rank] = static_cast<uint32_t>(id);
   __syncwarp();
   return lane < a.k ? static_cast<int>(s[lane]) : 0;
+}
+
+// Whether the lane's group is kept, from fp64 values of the few experts that
+// can be among its two largest (sums) or its largest: those whose fp32 value is
+// not clearly below `ref`, the group's second largest (largest).  list: the
+// lane's sorted keys in shared memory.  Sigmoid scores, or groups by their
+// largest logit; finite values.
+template <typename TIn, int C, bool PACKED>
+__device__ bool warp_groups(const GateArgs& a, const TIn* row, const uint32_t* list, int e0, int g, float ref,
+                            bool biased, bool sums, int lane) {
+  const float key_width = PACKED ? 0.f : C * 1.1920929e-07f;
+  const float least = ref - 4.f * (gate_tau(ref, 0) + key_width * fabsf(ref));
+  unsigned long long k1 = 0, k2 = 0;
+  for (int i = 0; i < C; ++i) {
+    const uint32_t key = list[32 * i];
+    if (PACKED ? key == 0u : key < C) break;  // the lane has no more
+    const float x = logit_of_key<TIn, PACKED>(key);
+    if ((!biased && sums ? rank_score(a, x, 0.f, 0.f) : x) < least) break;
+    const int id = PACKED ? static_cast<int>(0xFFFFu - (key & 0xFFFFu)) : e0 + static_cast<int>(~key & (C - 1u));
+    double v = static_cast<double>(load_logit(a, row, id));
+    if (biased || sums) v = 1.0 / (1.0 + exp(-v));
+    if (biased) v += static_cast<double>(a.bias[id]);
+    const unsigned long long k = key64(v);
+    k2 = max(k2, min(k1, k));
+    k1 = max(k1, k);
+  }
+  __syncwarp();
+  for (int o = 1; o < a.group_lanes; o *= 2) {
+    const unsigned long long o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+    k2 = max(max(k2, o2), min(k1, o1));
+    k1 = max(k1, o1);
+  }
+  const unsigned long long gk = sums ? key64(unkey64(k1) + unkey64(k2)) : k1;
+  int rank = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const unsigned long long o = __shfl_sync(0xffffffffu, gk, j * a.group_lanes);
+    rank += o > gk || (o == gk && j < g);
+  }
+  return g < a.groups && rank < a.top;
 }
 
 // Descending sort of a lane's keys (Batcher's odd-even merge sort): all steps
@@ -389,6 +436,12 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
     lane_sort<C>(key);
     // a value known by its key: rounded down by up to C - 1 ulp
     constexpr float key_width = PACKED ? 0.f : C * 1.1920929e-07f;
+    // sorted keys to shared memory: a lane's head moves down by one place when
+    // it wins a round
+    uint32_t* list = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)) + lane;
+#pragma unroll
+    for (int i = 0; i < C; ++i) list[32 * i] = key[i];
+    list[32 * C] = 0u;
     bool alive = true;  // the lane's group is kept
     if (a.groups > 1) {
       const int lanes = a.group_lanes;
@@ -441,14 +494,16 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
         exact = __any_sync(0xffffffffu, open);
       }
       alive = has && rank < a.top;
+      if (exact && a.group_shift >= 0 && !(a.softmax && (biased || sums))) {
+        const float ref = unkey32(sums ? g2 : g1), v1 = unkey32(g1);
+        const bool finite = fabsf(ref) <= 3.4028235e38f && fabsf(v1) <= 3.4028235e38f;
+        if (__all_sync(0xffffffffu, finite || !has)) {
+          alive = warp_groups<TIn, C, PACKED>(a, row, list, e0, g, ref, biased, sums, lane);
+          exact = false;
+        }
+      }
     }
-    // sorted keys to shared memory: a lane's head moves down by one place when
-    // it wins a round
-    uint32_t* list = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)) + lane;
     uint32_t head = alive ? key[0] : 0u;
-#pragma unroll
-    for (int i = 1; i < C; ++i) list[32 * i] = key[i];
-    list[32 * C] = 0u;
     if (PACKED) {
       for (int r = 0; r < a.k; ++r) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, head);
@@ -459,13 +514,28 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
         }
       }
     } else {
-      uint32_t won = 0u;  // lane r: the key of round r; one round more than k: the k-th has to be apart from the next
-      for (int r = 0; r <= a.k; ++r) {
+      // lane r: the key of round r.  Rounds go on behind the k-th while the
+      // values are too close to be told apart; then n experts hold the first k.
+      auto apart = [&](uint32_t k0, uint32_t k1) {
+        const float v0 = unkey32(k0), v1 = unkey32(k1);
+        return v0 - v1 > (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
+                             key_width * (fabsf(v0) + fabsf(v1)) + 2.3509887e-38f;  // (places alone, next to 0)
+      };
+      uint32_t won = 0u, last = 0u;
+      int n = 0;
+      for (;;) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, head);
-        if (top == 0u) break;  // no expert is left (round k + 1): no lane's list may move past its end
+        if (top == 0u) break;  // no expert is left: no lane's list may move past its end
+        if (n >= a.k) {
+          if (apart(last, top)) break;
+          if (n == 32) {
+            exact = true;
+            break;
+          }
+        }
         const uint32_t id = static_cast<uint32_t>(e0) + (~head & (C - 1u));
         const uint32_t best = __reduce_min_sync(0xffffffffu, head == top ? id : 0xFFFFFFFFu);
-        if (lane == r) {
+        if (lane == n) {
           mine = static_cast<int>(best);
           won = top;
         }
@@ -473,20 +543,15 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
           list += 32;
           head = *list;
         }
+        last = top;
+        ++n;
       }
-      // neighbours in the order: equal keys, or values too close.  Apart from the
-      // last pair that is a question of order alone.
+      // neighbours in the order: equal keys, or values too close
       const uint32_t next = __shfl_down_sync(0xffffffffu, won, 1);
-      bool open = false;
-      if (lane < a.k && next != 0u) {  // (0: no expert was left for round k + 1)
-        const float v0 = unkey32(won), v1 = unkey32(next);
-        open = !(v0 - v1 > (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
-                               key_width * (fabsf(v0) + fabsf(v1)));
-      }
-      const uint32_t opens = __ballot_sync(0xffffffffu, open);
-      exact = exact || ((opens >> (a.k - 1)) & 1u) || (opens != 0u && biased && a.softmax);
+      const uint32_t opens = __ballot_sync(0xffffffffu, lane + 1 < n && !apart(won, next));
+      exact = exact || (opens != 0u && biased && a.softmax);
       if (opens != 0u && !exact)
-        mine = warp_order(a, row, mine, reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
+        mine = warp_order(a, row, mine, n, reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
     }
     __syncwarp();
   }

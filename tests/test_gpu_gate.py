@@ -98,6 +98,37 @@ def test_ties_and_near_ties_follow_the_exact_order():
     check(torch.zeros(5, 256), torch.zeros(256), 8, groups=8, top=2)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("group_max", [False, True])
+def test_close_values_everywhere(group_max, dtype):
+    """Logits on a coarse grid and biases of a few 1e-7: most borders, between
+    groups, at the k-th place and inside, are closer than fp32 scores can tell."""
+    g = torch.Generator().manual_seed(11)
+    for E, groups, top, k, grid in ((256, 8, 4, 8, 8), (64, 16, 3, 6, 2), (160, 8, 3, 16, 16), (96, 12, 5, 8, 4),
+                                    (256, 32, 20, 8, 1), (1024, 8, 2, 16, 16), (64, 64 // 64, 1, 6, 4)):
+        z = ((torch.randn(150, E, generator=g) * grid).round() / grid).to(dtype)
+        for width in (1e-7, 3e-6):
+            bias = torch.randn(E, generator=g) * width
+            check(z, bias, k, groups=groups, top=top, group_max=group_max)
+            check(z[:20], bias, k, True, groups, top, group_max)
+        check(z, None, k, groups=groups, top=top, group_max=group_max)
+
+
+def test_more_close_values_than_places():
+    """Groups whose sums agree to 1e-8, and 40 experts of one value."""
+    g = torch.Generator().manual_seed(12)
+    for wide in (3, 40):
+        z = torch.randn(1, 256, generator=g)
+        target = torch.rand(256, generator=g).double() * 0.3
+        target[::32] = 0.9
+        target[1::32] = target[2::32] = 0.8
+        target[torch.randperm(256, generator=g)[:wide]] = 0.9
+        bias = (target - 1 / (1 + torch.exp(-z[0].double()))).float()
+        for groups, top in ((1, 1), (8, 4), (8, 1), (16, 9)):
+            check(z, bias, 8, groups=groups, top=top)
+            check(z, bias, 8, groups=groups, top=top, group_max=True)
+
+
 def test_saturated_scores_keep_the_order_of_the_logits():
     z = torch.tensor([[200.0, 300.0, 90.0, -200.0, -300.0, 250.0, 0.0, -90.0]])
     check(z, None, 4)
