@@ -152,10 +152,10 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
     if stream is None:
         tt = _tt()
-        return tt.stream(tt.device())
+        return tt.stream(tt.device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -269,7 +269,7 @@ class _Torch:
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.outs = (torch.bfloat16, torch.float32)
         # without a GPU no tensor is on the current device (the CPU's number is -1)
-        self.device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2
+        self.device = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2
         # the handle alone: building a torch.cuda.Stream around it takes 3 us
         self.stream = torch._C._cuda_getCurrentRawStream
 
@@ -331,7 +331,7 @@ def moe_gate_topk(cfg, logits, correction_bias, topk_ids, topk_w, stream=None):
     _want(topk_w, "topk_w", tt.f32, shape, where, dev)
     _check(load_library().moe_gate_topk(ctypes.byref(cfg), logits.data_ptr(), tt.types[logits.dtype], stride,
                                         _ptr(correction_bias), T, topk_ids.data_ptr(), topk_w.data_ptr(),
-                                        _stream(stream)), where)
+                                        _stream(stream, dev)), where)
 
 
 def moe_fp8_quantize(x, q, scale, src=None, src_div=1, stream=None):
@@ -348,7 +348,7 @@ def moe_fp8_quantize(x, q, scale, src=None, src_div=1, stream=None):
     _want(q, "q", tt.codes, (rows, K), where, dev)
     _want(scale, "scale", tt.f32, (_blocks(K), rows), where, dev)
     _check(load_library().moe_fp8_quantize(x.data_ptr(), tt.types[x.dtype], stride, _ptr(src), int(src_div), rows, K,
-                                           q.data_ptr(), scale.data_ptr(), _stream(stream)), where)
+                                           q.data_ptr(), scale.data_ptr(), _stream(stream, dev)), where)
 
 
 def moe_fp8_quantize_weight(w, q, scale, stream=None):
@@ -362,7 +362,7 @@ def moe_fp8_quantize_weight(w, q, scale, stream=None):
     _want(q, "q", tt.codes, (G, N, K), where, dev)
     _want(scale, "scale", tt.f32, (G, _blocks(N), _blocks(K)), where, dev)
     _check(load_library().moe_fp8_quantize_weight(w.data_ptr(), tt.types[w.dtype], G, N, K, q.data_ptr(),
-                                                  scale.data_ptr(), _stream(stream)), where)
+                                                  scale.data_ptr(), _stream(stream, dev)), where)
 
 
 def moe_fp8_gemm(a, a_scale, w, w_scale, expert_offsets, row_scale, out, ws, stream=None):
@@ -386,7 +386,7 @@ def moe_fp8_gemm(a, a_scale, w, w_scale, expert_offsets, row_scale, out, ws, str
     _want(ws, "ws", tt.u8, None, where, dev)
     _check(load_library().moe_fp8_gemm(a.data_ptr(), a_scale.data_ptr(), rows, _ptr(expert_offsets), G, w.data_ptr(),
                                        w_scale.data_ptr(), N, K, _ptr(row_scale), out.data_ptr(), tt.types[out.dtype],
-                                       ws.data_ptr(), ws.numel(), _stream(stream)), where)
+                                       ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
 
 
 def moe_permute_no_alloc(cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm, stream=None):
