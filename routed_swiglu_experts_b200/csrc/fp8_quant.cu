@@ -101,7 +101,9 @@ __device__ __forceinline__ Vec16<T> load16(const T* p) {
 // (one 16-byte store of codes) per lane, the slab's four loads in flight at
 // once.  Eight rows per block: their scales, neighbours in the block-major
 // layout, go through shared memory and are written 32 bytes at a time.
-// Rows outside [range[0], range[range_len]) are skipped (range given).
+// Rows outside [range[0], range[range_len]) are skipped (range given), and those
+// outside 0 .. rows whatever the range says, as in the products that follow
+// (scan_groups): the last block of eight may reach past the rows.
 constexpr int kRowWarps = 8;
 constexpr int kSlab = 2048;
 
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   int lo = 0, hi = rows;
   if (range != nullptr) {
     lo = __ldg(range);
-    hi = __ldg(range + range_len);
+    hi = min(__ldg(range + range_len), rows);
   }
   const int k0 = blockIdx.y * kSlab;
   if (r >= lo && r < hi) {
