@@ -233,7 +233,10 @@ MOE_API moe_status moe_router_topk(const moe_config* cfg, const moe_weights* w,
  *   the lower id;  w = alpha * s_id, renormalised over the k first if
  *   cfg->renormalize (0 where that sum is 0).
  * The order is that of the exact scores of the given logits: where fp32
- * leaves a decision open it is taken from fp64 scores.  The weights are fp32.
+ * leaves a decision open it is taken from fp64 scores (equal ones are a tie).
+ * The weights are fp32; renormalised ones keep their precision where scores
+ * leave fp32's range (fp64's range decides which scores are 0: sigmoid logits
+ * below about -709, softmax logits as far below the row's largest).
  * Logits may be infinite: an expert with -inf has score 0, a softmax row of
  * -inf alone has scores 0; NaN counts as the largest value.  The ids of a
  * token are distinct and in [0, E) whatever the logits hold.

@@ -166,9 +166,26 @@ __device__ __forceinline__ float rank_score(const GateArgs& a, float l, float m,
 }
 
 // Unbiased fp32 score.  m, inv_z: the row's maximum and 1 / sum (softmax).
+// (Below -80 the divisor's 1 is far under its last bit, and exp(-l) soon above
+// fp32's range.)
 __device__ __forceinline__ float gate_score(const GateArgs& a, float l, float m, float inv_z) {
   if (a.softmax) return l == -INFINITY ? 0.f : expf(l - m) * inv_z;
-  return 1.f / (1.f + expf(-l));
+  const bool low = l < -80.f;
+  const float e = expf(low ? l : -l);
+  return low ? e : 1.f / (1.f + e);
+}
+
+// Share of the lane's expert in the sum of the k selected scores, in fp64: for
+// rows where one of them is at or below the end of fp32's range, while the
+// shares may be of any size.  Softmax: its denominator cancels.  0 where the
+// sum is 0: sigmoid logits below fp64's exp (about -709), as masks are.
+__device__ __forceinline__ float wide_share(float l, float m, bool softmax, bool selected) {
+  double s = 0.0;
+  if (selected) s = softmax ? exp(static_cast<double>(l) - m) : 1.0 / (1.0 + exp(-static_cast<double>(l)));
+  double sum = s;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum == 0.0 ? 0.f : static_cast<float>(s / sum);
 }
 
 // Selection of one token from fp64 scores: v and its keys in shared memory.
@@ -571,14 +588,21 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
     z = warp_sum(z);
     inv_z = z == 0.f ? 0.f : 1.f / z;
   }
-  const float s = lane < a.k ? gate_score(a, load_logit(a, row, mine), m, inv_z) : 0.f;
+  const float l_sel = lane < a.k ? load_logit(a, row, mine) : 0.f;
+  const float s = lane < a.k ? gate_score(a, l_sel, m, inv_z) : 0.f;
   float sum = s;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const size_t o = static_cast<size_t>(t) * a.k + lane;
   if (lane < a.k) {
-    const size_t o = static_cast<size_t>(t) * a.k + lane;
     a.ids[o] = mine;
     a.w[o] = a.renorm ? (sum == 0.f ? 0.f : s / sum * a.alpha) : s * a.alpha;
+  }
+  // a score that is not far inside fp32's range, and no masked expert's (0 in fp64 too)
+  const bool tiny = a.renorm && lane < a.k && s < 7.8886091e-31f && (a.softmax ? l_sel - m : l_sel) > -746.f;
+  if (__any_sync(0xffffffffu, tiny)) {
+    const float share = wide_share(l_sel, m, a.softmax, lane < a.k);
+    if (lane < a.k) a.w[o] = share * a.alpha;
   }
 }
 
