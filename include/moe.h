@@ -220,8 +220,11 @@ MOE_API moe_status moe_router_topk(const moe_config* cfg, const moe_weights* w,
                            void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* With cfg->score = MOE_SCORE_SOFTMAX or cfg->num_groups > 1, moe_router_topk
- * (and every call that routes) takes the same fp32 tensor-core logits and
- * selects from them as moe_gate_topk does. */
+ * (and every call that routes) selects as moe_gate_topk does, from the same
+ * tensor-core logits; decisions closer than those logits' error may be are
+ * taken from fp64 logits here too, so the ids equal the exact-arithmetic
+ * selection.  (Softmax scores with a bias need all of a token's exact logits
+ * where the softmax's denominator decides: a second, short launch.) */
 
 /* Expert selection from given router logits (any router in front: one with a
  * linear bias, a quantised one, logits gathered from another rank):

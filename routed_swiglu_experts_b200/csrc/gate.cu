@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "moe_internal.h"
+#include "router_dot.cuh"
 
 namespace moe {
 
@@ -102,6 +103,10 @@ struct GateArgs {
   float alpha;
   int32_t* ids;
   float* w;
+  const __nv_bfloat16* x;  // ROUTER: tokens [T, H] and the router weight [E, H] behind the logits
+  const float* wr;
+  int H;
+  int defer;  // tokens that need all their logits exactly are left to router_finish_kernel
 };
 
 // One logit (fp32: the sum of its slices).
@@ -188,6 +193,81 @@ __device__ __forceinline__ float wide_share(float l, float m, bool softmax, bool
   return sum == 0.0 ? 0.f : static_cast<float>(s / sum);
 }
 
+// Maximum and 1 / sum of a row's softmax, by a warp whose lanes hold no chunks.
+template <typename TIn>
+__device__ __forceinline__ void wide_statistics(const GateArgs& a, const TIn* row, int lane, float& m, float& inv_z) {
+  m = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit(a, row, e));
+  m = warp_max(m);
+  float z = 0.f;
+  for (int e = lane; e < a.E; e += 32) {
+    const float x = load_logit(a, row, e);
+    z += x == -INFINITY ? 0.f : expf(x - m);
+  }
+  z = warp_sum(z);
+  inv_z = z == 0.f ? 0.f : 1.f / z;
+}
+
+// Ids and weights of one token: lane r < k holds the r-th expert.
+template <typename TIn>
+__device__ __forceinline__ void emit(const GateArgs& a, const TIn* row, int t, int mine, float m, float inv_z, int lane) {
+  const float l_sel = lane < a.k ? load_logit(a, row, mine) : 0.f;
+  const float s = lane < a.k ? gate_score(a, l_sel, m, inv_z) : 0.f;
+  float sum = s;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const size_t o = static_cast<size_t>(t) * a.k + lane;
+  if (lane < a.k) {
+    a.ids[o] = mine;
+    a.w[o] = a.renorm ? (sum == 0.f ? 0.f : s / sum * a.alpha) : s * a.alpha;
+  }
+  // a score that is not far inside fp32's range, and no masked expert's (0 in fp64 too)
+  const bool tiny = a.renorm && lane < a.k && s < 7.8886091e-31f && (a.softmax ? l_sel - m : l_sel) > -746.f;
+  if (__any_sync(0xffffffffu, tiny)) {
+    const float share = wide_share(l_sel, m, a.softmax, lane < a.k);
+    if (lane < a.k) a.w[o] = share * a.alpha;
+  }
+}
+
+// The k largest of E fp64 keys in shared memory, which are spent: each lane
+// keeps its best (of e = lane, lane + 32, ...; the lowest e among equals), and
+// the winner's lane looks for its next.  Lane r < k gets the r-th's e; all get
+// taken(r, key).
+template <typename F>
+__device__ __forceinline__ int pick_keys(unsigned long long* keys, int E, int k, int lane, F&& taken) {
+  int mine = 0;
+  unsigned long long best;
+  int at;
+  auto scan = [&] {
+    best = 0ull;
+    at = 0x7fffffff;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) {
+      const unsigned long long x = keys[e];
+      if (x > best) {
+        best = x;
+        at = e;
+      }
+    }
+  };
+  scan();
+  for (int r = 0; r < k; ++r) {
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+    const uint32_t top_hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t top_lo = __reduce_max_sync(0xffffffffu, hi == top_hi ? lo : 0u);
+    taken(r, static_cast<unsigned long long>(top_hi) << 32 | top_lo);
+    const bool top = hi == top_hi && lo == top_lo;
+    const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
+    if (lane == r) mine = id;
+    if (top && at == id) {
+      keys[id] = 0ull;
+      scan();
+    }
+    __syncwarp();
+  }
+  return mine;
+}
+
 // Selection of one token from fp64 scores: v and its keys in shared memory.
 // Returns in lane r < k the id of the r-th expert.
 template <typename TIn>
@@ -249,44 +329,13 @@ __device__ int warp_exact(const GateArgs& a, const TIn* row, double* v, int lane
   }
   // within the groups the order of the logits again, where there is no bias
   const bool by_logit = a.bias == nullptr;
-  int mine = 0;
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(v);
   for (int e = lane; e < E; e += 32) {
     const double x = by_logit ? static_cast<double>(load_logit(a, row, e)) : v[e];
     keys[e] = ((keep >> (a.groups > 1 ? e / per : 0)) & 1u) ? key64(x) : 0ull;
   }
   __syncwarp();
-  // each lane keeps its best key (of e = lane, lane + 32, ...; the lowest e
-  // among equals); the winner's lane looks for its next
-  unsigned long long best;
-  int at;
-  auto scan = [&] {
-    best = 0ull;
-    at = 0x7fffffff;
-#pragma unroll 4
-    for (int e = lane; e < E; e += 32) {
-      const unsigned long long x = keys[e];
-      if (x > best) {
-        best = x;
-        at = e;
-      }
-    }
-  };
-  scan();
-  for (int r = 0; r < a.k; ++r) {
-    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
-    const uint32_t top_hi = __reduce_max_sync(0xffffffffu, hi);
-    const uint32_t top_lo = __reduce_max_sync(0xffffffffu, hi == top_hi ? lo : 0u);
-    const bool top = hi == top_hi && lo == top_lo;
-    const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
-    if (lane == r) mine = id;
-    if (top && at == id) {
-      keys[id] = 0ull;
-      scan();
-    }
-    __syncwarp();
-  }
-  return mine;
+  return pick_keys(keys, E, a.k, lane, [](int, unsigned long long) {});
 }
 
 // A 16-bit logit (given as the fp32 it was widened to) and expert id in one
@@ -373,6 +422,289 @@ __device__ bool warp_groups(const GateArgs& a, const TIn* row, const uint32_t* l
   return g < a.groups && rank < a.top;
 }
 
+// ---- ROUTER: the layer's own logits ----------------------------------------
+// They are the tensor cores' fp32 sums, so a decision is open already where
+// their error may have made it; it is then taken from exact products x . w,
+// computed for the experts in question alone.  The whole router call (split of
+// the weight, logits, selection; graph replay), random inputs, before this was
+// done and with it: 4096 tokens, H 2048, 64 experts: groups of sums 17.5, 29.0
+// us, softmax 16.5, 23.7, softmax and bias 21.2, 44.0; 32 tokens, H 6144, 256
+// experts: 21.8, 22.7; 21.9, 22.5; 41.0, 34.5; 16384 of them: 183, 235; 176, 212;
+// 195, 536 (the default route: 25, 21 and 244).
+
+// By how much two values that the selection compares have to differ for their
+// order to be certain.
+//   logits:  the fp32 sum of 3 H products, 16 to an addition, rounds 3 H / 16
+//            times, each by at most 2^-23 of the running sum, which is of the
+//            size of the token's largest logits; adding the slices 32 times
+//            more.  The running sums of S slices are smaller by sqrt(S) at least,
+//            unless slices cancel.  Two logits:
+//            d = (0.75 H / sqrt(S) + 64) 2^-24 max(1, largest |l|).
+//            (The tensor cores truncate.  Measured, H 128 to 12288: errors of up
+//            to 0.32 of d / 2 from normal, one-signed, scaled and outlying inputs:
+//            1.4e-4 for normal ones at H 6144.)
+//   scores:  sigmoid' <= 1/4; a softmax score moves relatively by its logit's
+//            error and by as much again through the denominator.
+//   z:       the denominator, relatively: the logits' errors weighted by their
+//            scores (those by each logit's own size; measured: up to 0.29 of it),
+//            and its fp32 sum's rounding.
+struct Slack {
+  float logit, score, z;
+};
+__device__ __forceinline__ Slack slack_of(const GateArgs& a, float largest, float inv_z, float z_sizes) {
+  const float unit = (0.75f * static_cast<float>(a.H) * rsqrtf(static_cast<float>(a.slices)) + 64.f) * 5.9604645e-08f;
+  const float d = unit * fmaxf(1.f, largest);
+  return Slack{d, a.softmax ? 2.f * inv_z * d : 0.25f * d, 0.5f * unit * z_sizes * inv_z + 3.8146973e-06f};
+}
+
+// Exact logits of the experts `id` of the lanes that want one; the whole warp
+// takes two at a time.
+__device__ __noinline__ double router_logits(const __nv_bfloat16* xr, const float* wr, int H, int id, bool want, int lane) {
+  double mine = 0.0;
+  for (uint32_t todo = __ballot_sync(0xffffffffu, want); todo != 0u;) {
+    const int l0 = __ffs(todo) - 1;
+    todo &= todo - 1u;
+    const int l1 = todo != 0u ? __ffs(todo) - 1 : l0;
+    todo &= todo - 1u;  // (0 stays 0)
+    const int e0 = __shfl_sync(0xffffffffu, id, l0), e1 = __shfl_sync(0xffffffffu, id, l1);
+    double l[2];
+    exact_dots<2>(xr, {wr + static_cast<size_t>(e0) * H, wr + static_cast<size_t>(e1) * H}, H, lane, l);
+    if (lane == l1) mine = l[1];
+    if (lane == l0) mine = l[0];
+  }
+  return mine;
+}
+
+// Selection from all the fp64 logits of a token, v [E]; as warp_exact's, in
+// three steps.  First the softmax's statistics,
+__device__ __forceinline__ void router_statistics(const GateArgs& a, const double* v, int lane, double& m, double& z) {
+  m = -INFINITY, z = 0.0;
+  if (!a.softmax) return;
+  for (int e = lane; e < a.E; e += 32) m = fmax(m, v[e]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+  for (int e = lane; e < a.E; e += 32) z += exp(v[e] - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+}
+
+// then what is compared, of experts e0, e0 + step, ...: v becomes the biased
+// scores (without a bias it stays the logits, in the same order with no
+// rounding) and u [E], for groups by sums, the scores.
+__device__ __forceinline__ bool router_sums(const GateArgs& a) { return a.groups > 1 && !a.max_score && a.E > a.groups; }
+__device__ __forceinline__ void router_values(const GateArgs& a, double* v, double* u, int e0, int step, double m, double z) {
+  const bool biased = a.bias != nullptr;
+  if (!biased && !router_sums(a)) return;
+#pragma unroll 2
+  for (int e = e0; e < a.E; e += step) {
+    const double l = v[e], s = a.softmax ? exp(l - m) / z : 1.0 / (1.0 + exp(-l));
+    if (biased)
+      v[e] = s + static_cast<double>(a.bias[e]);
+    else
+      u[e] = s;
+  }
+}
+
+// then the groups and the k experts, by one warp.  draft: the logits were the
+// fp32 ones; `sure` is false when their error may have decided.
+__device__ __noinline__ int router_select(const GateArgs& a, double* v, const double* u, int lane, bool draft, Slack slack,
+                                          bool& sure) {
+  const int E = a.E, per = E / a.groups;
+  const bool biased = a.bias != nullptr, sums = router_sums(a);
+  const double width = biased ? slack.score : slack.logit;
+  double least = INFINITY;  // smallest difference that decided, in widths
+  uint32_t keep = 0xffffffffu;
+  if (a.groups > 1) {
+    const double* by = sums && !biased ? u : v;
+    unsigned long long k1 = 0, k2 = 0;
+    for (int i = 0; i < per && lane < a.groups; ++i) {
+      const unsigned long long k = key64(by[lane * per + i]);
+      k2 = max(k2, min(k1, k));
+      k1 = max(k1, k);
+    }
+    const unsigned long long gk = sums && k1 != ~0ull ? key64(unkey64(k1) + unkey64(k2)) : k1;  // (NaN stays the largest)
+    int rank = 0;
+    for (int j = 0; j < a.groups; ++j) {
+      const unsigned long long o = __shfl_sync(0xffffffffu, gk, j);
+      rank += o > gk || (o == gk && j < lane);
+    }
+    const bool has = lane < a.groups;
+    keep = __ballot_sync(0xffffffffu, has && rank < a.top);
+    if (a.top < a.groups) {
+      const int last = __ffs(__ballot_sync(0xffffffffu, has && rank == a.top - 1)) - 1;
+      const int next = __ffs(__ballot_sync(0xffffffffu, has && rank == a.top)) - 1;
+      least = (unkey64(__shfl_sync(0xffffffffu, gk, last)) - unkey64(__shfl_sync(0xffffffffu, gk, next))) /
+              (sums ? 2.0 * slack.score : width);
+    }
+    __syncwarp();  // the groups' values are read: v becomes the keys
+  }
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(v);
+  for (int e = lane; e < E; e += 32) keys[e] = ((keep >> (a.groups > 1 ? e / per : 0)) & 1u) ? key64(v[e]) : 0ull;
+  __syncwarp();
+  unsigned long long before = 0ull;
+  const int mine = pick_keys(keys, E, a.k, lane, [&](int r, unsigned long long key) {
+    if (r > 0) least = fmin(least, (unkey64(before) - unkey64(key)) / width);
+    before = key;
+  });
+  // the best of those left out
+  unsigned long long best = 0ull;
+  for (int e = lane; e < E; e += 32) best = max(best, keys[e]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (best != 0ull) least = fmin(least, (unkey64(before) - unkey64(best)) / width);
+  __syncwarp();
+  sure = !draft || least > 1.0;
+  return mine;
+}
+
+// The three by one warp.
+__device__ __noinline__ int router_steps(const GateArgs& a, double* v, int lane, bool draft, Slack slack, bool& sure) {
+  double m, z;
+  __syncwarp();
+  router_statistics(a, v, lane, m, z);
+  __syncwarp();
+  router_values(a, v, v + a.E, lane, 32, m, z);
+  __syncwarp();
+  return router_select(a, v, v + a.E, lane, draft, slack, sure);
+}
+
+// Exact logits of experts e .. e + 3 (those of them that there are) into v, by one warp.
+__device__ __forceinline__ void four_logits(const GateArgs& a, const __nv_bfloat16* xr, int e, int lane, double* v) {
+  auto w = [&](int i) { return a.wr + static_cast<size_t>(min(e + i, a.E - 1)) * a.H; };
+  double l[4];
+  exact_dots<4>(xr, {w(0), w(1), w(2), w(3)}, a.H, lane, l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane == i && e + i < a.E) v[e + i] = l[i];
+}
+
+// Whether a token is all zeros (padding): its logits are exact, and all alike.
+__device__ __noinline__ bool zero_token(const __nv_bfloat16* xr, int H, int lane) {
+  uint32_t any = 0u;
+  for (int h = lane * 8; h < H; h += 256) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(xr + h));
+    any |= (v.x | v.y | v.z | v.w) & 0x7FFF7FFFu;
+  }
+  return !__any_sync(0xffffffffu, any != 0u);
+}
+
+// A token whose fp32 logits cannot tell, from all its exact logits; those
+// themselves for zero tokens, and as a draft where no run of lanes holds a group.
+template <typename TIn>
+__device__ __noinline__ int router_exact(const GateArgs& a, const TIn* row, const __nv_bfloat16* xr, double* v, int lane,
+                                         bool zero, Slack slack, bool& sure) {
+  int mine = 0;
+  sure = false;
+  if (a.chunk == 0 || zero) {
+    for (int e = lane; e < a.E; e += 32) v[e] = static_cast<double>(load_logit(a, row, e));
+    mine = router_steps(a, v, lane, !zero, slack, sure);
+  }
+  if (!sure && !a.defer) {
+    __syncwarp();
+    for (int e = 0; e < a.E; e += 4) four_logits(a, xr, e, lane, v);
+    mine = router_steps(a, v, lane, false, slack, sure);
+  }
+  return mine;
+}
+
+// As warp_order; bit r of `opens`: the r-th and its successor are too close to
+// be told apart.  Only runs of such experts need exact logits, and only their
+// own order is open.  Softmax scores with a bias have exact numerators here
+// over the fp32 logits' denominator, off by a factor of 1 +- slack.z: sure is
+// false when a factor in that range would turn a pair of neighbours round (in
+// `mine`, the order, no other pair turns before one of neighbours does).
+__device__ __noinline__ int router_order(const GateArgs& a, const __nv_bfloat16* xr, int id, int n, uint32_t opens,
+                                         uint32_t* order, int lane, float m, float inv_z, Slack slack, bool& sure) {
+  const uint32_t apart = ~opens & ((1u << lane) - 1u);
+  const int first = apart != 0u ? 32 - __clz(apart) : 0;  // of the lane's run
+  const bool want = lane < n && (first < lane || ((opens >> lane) & 1u));
+  double v = router_logits(xr, a.wr, a.H, id, want, lane), s = 0.0;
+  if (a.bias != nullptr && want) {
+    s = a.softmax ? exp(v - m) * inv_z : 1.0 / (1.0 + exp(-v));
+    v = s + static_cast<double>(a.bias[id]);
+  }
+  const unsigned long long key = key64(v);
+  int rank = first, behind = -1;
+  unsigned long long below = 0ull;
+  for (int j = 0; j < n; ++j) {
+    const unsigned long long o = __shfl_sync(0xffffffffu, key, j);
+    const int oid = __shfl_sync(0xffffffffu, id, j), run = __shfl_sync(0xffffffffu, first, j);
+    const bool ahead = o > key || (o == key && oid < id);
+    rank += run == first && ahead;
+    if (run == first && !ahead && j != lane && (behind < 0 || o > below)) {
+      below = o;
+      behind = j;
+    }
+  }
+  sure = true;
+  if (a.bias != nullptr && a.softmax) {
+    const double s1 = __shfl_sync(0xffffffffu, s, behind < 0 ? lane : behind);
+    const double gap = v - unkey64(behind < 0 ? key : below), turn = fabs(s - s1) * slack.z;
+    sure = __all_sync(0xffffffffu, !want || behind < 0 || (s == s1 ? gap >= 0.0 : gap > turn + 1e-15));
+  }
+  __syncwarp();
+  if (lane < n) order[rank] = static_cast<uint32_t>(id);
+  __syncwarp();
+  return lane < a.k ? static_cast<int>(order[lane]) : 0;
+}
+
+// As warp_groups, for the groups in question alone (`open`: the lane's is one):
+// of the others those are kept that are above the border (`above`).  Softmax
+// scores have the fp32 logits' denominator (m, inv_z): without a bias it does
+// not matter; with one, sure is false when its error may.  x_of(key): a key's
+// value in the order of the list; least: the smallest that can be among the two
+// largest.
+template <int C, typename F>
+__device__ __forceinline__ bool router_groups(const GateArgs& a, const __nv_bfloat16* xr, const uint32_t* list, int e0,
+                                              int g, float least, bool biased, bool sums, float m, float inv_z, Slack slack,
+                                              bool open, bool above, int lane, bool& sure, F&& x_of) {
+  unsigned long long k1 = 0, k2 = 0;
+  double top = 0.0;  // largest score in question
+  bool more = open;
+  for (int i = 0; i < C; ++i) {
+    const uint32_t key = list[32 * i];
+    more = more && key >= C && !(x_of(key) < least);  // (keys below C: the lane has no more)
+    if (!__any_sync(0xffffffffu, more)) break;
+    const int id = e0 + static_cast<int>(~key & (C - 1u));
+    double v = router_logits(xr, a.wr, a.H, id, more, lane);
+    if (!more) continue;
+    if (biased || sums) v = a.softmax ? exp(v - m) * inv_z : 1.0 / (1.0 + exp(-v));
+    top = fmax(top, v);
+    if (biased) v += static_cast<double>(a.bias[id]);
+    const unsigned long long k = key64(v);
+    k2 = max(k2, min(k1, k));
+    k1 = max(k1, k);
+  }
+  __syncwarp();
+  for (int o = 1; o < a.group_lanes; o *= 2) {
+    const unsigned long long o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+    k2 = max(max(k2, o2), min(k1, o1));
+    k1 = max(k1, o1);
+  }
+  // (finite values' keys lie between 0 and all ones)
+  const unsigned long long gk = !open ? (above ? ~0ull : 0ull) : sums ? key64(unkey64(k1) + unkey64(k2)) : k1;
+  int rank = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const unsigned long long o = __shfl_sync(0xffffffffu, gk, j * a.group_lanes);
+    rank += o > gk || (o == gk && j < g);
+  }
+  const bool kept = g < a.groups && rank < a.top;
+  sure = true;
+  if (biased && a.softmax) {  // the border's values, each off by the scores in it times slack.z
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    double low = kept && open ? unkey64(gk) : INFINITY, high = !kept && open ? unkey64(gk) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      low = fmin(low, __shfl_xor_sync(0xffffffffu, low, o));
+      high = fmax(high, __shfl_xor_sync(0xffffffffu, high, o));
+    }
+    sure = low - high > 2.0 * (sums ? 2.0 : 1.0) * top * slack.z + 1e-15;
+  }
+  return kept;
+}
+
 // Descending sort of a lane's keys (Batcher's odd-even merge sort): all steps
 // (P, K) in order, each one flat loop, so that every index is a constant.
 template <int C, int P, int K>
@@ -394,17 +726,19 @@ __device__ __forceinline__ void lane_sort(uint32_t (&key)[C]) {
 }
 
 // Shared memory of a warp: its lanes' sorted keys [C + 1][32], or the E fp64
-// values of warp_exact.
-__host__ __device__ constexpr size_t gate_smem(int E, int C) {
-  const size_t keys = static_cast<size_t>(C + 1) * 32 * 4, exact = static_cast<size_t>(E) * 8;
+// values of warp_exact (ROUTER: two arrays of E).
+__host__ __device__ constexpr size_t gate_smem(int E, int C, bool router) {
+  const size_t keys = static_cast<size_t>(C + 1) * 32 * 4, exact = static_cast<size_t>(E) * (router ? 16 : 8);
   return ((keys > exact ? keys : exact) + 15) / 16 * 16;
 }
 
 // C: register entries per lane (the chunk a.chunk <= C); VEC: 16-byte loads;
 // PACKED: 16-bit logits without a bias, key = logit bits above 65535 - id;
 // otherwise the low bits of a key hold C - 1 - its place in the lane's chunk.
-template <typename TIn, int C, bool VEC, bool PACKED>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a) {
+// ROUTER: the logits are the layer's own, off by the fp32 product's error:
+// decisions closer than that (slack_of) are taken from exact products x . w.
+template <typename TIn, int C, bool VEC, bool PACKED, bool ROUTER>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const __grid_constant__ GateArgs a) {
   extern __shared__ __align__(16) unsigned char gate_smem_raw[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
@@ -427,7 +761,15 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
   }
   float l[C];
   load_chunk<TIn, C, VEC>(a, row, e0, l);
-  float m = 0.f, inv_z = 0.f;
+  float m = 0.f, inv_z = 0.f, largest = 0.f, z_sizes = 0.f;
+  if (ROUTER) {  // (experts past the end are -inf)
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (VEC ? e0 < E : i < c && e0 + i < E) largest = fmaxf(largest, fabsf(l[i]));
+    if (c == 0)
+      for (int e = lane; e < E; e += 32) largest = fmaxf(largest, fabsf(load_logit(a, row, e)));
+    largest = warp_max(largest);
+  }
   if (c > 0 && a.softmax) {
     m = -INFINITY;
 #pragma unroll
@@ -438,11 +780,25 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
     for (int i = 0; i < C; ++i) z += l[i] == -INFINITY ? 0.f : expf(l[i] - m);
     z = warp_sum(z);
     inv_z = z == 0.f ? 0.f : 1.f / z;
+    if (ROUTER && biased) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) z_sizes += l[i] == -INFINITY ? 0.f : expf(l[i] - m) * fmaxf(1.f, fabsf(l[i]));
+      z_sizes = warp_sum(z_sizes);
+    }
   }
 
-  bool exact = c == 0;
+  Slack slack{};
+  const __nv_bfloat16* xr = nullptr;
+  if (ROUTER) {
+    if (c == 0 && a.softmax) wide_statistics(a, row, lane, m, inv_z);
+    slack = slack_of(a, largest, inv_z, z_sizes);
+    xr = a.x + static_cast<size_t>(t) * a.H;
+  }
+
+  const bool zero = ROUTER && largest == 0.f && zero_token(xr, a.H, lane);
+  bool exact = c == 0 || zero;
   int mine = 0;  // lane r < k: the r-th expert
-  if (c > 0) {
+  if (c > 0 && !zero) {
     uint32_t key[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -455,7 +811,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
     constexpr float key_width = PACKED ? 0.f : C * 1.1920929e-07f;
     // sorted keys to shared memory: a lane's head moves down by one place when
     // it wins a round
-    uint32_t* list = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)) + lane;
+    uint32_t* list = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C, ROUTER)) + lane;
 #pragma unroll
     for (int i = 0; i < C; ++i) list[32 * i] = key[i];
     list[32 * C] = 0u;
@@ -500,23 +856,46 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
         if (!ahead && j != g) below = max(below, o);
       }
       const bool has = g < a.groups;
+      // what the difference of two groups' values has to be above to be certain
+      auto group_width = [&](float v0, float v1) {
+        float w = 2.f * (gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax)) + 2.f * key_width * (fabsf(v0) + fabsf(v1));
+        if (ROUTER) w += sums ? 2.f * slack.score : biased ? slack.score : slack.logit;
+        return w;
+      };
       // the border between the last group kept and the first left out
       bool open = false;
       if (!PACKED || sums) {
         if (has && rank == a.top - 1 && a.top < a.groups) {
           const float vg = unkey32(gk), vb = unkey32(below);
-          open = !(vg - vb > 2.f * (gate_tau(vg, a.softmax) + gate_tau(vb, a.softmax)) +
-                                 2.f * key_width * (fabsf(vg) + fabsf(vb)));
+          open = !(vg - vb > group_width(vg, vb));
         }
         exact = __any_sync(0xffffffffu, open);
       }
       alive = has && rank < a.top;
-      if (exact && a.group_shift >= 0 && !(a.softmax && (biased || sums))) {
+      if (exact && a.group_shift >= 0 && (ROUTER || !(a.softmax && (biased || sums)))) {
         const float ref = unkey32(sums ? g2 : g1), v1 = unkey32(g1);
         const bool finite = fabsf(ref) <= 3.4028235e38f && fabsf(v1) <= 3.4028235e38f;
         if (__all_sync(0xffffffffu, finite || !has)) {
-          alive = warp_groups<TIn, C, PACKED>(a, row, list, e0, g, ref, biased, sums, lane);
-          exact = false;
+          if constexpr (ROUTER) {
+            // the border's two values, and on which side of both the lane's group clearly is
+            const int at = __ffs(__ballot_sync(0xffffffffu, open)) - 1;
+            const float vg = __shfl_sync(0xffffffffu, unkey32(gk), at), vb = __shfl_sync(0xffffffffu, unkey32(below), at);
+            const float v = unkey32(gk);
+            const bool above = has && v - vg > 2.f * group_width(v, vg);
+            const bool asked = has && !above && !(vb - v > 2.f * group_width(v, vb));
+            const float least = ref - 4.f * (gate_tau(ref, a.softmax) + key_width * fabsf(ref)) -
+                                (biased || sums ? slack.score : slack.logit);
+            bool sure;
+            alive = router_groups<C>(a, xr, list, e0, g, least, biased, sums, m, inv_z, slack, asked, above, lane, sure,
+                                     [&](uint32_t key) {
+                                       const float x = unkey32(key);
+                                       return !biased && sums ? rank_score(a, x, m, inv_z) : x;
+                                     });
+            exact = !sure;
+          } else {
+            alive = warp_groups<TIn, C, PACKED>(a, row, list, e0, g, ref, biased, sums, lane);
+            exact = false;
+          }
         }
       }
     }
@@ -535,8 +914,10 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
       // values are too close to be told apart; then n experts hold the first k.
       auto apart = [&](uint32_t k0, uint32_t k1) {
         const float v0 = unkey32(k0), v1 = unkey32(k1);
-        return v0 - v1 > (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
-                             key_width * (fabsf(v0) + fabsf(v1)) + 2.3509887e-38f;  // (places alone, next to 0)
+        float w = (biased ? gate_tau(v0, a.softmax) + gate_tau(v1, a.softmax) : 0.f) +
+                  key_width * (fabsf(v0) + fabsf(v1)) + 2.3509887e-38f;  // (places alone, next to 0)
+        if (ROUTER) w += biased ? slack.score : slack.logit;
+        return v0 - v1 > w;
       };
       uint32_t won = 0u, last = 0u;
       int n = 0;
@@ -566,43 +947,77 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a)
       // neighbours in the order: equal keys, or values too close
       const uint32_t next = __shfl_down_sync(0xffffffffu, won, 1);
       const uint32_t opens = __ballot_sync(0xffffffffu, lane + 1 < n && !apart(won, next));
-      exact = exact || (opens != 0u && biased && a.softmax);
-      if (opens != 0u && !exact)
-        mine = warp_order(a, row, mine, n, reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
+      exact = exact || (!ROUTER && opens != 0u && biased && a.softmax);
+      if (opens != 0u && !exact) {
+        uint32_t* s = reinterpret_cast<uint32_t*>(gate_smem_raw + warp * gate_smem(E, C, ROUTER));
+        if constexpr (ROUTER) {
+          bool sure;
+          mine = router_order(a, xr, mine, n, opens, s, lane, m, inv_z, slack, sure);
+          exact = !sure;
+        } else {
+          mine = warp_order(a, row, mine, n, s, lane);
+        }
+      }
     }
     __syncwarp();
   }
   if (exact) {
-    mine = warp_exact(a, row, reinterpret_cast<double*>(gate_smem_raw + warp * gate_smem(E, C)), lane);
+    double* v = reinterpret_cast<double*>(gate_smem_raw + warp * gate_smem(E, C, ROUTER));
+    if constexpr (ROUTER) {
+      bool sure;
+      mine = router_exact(a, row, xr, v, lane, zero, slack, sure);
+      if (!sure) {  // for router_finish_kernel
+        if (lane == 0) a.ids[static_cast<size_t>(t) * a.k] = -1;
+        return;
+      }
+    } else {
+      mine = warp_exact(a, row, v, lane);
+    }
   }
 
-  if (c == 0 && a.softmax) {  // statistics for the weights: not taken above
-    m = -INFINITY;
-    for (int e = lane; e < E; e += 32) m = fmaxf(m, load_logit(a, row, e));
-    m = warp_max(m);
-    float z = 0.f;
-    for (int e = lane; e < E; e += 32) {
-      const float x = load_logit(a, row, e);
-      z += x == -INFINITY ? 0.f : expf(x - m);
+  if (!ROUTER && c == 0 && a.softmax) wide_statistics(a, row, lane, m, inv_z);  // for the weights
+  emit(a, row, t, mine, m, inv_z, lane);
+}
+
+// The tokens that gate_kernel left: all exact logits of a token by the warps of
+// a block, the selection by one of them.  (256 experts of H 6144 are 6.3 MB of
+// weights: 90 us at the rate an SM is fed, 650 for one warp.  Eight SMs to a token
+// gave 60 us, but a third of the tokens a second, as most of them wait for the
+// selection.)
+constexpr int kFinishWarps = 16, kFinishThreads = kFinishWarps * 32;
+__global__ void __launch_bounds__(kFinishThreads, 1) router_finish_kernel(const __grid_constant__ GateArgs a) {
+  extern __shared__ __align__(16) unsigned char gate_smem_raw[];
+  __shared__ int todo[kFinishThreads], n;
+  double* v = reinterpret_cast<double*>(gate_smem_raw);
+  double* u = v + a.E;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int t0 = blockIdx.x; t0 < a.T; t0 += gridDim.x * kFinishThreads) {
+    __syncthreads();
+    if (threadIdx.x == 0) n = 0;
+    __syncthreads();
+    const int64_t at = t0 + static_cast<int64_t>(threadIdx.x) * gridDim.x;
+    if (at < a.T && a.ids[at * a.k] < 0) todo[atomicAdd(&n, 1)] = static_cast<int>(at);  // (any order)
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+      const int t = todo[i];
+      const __nv_bfloat16* xr = a.x + static_cast<size_t>(t) * a.H;
+      for (int e = 4 * warp; e < a.E; e += 4 * kFinishWarps) four_logits(a, xr, e, lane, v);
+      __syncthreads();
+      double m, z;
+      router_statistics(a, v, lane, m, z);  // (every warp: no exchange)
+      __syncthreads();
+      router_values(a, v, u, threadIdx.x, kFinishThreads, m, z);
+      __syncthreads();
+      if (warp == 0) {
+        const float* row = static_cast<const float*>(a.logits) + static_cast<size_t>(t) * a.stride;
+        bool sure;
+        const int mine = router_select(a, v, u, lane, false, Slack{}, sure);
+        float m32 = 0.f, inv_z = 0.f;
+        if (a.softmax) wide_statistics(a, row, lane, m32, inv_z);
+        emit(a, row, t, mine, m32, inv_z, lane);
+      }
+      __syncthreads();
     }
-    z = warp_sum(z);
-    inv_z = z == 0.f ? 0.f : 1.f / z;
-  }
-  const float l_sel = lane < a.k ? load_logit(a, row, mine) : 0.f;
-  const float s = lane < a.k ? gate_score(a, l_sel, m, inv_z) : 0.f;
-  float sum = s;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const size_t o = static_cast<size_t>(t) * a.k + lane;
-  if (lane < a.k) {
-    a.ids[o] = mine;
-    a.w[o] = a.renorm ? (sum == 0.f ? 0.f : s / sum * a.alpha) : s * a.alpha;
-  }
-  // a score that is not far inside fp32's range, and no masked expert's (0 in fp64 too)
-  const bool tiny = a.renorm && lane < a.k && s < 7.8886091e-31f && (a.softmax ? l_sel - m : l_sel) > -746.f;
-  if (__any_sync(0xffffffffu, tiny)) {
-    const float share = wide_share(l_sel, m, a.softmax, lane < a.k);
-    if (lane < a.k) a.w[o] = share * a.alpha;
   }
 }
 
@@ -625,30 +1040,37 @@ bool gate_vec(const GateArgs& a, int C) {
          (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
 }
 
-template <typename TIn, int C, bool PACKED>
+template <typename TIn, int C, bool PACKED, bool ROUTER>
 cudaError_t launch_gate_chunk(const GateArgs& a, cudaStream_t stream) {
   constexpr bool kCan = C % (16 / sizeof(TIn)) == 0 && C < 32;  // (more than 512 experts, or odd groups: element loads)
-  void (*fn)(GateArgs) = kCan && gate_vec<TIn>(a, C) ? gate_kernel<TIn, C, kCan, PACKED> : gate_kernel<TIn, C, false, PACKED>;
-  const size_t smem = kGateWarps * gate_smem(a.E, C);
-  static_assert(kGateWarps * gate_smem(MOE_MAX_EXPERTS, C) <= 48 * 1024, "no opt-in shared memory needed");
+  void (*fn)(GateArgs) = kCan && gate_vec<TIn>(a, C) ? gate_kernel<TIn, C, kCan, PACKED, ROUTER>
+                                                     : gate_kernel<TIn, C, false, PACKED, ROUTER>;
+  const size_t smem = kGateWarps * gate_smem(a.E, C, ROUTER);
+  static_assert(ROUTER || kGateWarps * gate_smem(MOE_MAX_EXPERTS, C, false) <= 48 * 1024, "no opt-in shared memory needed");
+  if (ROUTER) {
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn),
+                                           static_cast<int>(kGateWarps * gate_smem(MOE_MAX_EXPERTS, C, true)));
+    if (e != cudaSuccess) return e;
+  }
   return launch_kernel(fn, dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), dim3(kGateWarps * 32), smem,
                        stream, a);
 }
 
-template <typename TIn, bool PACKED>
+template <typename TIn, bool PACKED, bool ROUTER = false>
 cudaError_t launch_gate_typed(const GateArgs& a, cudaStream_t stream) {
-  if (a.chunk <= 1) return launch_gate_chunk<TIn, 1, PACKED>(a, stream);
-  if (a.chunk <= 2) return launch_gate_chunk<TIn, 2, PACKED>(a, stream);
-  if (a.chunk <= 4) return launch_gate_chunk<TIn, 4, PACKED>(a, stream);
-  if (a.chunk <= 8) return launch_gate_chunk<TIn, 8, PACKED>(a, stream);
-  if (a.chunk <= 16) return launch_gate_chunk<TIn, 16, PACKED>(a, stream);
-  return launch_gate_chunk<TIn, 32, PACKED>(a, stream);
+  if (a.chunk <= 1) return launch_gate_chunk<TIn, 1, PACKED, ROUTER>(a, stream);
+  if (a.chunk <= 2) return launch_gate_chunk<TIn, 2, PACKED, ROUTER>(a, stream);
+  if (a.chunk <= 4) return launch_gate_chunk<TIn, 4, PACKED, ROUTER>(a, stream);
+  if (a.chunk <= 8) return launch_gate_chunk<TIn, 8, PACKED, ROUTER>(a, stream);
+  if (a.chunk <= 16) return launch_gate_chunk<TIn, 16, PACKED, ROUTER>(a, stream);
+  return launch_gate_chunk<TIn, 32, PACKED, ROUTER>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gate(const moe_config& cfg, const void* logits, int dtype, int64_t stride, int slices,
-                        int64_t slice_stride, const float* bias, int T, int32_t* ids, float* w, cudaStream_t stream) {
+                        int64_t slice_stride, const float* bias, int T, int32_t* ids, float* w, cudaStream_t stream,
+                        const __nv_bfloat16* x, const float* router_w, int num_sms) {
   GateArgs a;
   a.logits = logits;
   a.stride = stride;
@@ -671,6 +1093,17 @@ cudaError_t launch_gate(const moe_config& cfg, const void* logits, int dtype, in
   a.alpha = cfg.routed_scaling_factor;
   a.ids = ids;
   a.w = w;
+  a.x = x;
+  a.wr = router_w;
+  a.H = cfg.hidden;
+  a.defer = 0;
+  if (x != nullptr) {
+    a.defer = a.chunk == 0 || a.group_shift < 0 || (a.softmax && bias != nullptr);
+    const cudaError_t e = launch_gate_typed<float, false, true>(a, stream);
+    if (e != cudaSuccess || !a.defer) return e;
+    return launch_kernel(router_finish_kernel, dim3(static_cast<unsigned>(std::min(T, num_sms))), dim3(kFinishThreads),
+                         static_cast<size_t>(a.E) * 16, stream, a);
+  }
   if (dtype == MOE_F32) return launch_gate_typed<float, false>(a, stream);
   const bool packed = bias == nullptr;
   if (dtype == MOE_BF16)

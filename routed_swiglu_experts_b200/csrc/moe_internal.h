@@ -145,9 +145,12 @@ cudaError_t launch_int4_ffn_prefill(const moe_config& cfg, const moe_weights& w,
                                     int num_sms, cudaStream_t stream);
 
 // Expert selection from logits (gate.cu): `slices` fp32 partial logits per
-// value are added in ascending order (1: the logits themselves).
+// value are added in ascending order (1: the logits themselves).  x [T, hidden]
+// and router_w [E, hidden], when given, are what the fp32 logits were computed
+// from: decisions those leave open are taken from exact ones.
 cudaError_t launch_gate(const moe_config& cfg, const void* logits, int dtype, int64_t stride, int slices,
-                        int64_t slice_stride, const float* bias, int T, int32_t* ids, float* w, cudaStream_t stream);
+                        int64_t slice_stride, const float* bias, int T, int32_t* ids, float* w, cudaStream_t stream,
+                        const __nv_bfloat16* x = nullptr, const float* router_w = nullptr, int num_sms = 1);
 // Routing choices beyond sigmoid scores over all experts go through launch_gate.
 inline bool plain_routing(const moe_config& cfg) { return cfg.score == MOE_SCORE_SIGMOID && cfg.num_groups <= 1; }
 

@@ -8,6 +8,7 @@
 // routed_scaling_factor.  "bridge.models.beam.modeling_beam"
 // beam_router_gating_linear: logits = inp @ weight.T with fp32 operands.
 #include "moe_internal.h"
+#include "router_dot.cuh"
 
 namespace moe {
 
@@ -72,60 +73,23 @@ __host__ __device__ inline size_t topk_smem_per_warp(int E) {
   return (static_cast<size_t>(E) * (8 + 4 + 4 + 4 + 4) + MOE_MAX_TOP_K * 4 + 15) / 16 * 16;
 }
 
-// fp64 biased score of expert e for one token: exact bf16 x fp32 products,
-// fp64 sum split over the warp's lanes.  Two experts per pass.
+// fp64 biased scores of two experts for one token.
 __device__ __forceinline__ void exact_biased_pair(const __nv_bfloat16* __restrict__ xr,
                                                   const float* __restrict__ wr, const float* __restrict__ bias,
                                                   int H, int lane, int e0, int e1, double& b0, double& b1) {
-  const float* w0r = wr + static_cast<size_t>(e0) * H;
-  const float* w1r = wr + static_cast<size_t>(e1) * H;
-  double a0 = 0.0, a1 = 0.0;
-#pragma unroll 4
-  for (int h = lane * 8; h < H; h += 256) {
-    const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + h));
-    const float4 p0 = __ldg(reinterpret_cast<const float4*>(w0r + h));
-    const float4 p1 = __ldg(reinterpret_cast<const float4*>(w0r + h + 4));
-    const float4 q0 = __ldg(reinterpret_cast<const float4*>(w1r + h));
-    const float4 q1 = __ldg(reinterpret_cast<const float4*>(w1r + h + 4));
-    const double xv8[8] = {bf16lo(xv.x), bf16hi(xv.x), bf16lo(xv.y), bf16hi(xv.y),
-                           bf16lo(xv.z), bf16hi(xv.z), bf16lo(xv.w), bf16hi(xv.w)};
-    const float pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-    const float qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a0 = fma(xv8[j], static_cast<double>(pw[j]), a0);
-      a1 = fma(xv8[j], static_cast<double>(qw[j]), a1);
-    }
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    a0 += __shfl_xor_sync(0xffffffffu, a0, off);
-    a1 += __shfl_xor_sync(0xffffffffu, a1, off);
-  }
-  b0 = 1.0 / (1.0 + exp(-a0)) + (bias != nullptr ? static_cast<double>(bias[e0]) : 0.0);
-  b1 = 1.0 / (1.0 + exp(-a1)) + (bias != nullptr ? static_cast<double>(bias[e1]) : 0.0);
+  double l[2];
+  exact_dots<2>(xr, {wr + static_cast<size_t>(e0) * H, wr + static_cast<size_t>(e1) * H}, H, lane, l);
+  b0 = 1.0 / (1.0 + exp(-l[0])) + (bias != nullptr ? static_cast<double>(bias[e0]) : 0.0);
+  b1 = 1.0 / (1.0 + exp(-l[1])) + (bias != nullptr ? static_cast<double>(bias[e1]) : 0.0);
 }
 
 // Single-expert form of exact_biased_pair (same per-lane summation order).
 __device__ __forceinline__ double exact_biased_one(const __nv_bfloat16* __restrict__ xr,
                                                    const float* __restrict__ wr, const float* __restrict__ bias,
                                                    int H, int lane, int e0) {
-  const float* w0r = wr + static_cast<size_t>(e0) * H;
-  double a0 = 0.0;
-#pragma unroll 4
-  for (int h = lane * 8; h < H; h += 256) {
-    const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr + h));
-    const float4 p0 = __ldg(reinterpret_cast<const float4*>(w0r + h));
-    const float4 p1 = __ldg(reinterpret_cast<const float4*>(w0r + h + 4));
-    const double xv8[8] = {bf16lo(xv.x), bf16hi(xv.x), bf16lo(xv.y), bf16hi(xv.y),
-                           bf16lo(xv.z), bf16hi(xv.z), bf16lo(xv.w), bf16hi(xv.w)};
-    const float pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a0 = fma(xv8[j], static_cast<double>(pw[j]), a0);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) a0 += __shfl_xor_sync(0xffffffffu, a0, off);
-  return 1.0 / (1.0 + exp(-a0)) + (bias != nullptr ? static_cast<double>(bias[e0]) : 0.0);
+  double l[1];
+  exact_dots<1>(xr, {wr + static_cast<size_t>(e0) * H}, H, lane, l);
+  return 1.0 / (1.0 + exp(-l[0])) + (bias != nullptr ? static_cast<double>(bias[e0]) : 0.0);
 }
 
 // A warp's scratch for selecting one token's experts (see
@@ -475,9 +439,10 @@ cudaError_t launch_router(const moe_config& cfg, const moe_weights& w, const voi
   if (err_c != cudaSuccess) return err_c;
   err_c = launch_router_gemm(x, T, H, w_split, E, p.ks, part, err, num_sms, stream);
   if (err_c != cudaSuccess) return err_c;
-  if (!plain_routing(cfg))  // softmax scores or expert groups: select from the fp32 logits
-    return launch_gate(cfg, part, MOE_F32, E, p.ks, static_cast<int64_t>(T) * E, w.correction_bias, T, ids, wts, stream);
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+  if (!plain_routing(cfg))  // softmax scores or expert groups
+    return launch_gate(cfg, part, MOE_F32, E, p.ks, static_cast<int64_t>(T) * E, w.correction_bias, T, ids, wts, stream,
+                       xb, w.router_w, num_sms);
   if (T < num_sms * kTopkWarps) {
     // few tokens: one token per block, so 256 threads read its partial sums
     err_c = ensure_smem_attr(reinterpret_cast<const void*>(router_topk_coop_kernel),
