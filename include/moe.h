@@ -99,6 +99,9 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
  * workspace that moe_fp8_gemm needs. */
 #define MOE_WS_HEADER_BYTES 256
 
+/* In moe_config.renormalize, beside its 0 or 1: the routing fields are set. */
+#define MOE_ROUTING_FIELDS 2
+
 /* Geometry and numerics of one MoE layer. */
 typedef struct moe_config {
   int32_t hidden;                /* H  (multiple of 8) */
@@ -114,9 +117,16 @@ typedef struct moe_config {
   float routed_scaling_factor;   /* alpha: multiplies the routed weights; the
                                     shared expert is added unscaled */
   int32_t renormalize;           /* 1: divide the k unbiased scores by their
-                                    sum before alpha; 0: no renormalisation */
+                                    sum before alpha; 0: no renormalisation;
+                                    + MOE_ROUTING_FIELDS: the fields behind
+                                    expert_format are set */
   int32_t expert_format;         /* moe_weight_format */
-  /* Routing; all zero: sigmoid scores, no groups. */
+  /* Routing; all zero: sigmoid scores, no groups.  Not read (and taken for
+   * zero) unless renormalize holds MOE_ROUTING_FIELDS, so that callers built
+   * against the header that ended the struct here, or that fill it field by
+   * field, keep their routing.  moe_gate_topk alone, which those callers do
+   * not know, looks at them without the flag, and refuses values other than
+   * zero (MOE_ERR_INVALID_ARG). */
   int32_t score;                 /* moe_score_func */
   int32_t num_groups;            /* 0 or 1: no groups; else the experts form
                                     num_groups groups of E / num_groups

@@ -27,6 +27,7 @@ MOE_W_BF16 = 0
 MOE_W_INT4_G128 = 1
 MOE_W_NVFP4 = 2
 MOE_W_FP8_B128 = 4
+MOE_ROUTING_FIELDS = 2
 MOE_SCORE_SIGMOID = 0
 MOE_SCORE_SOFTMAX = 1
 MOE_GROUP_SUM2 = 0
@@ -76,6 +77,14 @@ class moe_config(ctypes.Structure):
         ("top_groups", ctypes.c_int32),
         ("group_score", ctypes.c_int32),
     ]
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        self.renormalize = self.renormalize
+
+    def __setattr__(self, name, value):
+        # this struct always has the routing fields
+        super().__setattr__(name, value | MOE_ROUTING_FIELDS if name == "renormalize" else value)
 
 
 class moe_weights(ctypes.Structure):

@@ -268,27 +268,9 @@ WsLayout ws_layout(const moe_config& cfg, int Tmax) {
   return L;
 }
 
-}  // namespace moe
+namespace {
 
-using namespace moe;
-
-extern "C" {
-
-const char* moe_status_string(moe_status s) {
-  switch (s) {
-    case MOE_OK: return "MOE_OK";
-    case MOE_ERR_INVALID_ARG: return "MOE_ERR_INVALID_ARG";
-    case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED";
-    case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
-    case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
-    case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT";
-  }
-  return "MOE_ERR_UNKNOWN";
-}
-
-moe_status moe_config_validate(const moe_config* cfg) {
-  if (cfg == nullptr) return MOE_ERR_INVALID_ARG;
-  const moe_config& c = *cfg;
+moe_status check_config(const moe_config& c) {
   if (c.hidden < 8 || c.hidden % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (c.expert_inter < 8 || c.expert_inter % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (c.shared_inter < 0 || c.shared_inter % 8 != 0) return MOE_ERR_INVALID_ARG;
@@ -323,11 +305,48 @@ moe_status moe_config_validate(const moe_config* cfg) {
   return MOE_OK;
 }
 
+}  // namespace
+
+moe_status take_config(const moe_config* cfg, moe_config& c) {
+  if (cfg == nullptr) return MOE_ERR_INVALID_ARG;
+  std::memset(&c, 0, sizeof(c));
+  std::memcpy(&c, cfg, offsetof(moe_config, score));
+  if ((c.renormalize & ~1) == MOE_ROUTING_FIELDS) {  // (2 or 3)
+    std::memcpy(&c, cfg, sizeof(c));
+    c.renormalize &= ~MOE_ROUTING_FIELDS;
+  }
+  return check_config(c);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+const char* moe_status_string(moe_status s) {
+  switch (s) {
+    case MOE_OK: return "MOE_OK";
+    case MOE_ERR_INVALID_ARG: return "MOE_ERR_INVALID_ARG";
+    case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED";
+    case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
+    case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
+    case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT";
+  }
+  return "MOE_ERR_UNKNOWN";
+}
+
+moe_status moe_config_validate(const moe_config* cfg) {
+  moe_config c;
+  return take_config(cfg, c);
+}
+
 moe_status moe_workspace_size(const moe_config* cfg, int32_t max_tokens, size_t* bytes) {
-  MOE_TRY(moe_config_validate(cfg));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_tokens(*cfg, max_tokens));
-  *bytes = ws_layout(*cfg, max_tokens).total;
+  MOE_TRY(check_tokens(c, max_tokens));
+  *bytes = ws_layout(c, max_tokens).total;
   return MOE_OK;
 }
 
@@ -339,32 +358,34 @@ moe_status moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
 
 moe_status moe_router_topk(const moe_config* cfg, const moe_weights* w, const void* x, int32_t T, int32_t* topk_ids,
                            float* topk_w, void* ws, size_t ws_bytes, moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   MOE_TRY(check_router_weights(w));
   if (x == nullptr || topk_ids == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(topk_w)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
-  return from_cuda(launch_router(*cfg, *w, x, T, topk_ids, topk_w, at<float>(ws, L.logits), at<void>(ws, L.w_split),
+  const WsLayout L = ws_layout(c, T);
+  return from_cuda(launch_router(c, *w, x, T, topk_ids, topk_w, at<float>(ws, L.logits), at<void>(ws, L.w_split),
                                  err_word(ws), num_sms_current_device(), stream));
 }
 
 moe_status moe_permute(const moe_config* cfg, const int32_t* topk_ids, const float* topk_w, const void* x, int32_t T,
                        int32_t* expert_offsets, int32_t* row_of, int32_t* src, float* w_perm, void* x_perm, void* ws,
                        size_t ws_bytes, moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   const void* ptrs[] = {topk_ids, topk_w, expert_offsets, row_of, src, w_perm};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARG;
   // x_perm == NULL: maps and weights only (x is then not read)
   if (x_perm != nullptr && (x == nullptr || !aligned16(x) || !aligned16(x_perm))) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
-  return from_cuda(launch_permute(*cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm,
+  const WsLayout L = ws_layout(c, T);
+  return from_cuda(launch_permute(c, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm,
                                   at<int32_t>(ws, L.block_base), at<int32_t>(ws, L.local_rank), perm_ticket(ws),
                                   stream));
 }
@@ -373,143 +394,152 @@ moe_status moe_grouped_swiglu_ffn(const moe_config* cfg, const moe_weights* w, c
                                   const int32_t* expert_offsets, const float* w_perm, int32_t T, void* y_perm,
                                   const void* x_shared, void* shared_out, void* ws, size_t ws_bytes,
                                   moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
-  MOE_TRY(check_expert_weights(*cfg, w));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
+  MOE_TRY(check_expert_weights(c, w));
   if (x_perm == nullptr || expert_offsets == nullptr || y_perm == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(expert_offsets) || !aligned16(y_perm)) return MOE_ERR_INVALID_ARG;
   if (w_perm != nullptr && !aligned16(w_perm)) return MOE_ERR_INVALID_ARG;
   if (x_shared != nullptr) {
-    if (cfg->shared_inter == 0 || shared_out == nullptr) return MOE_ERR_INVALID_ARG;
+    if (c.shared_inter == 0 || shared_out == nullptr) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x_shared) || !aligned16(shared_out)) return MOE_ERR_INVALID_ARG;
-    MOE_TRY(check_shared_weights(*cfg, w));
+    MOE_TRY(check_shared_weights(c, w));
   }
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
-  return run_ffn(*cfg, *w, x_perm, nullptr, expert_offsets, w_perm, T, y_perm, x_shared, shared_out, ws, L, stream,
-                 cfg->num_experts);
+  const WsLayout L = ws_layout(c, T);
+  return run_ffn(c, *w, x_perm, nullptr, expert_offsets, w_perm, T, y_perm, x_shared, shared_out, ws, L, stream,
+                 c.num_experts);
 }
 
 moe_status moe_grouped_swiglu_ffn_gather(const moe_config* cfg, const moe_weights* w, const void* x, int32_t T,
                                          const int32_t* src, const int32_t* expert_offsets, const float* w_perm,
                                          void* y_perm, void* shared_out, void* ws, size_t ws_bytes,
                                          moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
-  MOE_TRY(check_expert_weights(*cfg, w));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
+  MOE_TRY(check_expert_weights(c, w));
   if (x == nullptr || src == nullptr || expert_offsets == nullptr || y_perm == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(src) || !aligned16(expert_offsets) || !aligned16(y_perm))
     return MOE_ERR_INVALID_ARG;
   if (w_perm != nullptr && !aligned16(w_perm)) return MOE_ERR_INVALID_ARG;
   if (shared_out != nullptr) {
-    if (cfg->shared_inter == 0 || !aligned16(shared_out)) return MOE_ERR_INVALID_ARG;
-    MOE_TRY(check_shared_weights(*cfg, w));
+    if (c.shared_inter == 0 || !aligned16(shared_out)) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_shared_weights(c, w));
   }
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
-  return run_ffn(*cfg, *w, x, src, expert_offsets, w_perm, T, y_perm, shared_out != nullptr ? x : nullptr, shared_out,
-                 ws, L, stream, cfg->num_experts);
+  const WsLayout L = ws_layout(c, T);
+  return run_ffn(c, *w, x, src, expert_offsets, w_perm, T, y_perm, shared_out != nullptr ? x : nullptr, shared_out,
+                 ws, L, stream, c.num_experts);
 }
 
 moe_status moe_combine(const moe_config* cfg, const void* y_perm, const int32_t* row_of, const float* topk_w,
                        const void* shared_out, int32_t T, void* out, moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   if (y_perm == nullptr || row_of == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned16(y_perm) || !aligned16(row_of) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
   if (topk_w != nullptr && !aligned16(topk_w)) return MOE_ERR_INVALID_ARG;
   if (shared_out != nullptr && !aligned16(shared_out)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  return from_cuda(launch_combine(*cfg, y_perm, row_of, topk_w, shared_out, T, out, nullptr, 0, stream));
+  return from_cuda(launch_combine(c, y_perm, row_of, topk_w, shared_out, T, out, nullptr, 0, stream));
 }
 
 moe_status moe_forward(const moe_config* cfg, const moe_weights* w, const void* x, int32_t T, void* out,
                        int32_t* topk_ids_opt, float* topk_w_opt, void* ws, size_t ws_bytes, moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   MOE_TRY(check_router_weights(w));
-  MOE_TRY(check_expert_weights(*cfg, w));
-  MOE_TRY(check_shared_weights(*cfg, w));
+  MOE_TRY(check_expert_weights(c, w));
+  MOE_TRY(check_shared_weights(c, w));
   if (x == nullptr || out == nullptr || !aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
   if ((topk_ids_opt != nullptr && !aligned16(topk_ids_opt)) || (topk_w_opt != nullptr && !aligned16(topk_w_opt)))
     return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
+  const WsLayout L = ws_layout(c, T);
   int32_t* ids = topk_ids_opt != nullptr ? topk_ids_opt : at<int32_t>(ws, L.ids);
   float* wts = topk_w_opt != nullptr ? topk_w_opt : at<float>(ws, L.wts);
-  MOE_CUDA_TRY(launch_router(*cfg, *w, x, T, ids, wts, at<float>(ws, L.logits), at<void>(ws, L.w_split),
+  MOE_CUDA_TRY(launch_router(c, *w, x, T, ids, wts, at<float>(ws, L.logits), at<void>(ws, L.w_split),
                              err_word(ws), num_sms_current_device(), stream));
   int32_t* offsets = at<int32_t>(ws, L.offsets);
   int32_t* row_of = at<int32_t>(ws, L.row_of);
   float* w_perm = at<float>(ws, L.w_perm);
   int32_t* src = at<int32_t>(ws, L.src);
-  const Rows rows = routed_rows(*cfg, ws, L, x, src);
-  MOE_CUDA_TRY(launch_permute(*cfg, ids, wts, x, T, offsets, row_of, src, w_perm, rows.x_perm,
+  const Rows rows = routed_rows(c, ws, L, x, src);
+  MOE_CUDA_TRY(launch_permute(c, ids, wts, x, T, offsets, row_of, src, w_perm, rows.x_perm,
                               at<int32_t>(ws, L.block_base), at<int32_t>(ws, L.local_rank), perm_ticket(ws),
                               stream));
   void* y_perm = at<void>(ws, L.y_perm);
-  const bool shared = cfg->shared_inter > 0;
+  const bool shared = c.shared_inter > 0;
   void* shared_out = shared ? at<void>(ws, L.shared_out) : nullptr;
-  MOE_TRY(run_ffn(*cfg, *w, rows.x_rows, rows.gather_src, offsets, w_perm, T, y_perm, shared ? x : nullptr,
-                  shared_out, ws, L, stream, cfg->num_experts));
-  return from_cuda(launch_combine(*cfg, y_perm, row_of, nullptr, shared_out, T, out, nullptr, 0, stream));
+  MOE_TRY(run_ffn(c, *w, rows.x_rows, rows.gather_src, offsets, w_perm, T, y_perm, shared ? x : nullptr,
+                  shared_out, ws, L, stream, c.num_experts));
+  return from_cuda(launch_combine(c, y_perm, row_of, nullptr, shared_out, T, out, nullptr, 0, stream));
 }
 
 moe_status moe_forward_ep(const moe_config* cfg, const moe_weights* w, int32_t expert_begin, int32_t expert_end,
                           const void* x, int32_t T, void* out_partial, int32_t* topk_ids_opt, float* topk_w_opt,
                           void* ws, size_t ws_bytes, moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   MOE_TRY(check_router_weights(w));
-  if (expert_begin < 0 || expert_end < expert_begin || expert_end > cfg->num_experts) return MOE_ERR_INVALID_ARG;
+  if (expert_begin < 0 || expert_end < expert_begin || expert_end > c.num_experts) return MOE_ERR_INVALID_ARG;
   const int El = expert_end - expert_begin;
-  if (El > 0) MOE_TRY(check_expert_weights(*cfg, w));
-  MOE_TRY(check_shared_weights(*cfg, w));
+  if (El > 0) MOE_TRY(check_expert_weights(c, w));
+  MOE_TRY(check_shared_weights(c, w));
   if (x == nullptr || out_partial == nullptr || !aligned16(x) || !aligned16(out_partial)) return MOE_ERR_INVALID_ARG;
   if ((topk_ids_opt != nullptr && !aligned16(topk_ids_opt)) || (topk_w_opt != nullptr && !aligned16(topk_w_opt)))
     return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(*cfg, T, ws, ws_bytes));
+  MOE_TRY(check_ws(c, T, ws, ws_bytes));
   if (T == 0) return MOE_OK;
-  const WsLayout L = ws_layout(*cfg, T);
+  const WsLayout L = ws_layout(c, T);
   int32_t* ids = topk_ids_opt != nullptr ? topk_ids_opt : at<int32_t>(ws, L.ids);
   float* wts = topk_w_opt != nullptr ? topk_w_opt : at<float>(ws, L.wts);
   // the router ranks every expert ([glm5next]: it is given the full count)
-  MOE_CUDA_TRY(launch_router(*cfg, *w, x, T, ids, wts, at<float>(ws, L.logits), at<void>(ws, L.w_split),
+  MOE_CUDA_TRY(launch_router(c, *w, x, T, ids, wts, at<float>(ws, L.logits), at<void>(ws, L.w_split),
                              err_word(ws), num_sms_current_device(), stream));
   int32_t* offsets = at<int32_t>(ws, L.offsets);
   int32_t* row_of = at<int32_t>(ws, L.row_of);
   float* w_perm = at<float>(ws, L.w_perm);
   int32_t* src = at<int32_t>(ws, L.src);
-  const Rows rows = routed_rows(*cfg, ws, L, x, src);
-  MOE_CUDA_TRY(launch_permute(*cfg, ids, wts, x, T, offsets, row_of, src, w_perm, rows.x_perm,
+  const Rows rows = routed_rows(c, ws, L, x, src);
+  MOE_CUDA_TRY(launch_permute(c, ids, wts, x, T, offsets, row_of, src, w_perm, rows.x_perm,
                               at<int32_t>(ws, L.block_base), at<int32_t>(ws, L.local_rank), perm_ticket(ws), stream,
                               expert_begin, expert_end));
   void* y_perm = at<void>(ws, L.y_perm);
-  const bool shared = cfg->shared_inter > 0;
+  const bool shared = c.shared_inter > 0;
   void* shared_out = shared ? at<void>(ws, L.shared_out) : nullptr;
-  moe_config local = *cfg;
+  moe_config local = c;
   local.num_experts = El;
   MOE_TRY(run_ffn(local, *w, rows.x_rows, rows.gather_src, offsets + expert_begin, w_perm, T, y_perm,
-                  shared ? x : nullptr, shared_out, ws, L, stream, cfg->num_experts));
-  return from_cuda(launch_combine(*cfg, y_perm, row_of, nullptr, shared_out, T, out_partial, offsets + expert_begin,
+                  shared ? x : nullptr, shared_out, ws, L, stream, c.num_experts));
+  return from_cuda(launch_combine(c, y_perm, row_of, nullptr, shared_out, T, out_partial, offsets + expert_begin,
                                   El, stream));
 }
 
 moe_status moe_gate_topk(const moe_config* cfg, const void* logits, int32_t logits_type, int64_t row_stride,
                          const float* correction_bias, int32_t T, int32_t* topk_ids, float* topk_w,
                          moe_stream_t stream) {
-  MOE_TRY(moe_config_validate(cfg));
-  MOE_TRY(check_tokens(*cfg, T));
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
   if (logits_type != MOE_F32 && logits_type != MOE_BF16 && logits_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  // (routing that was set but not announced would be left out silently)
+  if (!(cfg->renormalize & MOE_ROUTING_FIELDS) && (cfg->score | cfg->num_groups | cfg->top_groups | cfg->group_score) != 0)
+    return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (row_stride < cfg->num_experts) return MOE_ERR_INVALID_ARG;
+  if (row_stride < c.num_experts) return MOE_ERR_INVALID_ARG;
   if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == MOE_F32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
   if (!aligned4(topk_ids) || !aligned4(topk_w) || !aligned4(correction_bias)) return MOE_ERR_INVALID_ARG;
-  return from_cuda(launch_gate(*cfg, logits, logits_type, row_stride, 1, 0, correction_bias, T, topk_ids, topk_w,
+  return from_cuda(launch_gate(c, logits, logits_type, row_stride, 1, 0, correction_bias, T, topk_ids, topk_w,
                                stream));
 }
 

@@ -10,6 +10,11 @@
 
 namespace moe {
 
+// A caller's configuration, validated: c is a copy with the routing fields zero
+// unless the caller's renormalize announces them (its struct may end before
+// them), and renormalize 0 or 1.
+moe_status take_config(const moe_config* cfg, moe_config& c);
+
 // Opt a kernel into `bytes` of dynamic shared memory on the current device
 // (cached per device and kernel).
 cudaError_t ensure_smem_attr(const void* func, int bytes);

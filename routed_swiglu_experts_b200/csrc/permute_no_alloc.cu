@@ -116,10 +116,11 @@ extern "C" MOE_API moe_status moe_permute_no_alloc(const moe_config* cfg, const 
                                                    int32_t* expert_offsets, int32_t* row_of, int32_t* src,
                                                    float* w_perm, void* x_perm, moe_stream_t stream) {
   using namespace moe;
-  const moe_status st = moe_config_validate(cfg);
+  moe_config c;
+  const moe_status st = take_config(cfg, c);
   if (st != MOE_OK) return st;
   if (T < 0) return MOE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(T) * cfg->top_k > MOE_NO_ALLOC_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(T) * c.top_k > MOE_NO_ALLOC_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
   const void* ptrs[] = {topk_ids, topk_w, x, expert_offsets, row_of, src, w_perm, x_perm};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARG;
@@ -129,7 +130,7 @@ extern "C" MOE_API moe_status moe_permute_no_alloc(const moe_config* cfg, const 
   int32_t* ticket = scratch;
   int32_t* block_base = scratch + kNoAllocTicketInts;
   int32_t* local_rank = block_base + kNoAllocBlockBaseInts;
-  const cudaError_t e = launch_permute(*cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm,
+  const cudaError_t e = launch_permute(c, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm,
                                        block_base, local_rank, ticket, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
