@@ -639,25 +639,8 @@ bool encode_x_rows(CUtensorMap* m, const void* base, int tokens, int K) {
 // sit in one GPC, so this can be below half the SM count); 0 if unknown.
 template <Kind KIND, bool GATHER>
 int resident_pairs() {
-  static int cached[64];
-  static bool known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!known[dev]) {
-    cudaLaunchConfig_t lc;
-    memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(2);
-    lc.blockDim = dim3(THREADS);
-    lc.dynamicSmemBytes = kSmem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, ffn_pair_kernel<KIND, GATHER>, &lc) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    cached[dev] = n;
-    known[dev] = true;
-  }
-  return cached[dev];
+  static DeviceCache cache;
+  return resident_clusters_of(cache, ffn_pair_kernel<KIND, GATHER>, 2, THREADS, kSmem);
 }
 
 template <Kind KIND, bool GATHER>

@@ -767,25 +767,8 @@ bool encode_tokens16(CUtensorMap* m, const void* base, int rows, int K) {
 
 template <Kind KIND, bool FP4>
 int resident_pairs_int4() {
-  static int cached[64];
-  static bool known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!known[dev]) {
-    cudaLaunchConfig_t lc;
-    memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(2);
-    lc.blockDim = dim3(THREADS);
-    lc.dynamicSmemBytes = kSmem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, ffn_int4_pair_kernel<KIND, FP4>, &lc) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    cached[dev] = n;
-    known[dev] = true;
-  }
-  return cached[dev];
+  static DeviceCache cache;
+  return resident_clusters_of(cache, ffn_int4_pair_kernel<KIND, FP4>, 2, THREADS, kSmem);
 }
 
 template <Kind KIND, bool FP4>

@@ -792,25 +792,8 @@ bool encode_x(CUtensorMap (&m)[kTokBoxes], const void* base, int rows, int K) {
 // Clusters that can be resident at once on the current device; 0 if unknown.
 template <Kind KIND, int SPLIT>
 int resident_clusters() {
-  static int cached[64];
-  static bool known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!known[dev]) {
-    cudaLaunchConfig_t lc;
-    memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(2 * SPLIT);
-    lc.blockDim = dim3(THREADS);
-    lc.dynamicSmemBytes = kSmem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_few_kernel<KIND, SPLIT>, &lc) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    cached[dev] = n;
-    known[dev] = true;
-  }
-  return cached[dev];
+  static DeviceCache cache;
+  return resident_clusters_of(cache, fp8_few_kernel<KIND, SPLIT>, 2 * SPLIT, THREADS, kSmem);
 }
 
 template <Kind KIND, int SPLIT>

@@ -712,25 +712,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // CTA pairs that can be resident at once on the current device; 0 if unknown.
 template <Kind KIND>
 int resident_pairs() {
-  static int cached[64];
-  static bool known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!known[dev]) {
-    cudaLaunchConfig_t lc;
-    memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(2);
-    lc.blockDim = dim3(THREADS);
-    lc.dynamicSmemBytes = kSmem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<KIND>, &lc) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    cached[dev] = n;
-    known[dev] = true;
-  }
-  return cached[dev];
+  static DeviceCache cache;
+  return resident_clusters_of(cache, fp8_wide_kernel<KIND>, 2, THREADS, kSmem);
 }
 
 template <Kind KIND>

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <utility>
 
+#include "device_cache.h"
 #include "moe_common.cuh"
 
 namespace moe {
@@ -30,6 +31,25 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   return cudaLaunchKernelEx(&lc, kernel, std::forward<Args>(args)...);
+}
+
+// Clusters of `kernel` (`ctas` blocks of `threads` threads with `smem` bytes)
+// that can be resident at once on the current device; 0 if unknown.  A cluster
+// must sit in one GPC, so this can be below the SM count's share.
+template <typename... KArgs>
+int resident_clusters_of(DeviceCache& cache, void (*kernel)(KArgs...), int ctas, int threads, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return cache.get(dev, [&] {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(ctas));
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = smem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc) == cudaSuccess) return n;
+    cudaGetLastError();
+    return -1;
+  });
 }
 
 // Encode a tiled TMA descriptor (strides in bytes for dims 1..rank-1).
