@@ -277,10 +277,17 @@ class _Torch:
         self.u8 = (torch.uint8,)
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.outs = (torch.bfloat16, torch.float32)
-        # without a GPU no tensor is on the current device (the CPU's number is -1)
-        self.device = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2
-        # the handle alone: building a torch.cuda.Stream around it takes 3 us
-        self.stream = torch._C._cuda_getCurrentRawStream
+        # the current device's number, and a device's current stream as its handle alone:
+        # building a torch.cuda.Stream around it takes 3 us, so the private look-ups are
+        # used where the build has them
+        device, stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+        if not torch.cuda.is_available():
+            # no tensor is on the current device (the CPU's number is -1); streams raise torch's error
+            self.device, self.stream = lambda: -2, lambda dev: torch.cuda.current_stream().cuda_stream
+        elif device is None or stream is None:
+            self.device, self.stream = torch.cuda.current_device, lambda dev: torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.device, self.stream = device, stream
 
 
 _torch = None
