@@ -414,7 +414,8 @@ MOE_API moe_status moe_fp8_quantize(const void* x, int32_t x_type, int64_t row_s
 
 /* Weights to FP8 E4M3 with a scale per 128 x 128 block (the edge blocks of N
  * and K smaller), scales and codes as above:
- *   w      [groups, N, K] of w_type, contiguous, 16-byte aligned; K a multiple of 16
+ *   w      [groups, N, K] of w_type, contiguous, 16-byte aligned; K a multiple of 16;
+ *          N and K at most 2^30
  *   q      E4M3 [groups, N, K] out
  *   scale  fp32 [groups, ceil(N / 128), ceil(K / 128)] out */
 MOE_API moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_t groups, int32_t N, int32_t K,
@@ -433,7 +434,8 @@ MOE_API moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_
  *   w               E4M3 [groups, N, K]   w_scale  fp32 [groups, ceil(N/128), ceil(K/128)]
  *   row_scale       fp32 [rows] (c) or NULL (1)
  *   out             MOE_BF16 or MOE_F32 [rows, N]
- * N a multiple of 8, K of 16; a, w and out 16-byte aligned.  The scales need
+ * N a multiple of 8, K of 16, both at most 2^30, (rows / 64 + groups) * N / 256
+ * below 2^31; a, w and out 16-byte aligned.  The scales need
  * not be powers of two.  ws: an initialised workspace of any size from
  * MOE_WS_HEADER_BYTES up (it holds the tile queue and the error word). */
 MOE_API moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const int32_t* expert_offsets,

@@ -63,6 +63,8 @@ bool is_fp8(const moe_config& cfg) { return cfg.expert_format == MOE_W_FP8_B128;
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // rows of moe_fp8_quantize and moe_fp8_gemm: the routed rows of kMaxTokens tokens
 constexpr int64_t kMaxRows = kMaxTokens * MOE_MAX_TOP_K;
+// sides of FP8 weights: the kernels round them up and add tile offsets in 32 bits
+constexpr int32_t kMaxSide = 1 << 30;
 
 moe_status check_expert_weights(const moe_config& cfg, const moe_weights* w) {
   if (w == nullptr) return MOE_ERR_INVALID_ARG;
@@ -560,6 +562,7 @@ moe_status moe_fp8_quantize_weight(const void* w, int32_t w_type, int32_t groups
                                    float* scale, moe_stream_t stream) {
   if (w_type != MOE_F32 && w_type != MOE_BF16 && w_type != MOE_F16) return MOE_ERR_INVALID_ARG;
   if (groups < 0 || N < 1 || K < 16 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (N > kMaxSide || K > kMaxSide) return MOE_ERR_UNSUPPORTED;
   const int64_t per = (static_cast<int64_t>(N) + 127) / 128 * ((static_cast<int64_t>(K) + 127) / 128);
   if (per >= (int64_t(1) << 31) || per * groups >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;  // one block each
   if (groups == 0) return MOE_OK;
@@ -576,6 +579,9 @@ moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const
   if (rows < 0 || groups < 1 || N < 8 || N % 8 != 0 || K < 16 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
   if (groups > 1 && expert_offsets == nullptr) return MOE_ERR_INVALID_ARG;
   if (groups > MOE_MAX_EXPERTS || static_cast<int64_t>(rows) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (N > kMaxSide || K > kMaxSide) return MOE_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(rows) / 64 + groups) * ((N + 255) / 256) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;  // tiles of 64 rows x 256 columns are counted in 32 bits
   if (rows == 0) return MOE_OK;
   if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
     return MOE_ERR_INVALID_ARG;
