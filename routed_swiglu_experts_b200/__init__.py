@@ -57,6 +57,9 @@ class MoELayer:
         st = moe_config_validate(self.cfg)
         if st != MOE_OK:
             raise MoEError(st, "moe_config_validate")
+        if fmt == MOE_W_FP8_B128:
+            _abi.check_fp8_weights("MoELayer", hidden, expert_inter, num_experts, w_gate_up=w_gate_up, w_down=w_down,
+                                   s_gate_up=s_gate_up, s_down=s_down)
         self.tensors = dict(router_w=router_w, correction_bias=correction_bias, w_gate_up=w_gate_up,
                             s_gate_up=s_gate_up, w_down=w_down, s_down=s_down,
                             shared_w_gate_up=shared_w_gate_up, shared_w_down=shared_w_down,

@@ -202,6 +202,24 @@ def weight_format(w_gate_up, g_gate_up=None) -> int:
     return MOE_W_INT4_G128 if str(w_gate_up.dtype) == "torch.uint8" else MOE_W_BF16
 
 
+def check_fp8_weights(where, hidden, inter, experts, *, w_gate_up, w_down, s_gate_up, s_down):
+    """The tensors of `experts` FP8 experts: E4M3 codes and fp32 block scales,
+    contiguous, of the sizes that the kernels read (they get pointers alone)."""
+    import torch
+    codes, H, I = (torch.float8_e4m3fn, torch.uint8), hidden, inter
+    for name, t, dtypes, n in (("w_gate_up", w_gate_up, codes, 2 * I * H), ("w_down", w_down, codes, H * I),
+                               ("s_gate_up", s_gate_up, (torch.float32,), 2 * I // 128 * (H // 128)),
+                               ("s_down", s_down, (torch.float32,), H // 128 * (I // 128))):
+        if t is None:
+            raise ValueError(f"{where}: {name} is missing")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if t.numel() != experts * n:
+            raise ValueError(f"{where}: {name} has {t.numel()} elements, expected {experts * n}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+
+
 # ------------------------------------------------------- C entry points ----
 
 def moe_config_validate(cfg: moe_config) -> int:

@@ -100,6 +100,9 @@ class ExpertParallelLayer:
         st = _abi.moe_config_validate(self.cfg)
         if st != _abi.MOE_OK:
             raise _abi.MoEError(st, "moe_config_validate")
+        if fmt == _abi.MOE_W_FP8_B128:
+            _abi.check_fp8_weights("ExpertParallelLayer", hidden, expert_inter, self.expert_range[1] - self.expert_range[0],
+                                   **{n: loc[n] for n in ("w_gate_up", "w_down", "s_gate_up", "s_down")})
         empty = self.expert_range[1] == self.expert_range[0]
         self.tensors = dict(router_w=router_w, correction_bias=correction_bias,
                             w_gate_up=None if empty else loc["w_gate_up"], w_down=None if empty else loc["w_down"],
