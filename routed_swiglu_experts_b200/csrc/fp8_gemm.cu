@@ -550,8 +550,8 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < TOK; i += 32)
             if (i + lane < ti.ntok)
-              cp_async4(smem_u32(&c.sx[slot][k][i + scale_at(lane)]), row + i + lane, true);
-          if (lane < 2) cp_async4(smem_u32(&c.sw[slot][k][lane]), sw + k0 + k, true);
+              cp_async4(smem_u32(&c.sx[slot][k][i + scale_at(lane)]), row + i + lane);
+          if (lane < 2) cp_async4(smem_u32(&c.sw[slot][k][lane]), sw + k0 + k);
         }
         cp_async_mbar_arrive(&c.sc_full[slot]);
         if (++slot == SC) {
@@ -861,10 +861,6 @@ Params base_params(const float* a_scale, int rows, const int32_t* offsets, int g
   P.wait_ns = kTimeoutNs;
   return P;
 }
-
-}  // namespace
-
-namespace {
 
 cudaError_t few_gemm(const Fp8Problem& p, int32_t* err, int32_t* queue, int num_sms, cudaStream_t stream,
                      bool selftest = false) {

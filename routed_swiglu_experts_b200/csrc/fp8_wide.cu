@@ -436,8 +436,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const float* row = sa + static_cast<size_t>(k0 + k) * P.rows;
 #pragma unroll
             for (int i = 0; i < ROWS; i += 32)
-              if (lane + i < mine) cp_async4(smem_u32(&c.sx[slot][k][lane + i]), row + lane + i, true);
-            if (lane < 2) cp_async4(smem_u32(&c.sw[slot][k][lane]), sw + k0 + k, true);
+              if (lane + i < mine) cp_async4(smem_u32(&c.sx[slot][k][lane + i]), row + lane + i);
+            if (lane < 2) cp_async4(smem_u32(&c.sw[slot][k][lane]), sw + k0 + k);
           }
           cp_async_mbar_arrive(&c.sc_full[slot]);
           if (++slot == SC) {
