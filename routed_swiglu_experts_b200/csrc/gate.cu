@@ -738,7 +738,7 @@ __host__ __device__ constexpr size_t gate_smem(int E, int C, bool router) {
 // ROUTER: the logits are the layer's own, off by the fp32 product's error:
 // decisions closer than that (slack_of) are taken from exact products x . w.
 template <typename TIn, int C, bool VEC, bool PACKED, bool ROUTER>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const __grid_constant__ GateArgs a) {
+__device__ __forceinline__ void gate_tokens(const GateArgs& a) {
   extern __shared__ __align__(16) unsigned char gate_smem_raw[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t = blockIdx.x * kGateWarps + warp;
@@ -979,7 +979,19 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const __grid_cons
   emit(a, row, t, mine, m, inv_z, lane);
 }
 
-// The tokens that gate_kernel left: all exact logits of a token by the warps of
+template <typename TIn, int C, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(const GateArgs a) {
+  gate_tokens<TIn, C, VEC, PACKED, false>(a);
+}
+
+// (__grid_constant__: its functions out of line take the arguments by reference,
+// without a copy; inlined as above it costs one token 0.1 us)
+template <int C, bool VEC>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_router_kernel(const __grid_constant__ GateArgs a) {
+  gate_tokens<float, C, VEC, false, true>(a);
+}
+
+// The tokens that gate_router_kernel left: all exact logits of a token by the warps of
 // a block, the selection by one of them.  (256 experts of H 6144 are 6.3 MB of
 // weights: 90 us at the rate an SM is fed, 650 for one warp.  Eight SMs to a token
 // gave 60 us, but a third of the tokens a second, as most of them wait for the
@@ -1043,8 +1055,12 @@ bool gate_vec(const GateArgs& a, int C) {
 template <typename TIn, int C, bool PACKED, bool ROUTER>
 cudaError_t launch_gate_chunk(const GateArgs& a, cudaStream_t stream) {
   constexpr bool kCan = C % (16 / sizeof(TIn)) == 0 && C < 32;  // (more than 512 experts, or odd groups: element loads)
-  void (*fn)(GateArgs) = kCan && gate_vec<TIn>(a, C) ? gate_kernel<TIn, C, kCan, PACKED, ROUTER>
-                                                     : gate_kernel<TIn, C, false, PACKED, ROUTER>;
+  const bool vec = kCan && gate_vec<TIn>(a, C);
+  void (*fn)(GateArgs);
+  if constexpr (ROUTER)
+    fn = vec ? gate_router_kernel<C, kCan> : gate_router_kernel<C, false>;
+  else
+    fn = vec ? gate_kernel<TIn, C, kCan, PACKED> : gate_kernel<TIn, C, false, PACKED>;
   const size_t smem = kGateWarps * gate_smem(a.E, C, ROUTER);
   static_assert(ROUTER || kGateWarps * gate_smem(MOE_MAX_EXPERTS, C, false) <= 48 * 1024, "no opt-in shared memory needed");
   if (ROUTER) {
