@@ -251,7 +251,8 @@ MOE_API moe_status moe_router_topk(const moe_config* cfg, const moe_weights* w,
  * leave fp32's range (fp64's range decides which scores are 0: sigmoid logits
  * below about -709, softmax logits as far below the row's largest).
  * Logits may be infinite: an expert with -inf has score 0, a softmax row of
- * -inf alone has scores 0; NaN counts as the largest value.  The ids of a
+ * -inf alone has scores 0 (one with +inf has weights NaN, as infinity by itself
+ * has no share); NaN counts as the largest value.  The ids of a
  * token are distinct and in [0, E) whatever the logits hold.
  *   logits           [T, E] of logits_type (moe_dtype), row t at
  *                    logits + t * row_stride elements (row_stride >= E);

@@ -23,8 +23,9 @@
 // gives a tile to a cluster of two to four pairs, each with its part of the K
 // blocks; the first pair adds the others' sums out of their shared memory, in
 // order, and writes.  Measured (graph replay, weights from memory), one row:
-// N 2048, K 8192: 24.9 us whole, 12.5 split in four; N 6144, K 2048: 10.3, 9.2
-// in three; 6.2 of these are the launch, its barriers and TMEM.
+// N 2048, K 8192: 25.2 us whole, 12.7 split in four; N 6144, K 2048: 10.6, 9.4
+// in three (8.3 with the weights in L2); 6.2 of these are the launch, its barriers
+// and TMEM.
 //
 // Measured with many groups: feed-forward of 64 experts, 32 tokens, 8 experts
 // each (H 6144, I 2048), 2.4 GB of weights in 420 to 440 us = 5.5 to 5.7 TB/s;

@@ -17,9 +17,11 @@
 // has a scale of its own to fetch: 1385 clocks a K block; here about 935.)
 //
 // A tile is 256 rows x 256 weight rows, the largest whose sums fit the scaling
-// warps' registers.  What bounds it: each CTA copies 32 KB a K block through
-// L2 (721 clocks with nothing else running; the four MMAs take 517), the K
-// loop 935, and the epilogue about 3000 clocks a tile, 15% at K = 2048.  A
+// warps' registers.  What bounds it: the K loop takes 935 clocks a block, though
+// each CTA's copies of 32 KB through L2 take 721 with nothing else running and the
+// four MMAs 517, and no pipe is full.  That leaves the round trip of the two TMEM
+// buffers (signal, five reads in a row, their FMAs, release), which was not
+// measured by itself.  The epilogue is about 3000 clocks a tile, 15% at K = 2048.  A
 // group's last tile, when it has at most 128 rows, is multiplied as 128 (64 a
 // CTA): the weights' copies stay, so it costs four fifths of a whole one.
 // Measured, 64 groups, N 2816, K 2048, rows per group: 128: 94 us (1.00

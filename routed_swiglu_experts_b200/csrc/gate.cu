@@ -15,12 +15,13 @@
 // bits; each lane sorts its keys once (Batcher's odd-even merge sort) and puts
 // them into shared memory, and each of the k rounds is one warp-wide max
 // (redux.sync) over the lanes' heads, after which the winner's head moves on.
-// Measured (graph replay): one token of 256 experts in 8 groups 3.7 us, 4096
-// tokens 6.8, 16384 tokens 18.8 us (0.9 TB/s of logits): issue slots bound it on
-// many tokens (about 850 instructions a token), latency on few.  Four tokens
-// per warp, eight lanes each, halve the instructions and came to 22.9 us there
-// (24.3 this form, both before the next paragraph's pruning), slower below 8192
-// tokens: the chain of one token stays as long.
+// Measured (graph replay): one token of 256 experts in 8 groups 3.3 us, 4096
+// tokens 6.3, 16384 tokens 18.7 us (0.9 TB/s of logits).  What bounds it is a
+// token's chain of dependent reductions and shuffles: about 900 instructions a
+// token fill 60% of the issue slots, with half of the warps that an SM can hold
+// there, and DRAM is at 9%.  Four tokens per warp, eight lanes each, halve the
+// instructions and came to 22.9 us there (24.3 this form, both before the next
+// paragraph's pruning), slower below 8192 tokens: the chain stays as long.
 //
 // The order is exact.  Without a bias the scores rise with the logits, so the
 // keys are the logits' own bits (16-bit logits share the key with the id: no
@@ -30,9 +31,11 @@
 // be among a group's two largest (warp_groups), at the k-th place and in the
 // order those of the rounds that go on until a gap is wide enough (warp_order).
 // Only more than 32 experts that close, softmax scores with a bias (or in group
-// sums), infinities next to a border and groups that no chunk of lanes divides
-// take fp64 scores of all experts (warp_exact: 5 us longer; when it decided
-// every close token, 4096 tokens took 11.2 us and 16384 took 23.7).
+// sums), infinities next to a border, close borders between groups whose lanes
+// are no power of two and groups that no chunk of lanes divides take fp64 scores
+// of all experts (warp_exact: 5 us longer; when it decided every close token, 4096
+// tokens took 11.2 us and 16384 took 23.7; 4096 tokens of 100 experts in 5 groups
+// take 5.7, of 148 in 4, all of them this way, 14.3).
 #include <cuda_fp16.h>
 
 #include <type_traits>
