@@ -99,6 +99,14 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
  * workspace that moe_fp8_gemm needs. */
 #define MOE_WS_HEADER_BYTES 256
 
+/* Largest rank and largest number of adapters of moe_lora. */
+#define MOE_LORA_MAX_RANK 128
+#define MOE_MAX_ADAPTERS 1024
+/* Bytes of the workspace that moe_balance_loss needs. */
+#define MOE_BALANCE_WS_BYTES 16384
+/* Longest row of moe_rmsnorm. */
+#define MOE_NORM_MAX_COLUMNS 32768
+
 /* In moe_config.renormalize, beside its 0 or 1: the routing fields are set. */
 #define MOE_ROUTING_FIELDS 2
 
@@ -443,6 +451,97 @@ MOE_API moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t row
                                 int32_t groups, const void* w, const float* w_scale, int32_t N, int32_t K,
                                 const float* row_scale, void* out, int32_t out_type, void* ws, size_t ws_bytes,
                                 moe_stream_t stream);
+
+/* RMS norm of rows, with the residual's addition before it and an 8-bit
+ * result for moe_fp8_gemm:
+ *   h[t] = x[t]                          (residual NULL), or
+ *   h[t] = round(x[t] + residual[t])     in residual_type; written to residual_out
+ *   y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * weight
+ *   out[t] = round(y[t]) in x_type;  q, scale of y as moe_fp8_quantize's
+ * The mean is summed in fp64, y is fp32 and rounded once for each result.
+ * (The norm sees the residual as it is held, so a later reader of
+ * residual_out finds the values that were normalised.)  A row that holds an
+ * infinity or a NaN becomes NaN.
+ *   x            [rows, H] of x_type, rows x_stride elements apart
+ *   residual     [rows, H] of residual_type (x_type or MOE_F32), or NULL
+ *   residual_out [rows, H] of residual_type; given with residual alone
+ *   weight       [H] of weight_type (x_type or MOE_F32), or NULL (1)
+ *   eps          finite, at least 2^-100
+ *   out          [rows, H] of x_type, or NULL
+ *   q, scale     E4M3 [rows, H] and fp32 [ceil(H / 128), rows], or both NULL
+ * At least one of out and q.  H a multiple of 16, at most
+ * MOE_NORM_MAX_COLUMNS; every pointer but scale 16-byte aligned and row
+ * strides multiples of 16 bytes.  residual_out may be residual or x, out may
+ * be x or residual (the same rows: pointer, type and stride); otherwise
+ * outputs alias nothing. */
+MOE_API moe_status moe_rmsnorm(const void* x, int32_t x_type, int64_t x_stride, const void* residual,
+                               int64_t residual_stride, void* residual_out, int64_t residual_out_stride,
+                               int32_t residual_type, const void* weight, int32_t weight_type, float eps,
+                               int32_t rows, int32_t H, void* out, int64_t out_stride, void* q, float* scale,
+                               moe_stream_t stream);
+
+/* Low-rank adapters of many requests beside a projection that they share:
+ *   out[t] = base[t] + scale[l] * B_l (A_l x[t])    l = adapters[t]
+ *   out[t] = base[t]                                tokens without an adapter
+ * in two calls.  The plan orders the batch's tokens by adapter; it depends on
+ * `adapters` alone, so one plan serves every projection of the step.
+ *   adapters     int32 [T]; values outside 0 .. num_adapters - 1: no adapter
+ *   plan         at least moe_lora_plan_size(T, num_adapters) bytes of device
+ *                memory, 16-byte aligned */
+MOE_API moe_status moe_lora_plan_size(int32_t T, int32_t num_adapters, size_t* bytes);
+MOE_API moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num_adapters, void* plan,
+                                 size_t plan_bytes, moe_stream_t stream);
+
+/* The adapters' products, by moe_lora_plan's plan for the same T and
+ * num_adapters (one for others is reported in the workspace's error word as
+ * MOE_ERR_INVALID_ARG, and nothing is written).
+ *   x        [T, K] of x_type (MOE_BF16 or MOE_F16), rows x_stride elements apart
+ *   a        [num_adapters, rank, K] of x_type (A);  b  [num_adapters, N, rank] (B)
+ *   scale    fp32 [num_adapters], or NULL (1)
+ *   base     [T, N] of out_type, or NULL (0)
+ *   out      [T, N] of out_type (x_type or MOE_F32); may be base (the same
+ *            rows: pointer and stride), else it aliases no input
+ * Products are summed in fp32; A_l x is carried to B as the sum of two values
+ * of x_type (an error of 2^-16 of it at most); one rounding to out_type at
+ * the end.  K and rank multiples of 8 (pad a smaller rank with zeros), rank at
+ * most MOE_LORA_MAX_RANK, num_adapters at most MOE_MAX_ADAPTERS, K and N at
+ * most 2^30; x, a and b 16-byte aligned, x's rows too.  ws: an initialised
+ * workspace of any size from MOE_WS_HEADER_BYTES up. */
+MOE_API moe_status moe_lora(const void* x, int32_t x_type, int64_t x_stride, const void* a, const void* b,
+                            const float* scale, int32_t T, int32_t K, int32_t N, int32_t rank, int32_t num_adapters,
+                            const void* plan, size_t plan_bytes, const void* base, int64_t base_stride, void* out,
+                            int32_t out_type, int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Balance loss of the router with the counts of each expert and the gradient
+ * of the logits, for one batch in one or more sequences.  s(l) are the scores
+ * of cfg (sigmoid or softmax, without bias), p_te = s_te / sum_e s_te; of the
+ * counted tokens of sequence b, n_b in number, c_be chose expert e:
+ *   loss = coef / S' * sum_b sum_e f_be * mean_t p_te     f_be = E c_be / (k n_b)
+ *   grad_logits[t] = grad_loss * d loss / d logits[t]     (f held constant)
+ * S' = sequences with at least one counted token (no such: loss 0).  A token
+ * is counted when it lies in a sequence and its mask is not 0; the others'
+ * logits and ids do not matter and their gradient is 0.
+ *   cfg           num_experts, top_k and score are used
+ *   logits        [T, E] of logits_type, rows row_stride elements apart
+ *   topk_ids      int32 [T, k]; ids outside 0 .. E - 1 are not counted in c
+ *   seq_offsets   int32 [num_seqs + 1] ascending: sequence b is tokens
+ *                 seq_offsets[b] .. seq_offsets[b + 1] - 1; or NULL with
+ *                 num_seqs == 1 (all tokens)
+ *   token_mask    uint8 [T] or NULL (every token)
+ *   grad_loss     fp32 [1], the upstream gradient, or NULL (1)
+ *   counts        int32 [num_seqs, E] out (c);  seq_tokens  int32 [num_seqs] out (n)
+ *   loss          fp32 [1] out
+ *   grad_logits   [T, E] of grad_type (logits_type or MOE_F32), rows
+ *                 grad_stride elements apart, out; or NULL.  Must not alias logits.
+ * Sums are fp32 within a token and fp64 over tokens, in an order that does not
+ * change from call to call.  T == 0 writes zeros.  ws: an initialised
+ * workspace of at least MOE_BALANCE_WS_BYTES. */
+MOE_API moe_status moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, int64_t row_stride,
+                                    const int32_t* topk_ids, const int32_t* seq_offsets, int32_t num_seqs,
+                                    const unsigned char* token_mask, int32_t T, float coef, const float* grad_loss,
+                                    int32_t* counts, int32_t* seq_tokens, float* loss, void* grad_logits,
+                                    int32_t grad_type, int64_t grad_stride, void* ws, size_t ws_bytes,
+                                    moe_stream_t stream);
 
 /* Permute without a workspace, for callers that may not allocate device
  * memory on their enqueue path (framework / inference-server plugins and

@@ -14,20 +14,23 @@ from typing import Optional
 
 from . import _abi
 from ._abi import (  # noqa: F401
-    EXPORTED, MOE_BF16, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
-    MOE_ERR_WORKSPACE, MOE_F16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_SUM2, MOE_MAX_EXPERTS, MOE_MAX_GROUPS, MOE_MAX_TOP_K,
+    EXPORTED, MOE_BALANCE_WS_BYTES, MOE_BF16, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
+    MOE_ERR_WORKSPACE, MOE_F16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_SUM2, MOE_LORA_MAX_RANK,
+    MOE_MAX_ADAPTERS, MOE_MAX_EXPERTS, MOE_MAX_GROUPS, MOE_MAX_TOP_K, MOE_NORM_MAX_COLUMNS,
     MOE_OK, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_BF16, MOE_W_FP8_B128, MOE_W_INT4_G128, MOE_W_NVFP4,
     MOE_WS_HEADER_BYTES, MoEError,
-    load_library, make_config, make_weights, moe_combine, moe_config, moe_config_validate, moe_forward,
+    load_library, make_config, make_weights, moe_balance_loss, moe_combine, moe_config, moe_config_validate, moe_forward,
     moe_fp8_gemm, moe_fp8_quantize, moe_fp8_quantize_weight, moe_gate_topk,
-    moe_grouped_swiglu_ffn, moe_grouped_swiglu_ffn_gather, moe_permute, moe_read_device_error, moe_router_topk,
+    moe_grouped_swiglu_ffn, moe_grouped_swiglu_ffn_gather, moe_lora, moe_lora_plan, moe_lora_plan_size, moe_permute,
+    moe_read_device_error, moe_rmsnorm, moe_router_topk,
     moe_weights,
     moe_workspace_init, moe_workspace_size, status_name,
 )
 
 __all__ = ["MoELayer", "load_library", "moe_forward", "moe_router_topk", "moe_permute",
            "moe_grouped_swiglu_ffn", "moe_grouped_swiglu_ffn_gather", "moe_combine", "moe_workspace_size", "MoEError",
-           "moe_gate_topk", "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_gemm"]
+           "moe_gate_topk", "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_gemm",
+           "moe_rmsnorm", "moe_lora_plan_size", "moe_lora_plan", "moe_lora", "moe_balance_loss"]
 
 
 class MoELayer:

@@ -37,6 +37,10 @@ MOE_BF16 = 1
 MOE_F16 = 2
 MOE_MAX_GROUPS = 32
 MOE_WS_HEADER_BYTES = 256
+MOE_LORA_MAX_RANK = 128
+MOE_MAX_ADAPTERS = 1024
+MOE_BALANCE_WS_BYTES = 16384
+MOE_NORM_MAX_COLUMNS = 32768
 MOE_MAX_TOP_K = 16
 MOE_MAX_EXPERTS = 1024
 MOE_INT4_MAX_SWIGLU_LIMIT = 255.0
@@ -45,6 +49,7 @@ EXPORTED = (
     "moe_status_string", "moe_config_validate", "moe_workspace_size", "moe_workspace_init",
     "moe_router_topk", "moe_permute", "moe_grouped_swiglu_ffn", "moe_grouped_swiglu_ffn_gather", "moe_combine",
     "moe_forward", "moe_forward_ep", "moe_gate_topk", "moe_fp8_quantize", "moe_fp8_quantize_weight", "moe_fp8_gemm",
+    "moe_rmsnorm", "moe_lora_plan_size", "moe_lora_plan", "moe_lora", "moe_balance_loss",
     "moe_read_device_error", "moe_permute_no_alloc", "moe_selftest_device_timeout", "moe_selftest_pair_timeout",
 )
 MOE_NO_ALLOC_MAX_ROWS = 131072
@@ -116,6 +121,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "`python -m routed_swiglu_experts_b200.build` (there is no CPU fallback)")
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F32 = ctypes.c_float
     CFG, W = ctypes.POINTER(moe_config), ctypes.POINTER(moe_weights)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -133,6 +139,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_fp8_quantize": (ctypes.c_int, [P, I32, I64, P, I32, I32, I32, P, P, P]),
         "moe_fp8_quantize_weight": (ctypes.c_int, [P, I32, I32, I32, I32, P, P, P]),
         "moe_fp8_gemm": (ctypes.c_int, [P, P, I32, P, I32, P, P, I32, I32, P, P, I32, P, SZ, P]),
+        "moe_rmsnorm": (ctypes.c_int, [P, I32, I64, P, I64, P, I64, I32, P, I32, F32, I32, I32, P, I64, P, P, P]),
+        "moe_lora_plan_size": (ctypes.c_int, [I32, I32, ctypes.POINTER(SZ)]),
+        "moe_lora_plan": (ctypes.c_int, [P, I32, I32, P, SZ, P]),
+        "moe_lora": (ctypes.c_int, [P, I32, I64, P, P, P, I32, I32, I32, I32, I32, P, SZ, P, I64, P, I32, I64, P, SZ, P]),
+        "moe_balance_loss": (ctypes.c_int, [CFG, P, I32, I64, P, P, I32, P, I32, F32, P, P, P, P, P, I32, I64, P, SZ, P]),
         "moe_read_device_error": (ctypes.c_int, [P, P, ctypes.POINTER(I32)]),
         "moe_selftest_device_timeout": (ctypes.c_int, [P, SZ, P]),
         "moe_selftest_pair_timeout": (ctypes.c_int, [P, SZ, I32, P]),
@@ -293,6 +304,8 @@ class _Torch:
         self.f32 = (torch.float32,)
         self.i32 = (torch.int32,)
         self.u8 = (torch.uint8,)
+        self.masks = (torch.bool, torch.uint8)
+        self.halves = (torch.bfloat16, torch.float16)
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.outs = (torch.bfloat16, torch.float32)
         # the current device's number, and a device's current stream as its handle alone:
@@ -421,6 +434,129 @@ def moe_fp8_gemm(a, a_scale, w, w_scale, expert_offsets, row_scale, out, ws, str
     _check(load_library().moe_fp8_gemm(a.data_ptr(), a_scale.data_ptr(), rows, _ptr(expert_offsets), G, w.data_ptr(),
                                        w_scale.data_ptr(), N, K, _ptr(row_scale), out.data_ptr(), tt.types[out.dtype],
                                        ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
+
+
+def moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, out=None, q=None, scale=None, stream=None):
+    """RMS norm of rows x [rows, H] (+ residual, the sum written to
+    residual_out, which may be residual itself) times weight [H] (None: 1), to
+    out (x's type) and/or E4M3 codes q [rows, H] with scale [ceil(H/128), rows].
+    Rows of x, residual, residual_out and out may be strided."""
+    where, tt = "moe_rmsnorm", _tt()
+    dev = tt.device()
+    _want(x, "x", tt.floats, None, where, dev, contiguous=False)
+    x_stride = _row_stride(x, "x", where)
+    shape = rows, H = x.shape
+    types = (x.dtype,) + tt.f32
+    res_stride = res_out_stride = out_stride = H
+    res_type = tt.types[x.dtype]
+    if residual is not None or residual_out is not None:
+        _want(residual, "residual", types, shape, where, dev, contiguous=False)
+        _want(residual_out, "residual_out", (residual.dtype,), shape, where, dev, contiguous=False)
+        res_stride, res_out_stride = _row_stride(residual, "residual", where), _row_stride(residual_out, "residual_out", where)
+        res_type = tt.types[residual.dtype]
+    w_type = 0
+    if weight is not None:
+        _want(weight, "weight", types, (H,), where, dev)
+        w_type = tt.types[weight.dtype]
+    if out is not None:
+        _want(out, "out", (x.dtype,), shape, where, dev, contiguous=False)
+        out_stride = _row_stride(out, "out", where)
+    if q is not None or scale is not None:
+        _want(q, "q", tt.codes, shape, where, dev)
+        _want(scale, "scale", tt.f32, (_blocks(H), rows), where, dev)
+    _check(load_library().moe_rmsnorm(x.data_ptr(), tt.types[x.dtype], x_stride, _ptr(residual), res_stride,
+                                      _ptr(residual_out), res_out_stride, res_type, _ptr(weight), w_type, eps, rows, H,
+                                      _ptr(out), out_stride, _ptr(q), _ptr(scale), _stream(stream, dev)), where)
+
+
+def moe_lora_plan_size(T: int, num_adapters: int) -> int:
+    """Bytes of a plan for T tokens and num_adapters adapters."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_lora_plan_size(int(T), int(num_adapters), ctypes.byref(n)), "moe_lora_plan_size")
+    return n.value
+
+
+def moe_lora_plan(adapters, num_adapters, plan, stream=None):
+    """The order of a batch by adapter: adapters int32 [T] (-1: none) to plan
+    (uint8, moe_lora_plan_size bytes), for every moe_lora call on that batch."""
+    where, tt = "moe_lora_plan", _tt()
+    dev = tt.device()
+    _want(adapters, "adapters", tt.i32, None, where, dev)
+    if adapters.dim() != 1:
+        raise ValueError(f"{where}: adapters must be [T]")
+    _want(plan, "plan", tt.u8, None, where, dev)
+    _check(load_library().moe_lora_plan(adapters.data_ptr(), adapters.shape[0], num_adapters, plan.data_ptr(), plan.numel(),
+                                        _stream(stream, dev)), where)
+
+
+def moe_lora(x, a, b, scale, plan, base, out, ws, stream=None):
+    """out [T, N] = base [T, N] (None: 0; may be out) + scale [L] * (x [T, K]
+    a_l^T) b_l^T by the plan's adapters; a [L, rank, K], b [L, N, rank]."""
+    where, tt = "moe_lora", _tt()
+    dev = tt.device()
+    _want(x, "x", tt.halves, None, where, dev, contiguous=False)
+    x_stride = _row_stride(x, "x", where)
+    same = (x.dtype,)
+    _want(a, "a", same, None, where, dev)
+    _want(b, "b", same, None, where, dev)
+    T, K = x.shape
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != K or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+        raise ValueError(f"{where}: a must be [adapters, rank, {K}] and b [adapters, N, rank]")
+    L, r, _ = a.shape
+    N = b.shape[1]
+    if scale is not None:
+        _want(scale, "scale", tt.f32, (L,), where, dev)
+    _want(plan, "plan", tt.u8, None, where, dev)
+    _want(out, "out", same + tt.f32, (T, N), where, dev, contiguous=False)
+    out_stride = base_stride = _row_stride(out, "out", where)
+    if base is not None and base is not out:
+        _want(base, "base", (out.dtype,), (T, N), where, dev, contiguous=False)
+        base_stride = _row_stride(base, "base", where)
+    _want(ws, "ws", tt.u8, None, where, dev)
+    _check(load_library().moe_lora(x.data_ptr(), tt.types[x.dtype], x_stride, a.data_ptr(), b.data_ptr(), _ptr(scale), T, K,
+                                   N, r, L, plan.data_ptr(), plan.numel(), _ptr(base), base_stride, out.data_ptr(),
+                                   tt.types[out.dtype], out_stride, ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
+
+
+def moe_balance_loss(cfg, logits, topk_ids, counts, seq_tokens, loss, ws, grad_logits=None, seq_offsets=None,
+                     token_mask=None, coef=1.0, grad_loss=None, stream=None):
+    """The router's balance loss (one fp32 value) over logits [T, E] and their
+    selection topk_ids [T, k]; counts int32 [S, E] and seq_tokens int32 [S] of
+    the sequences seq_offsets int32 [S + 1] (None: one); grad_logits [T, E]
+    (the logits' type or fp32) times grad_loss (one fp32 value; None: 1);
+    token_mask bool or uint8 [T]: tokens to count."""
+    where, tt = "moe_balance_loss", _tt()
+    dev = tt.device()
+    _want(logits, "logits", tt.floats, None, where, dev, contiguous=False)
+    stride = grad_stride = _row_stride(logits, "logits", where)
+    shape = T, E = logits.shape
+    if E != cfg.num_experts:
+        raise ValueError(f"{where}: logits has {E} columns for {cfg.num_experts} experts")
+    _want(topk_ids, "topk_ids", tt.i32, (T, cfg.top_k), where, dev)
+    S = 1
+    if seq_offsets is not None:
+        _want(seq_offsets, "seq_offsets", tt.i32, None, where, dev)
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError(f"{where}: seq_offsets must be [sequences + 1]")
+        S = seq_offsets.shape[0] - 1
+    _want(counts, "counts", tt.i32, (S, E), where, dev)
+    _want(seq_tokens, "seq_tokens", tt.i32, (S,), where, dev)
+    if token_mask is not None:
+        _want(token_mask, "token_mask", tt.masks, (T,), where, dev)
+    for t, name in ((loss, "loss"), (grad_loss, "grad_loss")):
+        if t is not None or name == "loss":
+            _want(t, name, tt.f32, None, where, dev)
+            if t.numel() != 1:
+                raise ValueError(f"{where}: {name} has {t.numel()} elements, expected 1")
+    grad_type = 0
+    if grad_logits is not None:
+        _want(grad_logits, "grad_logits", (logits.dtype,) + tt.f32, shape, where, dev, contiguous=False)
+        grad_stride, grad_type = _row_stride(grad_logits, "grad_logits", where), tt.types[grad_logits.dtype]
+    _want(ws, "ws", tt.u8, None, where, dev)
+    _check(load_library().moe_balance_loss(
+        ctypes.byref(cfg), logits.data_ptr(), tt.types[logits.dtype], stride, topk_ids.data_ptr(), _ptr(seq_offsets), S,
+        _ptr(token_mask), T, coef, _ptr(grad_loss), counts.data_ptr(), seq_tokens.data_ptr(), loss.data_ptr(),
+        _ptr(grad_logits), grad_type, grad_stride, ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
 
 
 def moe_permute_no_alloc(cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm, stream=None):

@@ -595,6 +595,103 @@ moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t rows, const
                                    rows));
 }
 
+moe_status moe_rmsnorm(const void* x, int32_t x_type, int64_t x_stride, const void* residual, int64_t residual_stride,
+                       void* residual_out, int64_t residual_out_stride, int32_t residual_type, const void* weight,
+                       int32_t weight_type, float eps, int32_t rows, int32_t H, void* out, int64_t out_stride, void* q,
+                       float* scale, moe_stream_t stream) {
+  if (x_type != MOE_F32 && x_type != MOE_BF16 && x_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || H < 16 || H % 16 != 0 || !std::isfinite(eps) || !(eps >= 0x1p-100f)) return MOE_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr) || (q == nullptr) != (scale == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (residual != nullptr && residual_type != x_type && residual_type != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (weight != nullptr && weight_type != x_type && weight_type != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (H > MOE_NORM_MAX_COLUMNS || static_cast<int64_t>(rows) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || (out == nullptr && q == nullptr)) return MOE_ERR_INVALID_ARG;
+  auto bad_rows = [&](const void* p, int64_t stride, int32_t type) {
+    return p != nullptr && (!aligned16(p) || stride < H || (stride * (type == MOE_F32 ? 4 : 2)) % 16 != 0);
+  };
+  if (bad_rows(x, x_stride, x_type) || bad_rows(residual, residual_stride, residual_type) ||
+      bad_rows(residual_out, residual_out_stride, residual_type) || bad_rows(out, out_stride, x_type))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(weight) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_rmsnorm(x, x_type, x_stride, residual, residual_stride, residual_out, residual_out_stride,
+                                  residual != nullptr ? residual_type : x_type, weight, weight_type, eps, rows, H, out,
+                                  out_stride, q, scale, stream));
+}
+
+moe_status moe_lora_plan_size(int32_t T, int32_t num_adapters, size_t* bytes) {
+  if (T < 0 || num_adapters < 1 || bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) > kMaxTokens || num_adapters > MOE_MAX_ADAPTERS) return MOE_ERR_UNSUPPORTED;
+  *bytes = lora_plan_bytes(T, num_adapters);
+  return MOE_OK;
+}
+
+moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num_adapters, void* plan, size_t plan_bytes,
+                         moe_stream_t stream) {
+  size_t need;
+  MOE_TRY(moe_lora_plan_size(T, num_adapters, &need));
+  if (T == 0) return MOE_OK;
+  if (adapters == nullptr || !aligned4(adapters) || plan == nullptr || !aligned16(plan)) return MOE_ERR_INVALID_ARG;
+  if (plan_bytes < need) return MOE_ERR_WORKSPACE;
+  return from_cuda(launch_lora_plan(adapters, T, num_adapters, plan, stream));
+}
+
+moe_status moe_lora(const void* x, int32_t x_type, int64_t x_stride, const void* a, const void* b, const float* scale,
+                    int32_t T, int32_t K, int32_t N, int32_t rank, int32_t num_adapters, const void* plan,
+                    size_t plan_bytes, const void* base, int64_t base_stride, void* out, int32_t out_type,
+                    int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (x_type != MOE_BF16 && x_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (out_type != x_type && out_type != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (K < 8 || K % 8 != 0 || N < 1 || rank < 8 || rank % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (rank > MOE_LORA_MAX_RANK || K > kMaxSide || N > kMaxSide) return MOE_ERR_UNSUPPORTED;
+  size_t need;
+  MOE_TRY(moe_lora_plan_size(T, num_adapters, &need));
+  if (T == 0) return MOE_OK;
+  if (x == nullptr || a == nullptr || b == nullptr || plan == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (x_stride < K || x_stride % 8 != 0 || out_stride < N || (base != nullptr && base_stride < N)) return MOE_ERR_INVALID_ARG;
+  if (base == out && base_stride != out_stride) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(plan) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  const uintptr_t unit = out_type == MOE_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(out) & unit) != 0 || (reinterpret_cast<uintptr_t>(base) & unit) != 0) return MOE_ERR_INVALID_ARG;
+  if (plan_bytes < need) return MOE_ERR_WORKSPACE;
+  if (ws == nullptr || ws_bytes < MOE_WS_HEADER_BYTES) return MOE_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_lora(x, x_type, x_stride, a, b, scale, T, K, N, rank, num_adapters, plan, base, base_stride, out,
+                               out_type, out_stride, err_word(ws), num_sms_current_device(), stream));
+}
+
+moe_status moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, int64_t row_stride,
+                            const int32_t* topk_ids, const int32_t* seq_offsets, int32_t num_seqs,
+                            const unsigned char* token_mask, int32_t T, float coef, const float* grad_loss,
+                            int32_t* counts, int32_t* seq_tokens, float* loss, void* grad_logits, int32_t grad_type,
+                            int64_t grad_stride, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_config c;
+  MOE_TRY(take_config(cfg, c));
+  MOE_TRY(check_tokens(c, T));
+  if (logits_type != MOE_F32 && logits_type != MOE_BF16 && logits_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (grad_logits != nullptr && grad_type != logits_type && grad_type != MOE_F32) return MOE_ERR_INVALID_ARG;
+  // (a score function that was set but not announced would be left out silently)
+  if (!(cfg->renormalize & MOE_ROUTING_FIELDS) && cfg->score != 0) return MOE_ERR_INVALID_ARG;
+  if (num_seqs < 1 || (seq_offsets == nullptr && num_seqs != 1) || !std::isfinite(coef)) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_seqs) > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (counts == nullptr || seq_tokens == nullptr || loss == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(counts) || !aligned4(seq_tokens) || !aligned4(loss) || !aligned4(topk_ids) || !aligned4(seq_offsets) ||
+      !aligned4(grad_loss))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (logits == nullptr || topk_ids == nullptr || row_stride < c.num_experts) return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == MOE_F32 ? 3u : 1u)) != 0) return MOE_ERR_INVALID_ARG;
+    if (grad_logits != nullptr && (grad_logits == logits || grad_stride < c.num_experts ||
+                                   (reinterpret_cast<uintptr_t>(grad_logits) & (grad_type == MOE_F32 ? 3u : 1u)) != 0))
+      return MOE_ERR_INVALID_ARG;
+  }
+  if (ws == nullptr || ws_bytes < MOE_BALANCE_WS_BYTES) return MOE_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  return from_cuda(launch_balance(c, logits, logits_type, row_stride, topk_ids, seq_offsets, num_seqs, token_mask, T, coef,
+                                  grad_loss, counts, seq_tokens, loss, grad_logits, grad_type, grad_stride, ws,
+                                  num_sms_current_device(), stream));
+}
+
 moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_bytes, moe_stream_t stream) {
   if (scratch == nullptr || scratch_bytes < MOE_SELFTEST_SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(scratch) & 255u) != 0) return MOE_ERR_INVALID_ARG;

@@ -23,7 +23,9 @@ struct WsHeader {
   // Ticket counter of the permute's count blocks: zero when a launch starts,
   // reset to zero by the block that takes the last ticket.
   int32_t perm_done;
-  int32_t pad[53];
+  // The same of the balance loss's blocks.
+  int32_t balance_done;
+  int32_t pad[52];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 // (a layer has 4-bit or FP8 experts, never both: their kernels share the slots)

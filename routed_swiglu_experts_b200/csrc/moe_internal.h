@@ -224,6 +224,47 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
                            const float* w_perm, void* y_perm, int32_t* err, int32_t* queues, int num_sms, int e_total,
                            cudaStream_t stream);
 
+// RMS norm (rmsnorm.cu): see moe_rmsnorm.
+cudaError_t launch_rmsnorm(const void* x, int x_type, int64_t x_stride, const void* res, int64_t res_stride,
+                           void* res_out, int64_t res_out_stride, int res_type, const void* w, int w_type, float eps,
+                           int rows, int H, void* out, int64_t out_stride, void* q, float* scale, cudaStream_t stream);
+
+// Adapters (lora.cu).  A plan is its head, the tokens sorted by adapter (those
+// without one last) and tiles of rows of one adapter each.
+struct LoraPlan {
+  int32_t magic, T, L, tiles, tile_rows, pad[3];
+};
+struct LoraTile {
+  int32_t adapter, row0, rows, pad;  // adapter -1: rows without one
+};
+constexpr int32_t kLoraPlanMagic = 0x4C6F5261;
+inline int lora_tile_rows(int) { return 128; }
+// Tiles that T tokens can make: whole ones, and a partial one per adapter that occurs.
+inline int64_t lora_max_tiles(int T, int L) { return T / lora_tile_rows(T) + std::min<int64_t>(T, int64_t(L) + 1); }
+__host__ __device__ inline size_t lora_tiles_at(int T) {
+  return sizeof(LoraPlan) + (static_cast<size_t>(T) * sizeof(int32_t) + 15) / 16 * 16;
+}
+inline size_t lora_plan_bytes(int T, int L) {
+  return lora_tiles_at(T) + static_cast<size_t>(lora_max_tiles(T, L)) * sizeof(LoraTile);
+}
+cudaError_t launch_lora_plan(const int32_t* ids, int T, int L, void* plan, cudaStream_t stream);
+cudaError_t launch_lora(const void* x, int dtype, int64_t x_stride, const void* w_a, const void* w_b,
+                        const float* scale, int T, int K, int N, int r, int L, const void* plan, const void* base,
+                        int64_t base_stride, void* out, int out_type, int64_t out_stride, int32_t* err, int num_sms,
+                        cudaStream_t stream);
+
+// Balance loss (balance.cu): workspace and launch; see moe_balance_loss.
+constexpr int kBalanceBlocks = 1024;
+struct BalanceWs {
+  WsHeader header;
+  double part[kBalanceBlocks];  // the blocks' shares of the loss
+};
+static_assert(sizeof(BalanceWs) <= MOE_BALANCE_WS_BYTES, "MOE_BALANCE_WS_BYTES");
+cudaError_t launch_balance(const moe_config& cfg, const void* logits, int dtype, int64_t stride, const int32_t* ids,
+                           const int32_t* offsets, int S, const unsigned char* mask, int T, float coef,
+                           const float* up, int32_t* counts, int32_t* tokens, float* loss, void* grad, int grad_type,
+                           int64_t grad_stride, void* ws, int num_sms, cudaStream_t stream);
+
 // Shared expert for T <= 32 tokens: split-K tensor-core GEMMs streaming the
 // weights across all SMs, then an ordered sum of the K slices.
 constexpr int kDenseSmallMaxTokens = 32;
