@@ -4,6 +4,9 @@
 // tiles; it serves every projection of the step.
 #include <cuda_fp16.h>
 
+#include <cstdlib>
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -100,6 +103,18 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
 }
 
 // --------------------------------------------------------------- apply ------
+// One cluster of C CTAs per tile (up to 128 tokens of one adapter): x is read
+// once, A x never leaves the cluster.
+//   shrink  each CTA multiplies its share of K: D[token, rank] in TMEM, x as the
+//           M operand (128 rows), A as N
+//   sum     the CTAs' shares are added through distributed shared memory, scaled
+//           and split into two 16-bit values hi + lo (the second is what the
+//           rounding of the first left), so that 16 bits or more of A x count
+//   expand  each CTA takes every C-th 128 features: D[feature, token] in TMEM, B
+//           as M, hi and lo as N, added to base by the epilogue: a lane holds a
+//           feature, so a warp reads and writes 32 neighbours of a token's row
+// Operands lie in shared memory as K-major rows of 128 bytes, 128-byte swizzle,
+// written by cp.async (rows of x come from anywhere).
 struct LoraArgs {
   const void* x;
   const void* a;
@@ -110,53 +125,520 @@ struct LoraArgs {
   void* out;
   int64_t x_stride, base_stride, out_stride;
   int T, K, N, r, L;
+  bool wide;  // base's and out's rows all start on 16-byte boundaries
   int32_t* err;
 };
 
-constexpr int kRowsAtOnce = 16;
+constexpr int kLoraThreads = 256;
+constexpr uint32_t kLoraTmemCols = 256;
+constexpr int kTurnRow = 36, kTurnTile = 16 * kTurnRow * 4;  // 16 tokens x 32 features of a warp (rows padded: no bank conflicts)
+constexpr uint64_t kTimeoutNs = 4000000000ull;
 
-template <typename T, typename TO>
-__global__ void __launch_bounds__(256) lora_kernel(const LoraArgs a) {
-  __shared__ float v[kRowsAtOnce][128];
+struct LoraCtl {
+  uint64_t stage_done[4];  // the MMAs that read a stage are done
+  uint64_t chunk_done[2];  // ... a chunk of features
+  uint64_t drained;        // after a wait that gave up: every MMA is done
+  uint32_t tmem_base;
+  int32_t abort_flag;
+  int32_t rows[128];       // the tile's tokens
+  float factor[128];       // fp16: what a token's hi and lo are to be multiplied by
+};
+
+template <int RP>
+struct LoraSmem {
+  static constexpr int kX = 128 * 128, kA = RP * 128, kStage = kX + kA;
+  static constexpr int kStages = RP == 16 || RP == 128 ? 4 : 3;
+  static constexpr int kChunks = RP == 128 ? 2 : 1;     // K chunks of 64 of the expand operands
+  static constexpr int kB = kChunks * 128 * 128;        // 128 features of B
+  // over the stages, once A x is summed: this CTA's share of it (of up to 16
+  // tokens while the epilogue runs, whose warps' tiles lie behind), then hi and lo
+  static constexpr int kPart = 128 * (RP + 4) * 4, kTurnAt = 16 * (RP + 4) * 4, kTurn = kTurnAt + 8 * kTurnTile;
+  static constexpr int kVAt = ((kPart > kTurn ? kPart : kTurn) + 1023) / 1024 * 1024;
+  static constexpr int kV = kChunks * 128 * 128;
+  static constexpr int kFront = kVAt + 2 * kV > kStages * kStage ? kVAt + 2 * kV : kStages * kStage;
+  // (two CTAs of 256 TMEM columns fit an SM, a third must not start: it would
+  // wait for columns that CTAs of waiting clusters hold)
+  static constexpr int kBytes = 1024 + kFront + 2 * kB + static_cast<int>(sizeof(LoraCtl));
+  // K blocks of tiles of at most 16 tokens, loaded at once: A, then 16 rows of x
+  // each (as the M operand 128 rows are read: what follows gives rows that are
+  // not used, and lies within the block's shared memory)
+  static constexpr int kFew = kFront / (RP * 128 + 2048);
+  static_assert(16384 <= 2 * kB, "the last rows that are read");
+  static_assert(kFront % 1024 == 0 && 3 * kBytes > 227 * 1024 && kBytes <= 232448, "shared memory of an SM");
+};
+
+// 16 bytes, or zeros where !valid.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u) : "memory");
+}
+
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk16) { return row * 128 + ((chunk16 ^ (row & 7)) << 4); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// What rounding v to T leaves, 0 where the rounding is not finite.
+template <typename T>
+__device__ __forceinline__ float rest_of(float v) {
+  const float h = static_cast<float>(static_cast<T>(v));
+  return fabsf(h) <= 3.4028234e38f ? v - h : 0.f;
+}
+
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// Eight neighbouring values of a row: 16 bytes at a time where every row allows
+// it (wide) and all eight are there, else one by one (`left` of them).
+template <typename TO>
+struct Piece {
+  static constexpr int kWords = sizeof(TO) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const TO* base, int64_t at, int left, bool wide) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    if (base == nullptr) return;
+    const TO* p = base + at;
+    if (wide && left >= 8) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) set(i, p[i]);
+    }
+  }
+  __device__ __forceinline__ void set(int i, TO v) {
+    if constexpr (sizeof(TO) == 4)
+      w[i] = __float_as_uint(v);
+    else
+      w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v)) << (i % 2 * 16);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(TO) == 4) return __uint_as_float(w[i]);
+    const uint16_t b = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+    return static_cast<float>(*reinterpret_cast<const TO*>(&b));
+  }
+  static __device__ __forceinline__ void store(TO* out, int64_t at, int left, bool wide, const float (&y)[8]) {
+    TO* p = out + at;
+    if (wide && left >= 8) {
+      uint32_t v[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(TO) == 4)
+          v[i] = __float_as_uint(y[i]);
+        else
+          v[i] = pack2<TO>(y[2 * i], y[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = static_cast<TO>(y[i]);
+    }
+  }
+};
+
+template <typename T, typename TO, int RP>
+__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(const LoraArgs a, const int C) {
+  using S = LoraSmem<RP>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const LoraPlan head = *reinterpret_cast<const LoraPlan*>(a.plan);
+  const int32_t* src = reinterpret_cast<const int32_t*>(a.plan + sizeof(LoraPlan));
+  const LoraTile* tiles = reinterpret_cast<const LoraTile*>(a.plan + lora_tiles_at(a.T));
+  LoraTile tile = tiles[blockIdx.x / C];  // (the plan has room for one per cluster; read before the head is known)
   if (head.magic != kLoraPlanMagic || head.T != a.T || head.L != a.L) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err, MOE_ERR_INVALID_ARG, 0);
     return;
   }
-  const int32_t* src = reinterpret_cast<const int32_t*>(a.plan + sizeof(LoraPlan));
-  const LoraTile* tiles = reinterpret_cast<const LoraTile*>(a.plan + lora_tiles_at(a.T));
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int i = blockIdx.x; i < head.tiles; i += gridDim.x) {
-    const LoraTile tile = tiles[i];
-    for (int r0 = 0; r0 < tile.rows; r0 += kRowsAtOnce) {
-      const int rows = min(kRowsAtOnce, tile.rows - r0);
-      if (tile.adapter >= 0) {
-        const float sc = a.scale != nullptr ? a.scale[tile.adapter] : 1.f;
-        const T* al = static_cast<const T*>(a.a) + static_cast<int64_t>(tile.adapter) * a.r * a.K;
-        for (int p = warp; p < rows * a.r; p += 8) {
-          const int row = p / a.r, j = p % a.r;
-          const T* xr = static_cast<const T*>(a.x) + src[tile.row0 + r0 + row] * a.x_stride;
-          float s = 0.f;
-          for (int k = lane; k < a.K; k += 32) s = fmaf(static_cast<float>(xr[k]), static_cast<float>(al[static_cast<int64_t>(j) * a.K + k]), s);
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == 0) v[row][j] = s * sc;
-        }
-      }
-      __syncthreads();
-      const T* bl = static_cast<const T*>(a.b) + static_cast<int64_t>(max(tile.adapter, 0)) * a.N * a.r;
-      for (int n = threadIdx.x; n < a.N; n += 256) {
-        for (int row = 0; row < rows; ++row) {
-          const int64_t t = src[tile.row0 + r0 + row];
-          float s = 0.f;
-          if (tile.adapter >= 0)
-            for (int j = 0; j < a.r; ++j) s = fmaf(v[row][j], static_cast<float>(bl[static_cast<int64_t>(n) * a.r + j]), s);
-          if (a.base != nullptr) s += static_cast<float>(static_cast<const TO*>(a.base)[t * a.base_stride + n]);
-          static_cast<TO*>(a.out)[t * a.out_stride + n] = static_cast<TO>(s);
-        }
-      }
-      __syncthreads();
-    }
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  const uint32_t s_stage = smem_u32(smem), s_v = s_stage + S::kVAt, s_b = s_stage + S::kFront;
+  float* part = reinterpret_cast<float*>(smem);
+  LoraCtl& ctl = *reinterpret_cast<LoraCtl*>(smem + S::kFront + 2 * S::kB);
+  volatile int32_t* abort_flag = &ctl.abort_flag;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = static_cast<int>(cluster_ctarank());
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl.stage_done[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl.chunk_done[i], 1);
+    mbar_init(&ctl.drained, 1);
+    ctl.abort_flag = 0;
+    fence_mbar_init();
   }
+  if (warp == 0) tmem_alloc(&ctl.tmem_base, kLoraTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t lane_addr = static_cast<uint32_t>(warp % 4 * 32) << 16;
+
+  const int kblocks = (a.K + 63) / 64, kb0 = kblocks * rank / C, nkb = kblocks * (rank + 1) / C - kb0;
+  const int nchunks = (a.N + 127) / 128;
+  const int mine = nchunks > rank ? (nchunks - rank + C - 1) / C : 0;  // chunks of features: rank, rank + C, ...
+  uint32_t stage_phase = 0, chunk_phase = 0;  // a bit per barrier
+
+  auto wait = [&](uint64_t* bar, uint32_t& phases, int i) {
+    if (!mbar_wait_bounded(bar, (phases >> i) & 1u, abort_flag, kTimeoutNs)) {
+      *abort_flag = 1;
+      report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 1);
+    }
+    phases ^= 1u << i;
+  };
+
+  for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
+    if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
+    const int rows = min(tile.rows, 128);
+    const bool few = rows <= 16;
+    __syncthreads();
+    if (tid < rows) ctl.rows[tid] = src[tile.row0 + tid];
+    if (tile.adapter < 0) {  // base as it is
+      if (a.base == a.out) continue;
+      __syncthreads();
+      for (int n = (rank * 32 + lane) * 8; n < a.N; n += C * 256)
+        for (int row = warp; row < rows; row += kLoraThreads / 32) {
+          const int64_t t = ctl.rows[row];
+          Piece<TO> v;
+          v.load(static_cast<const TO*>(a.base), t * a.base_stride + n, a.N - n, a.wide);
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = v.get(i);
+          Piece<TO>::store(static_cast<TO*>(a.out), t * a.out_stride + n, a.N - n, a.wide, y);
+        }
+      continue;
+    }
+
+    // ------------------------------------------------------------ shrink --
+    const T* wa = static_cast<const T*>(a.a) + static_cast<int64_t>(tile.adapter) * a.r * a.K;
+    const T* wb = static_cast<const T*>(a.b) + static_cast<int64_t>(tile.adapter) * a.N * a.r;
+    const uint32_t idesc_a = kBf16 ? umma_idesc_bf16(128, RP) : umma_idesc_f16(128, RP);
+    auto load_chunk = [&](int j) {  // this CTA's j-th 128 features of B
+      constexpr int kRow = RP < 64 ? RP / 8 : 8;  // 16-byte pieces of a feature's row in a K chunk
+      const int n0 = (rank + C * j) * 128;
+      for (int i = tid; i < S::kChunks * 128 * kRow; i += kLoraThreads) {
+        const int c = i % kRow, n = i / kRow % 128, ch = i / (128 * kRow);
+        const int k = ch * 64 + c * 8;
+        if (n0 + n < a.N)
+          cp_async16_or_zero(s_b + (j & 1) * S::kB + ch * 16384 + swizzled(n, c), k < a.r ? wb + static_cast<int64_t>(n0 + n) * a.r + k : wb,
+                             k < a.r);
+      }
+    };
+    auto first_chunks = [&] {  // on the way while A x is computed
+      if (mine > 0) load_chunk(0);
+      if (mine > 1) load_chunk(1);
+    };
+    auto multiply_block = [&](uint32_t at_x, uint32_t at_a, bool first) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_bf16(tmem, sw128_kmajor_desc(at_x + kk * 32), sw128_kmajor_desc(at_a + kk * 32), idesc_a, !first || kk > 0);
+    };
+    if (few) {
+      // as many K blocks at once as fit: what counts here is the latency
+      const int row = tid / 8 % 16, c = tid % 8;
+      const T* xr = row < rows ? static_cast<const T*>(a.x) + src[tile.row0 + row] * a.x_stride : nullptr;
+      const uint32_t s_x = s_stage + S::kFew * RP * 128;
+      for (int kb = 0; kb < nkb; kb += S::kFew) {
+        const int nb = min(S::kFew, nkb - kb);
+        for (int i = tid / 8; i < nb * RP; i += kLoraThreads / 8) {
+          const int j = i % RP, k = (kb0 + kb + i / RP) * 64 + c * 8;
+          const bool valid = k < a.K && j < a.r;
+          cp_async16_or_zero(s_stage + i / RP * (RP * 128) + swizzled(j, c), valid ? wa + static_cast<int64_t>(j) * a.K + k : wa, valid);
+        }
+        if (xr != nullptr)
+          for (int q = tid / 128; q < nb; q += kLoraThreads / 128) {
+            const int k = (kb0 + kb + q) * 64 + c * 8;
+            cp_async16_or_zero(s_x + q * 2048 + swizzled(row, c), k < a.K ? xr + k : xr, k < a.K);
+          }
+        cp_async_commit();
+        if (kb == 0) {
+          first_chunks();
+          cp_async_commit();
+          cp_async_wait<1>();
+        } else {
+          cp_async_wait<0>();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+          tc_fence_after();
+          for (int q = 0; q < nb; ++q) multiply_block(s_x + q * 2048, s_stage + q * (RP * 128), kb + q == 0);
+          umma_commit(&ctl.stage_done[0]);
+        }
+        wait(&ctl.stage_done[0], stage_phase, 0);
+      }
+      if (nkb == 0) first_chunks();
+    } else {
+    const T* xr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = tid / 8 + 32 * i;
+      xr[i] = row < rows ? static_cast<const T*>(a.x) + src[tile.row0 + row] * a.x_stride : nullptr;
+    }
+    auto load_stage = [&](int kb, int stage) {
+      const uint32_t at = s_stage + stage * S::kStage;
+      const int k = (kb0 + kb) * 64 + (tid % 8) * 8;
+      const bool in = k < a.K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (xr[i] != nullptr) cp_async16_or_zero(at + swizzled(tid / 8 + 32 * i, tid % 8), in ? xr[i] + k : xr[i], in);
+#pragma unroll
+      for (int i = 0; i < (RP + 31) / 32; ++i) {
+        const int j = tid / 8 + 32 * i;
+        if (j < RP) {
+          const bool valid = in && j < a.r;
+          cp_async16_or_zero(at + S::kX + swizzled(j, tid % 8), valid ? wa + static_cast<int64_t>(j) * a.K + k : wa, valid);
+        }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      if (i < nkb) load_stage(i, i);
+      if (i == S::kStages - 2) first_chunks();
+      cp_async_commit();
+    }
+    int stage = 0;
+    for (int kb = 0; kb < nkb; ++kb) {
+      cp_async_wait<S::kStages - 2>();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+        multiply_block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
+        umma_commit(&ctl.stage_done[stage]);
+      }
+      const int last = stage == 0 ? S::kStages - 1 : stage - 1;  // the stage that block kb - 1 was in
+      if (kb > 0) wait(&ctl.stage_done[last], stage_phase, last);
+      if (kb + S::kStages - 1 < nkb) load_stage(kb + S::kStages - 1, last);
+      cp_async_commit();
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    if (nkb > 0) {
+      const int last = stage == 0 ? S::kStages - 1 : stage - 1;
+      wait(&ctl.stage_done[last], stage_phase, last);
+    }
+    }
+    cp_async_wait<0>();
+    tc_fence_after();
+    __syncthreads();  // (every thread's copies have landed: the stages' place is taken over)
+    {
+      constexpr int kCols = RP >= 32 ? RP / 2 : RP;  // columns of a warp: two warps to a quarter of the lanes
+      const int row = warp % 4 * 32 + lane, c0 = RP >= 32 ? warp / 4 * kCols : 0;
+      if (RP >= 32 || warp < 4) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          uint32_t v[16];
+          if (nkb > 0) {
+            tmem_ld16(tmem + lane_addr + c0 + c, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0u;
+          }
+          if (row < rows) {
+            uint4* p = reinterpret_cast<uint4*>(part + row * (RP + 4) + c0 + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+
+    // --------------------------------------------------------------- sum --
+    // A token's ranks lie on RP / 4 lanes.  Of many tokens each CTA adds its
+    // share and hands the result to all; of few, each adds all for itself.
+    {
+      constexpr int LT = RP / 4;
+      const float sc = a.scale != nullptr ? a.scale[tile.adapter] : 1.f;
+      const int todo = few ? rows : (rows - rank + C - 1) / C;  // (>= 0: rows > 16 > rank otherwise)
+      const int r0 = 4 * (tid % LT);
+      for (int i0 = 0; i0 < todo; i0 += kLoraThreads / LT) {
+        const int i = i0 + tid / LT;
+        const bool live = i < todo;
+        const int row = live ? (few ? i : rank + C * i) : 0;
+        const uint32_t at = s_stage + (row * (RP + 4) + r0) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) {
+          const float4 u = ld_cluster_f32x4(map_to_rank(at, c));
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        v.x *= sc, v.y *= sc, v.z *= sc, v.w *= sc;
+        float factor = 1.f;
+        if (!kBf16) {
+          // fp16 has 5 bits of exponent: the token's values are brought to [1, 2) by a power of two
+          float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+          for (int o = LT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t e = __float_as_uint(m) >> 23;
+          if (e > 0u && e < 254u) {
+            factor = __uint_as_float(e << 23);
+            const float inv = __uint_as_float((254u - e) << 23);
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+          }
+        }
+        const uint32_t h0 = pack2<T>(v.x, v.y), h1 = pack2<T>(v.z, v.w);
+        const uint32_t l0 = pack2<T>(rest_of<T>(v.x), rest_of<T>(v.y)), l1 = pack2<T>(rest_of<T>(v.z), rest_of<T>(v.w));
+        if (live) {
+          const uint32_t to = s_v + r0 / 64 * 16384 + swizzled(row, r0 % 64 / 8) + (r0 & 4) * 2;
+          const uint32_t f_at = smem_u32(&ctl.factor[row]);
+          for (int c = few ? rank : 0; c < (few ? rank + 1 : C); ++c) {
+            st_cluster_v2(map_to_rank(to, c), h0, h1);
+            st_cluster_v2(map_to_rank(to + S::kV, c), l0, l1);
+            if (!kBf16 && r0 == 0) st_cluster_u32(map_to_rank(f_at, c), __float_as_uint(factor));
+          }
+        }
+      }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    if (few) {
+      // (the others may still read this CTA's share: waited for after the last chunk)
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      __syncthreads();
+    } else {
+      cluster_sync_all();
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+
+    // ------------------------------------------------------------ expand --
+    const int n_mma = (rows + 15) / 16 * 16;
+    const uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, n_mma) : umma_idesc_f16(128, n_mma);
+    auto multiply = [&](int j) {
+      const uint32_t wt = s_b + (j & 1) * S::kB, d = tmem + (j & 1) * 128;
+#pragma unroll
+      for (int kk = 0; kk < 2 * (RP / 16); ++kk) {  // hi, then lo
+        const int q = kk % (RP / 16);
+        const uint32_t at = q / 4 * 16384 + q % 4 * 32;
+        umma_bf16(d, sw128_kmajor_desc(wt + at), sw128_kmajor_desc(s_v + (kk / (RP / 16)) * S::kV + at), idesc_b, kk > 0);
+      }
+      umma_commit(&ctl.chunk_done[j & 1]);
+    };
+    if (tid == 0 && mine > 0) {
+      tc_fence_after();
+      multiply(0);
+    }
+    // A warp has 32 features (its quarter of the lanes) and every second 16
+    // tokens.  It turns 16 x 32 sums through shared memory, so that a lane
+    // holds 8 neighbouring features of a token.
+    float* turn = reinterpret_cast<float*>(smem + S::kTurnAt) + warp * (kTurnTile / 4);
+    for (int j = 0; j < mine; ++j) {
+      const int n0 = (rank + C * j) * 128 + warp % 4 * 32;
+      const int n = n0 + lane % 4 * 8;
+      Piece<TO> bv[4][2];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = (2 * g + warp / 4) * 16 + h * 8 + lane / 4;
+          if (row < rows && n < a.N) bv[g][h].load(static_cast<const TO*>(a.base), ctl.rows[row] * a.base_stride + n, a.N - n, a.wide);
+        }
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0 && j + 1 < mine) {
+        tc_fence_after();
+        multiply(j + 1);
+      }
+      wait(&ctl.chunk_done[j & 1], chunk_phase, j & 1);
+      tc_fence_after();
+      if (j + 2 < mine) load_chunk(j + 2);
+      cp_async_commit();
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int t0 = (2 * g + warp / 4) * 16;
+        if (t0 >= rows) break;
+        uint32_t v[16];
+        tmem_ld16(tmem + (j & 1) * 128 + lane_addr + t0, v);
+        tmem_ld_wait();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) turn[i * kTurnRow + lane] = __uint_as_float(v[i]);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = h * 8 + lane / 4, row = t0 + i;
+          if (row < rows && n < a.N) {
+            float y[8];
+            const float f = kBf16 ? 1.f : ctl.factor[row];
+            const float4 lo = *reinterpret_cast<const float4*>(turn + i * kTurnRow + lane % 4 * 8);
+            const float4 hi = *reinterpret_cast<const float4*>(turn + i * kTurnRow + lane % 4 * 8 + 4);
+            const float u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = fmaf(u[q], f, bv[g][h].get(q));
+            Piece<TO>::store(static_cast<TO*>(a.out), ctl.rows[row] * a.out_stride + n, a.N - n, a.wide, y);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (few) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (tid == 0 && *abort_flag) {
+    volatile int32_t never = 0;
+    umma_commit(&ctl.drained);
+    if (!mbar_wait_bounded(&ctl.drained, 0, &never, kTimeoutNs)) report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 2);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kLoraTmemCols);
+  }
+}
+
+// CTAs of a cluster.
+#ifdef LORA_EXP
+int lora_cluster(int) { return atoi(getenv("LORA_C")); }
+#else
+int lora_cluster(int T) { return T <= 1024 ? 8 : 4; }
+#endif
+
+template <typename T, typename TO, int RP>
+cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  using S = LoraSmem<RP>;
+  auto kernel = lora_kernel<T, TO, RP>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kBytes);
+  if (e != cudaSuccess) return e;
+  const int C = lora_cluster(a.T);
+  // (clusters that do not fit wait; each takes every gridDim.x / C-th tile)
+  const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(max_tiles, std::max(1, 4 * num_sms / C)));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(clusters * C);
+  lc.blockDim = dim3(kLoraThreads);
+  lc.dynamicSmemBytes = S::kBytes;
+  lc.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, a, C);
+}
+
+template <typename T, typename TO>
+cudaError_t lora_by_rank(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  if (a.r <= 16) return lora_typed<T, TO, 16>(a, max_tiles, num_sms, stream);
+  if (a.r <= 32) return lora_typed<T, TO, 32>(a, max_tiles, num_sms, stream);
+  if (a.r <= 64) return lora_typed<T, TO, 64>(a, max_tiles, num_sms, stream);
+  return lora_typed<T, TO, 128>(a, max_tiles, num_sms, stream);
 }
 
 }  // namespace
@@ -173,14 +655,18 @@ cudaError_t launch_lora(const void* x, int dtype, int64_t x_stride, const void* 
                         const float* scale, int T, int K, int N, int r, int L, const void* plan, const void* base,
                         int64_t base_stride, void* out, int out_type, int64_t out_stride, int32_t* err, int num_sms,
                         cudaStream_t stream) {
+  auto rows16 = [&](const void* p, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * (out_type == MOE_F32 ? 4 : 2) % 16 == 0;
+  };
+  const bool wide = rows16(out, out_stride) && (base == nullptr || rows16(base, base_stride));
   const LoraArgs a{x, w_a, w_b, scale, static_cast<const unsigned char*>(plan), base, out,
-                   x_stride, base_stride, out_stride, T, K, N, r, L, err};
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(lora_max_tiles(T, L), 4 * num_sms)));
+                   x_stride, base_stride, out_stride, T, K, N, r, L, wide, err};
+  const int64_t tiles = lora_max_tiles(T, L);
   if (dtype == MOE_BF16)
-    return out_type == MOE_F32 ? launch_kernel(lora_kernel<__nv_bfloat16, float>, grid, dim3(256), 0, stream, a)
-                               : launch_kernel(lora_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(256), 0, stream, a);
-  return out_type == MOE_F32 ? launch_kernel(lora_kernel<__half, float>, grid, dim3(256), 0, stream, a)
-                             : launch_kernel(lora_kernel<__half, __half>, grid, dim3(256), 0, stream, a);
+    return out_type == MOE_F32 ? lora_by_rank<__nv_bfloat16, float>(a, tiles, num_sms, stream)
+                               : lora_by_rank<__nv_bfloat16, __nv_bfloat16>(a, tiles, num_sms, stream);
+  return out_type == MOE_F32 ? lora_by_rank<__half, float>(a, tiles, num_sms, stream)
+                             : lora_by_rank<__half, __half>(a, tiles, num_sms, stream);
 }
 
 }  // namespace moe

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 #include <utility>
 
 #include "device_cache.h"
@@ -238,7 +239,12 @@ struct LoraTile {
   int32_t adapter, row0, rows, pad;  // adapter -1: rows without one
 };
 constexpr int32_t kLoraPlanMagic = 0x4C6F5261;
-inline int lora_tile_rows(int) { return 128; }
+// Rows of a tile: few tokens in tiles of 16 or 32, so that their clusters cover the device.
+#ifdef LORA_EXP
+inline int lora_tile_rows(int T) { return atoi(getenv("LORA_M")); }
+#else
+inline int lora_tile_rows(int T) { return T <= 512 ? 16 : T <= 1024 ? 32 : T <= 2048 ? 64 : 128; }
+#endif
 // Tiles that T tokens can make: whole ones, and a partial one per adapter that occurs.
 inline int64_t lora_max_tiles(int T, int L) { return T / lora_tile_rows(T) + std::min<int64_t>(T, int64_t(L) + 1); }
 __host__ __device__ inline size_t lora_tiles_at(int T) {
