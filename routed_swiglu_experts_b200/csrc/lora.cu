@@ -129,14 +129,17 @@ struct LoraArgs {
   int32_t* err;
 };
 
-constexpr int kLoraThreads = 256;
+constexpr int kLoraWorkers = 256, kLoraThreads = kLoraWorkers + 32;  // and a warp that issues the MMAs
 constexpr uint32_t kLoraTmemCols = 256;
 constexpr int kTurnRow = 36, kTurnTile = 16 * kTurnRow * 4;  // 16 tokens x 32 features of a warp (rows padded: no bank conflicts)
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 
 struct LoraCtl {
-  uint64_t stage_done[4];  // the MMAs that read a stage are done
-  uint64_t chunk_done[2];  // ... a chunk of features
+  uint64_t full[4];        // a stage's copies have landed (every worker)
+  uint64_t empty[4];       // the MMAs that read a stage are done
+  uint64_t b_full[2];      // 128 features of B have landed
+  uint64_t acc_full[2];    // an accumulator is complete: features, or A x (the first)
+  uint64_t acc_empty[2];   // ... and read (every worker's warp)
   uint64_t drained;        // after a wait that gave up: every MMA is done
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -274,8 +277,15 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&ctl.stage_done[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&ctl.chunk_done[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ctl.full[i], kLoraWorkers);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.b_full[i], kLoraWorkers);
+      mbar_init(&ctl.acc_full[i], 1);
+      mbar_init(&ctl.acc_empty[i], kLoraWorkers / 32);
+    }
     mbar_init(&ctl.drained, 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
@@ -290,27 +300,100 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
   const int kblocks = (a.K + 63) / 64, kb0 = kblocks * rank / C, nkb = kblocks * (rank + 1) / C - kb0;
   const int nchunks = (a.N + 127) / 128;
   const int mine = nchunks > rank ? (nchunks - rank + C - 1) / C : 0;  // chunks of features: rank, rank + C, ...
-  uint32_t stage_phase = 0, chunk_phase = 0;  // a bit per barrier
 
-  auto wait = [&](uint64_t* bar, uint32_t& phases, int i) {
-    if (!mbar_wait_bounded(bar, (phases >> i) & 1u, abort_flag, kTimeoutNs)) {
+  // Waits for a barrier's next phase (`phases`: one bit per barrier).
+  auto wait = [&](uint64_t* bars, uint32_t& phases, int i) {
+    if (!mbar_wait_bounded(bars + i, (phases >> i) & 1u, abort_flag, kTimeoutNs)) {
       *abort_flag = 1;
       report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 1);
     }
     phases ^= 1u << i;
   };
 
+  if (warp == kLoraWorkers / 32) {
+    // -------------------------------------------------------- MMA issuer --
+    uint32_t full_ph = 0, b_ph = 0, empty_ph = 3;  // (both accumulators start empty)
+    const uint32_t idesc_a = kBf16 ? umma_idesc_bf16(128, RP) : umma_idesc_f16(128, RP);
+    for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
+      if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
+      if (tile.adapter < 0) continue;
+      const int rows = min(tile.rows, 128);
+      if (lane == 0 && nkb > 0) {
+        wait(ctl.acc_empty, empty_ph, 0);
+        auto block = [&](uint32_t at_x, uint32_t at_a, bool first) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem, sw128_kmajor_desc(at_x + kk * 32), sw128_kmajor_desc(at_a + kk * 32), idesc_a, !first || kk > 0);
+        };
+        if (rows <= 16) {
+          const uint32_t s_x = s_stage + S::kFew * RP * 128;
+          for (int kb = 0; kb < nkb; kb += S::kFew) {
+            wait(ctl.full, full_ph, 0);
+            fence_proxy_async_smem();
+            tc_fence_after();
+            for (int q = 0; q < min(S::kFew, nkb - kb); ++q) block(s_x + q * 2048, s_stage + q * (RP * 128), kb + q == 0);
+            umma_commit(&ctl.empty[0]);
+          }
+        } else {
+          int stage = 0;
+          for (int kb = 0; kb < nkb; ++kb) {
+            wait(ctl.full, full_ph, stage);
+            fence_proxy_async_smem();
+            tc_fence_after();
+            block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
+            umma_commit(&ctl.empty[stage]);
+            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+          }
+        }
+        umma_commit(&ctl.acc_full[0]);
+      }
+      __syncwarp();
+      cluster_sync_all();
+      if (rows <= 16) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        named_barrier_sync(1, kLoraThreads);
+      } else {
+        cluster_sync_all();
+      }
+      if (lane == 0) {
+        const int n_mma = (rows + 15) / 16 * 16;
+        const uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, n_mma) : umma_idesc_f16(128, n_mma);
+        for (int j = 0; j < mine; ++j) {
+          const uint32_t wt = s_b + (j & 1) * S::kB, d = tmem + (j & 1) * 128;
+          wait(ctl.acc_empty, empty_ph, j & 1);
+          wait(ctl.b_full, b_ph, j & 1);
+          asm volatile("fence.proxy.async;" ::: "memory");
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 2 * (RP / 16); ++kk) {  // hi, then lo
+            const int q = kk % (RP / 16);
+            const uint32_t at = q / 4 * 16384 + q % 4 * 32;
+            umma_bf16(d, sw128_kmajor_desc(wt + at), sw128_kmajor_desc(s_v + (kk / (RP / 16)) * S::kV + at), idesc_b, kk > 0);
+          }
+          umma_commit(&ctl.acc_full[j & 1]);
+        }
+      }
+      __syncwarp();
+      if (rows <= 16) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    if (lane == 0 && *abort_flag) {
+      volatile int32_t never = 0;
+      umma_commit(&ctl.drained);
+      if (!mbar_wait_bounded(&ctl.drained, 0, &never, kTimeoutNs)) report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 2);
+    }
+  } else {
+  uint32_t empty_ph = 0xF, full_ph = 0;  // (every stage starts empty)
   for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
     if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
     const int rows = min(tile.rows, 128);
     const bool few = rows <= 16;
-    __syncthreads();
+    named_barrier_sync(2, kLoraWorkers);
     if (tid < rows) ctl.rows[tid] = src[tile.row0 + tid];
     if (tile.adapter < 0) {  // base as it is
       if (a.base == a.out) continue;
-      __syncthreads();
+      named_barrier_sync(2, kLoraWorkers);
       for (int n = (rank * 32 + lane) * 8; n < a.N; n += C * 256)
-        for (int row = warp; row < rows; row += kLoraThreads / 32) {
+        for (int row = warp; row < rows; row += kLoraWorkers / 32) {
           const int64_t t = ctl.rows[row];
           Piece<TO> v;
           v.load(static_cast<const TO*>(a.base), t * a.base_stride + n, a.N - n, a.wide);
@@ -325,26 +408,21 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
     // ------------------------------------------------------------ shrink --
     const T* wa = static_cast<const T*>(a.a) + static_cast<int64_t>(tile.adapter) * a.r * a.K;
     const T* wb = static_cast<const T*>(a.b) + static_cast<int64_t>(tile.adapter) * a.N * a.r;
-    const uint32_t idesc_a = kBf16 ? umma_idesc_bf16(128, RP) : umma_idesc_f16(128, RP);
     auto load_chunk = [&](int j) {  // this CTA's j-th 128 features of B
       constexpr int kRow = RP < 64 ? RP / 8 : 8;  // 16-byte pieces of a feature's row in a K chunk
       const int n0 = (rank + C * j) * 128;
-      for (int i = tid; i < S::kChunks * 128 * kRow; i += kLoraThreads) {
+      for (int i = tid; i < S::kChunks * 128 * kRow; i += kLoraWorkers) {
         const int c = i % kRow, n = i / kRow % 128, ch = i / (128 * kRow);
         const int k = ch * 64 + c * 8;
         if (n0 + n < a.N)
           cp_async16_or_zero(s_b + (j & 1) * S::kB + ch * 16384 + swizzled(n, c), k < a.r ? wb + static_cast<int64_t>(n0 + n) * a.r + k : wb,
                              k < a.r);
       }
+      cp_async_mbar_arrive(&ctl.b_full[j & 1]);
     };
     auto first_chunks = [&] {  // on the way while A x is computed
       if (mine > 0) load_chunk(0);
       if (mine > 1) load_chunk(1);
-    };
-    auto multiply_block = [&](uint32_t at_x, uint32_t at_a, bool first) {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_bf16(tmem, sw128_kmajor_desc(at_x + kk * 32), sw128_kmajor_desc(at_a + kk * 32), idesc_a, !first || kk > 0);
     };
     if (few) {
       // as many K blocks at once as fit: what counts here is the latency
@@ -353,33 +431,19 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
       const uint32_t s_x = s_stage + S::kFew * RP * 128;
       for (int kb = 0; kb < nkb; kb += S::kFew) {
         const int nb = min(S::kFew, nkb - kb);
-        for (int i = tid / 8; i < nb * RP; i += kLoraThreads / 8) {
+        wait(ctl.empty, empty_ph, 0);
+        for (int i = tid / 8; i < nb * RP; i += kLoraWorkers / 8) {
           const int j = i % RP, k = (kb0 + kb + i / RP) * 64 + c * 8;
           const bool valid = k < a.K && j < a.r;
           cp_async16_or_zero(s_stage + i / RP * (RP * 128) + swizzled(j, c), valid ? wa + static_cast<int64_t>(j) * a.K + k : wa, valid);
         }
         if (xr != nullptr)
-          for (int q = tid / 128; q < nb; q += kLoraThreads / 128) {
+          for (int q = tid / 128; q < nb; q += kLoraWorkers / 128) {
             const int k = (kb0 + kb + q) * 64 + c * 8;
             cp_async16_or_zero(s_x + q * 2048 + swizzled(row, c), k < a.K ? xr + k : xr, k < a.K);
           }
-        cp_async_commit();
-        if (kb == 0) {
-          first_chunks();
-          cp_async_commit();
-          cp_async_wait<1>();
-        } else {
-          cp_async_wait<0>();
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-          tc_fence_after();
-          for (int q = 0; q < nb; ++q) multiply_block(s_x + q * 2048, s_stage + q * (RP * 128), kb + q == 0);
-          umma_commit(&ctl.stage_done[0]);
-        }
-        wait(&ctl.stage_done[0], stage_phase, 0);
+        cp_async_mbar_arrive(&ctl.full[0]);
+        if (kb == 0) first_chunks();
       }
       if (nkb == 0) first_chunks();
     } else {
@@ -405,37 +469,19 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
         }
       }
     };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      if (i < nkb) load_stage(i, i);
-      if (i == S::kStages - 2) first_chunks();
-      cp_async_commit();
-    }
     int stage = 0;
     for (int kb = 0; kb < nkb; ++kb) {
-      cp_async_wait<S::kStages - 2>();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        multiply_block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
-        umma_commit(&ctl.stage_done[stage]);
-      }
-      const int last = stage == 0 ? S::kStages - 1 : stage - 1;  // the stage that block kb - 1 was in
-      if (kb > 0) wait(&ctl.stage_done[last], stage_phase, last);
-      if (kb + S::kStages - 1 < nkb) load_stage(kb + S::kStages - 1, last);
-      cp_async_commit();
+      wait(ctl.empty, empty_ph, stage);
+      load_stage(kb, stage);
+      cp_async_mbar_arrive(&ctl.full[stage]);
+      if (kb == min(nkb, S::kStages) - 1) first_chunks();
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
-    if (nkb > 0) {
-      const int last = stage == 0 ? S::kStages - 1 : stage - 1;
-      wait(&ctl.stage_done[last], stage_phase, last);
+    if (nkb == 0) first_chunks();
     }
-    }
-    cp_async_wait<0>();
+    // (complete: every copy into the stages has been read, their place is taken over)
+    if (nkb > 0) wait(ctl.acc_full, full_ph, 0);
     tc_fence_after();
-    __syncthreads();  // (every thread's copies have landed: the stages' place is taken over)
     {
       constexpr int kCols = RP >= 32 ? RP / 2 : RP;  // columns of a warp: two warps to a quarter of the lanes
       const int row = warp % 4 * 32 + lane, c0 = RP >= 32 ? warp / 4 * kCols : 0;
@@ -459,6 +505,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
       }
     }
     tc_fence_before();
+    if (nkb > 0 && lane == 0) mbar_arrive(&ctl.acc_empty[0]);
     cluster_sync_all();
 
     // --------------------------------------------------------------- sum --
@@ -469,7 +516,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
       const float sc = a.scale != nullptr ? a.scale[tile.adapter] : 1.f;
       const int todo = few ? rows : (rows - rank + C - 1) / C;  // (>= 0: rows > 16 > rank otherwise)
       const int r0 = 4 * (tid % LT);
-      for (int i0 = 0; i0 < todo; i0 += kLoraThreads / LT) {
+      for (int i0 = 0; i0 < todo; i0 += kLoraWorkers / LT) {
         const int i = i0 + tid / LT;
         const bool live = i < todo;
         const int row = live ? (few ? i : rank + C * i) : 0;
@@ -511,29 +558,12 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
     if (few) {
       // (the others may still read this CTA's share: waited for after the last chunk)
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      __syncthreads();
+      named_barrier_sync(1, kLoraThreads);
     } else {
       cluster_sync_all();
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
 
     // ------------------------------------------------------------ expand --
-    const int n_mma = (rows + 15) / 16 * 16;
-    const uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, n_mma) : umma_idesc_f16(128, n_mma);
-    auto multiply = [&](int j) {
-      const uint32_t wt = s_b + (j & 1) * S::kB, d = tmem + (j & 1) * 128;
-#pragma unroll
-      for (int kk = 0; kk < 2 * (RP / 16); ++kk) {  // hi, then lo
-        const int q = kk % (RP / 16);
-        const uint32_t at = q / 4 * 16384 + q % 4 * 32;
-        umma_bf16(d, sw128_kmajor_desc(wt + at), sw128_kmajor_desc(s_v + (kk / (RP / 16)) * S::kV + at), idesc_b, kk > 0);
-      }
-      umma_commit(&ctl.chunk_done[j & 1]);
-    };
-    if (tid == 0 && mine > 0) {
-      tc_fence_after();
-      multiply(0);
-    }
     // A warp has 32 features (its quarter of the lanes) and every second 16
     // tokens.  It turns 16 x 32 sums through shared memory, so that a lane
     // holds 8 neighbouring features of a token.
@@ -549,18 +579,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           const int row = (2 * g + warp / 4) * 16 + h * 8 + lane / 4;
           if (row < rows && n < a.N) bv[g][h].load(static_cast<const TO*>(a.base), ctl.rows[row] * a.base_stride + n, a.N - n, a.wide);
         }
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0 && j + 1 < mine) {
-        tc_fence_after();
-        multiply(j + 1);
-      }
-      wait(&ctl.chunk_done[j & 1], chunk_phase, j & 1);
+      wait(ctl.acc_full, full_ph, j & 1);
       tc_fence_after();
       if (j + 2 < mine) load_chunk(j + 2);
-      cp_async_commit();
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int t0 = (2 * g + warp / 4) * 16;
@@ -587,14 +608,12 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.acc_empty[j & 1]);
     }
-    cp_async_wait<0>();
     if (few) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
-  if (tid == 0 && *abort_flag) {
-    volatile int32_t never = 0;
-    umma_commit(&ctl.drained);
-    if (!mbar_wait_bounded(&ctl.drained, 0, &never, kTimeoutNs)) report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -608,7 +627,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
 #ifdef LORA_EXP
 int lora_cluster(int) { return atoi(getenv("LORA_C")); }
 #else
-int lora_cluster(int T) { return T <= 1024 ? 8 : 4; }
+int lora_cluster(int T) { return T <= 4096 ? 8 : 4; }
 #endif
 
 template <typename T, typename TO, int RP>
