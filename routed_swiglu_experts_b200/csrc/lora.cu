@@ -110,11 +110,12 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
 //   sum     the CTAs' shares are added through distributed shared memory, scaled
 //           and split into two 16-bit values hi + lo (the second is what the
 //           rounding of the first left), so that 16 bits or more of A x count
-//   expand  each CTA takes every C-th 128 features: D[feature, token] in TMEM, B
-//           as M, hi and lo as N, added to base by the epilogue: a lane holds a
-//           feature, so a warp reads and writes 32 neighbours of a token's row
-// Operands lie in shared memory as K-major rows of 128 bytes, 128-byte swizzle,
-// written by cp.async (rows of x come from anywhere).
+//   expand  each CTA takes every C-th 128 features: D[token, feature], hi and lo as
+//           M, B as N; base comes through shared memory 128 bytes of a row at a
+//           time, is added to in place, and the rows leave from there
+// Operands lie in shared memory as K-major rows of 128 bytes, 128-byte swizzle:
+// A and B by TMA (which fills up ranks, features and K with zeros), x and base by
+// cp.async, since their rows come from anywhere.
 struct LoraArgs {
   const void* x;
   const void* a;
@@ -131,11 +132,10 @@ struct LoraArgs {
 
 constexpr int kLoraWorkers = 256, kLoraThreads = kLoraWorkers + 32;  // and a warp that issues the MMAs
 constexpr uint32_t kLoraTmemCols = 256;
-constexpr int kTurnRow = 36, kTurnTile = 16 * kTurnRow * 4;  // 16 tokens x 32 features of a warp (rows padded: no bank conflicts)
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 
 struct LoraCtl {
-  uint64_t full[4];        // a stage's copies have landed (every worker)
+  uint64_t full[4];        // a stage's copies have landed (every worker's, and A)
   uint64_t empty[4];       // the MMAs that read a stage are done
   uint64_t b_full[2];      // 128 features of B have landed
   uint64_t acc_full[2];    // an accumulator is complete: features, or A x (the first)
@@ -144,35 +144,57 @@ struct LoraCtl {
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t rows[128];       // the tile's tokens
-  float factor[128];       // fp16: what a token's hi and lo are to be multiplied by
+  uint8_t exponent[128];   // fp16: what a token's hi and lo are to be multiplied by, 2^(exponent - 127)
+};
+
+// Maps of A [L, r, K] and B [L, N, r], boxes of 64 along the last dimension.
+struct alignas(64) LoraMaps {
+  CUtensorMap a, b;
 };
 
 template <int RP>
 struct LoraSmem {
   static constexpr int kX = 128 * 128, kA = RP * 128, kStage = kX + kA;
-  static constexpr int kStages = RP == 16 || RP == 128 ? 4 : 3;
+  static constexpr int kStages = RP == 128 ? 4 : 3;
   static constexpr int kChunks = RP == 128 ? 2 : 1;     // K chunks of 64 of the expand operands
   static constexpr int kB = kChunks * 128 * 128;        // 128 features of B
-  // over the stages, once A x is summed: this CTA's share of it (of up to 16
-  // tokens while the epilogue runs, whose warps' tiles lie behind), then hi and lo
-  static constexpr int kPart = 128 * (RP + 4) * 4, kTurnAt = 16 * (RP + 4) * 4, kTurn = kTurnAt + 8 * kTurnTile;
-  static constexpr int kVAt = ((kPart > kTurn ? kPart : kTurn) + 1023) / 1024 * 1024;
-  static constexpr int kV = kChunks * 128 * 128;
-  static constexpr int kFront = kVAt + 2 * kV > kStages * kStage ? kVAt + 2 * kV : kStages * kStage;
-  // (two CTAs of 256 TMEM columns fit an SM, a third must not start: it would
-  // wait for columns that CTAs of waiting clusters hold)
-  static constexpr int kBytes = 1024 + kFront + 2 * kB + static_cast<int>(sizeof(LoraCtl));
+  // In the stages' place, once A x is summed: hi and lo (side by side in one
+  // row where both fit), and kBoxes boxes of base, 128 bytes of each token; until
+  // then this CTA's share of A x lies where the boxes will be.
+  static constexpr int kLoAt = RP <= 32 ? 2 * RP : kChunks * 128 * 128;  // lo behind hi, bytes
+  static constexpr int kV = RP <= 32 ? 128 * 128 : 2 * kChunks * 128 * 128;
+  static constexpr int kBoxes = RP == 128 ? 4 : 3;
+  static constexpr int kPart = (128 * (RP + 4) * 4 + 1023) / 1024 * 1024;
+  static constexpr int kAfter = kV + (kPart > kBoxes * 16384 ? kPart : kBoxes * 16384);
+  static constexpr int kFront = kAfter > kStages * kStage ? kAfter : kStages * kStage;
   // K blocks of tiles of at most 16 tokens, loaded at once: A, then 16 rows of x
   // each (as the M operand 128 rows are read: what follows gives rows that are
   // not used, and lies within the block's shared memory)
   static constexpr int kFew = kFront / (RP * 128 + 2048);
   static_assert(16384 <= 2 * kB, "the last rows that are read");
+  // (two CTAs of 256 TMEM columns fit an SM, a third must not start: it would
+  // wait for columns that CTAs of waiting clusters hold)
+  static constexpr int kBytes = kFront + 2 * kB + static_cast<int>(sizeof(LoraCtl));
   static_assert(kFront % 1024 == 0 && 3 * kBytes > 227 * 1024 && kBytes <= 232448, "shared memory of an SM");
+  static_assert(RP == 128 || 2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
 // 16 bytes, or zeros where !valid.
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u) : "memory");
+}
+
+// The first `bytes` (0 to 16) of 16 bytes, zeros behind them.
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk16) { return row * 128 + ((chunk16 ^ (row & 7)) << 4); }
@@ -198,78 +220,95 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// Eight neighbouring values of a row: 16 bytes at a time where every row allows
-// it (wide) and all eight are there, else one by one (`left` of them).
+// 16 bytes of a row as numbers and back.
+__device__ __forceinline__ void unpack16(uint4 w, float (&y)[4], float) {
+  y[0] = __uint_as_float(w.x), y[1] = __uint_as_float(w.y), y[2] = __uint_as_float(w.z), y[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack16(uint4 w, float (&y)[8], __nv_bfloat16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[2 * i] = bf16lo(u[i]), y[2 * i + 1] = bf16hi(u[i]);
+}
+__device__ __forceinline__ void unpack16(uint4 w, float (&y)[8], __half) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    y[2 * i] = f.x, y[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 pack16(const float (&y)[4], float) {
+  return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float (&y)[8], T) {
+  return make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+}
+
+// 16 bytes of base from `at` on, `left` values of them there (left > 0), to
+// shared memory: by cp.async where every row starts on 16 bytes (wide), else value
+// by value.  No base: zeros.
 template <typename TO>
-struct Piece {
-  static constexpr int kWords = sizeof(TO) * 2;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const TO* base, int64_t at, int left, bool wide) {
+__device__ __forceinline__ void base_to_shared(uint32_t dst, const TO* base, int64_t at, int left, bool wide) {
+  constexpr int kPer = 16 / sizeof(TO);
+  if (base == nullptr) {
+    sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+  } else if (wide) {
+    cp_async16_part(dst, base + at, static_cast<uint32_t>(min(left, kPer) * static_cast<int>(sizeof(TO))));
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-    if (base == nullptr) return;
-    const TO* p = base + at;
-    if (wide && left >= 8) {
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) set(i, p[i]);
-    }
-  }
-  __device__ __forceinline__ void set(int i, TO v) {
-    if constexpr (sizeof(TO) == 4)
-      w[i] = __float_as_uint(v);
-    else
-      w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v)) << (i % 2 * 16);
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (sizeof(TO) == 4) return __uint_as_float(w[i]);
-    const uint16_t b = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
-    return static_cast<float>(*reinterpret_cast<const TO*>(&b));
-  }
-  static __device__ __forceinline__ void store(TO* out, int64_t at, int left, bool wide, const float (&y)[8]) {
-    TO* p = out + at;
-    if (wide && left >= 8) {
-      uint32_t v[kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
+    for (int i = 0; i < kPer; ++i)
+      if (i < left) {
+        const TO v = base[at + i];
         if constexpr (sizeof(TO) == 4)
-          v[i] = __float_as_uint(y[i]);
+          w[i] = __float_as_uint(v);
         else
-          v[i] = pack2<TO>(y[2 * i], y[2 * i + 1]);
+          w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v)) << (i % 2 * 16);
       }
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = static_cast<TO>(y[i]);
-    }
+    sts128(dst, make_uint4(w[0], w[1], w[2], w[3]));
   }
-};
+}
+template <typename TO>
+__device__ __forceinline__ void shared_to_out(TO* out, int64_t at, int left, bool wide, uint4 v) {
+  constexpr int kPer = 16 / sizeof(TO);
+  if (wide && left >= kPer) {
+    *reinterpret_cast<uint4*>(out + at) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < left) {
+        if constexpr (sizeof(TO) == 4) {
+          out[at + i] = __uint_as_float(w[i]);
+        } else {
+          const uint16_t b = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+          out[at + i] = *reinterpret_cast<const TO*>(&b);
+        }
+      }
+  }
+}
+
+__device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 template <typename T, typename TO, int RP>
-__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(const LoraArgs a, const int C) {
+__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
+    lora_kernel(const __grid_constant__ LoraMaps maps, const LoraArgs a, const int C) {
   using S = LoraSmem<RP>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const LoraPlan head = *reinterpret_cast<const LoraPlan*>(a.plan);
   const int32_t* src = reinterpret_cast<const int32_t*>(a.plan + sizeof(LoraPlan));
   const LoraTile* tiles = reinterpret_cast<const LoraTile*>(a.plan + lora_tiles_at(a.T));
   LoraTile tile = tiles[blockIdx.x / C];  // (the plan has room for one per cluster; read before the head is known)
-  if (head.magic != kLoraPlanMagic || head.T != a.T || head.L != a.L) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err, MOE_ERR_INVALID_ARG, 0);
+  const bool placed = (smem_u32(smem_raw) & 1023u) == 0;  // (the swizzle goes by address)
+  if (!placed || head.magic != kLoraPlanMagic || head.T != a.T || head.L != a.L) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err, placed ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED, 0);
     return;
   }
-  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                         ~static_cast<uintptr_t>(1023));
-  const uint32_t s_stage = smem_u32(smem), s_v = s_stage + S::kVAt, s_b = s_stage + S::kFront;
-  float* part = reinterpret_cast<float*>(smem);
+  unsigned char* smem = smem_raw;
+  const uint32_t s_stage = smem_u32(smem), s_v = s_stage, s_box = s_stage + S::kV, s_b = s_stage + S::kFront;
   LoraCtl& ctl = *reinterpret_cast<LoraCtl*>(smem + S::kFront + 2 * S::kB);
   volatile int32_t* abort_flag = &ctl.abort_flag;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -278,17 +317,21 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&ctl.full[i], kLoraWorkers);
+      mbar_init(&ctl.full[i], kLoraWorkers + 1);
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.b_full[i], kLoraWorkers);
+      mbar_init(&ctl.b_full[i], 1);
       mbar_init(&ctl.acc_full[i], 1);
       mbar_init(&ctl.acc_empty[i], kLoraWorkers / 32);
     }
     mbar_init(&ctl.drained, 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
+  }
+  if (tid == kLoraWorkers) {
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
   }
   if (warp == 0) tmem_alloc(&ctl.tmem_base, kLoraTmemCols);
   tc_fence_before();
@@ -312,12 +355,23 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
 
   if (warp == kLoraWorkers / 32) {
     // -------------------------------------------------------- MMA issuer --
-    uint32_t full_ph = 0, b_ph = 0, empty_ph = 3;  // (both accumulators start empty)
+    uint32_t full_ph = 0, b_ph = 0, acc_ph = 0, empty_ph = 3;  // (both accumulators start empty)
+    auto load_chunk = [&](int j) {  // this CTA's j-th 128 features of B
+      mbar_arrive_expect_tx(&ctl.b_full[j & 1], S::kB);
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c)
+        tma_load_3d(smem + S::kFront + (j & 1) * S::kB + c * 16384, &maps.b, c * 64, (rank + C * j) * 128, tile.adapter,
+                    &ctl.b_full[j & 1]);
+    };
     const uint32_t idesc_a = kBf16 ? umma_idesc_bf16(128, RP) : umma_idesc_f16(128, RP);
     for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
       if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
       if (tile.adapter < 0) continue;
       const int rows = min(tile.rows, 128);
+      if (lane == 0) {
+        if (mine > 0) load_chunk(0);
+        if (mine > 1) load_chunk(1);
+      }
       if (lane == 0 && nkb > 0) {
         wait(ctl.acc_empty, empty_ph, 0);
         auto block = [&](uint32_t at_x, uint32_t at_a, bool first) {
@@ -346,6 +400,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           }
         }
         umma_commit(&ctl.acc_full[0]);
+        wait(ctl.acc_full, acc_ph, 0);
       }
       __syncwarp();
       cluster_sync_all();
@@ -356,10 +411,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
         cluster_sync_all();
       }
       if (lane == 0) {
-        const int n_mma = (rows + 15) / 16 * 16;
-        const uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, n_mma) : umma_idesc_f16(128, n_mma);
+        constexpr uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, 128) : umma_idesc_f16(128, 128);
         for (int j = 0; j < mine; ++j) {
           const uint32_t wt = s_b + (j & 1) * S::kB, d = tmem + (j & 1) * 128;
+          if (j > 0) {
+            wait(ctl.acc_full, acc_ph, (j - 1) & 1);  // (its B buffer is free)
+            if (j + 1 < mine) load_chunk(j + 1);
+          }
           wait(ctl.acc_empty, empty_ph, j & 1);
           wait(ctl.b_full, b_ph, j & 1);
           asm volatile("fence.proxy.async;" ::: "memory");
@@ -368,10 +426,11 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           for (int kk = 0; kk < 2 * (RP / 16); ++kk) {  // hi, then lo
             const int q = kk % (RP / 16);
             const uint32_t at = q / 4 * 16384 + q % 4 * 32;
-            umma_bf16(d, sw128_kmajor_desc(wt + at), sw128_kmajor_desc(s_v + (kk / (RP / 16)) * S::kV + at), idesc_b, kk > 0);
+            umma_bf16(d, sw128_kmajor_desc(s_v + (kk >= RP / 16 ? S::kLoAt : 0) + at), sw128_kmajor_desc(wt + at), idesc_b, kk > 0);
           }
           umma_commit(&ctl.acc_full[j & 1]);
         }
+        if (mine > 0) wait(ctl.acc_full, acc_ph, (mine - 1) & 1);
       }
       __syncwarp();
       if (rows <= 16) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -387,43 +446,30 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
     if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
     const int rows = min(tile.rows, 128);
     const bool few = rows <= 16;
+    // this CTA's share of A x: where the boxes will be (few tokens: in the first
+    // one's rows behind them, the other CTAs read it while boxes arrive)
+    const int part_at = S::kV + (few ? 2048 : 0);
+    static_assert(2048 + 16 * (RP + 4) * 4 <= 16384, "in one box");
+    fence_proxy_async_smem();  // (the last tile's loads and stores are behind, copies of A may follow)
     named_barrier_sync(2, kLoraWorkers);
     if (tid < rows) ctl.rows[tid] = src[tile.row0 + tid];
     if (tile.adapter < 0) {  // base as it is
       if (a.base == a.out) continue;
       named_barrier_sync(2, kLoraWorkers);
-      for (int n = (rank * 32 + lane) * 8; n < a.N; n += C * 256)
+      constexpr int kPer = 16 / sizeof(TO);
+      for (int n = (rank * 32 + lane) * kPer; n < a.N; n += C * 32 * kPer)
         for (int row = warp; row < rows; row += kLoraWorkers / 32) {
           const int64_t t = ctl.rows[row];
-          Piece<TO> v;
-          v.load(static_cast<const TO*>(a.base), t * a.base_stride + n, a.N - n, a.wide);
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = v.get(i);
-          Piece<TO>::store(static_cast<TO*>(a.out), t * a.out_stride + n, a.N - n, a.wide, y);
+          const uint32_t at = s_stage + tid * 16;
+          base_to_shared(at, static_cast<const TO*>(a.base), t * a.base_stride + n, a.N - n, a.wide);
+          cp_async_commit();
+          cp_async_wait<0>();
+          shared_to_out(static_cast<TO*>(a.out), t * a.out_stride + n, a.N - n, a.wide, lds128(at));
         }
       continue;
     }
 
     // ------------------------------------------------------------ shrink --
-    const T* wa = static_cast<const T*>(a.a) + static_cast<int64_t>(tile.adapter) * a.r * a.K;
-    const T* wb = static_cast<const T*>(a.b) + static_cast<int64_t>(tile.adapter) * a.N * a.r;
-    auto load_chunk = [&](int j) {  // this CTA's j-th 128 features of B
-      constexpr int kRow = RP < 64 ? RP / 8 : 8;  // 16-byte pieces of a feature's row in a K chunk
-      const int n0 = (rank + C * j) * 128;
-      for (int i = tid; i < S::kChunks * 128 * kRow; i += kLoraWorkers) {
-        const int c = i % kRow, n = i / kRow % 128, ch = i / (128 * kRow);
-        const int k = ch * 64 + c * 8;
-        if (n0 + n < a.N)
-          cp_async16_or_zero(s_b + (j & 1) * S::kB + ch * 16384 + swizzled(n, c), k < a.r ? wb + static_cast<int64_t>(n0 + n) * a.r + k : wb,
-                             k < a.r);
-      }
-      cp_async_mbar_arrive(&ctl.b_full[j & 1]);
-    };
-    auto first_chunks = [&] {  // on the way while A x is computed
-      if (mine > 0) load_chunk(0);
-      if (mine > 1) load_chunk(1);
-    };
     if (few) {
       // as many K blocks at once as fit: what counts here is the latency
       const int row = tid / 8 % 16, c = tid % 8;
@@ -432,10 +478,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
       for (int kb = 0; kb < nkb; kb += S::kFew) {
         const int nb = min(S::kFew, nkb - kb);
         wait(ctl.empty, empty_ph, 0);
-        for (int i = tid / 8; i < nb * RP; i += kLoraWorkers / 8) {
-          const int j = i % RP, k = (kb0 + kb + i / RP) * 64 + c * 8;
-          const bool valid = k < a.K && j < a.r;
-          cp_async16_or_zero(s_stage + i / RP * (RP * 128) + swizzled(j, c), valid ? wa + static_cast<int64_t>(j) * a.K + k : wa, valid);
+        if (tid == 0) {
+          mbar_arrive_expect_tx(&ctl.full[0], nb * (RP * 128));
+          for (int q = 0; q < nb; ++q)
+            tma_load_3d(smem + q * (RP * 128), &maps.a, (kb0 + kb + q) * 64, 0, tile.adapter, &ctl.full[0]);
         }
         if (xr != nullptr)
           for (int q = tid / 128; q < nb; q += kLoraWorkers / 128) {
@@ -443,9 +489,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
             cp_async16_or_zero(s_x + q * 2048 + swizzled(row, c), k < a.K ? xr + k : xr, k < a.K);
           }
         cp_async_mbar_arrive(&ctl.full[0]);
-        if (kb == 0) first_chunks();
       }
-      if (nkb == 0) first_chunks();
     } else {
     const T* xr[4];
 #pragma unroll
@@ -460,13 +504,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (xr[i] != nullptr) cp_async16_or_zero(at + swizzled(tid / 8 + 32 * i, tid % 8), in ? xr[i] + k : xr[i], in);
-#pragma unroll
-      for (int i = 0; i < (RP + 31) / 32; ++i) {
-        const int j = tid / 8 + 32 * i;
-        if (j < RP) {
-          const bool valid = in && j < a.r;
-          cp_async16_or_zero(at + S::kX + swizzled(j, tid % 8), valid ? wa + static_cast<int64_t>(j) * a.K + k : wa, valid);
-        }
+      if (tid == 0) {
+        mbar_arrive_expect_tx(&ctl.full[stage], S::kA);
+        tma_load_3d(smem + stage * S::kStage + S::kX, &maps.a, (kb0 + kb) * 64, 0, tile.adapter, &ctl.full[stage]);
       }
     };
     int stage = 0;
@@ -474,10 +514,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
       wait(ctl.empty, empty_ph, stage);
       load_stage(kb, stage);
       cp_async_mbar_arrive(&ctl.full[stage]);
-      if (kb == min(nkb, S::kStages) - 1) first_chunks();
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
-    if (nkb == 0) first_chunks();
     }
     // (complete: every copy into the stages has been read, their place is taken over)
     if (nkb > 0) wait(ctl.acc_full, full_ph, 0);
@@ -497,7 +535,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
             for (int i = 0; i < 16; ++i) v[i] = 0u;
           }
           if (row < rows) {
-            uint4* p = reinterpret_cast<uint4*>(part + row * (RP + 4) + c0 + c);
+            uint4* p = reinterpret_cast<uint4*>(smem + part_at + (row * (RP + 4) + c0 + c) * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
@@ -520,7 +558,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
         const int i = i0 + tid / LT;
         const bool live = i < todo;
         const int row = live ? (few ? i : rank + C * i) : 0;
-        const uint32_t at = s_stage + (row * (RP + 4) + r0) * 4;
+        const uint32_t at = s_stage + part_at + (row * (RP + 4) + r0) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < C; ++c) {
@@ -528,7 +566,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
         }
         v.x *= sc, v.y *= sc, v.z *= sc, v.w *= sc;
-        float factor = 1.f;
+        uint32_t exponent = 127u;
         if (!kBf16) {
           // fp16 has 5 bits of exponent: the token's values are brought to [1, 2) by a power of two
           float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -536,7 +574,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
           for (int o = LT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const uint32_t e = __float_as_uint(m) >> 23;
           if (e > 0u && e < 254u) {
-            factor = __uint_as_float(e << 23);
+            exponent = e;
             const float inv = __uint_as_float((254u - e) << 23);
             v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
           }
@@ -545,11 +583,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
         const uint32_t l0 = pack2<T>(rest_of<T>(v.x), rest_of<T>(v.y)), l1 = pack2<T>(rest_of<T>(v.z), rest_of<T>(v.w));
         if (live) {
           const uint32_t to = s_v + r0 / 64 * 16384 + swizzled(row, r0 % 64 / 8) + (r0 & 4) * 2;
-          const uint32_t f_at = smem_u32(&ctl.factor[row]);
+          const int k_lo = RP <= 32 ? RP + r0 : r0;  // lo's column in its row
+          const uint32_t lo = s_v + (RP <= 32 ? 0 : S::kLoAt) + k_lo / 64 * 16384 + swizzled(row, k_lo % 64 / 8) + (k_lo & 4) * 2;
+          const uint32_t e_at = smem_u32(&ctl.exponent[row]);
           for (int c = few ? rank : 0; c < (few ? rank + 1 : C); ++c) {
             st_cluster_v2(map_to_rank(to, c), h0, h1);
-            st_cluster_v2(map_to_rank(to + S::kV, c), l0, l1);
-            if (!kBf16 && r0 == 0) st_cluster_u32(map_to_rank(f_at, c), __float_as_uint(factor));
+            st_cluster_v2(map_to_rank(lo, c), l0, l1);
+            if (!kBf16 && r0 == 0) st_cluster_u8(map_to_rank(e_at, c), exponent);
           }
         }
       }
@@ -564,53 +604,76 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2) lora_kernel(c
     }
 
     // ------------------------------------------------------------ expand --
-    // A warp has 32 features (its quarter of the lanes) and every second 16
-    // tokens.  It turns 16 x 32 sums through shared memory, so that a lane
-    // holds 8 neighbouring features of a token.
-    float* turn = reinterpret_cast<float*>(smem + S::kTurnAt) + warp * (kTurnTile / 4);
-    for (int j = 0; j < mine; ++j) {
-      const int n0 = (rank + C * j) * 128 + warp % 4 * 32;
-      const int n = n0 + lane % 4 * 8;
-      Piece<TO> bv[4][2];
+    // A warp has 32 tokens (its quarter of the lanes) and half of each box, 64
+    // bytes of a row: it fetches them, adds its sums and stores them by itself.
+    constexpr int kBox = 128 / sizeof(TO), kHalf = kBox / 2, kPer = 16 / sizeof(TO);  // features
+    constexpr int kOfChunk = 128 / kBox, kRing = S::kBoxes;
+    const int q32 = warp % 4 * 32, half = warp / 4;
+    const bool busy = q32 < rows;
+    const int boxes = mine * kOfChunk;
+    auto feature = [&](int box) { return (rank + C * (box / kOfChunk)) * 128 + box % kOfChunk * kBox + half * kHalf; };
+    auto fetch = [&](int box) {
+      const int n = feature(box) + lane % 4 * kPer;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int i = 0; i < 4; ++i) {
+        const int row = q32 + 8 * i + lane / 4;
+        if (row < rows && n < a.N)
+          base_to_shared(s_box + box % kRing * 16384 + swizzled(row, half * 4 + lane % 4), static_cast<const TO*>(a.base),
+                         ctl.rows[row] * a.base_stride + n, a.N - n, a.wide);
+      }
+    };
+    if (busy) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = (2 * g + warp / 4) * 16 + h * 8 + lane / 4;
-          if (row < rows && n < a.N) bv[g][h].load(static_cast<const TO*>(a.base), ctl.rows[row] * a.base_stride + n, a.N - n, a.wide);
-        }
-      wait(ctl.acc_full, full_ph, j & 1);
-      tc_fence_after();
-      if (j + 2 < mine) load_chunk(j + 2);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int t0 = (2 * g + warp / 4) * 16;
-        if (t0 >= rows) break;
-        uint32_t v[16];
-        tmem_ld16(tmem + (j & 1) * 128 + lane_addr + t0, v);
+      for (int i = 0; i < kRing - 1; ++i) {
+        if (i < boxes) fetch(i);
+        cp_async_commit();
+      }
+    }
+    for (int box = 0; box < boxes; ++box) {
+      const int j = box / kOfChunk;
+      if (box % kOfChunk == 0) {
+        wait(ctl.acc_full, full_ph, j & 1);
+        tc_fence_after();
+      }
+      if (busy) {
+        __syncwarp();  // (the box before is read: its place is free)
+        if (box + kRing - 1 < boxes) fetch(box + kRing - 1);
+        cp_async_commit();
+        uint32_t v[kHalf];
+        const uint32_t acc = tmem + (j & 1) * 128 + lane_addr + box % kOfChunk * kBox + half * kHalf;
+        if constexpr (kHalf == 32)
+          tmem_ld32(acc, v);
+        else
+          tmem_ld16(acc, v);
+        cp_async_wait<kRing - 1>();
+        __syncwarp();
         tmem_ld_wait();
+        const float f = kBf16 ? 1.f : __uint_as_float(static_cast<uint32_t>(ctl.exponent[q32 + lane]) << 23);
+        const uint32_t at = s_box + box % kRing * 16384;
+#pragma unroll
+        for (int c = 0; c < 4 && q32 + lane < rows; ++c) {
+          const uint32_t p = at + swizzled(q32 + lane, half * 4 + c);
+          float y[kPer];
+          unpack16(lds128(p), y, TO());
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) y[i] = fmaf(__uint_as_float(v[c * kPer + i]), f, y[i]);
+          sts128(p, pack16(y, TO()));
+        }
         __syncwarp();
+        const int n = feature(box) + lane % 4 * kPer;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) turn[i * kTurnRow + lane] = __uint_as_float(v[i]);
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = h * 8 + lane / 4, row = t0 + i;
-          if (row < rows && n < a.N) {
-            float y[8];
-            const float f = kBf16 ? 1.f : ctl.factor[row];
-            const float4 lo = *reinterpret_cast<const float4*>(turn + i * kTurnRow + lane % 4 * 8);
-            const float4 hi = *reinterpret_cast<const float4*>(turn + i * kTurnRow + lane % 4 * 8 + 4);
-            const float u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = fmaf(u[q], f, bv[g][h].get(q));
-            Piece<TO>::store(static_cast<TO*>(a.out), ctl.rows[row] * a.out_stride + n, a.N - n, a.wide, y);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int row = q32 + 8 * i + lane / 4;
+          if (row < rows && n < a.N)
+            shared_to_out(static_cast<TO*>(a.out), ctl.rows[row] * a.out_stride + n, a.N - n, a.wide,
+                          lds128(at + swizzled(row, half * 4 + lane % 4)));
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.acc_empty[j & 1]);
+      if (box % kOfChunk == kOfChunk - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.acc_empty[j & 1]);
+      }
     }
     if (few) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
@@ -649,7 +712,15 @@ cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaSt
   at[0].val.clusterDim.x = C, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, a, C);
+  LoraMaps maps;
+  const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t K = a.K, N = a.N, r = a.r, L = a.L;
+  const uint64_t da[3] = {K, r, L}, sa[2] = {2 * K, 2 * r * K}, db[3] = {r, N, L}, sb[2] = {2 * r, 2 * r * N};
+  const uint32_t ba[3] = {64, RP, 1}, bb[3] = {64, 128, 1};
+  if (!encode_tma(&maps.a, type, 3, a.a, da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tma(&maps.b, type, 3, a.b, db, sb, bb, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  return cudaLaunchKernelEx(&lc, kernel, maps, a, C);
 }
 
 template <typename T, typename TO>
