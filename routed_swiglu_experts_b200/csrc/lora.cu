@@ -167,11 +167,6 @@ struct LoraSmem {
   static constexpr int kPart = (128 * (RP + 4) * 4 + 1023) / 1024 * 1024;
   static constexpr int kAfter = kV + (kPart > kBoxes * 16384 ? kPart : kBoxes * 16384);
   static constexpr int kFront = kAfter > kStages * kStage ? kAfter : kStages * kStage;
-  // K blocks of tiles of at most 16 tokens, loaded at once: A, then 16 rows of x
-  // each (as the M operand 128 rows are read: what follows gives rows that are
-  // not used, and lies within the block's shared memory)
-  static constexpr int kFew = kFront / (RP * 128 + 2048);
-  static_assert(16384 <= 2 * kB, "the last rows that are read");
   // (two CTAs of 256 TMEM columns fit an SM, a third must not start: it would
   // wait for columns that CTAs of waiting clusters hold)
   static constexpr int kBytes = kFront + 2 * kB + static_cast<int>(sizeof(LoraCtl));
@@ -367,7 +362,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
       if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
       if (tile.adapter < 0) continue;
-      const int rows = min(tile.rows, 128);
       if (lane == 0) {
         if (mine > 0) load_chunk(0);
         if (mine > 1) load_chunk(1);
@@ -379,37 +373,21 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16(tmem, sw128_kmajor_desc(at_x + kk * 32), sw128_kmajor_desc(at_a + kk * 32), idesc_a, !first || kk > 0);
         };
-        if (rows <= 16) {
-          const uint32_t s_x = s_stage + S::kFew * RP * 128;
-          for (int kb = 0; kb < nkb; kb += S::kFew) {
-            wait(ctl.full, full_ph, 0);
-            fence_proxy_async_smem();
-            tc_fence_after();
-            for (int q = 0; q < min(S::kFew, nkb - kb); ++q) block(s_x + q * 2048, s_stage + q * (RP * 128), kb + q == 0);
-            umma_commit(&ctl.empty[0]);
-          }
-        } else {
-          int stage = 0;
-          for (int kb = 0; kb < nkb; ++kb) {
-            wait(ctl.full, full_ph, stage);
-            fence_proxy_async_smem();
-            tc_fence_after();
-            block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
-            umma_commit(&ctl.empty[stage]);
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
-          }
+        int stage = 0;
+        for (int kb = 0; kb < nkb; ++kb) {
+          wait(ctl.full, full_ph, stage);
+          fence_proxy_async_smem();
+          tc_fence_after();
+          block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
+          umma_commit(&ctl.empty[stage]);
+          stage = stage + 1 == S::kStages ? 0 : stage + 1;
         }
         umma_commit(&ctl.acc_full[0]);
         wait(ctl.acc_full, acc_ph, 0);
       }
       __syncwarp();
       cluster_sync_all();
-      if (rows <= 16) {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        named_barrier_sync(1, kLoraThreads);
-      } else {
-        cluster_sync_all();
-      }
+      cluster_sync_all();
       if (lane == 0) {
         constexpr uint32_t idesc_b = kBf16 ? umma_idesc_bf16(128, 128) : umma_idesc_f16(128, 128);
         for (int j = 0; j < mine; ++j) {
@@ -433,7 +411,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         if (mine > 0) wait(ctl.acc_full, acc_ph, (mine - 1) & 1);
       }
       __syncwarp();
-      if (rows <= 16) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     if (lane == 0 && *abort_flag) {
       volatile int32_t never = 0;
@@ -445,11 +422,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
     if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
     const int rows = min(tile.rows, 128);
-    const bool few = rows <= 16;
-    // this CTA's share of A x: where the boxes will be (few tokens: in the first
-    // one's rows behind them, the other CTAs read it while boxes arrive)
-    const int part_at = S::kV + (few ? 2048 : 0);
-    static_assert(2048 + 16 * (RP + 4) * 4 <= 16384, "in one box");
     fence_proxy_async_smem();  // (the last tile's loads and stores are behind, copies of A may follow)
     named_barrier_sync(2, kLoraWorkers);
     if (tid < rows) ctl.rows[tid] = src[tile.row0 + tid];
@@ -470,27 +442,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     }
 
     // ------------------------------------------------------------ shrink --
-    if (few) {
-      // as many K blocks at once as fit: what counts here is the latency
-      const int row = tid / 8 % 16, c = tid % 8;
-      const T* xr = row < rows ? static_cast<const T*>(a.x) + src[tile.row0 + row] * a.x_stride : nullptr;
-      const uint32_t s_x = s_stage + S::kFew * RP * 128;
-      for (int kb = 0; kb < nkb; kb += S::kFew) {
-        const int nb = min(S::kFew, nkb - kb);
-        wait(ctl.empty, empty_ph, 0);
-        if (tid == 0) {
-          mbar_arrive_expect_tx(&ctl.full[0], nb * (RP * 128));
-          for (int q = 0; q < nb; ++q)
-            tma_load_3d(smem + q * (RP * 128), &maps.a, (kb0 + kb + q) * 64, 0, tile.adapter, &ctl.full[0]);
-        }
-        if (xr != nullptr)
-          for (int q = tid / 128; q < nb; q += kLoraWorkers / 128) {
-            const int k = (kb0 + kb + q) * 64 + c * 8;
-            cp_async16_or_zero(s_x + q * 2048 + swizzled(row, c), k < a.K ? xr + k : xr, k < a.K);
-          }
-        cp_async_mbar_arrive(&ctl.full[0]);
-      }
-    } else {
     const T* xr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -516,7 +467,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       cp_async_mbar_arrive(&ctl.full[stage]);
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
-    }
     // (complete: every copy into the stages has been read, their place is taken over)
     if (nkb > 0) wait(ctl.acc_full, full_ph, 0);
     tc_fence_after();
@@ -535,7 +485,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
             for (int i = 0; i < 16; ++i) v[i] = 0u;
           }
           if (row < rows) {
-            uint4* p = reinterpret_cast<uint4*>(smem + part_at + (row * (RP + 4) + c0 + c) * 4);
+            uint4* p = reinterpret_cast<uint4*>(smem + S::kV + (row * (RP + 4) + c0 + c) * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
@@ -547,18 +497,18 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     cluster_sync_all();
 
     // --------------------------------------------------------------- sum --
-    // A token's ranks lie on RP / 4 lanes.  Of many tokens each CTA adds its
-    // share and hands the result to all; of few, each adds all for itself.
+    // A token's ranks lie on RP / 4 lanes; each CTA adds every C-th token and
+    // hands the result to all.
     {
       constexpr int LT = RP / 4;
       const float sc = a.scale != nullptr ? a.scale[tile.adapter] : 1.f;
-      const int todo = few ? rows : (rows - rank + C - 1) / C;  // (>= 0: rows > 16 > rank otherwise)
+      const int todo = rows > rank ? (rows - rank + C - 1) / C : 0;
       const int r0 = 4 * (tid % LT);
       for (int i0 = 0; i0 < todo; i0 += kLoraWorkers / LT) {
         const int i = i0 + tid / LT;
         const bool live = i < todo;
-        const int row = live ? (few ? i : rank + C * i) : 0;
-        const uint32_t at = s_stage + part_at + (row * (RP + 4) + r0) * 4;
+        const int row = live ? rank + C * i : 0;
+        const uint32_t at = s_box + (row * (RP + 4) + r0) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < C; ++c) {
@@ -586,7 +536,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
           const int k_lo = RP <= 32 ? RP + r0 : r0;  // lo's column in its row
           const uint32_t lo = s_v + (RP <= 32 ? 0 : S::kLoAt) + k_lo / 64 * 16384 + swizzled(row, k_lo % 64 / 8) + (k_lo & 4) * 2;
           const uint32_t e_at = smem_u32(&ctl.exponent[row]);
-          for (int c = few ? rank : 0; c < (few ? rank + 1 : C); ++c) {
+          for (int c = 0; c < C; ++c) {
             st_cluster_v2(map_to_rank(to, c), h0, h1);
             st_cluster_v2(map_to_rank(lo, c), l0, l1);
             if (!kBf16 && r0 == 0) st_cluster_u8(map_to_rank(e_at, c), exponent);
@@ -595,13 +545,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       }
     }
     asm volatile("fence.proxy.async;" ::: "memory");
-    if (few) {
-      // (the others may still read this CTA's share: waited for after the last chunk)
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      named_barrier_sync(1, kLoraThreads);
-    } else {
-      cluster_sync_all();
-    }
+    cluster_sync_all();
 
     // ------------------------------------------------------------ expand --
     // A warp has 32 tokens (its quarter of the lanes) and half of each box, 64
@@ -675,7 +619,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         if (lane == 0) mbar_arrive(&ctl.acc_empty[j & 1]);
       }
     }
-    if (few) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   }
   tc_fence_before();
@@ -686,12 +629,304 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   }
 }
 
-// CTAs of a cluster.
+// CTAs of a cluster: of tiles of up to 128 tokens, and of tiles of at most 16
+// by how many of them there may be.
 #ifdef LORA_EXP
 int lora_cluster(int) { return atoi(getenv("LORA_C")); }
+int lora_few_cluster(int64_t) { return atoi(getenv("LORA_C")); }
 #else
-int lora_cluster(int T) { return T <= 4096 ? 8 : 4; }
+int lora_cluster(int T) { return T <= 4096 ? 8 : T <= 8192 ? 4 : 2; }
+int lora_few_cluster(int64_t max_tiles) { return max_tiles <= 56 ? 8 : max_tiles <= 128 ? 4 : 2; }
 #endif
+
+// Clusters for the tiles; those that do not fit at once wait, and each takes
+// every so-manieth tile where there are more.
+struct LoraLaunch {
+  cudaLaunchConfig_t config = {};
+  cudaLaunchAttribute cluster[1];
+  LoraLaunch(int64_t max_tiles, int C, int threads, int bytes, int num_sms, cudaStream_t stream) {
+    const int64_t clusters = std::min<int64_t>(max_tiles, std::max(1, 4 * num_sms / C));
+    config.gridDim = dim3(static_cast<unsigned>(clusters) * C);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    cluster[0].id = cudaLaunchAttributeClusterDimension;
+    cluster[0].val.clusterDim.x = C, cluster[0].val.clusterDim.y = 1, cluster[0].val.clusterDim.z = 1;
+    config.attrs = cluster;
+    config.numAttrs = 1;
+  }
+};
+
+// ---------------------------------------------------- tiles of few tokens ---
+// Tiles of at most 16 tokens (decode batches): bytes are few and latency is all,
+// so nothing is staged.  Fragments of m16n8k16 products come straight from
+// global memory: K is taken in an order in which a lane's values are neighbours
+// (both operands in the same one).  A cluster of C CTAs x 8 warps shares K, the
+// sums go through shared memory twice (warps, then CTAs), and every warp adds
+// 32 features at a time to base; the first ones' B and base are on the way
+// while A x is summed.  (tcgen05 on the same tiles: 128 rows per instruction
+// whatever the tile has, 71 clocks for each k16 of a 16-row tile.)
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+constexpr int kFewThreads = 256, kFewMaxCluster = 8, kFewRows = 16;
+
+// Two neighbouring values of a row; `pair`: they may be read and written at once.
+template <typename TO>
+__device__ __forceinline__ float2 load_pair(const TO* p, int left, bool pair) {
+  if (pair && left >= 2) {
+    if constexpr (sizeof(TO) == 4) {
+      return *reinterpret_cast<const float2*>(p);
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+      if constexpr (std::is_same<TO, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+      return make_float2(bf16lo(w), bf16hi(w));
+    }
+  }
+  return make_float2(left > 0 ? static_cast<float>(p[0]) : 0.f, left > 1 ? static_cast<float>(p[1]) : 0.f);
+}
+template <typename TO>
+__device__ __forceinline__ void store_pair(TO* p, int left, bool pair, float x, float y) {
+  if (pair && left >= 2) {
+    if constexpr (sizeof(TO) == 4)
+      *reinterpret_cast<float2*>(p) = make_float2(x, y);
+    else
+      *reinterpret_cast<uint32_t*>(p) = pack2<TO>(x, y);
+  } else {
+    if (left > 0) p[0] = static_cast<TO>(x);
+    if (left > 1) p[1] = static_cast<TO>(y);
+  }
+}
+
+template <typename T, typename TO, int RP>
+__global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(const LoraArgs a, const int C) {
+  constexpr int kTiles = RP / 8;
+  extern __shared__ __align__(16) float few_smem[];
+  float* red = few_smem;                                // [8 warps][16][RP]
+  float* part = red + 8 * kFewRows * RP;                // [16][RP] this CTA's share
+  float* vsum = part + kFewRows * RP;                   // [16][RP] A x, scaled
+  float* factor = vsum + kFewRows * RP;                 // [16]
+  const LoraPlan head = *reinterpret_cast<const LoraPlan*>(a.plan);
+  const int32_t* src = reinterpret_cast<const int32_t*>(a.plan + sizeof(LoraPlan));
+  const LoraTile* tiles = reinterpret_cast<const LoraTile*>(a.plan + lora_tiles_at(a.T));
+  LoraTile tile = tiles[blockIdx.x / C];  // (the plan has room for one per cluster; read before the head is known)
+  if (head.magic != kLoraPlanMagic || head.T != a.T || head.L != a.L) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err, MOE_ERR_INVALID_ARG, 0);
+    return;
+  }
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, q = lane % 4;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int kblocks = (a.K + 63) / 64, kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / C),
+            kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / C);
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+
+  for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
+    if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
+    const int rows = min(tile.rows, kFewRows);
+    // this lane's tokens: rows g and g + 8 of the tile
+    int64_t t[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) t[h] = g + 8 * h < rows ? src[tile.row0 + g + 8 * h] : -1;
+    constexpr int kUnit = RP >= 64 ? 16 : 32, kN = kUnit / 8;  // features of a warp at a time
+    const int units = (a.N + kUnit - 1) / kUnit;
+    float2 bv[kN][2];
+    auto load_base = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = u * kUnit + i * 8 + 2 * q;
+          bv[i][h] = make_float2(0.f, 0.f);
+          if (a.base != nullptr && t[h] >= 0 && n < a.N)
+            bv[i][h] = load_pair(static_cast<const TO*>(a.base) + t[h] * a.base_stride + n, a.N - n, a.wide);
+        }
+    };
+    auto store_out = [&](int u, const float (&d)[kN][4]) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = u * kUnit + i * 8 + 2 * q;
+          const float f = kBf16 ? 1.f : factor[g + 8 * h];
+          if (t[h] >= 0 && n < a.N)
+            store_pair(static_cast<TO*>(a.out) + t[h] * a.out_stride + n, a.N - n, a.wide, fmaf(d[i][2 * h], f, bv[i][h].x),
+                       fmaf(d[i][2 * h + 1], f, bv[i][h].y));
+        }
+    };
+    int u = rank * 8 + warp;
+    if (tile.adapter < 0) {  // base as it is
+      if (a.base == a.out) continue;
+      for (; u < units; u += C * 8) {
+        load_base(u);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = u * kUnit + i * 8 + 2 * q;
+            if (t[h] >= 0 && n < a.N)
+              store_pair(static_cast<TO*>(a.out) + t[h] * a.out_stride + n, a.N - n, a.wide, bv[i][h].x, bv[i][h].y);
+          }
+      }
+      continue;
+    }
+    const T* wa = static_cast<const T*>(a.a) + static_cast<int64_t>(tile.adapter) * a.r * a.K;
+    const T* wb = static_cast<const T*>(a.b) + static_cast<int64_t>(tile.adapter) * a.N * a.r;
+
+    // shrink: K blocks of 64, a warp takes every eighth of its CTA's; of a block a
+    // lane has values 16 q .. 16 q + 15 of a row, four for each of four products
+    float d[kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    for (int kb = kb0 + warp; kb < kb1; kb += 8) {
+      const int k = kb * 64 + q * 16;
+      auto load_row = [&](const T* row, uint32_t (&w)[8]) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row != nullptr && k + 8 * p < a.K) v = __ldg(reinterpret_cast<const uint4*>(row + k + 8 * p));
+          w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
+        }
+      };
+      constexpr int kHold = RP == 128 || kTiles < 4 ? 2 : 4;  // rank tiles held at once
+      uint32_t x0[8], x1[8], w[kHold][8];
+#pragma unroll
+      for (int i0 = 0; i0 < kTiles; i0 += kHold) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          const int j = (i0 + i) * 8 + g;
+          load_row(j < a.r ? wa + static_cast<int64_t>(j) * a.K : nullptr, w[i]);
+        }
+        if (i0 == 0) {
+          load_row(t[0] >= 0 ? static_cast<const T*>(a.x) + t[0] * a.x_stride : nullptr, x0);
+          load_row(t[1] >= 0 ? static_cast<const T*>(a.x) + t[1] * a.x_stride : nullptr, x1);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < kHold; ++i)
+            mma16816<T>(d[i0 + i], x0[2 * s], x1[2 * s], x0[2 * s + 1], x1[2 * s + 1], w[i][2 * s], w[i][2 * s + 1]);
+      }
+    }
+    // the first features' B and base, on the way until A x is there
+    uint2 bw[kN][RP / 16];
+    auto load_b = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int s = 0; s < RP / 16; ++s) {
+          const int n = u * kUnit + i * 8 + g, j = 16 * s + 4 * q;
+          bw[i][s] = n < a.N && j < a.r ? __ldg(reinterpret_cast<const uint2*>(wb + static_cast<int64_t>(n) * a.r + j)) : make_uint2(0u, 0u);
+        }
+    };
+    if (u < units) {
+      load_b(u);
+      load_base(u);
+    }
+
+    // sum over the warps, then over the CTAs; warp w has tokens w and w + 8
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      float* p = red + (warp * kFewRows + g) * RP + i * 8 + 2 * q;
+      *reinterpret_cast<float2*>(p) = make_float2(d[i][0], d[i][1]);
+      *reinterpret_cast<float2*>(p + 8 * RP) = make_float2(d[i][2], d[i][3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFewRows * RP; i += kFewThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += red[w * kFewRows * RP + i];
+      part[i] = s;
+    }
+    cluster_sync_all();
+    const float sc = a.scale != nullptr ? a.scale[tile.adapter] : 1.f;
+    for (int row = warp; row < rows; row += 8) {
+      constexpr int kPerLane = (RP + 31) / 32;
+      float v[kPerLane], m = 0.f;
+#pragma unroll
+      for (int p = 0; p < kPerLane; ++p) {
+        const int j = p * 32 + lane;
+        v[p] = 0.f;
+        if (j < RP) {
+          const uint32_t at = smem_u32(part + row * RP + j);
+          float s[kFewMaxCluster];
+#pragma unroll
+          for (int c = 0; c < kFewMaxCluster; ++c) s[c] = c < C ? ld_cluster_f32(map_to_rank(at, c)) : 0.f;
+#pragma unroll
+          for (int c = 0; c < kFewMaxCluster; ++c) v[p] += s[c];
+          v[p] *= sc;
+        }
+        m = fmaxf(m, fabsf(v[p]));
+      }
+      float inv = 1.f;
+      if (!kBf16) {  // fp16 has 5 bits of exponent: the token's values are brought to [1, 2) by a power of two
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t e = __float_as_uint(m) >> 23;
+        const bool scaled = e > 0u && e < 254u;
+        inv = scaled ? __uint_as_float((254u - e) << 23) : 1.f;
+        if (lane == 0) factor[row] = scaled ? __uint_as_float(e << 23) : 1.f;
+      }
+#pragma unroll
+      for (int p = 0; p < kPerLane; ++p)
+        if (p * 32 + lane < RP) vsum[row * RP + p * 32 + lane] = v[p] * inv;
+    }
+    // (the others may still read `part`: waited for at the tile's end)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    __syncthreads();
+
+    // expand: of 16 ranks a lane has 4 q .. 4 q + 3
+    for (; u < units; u += C * 8) {
+      float y[kN][4];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < RP / 16; ++s) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 f = *reinterpret_cast<const float4*>(vsum + (g + 8 * h) * RP + 16 * s + 4 * q);
+          hi[h] = pack2<T>(f.x, f.y), hi[2 + h] = pack2<T>(f.z, f.w);
+          lo[h] = pack2<T>(rest_of<T>(f.x), rest_of<T>(f.y)), lo[2 + h] = pack2<T>(rest_of<T>(f.z), rest_of<T>(f.w));
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          mma16816<T>(y[i], lo[0], lo[1], lo[2], lo[3], bw[i][s].x, bw[i][s].y);
+          mma16816<T>(y[i], hi[0], hi[1], hi[2], hi[3], bw[i][s].x, bw[i][s].y);
+        }
+      }
+      store_out(u, y);
+      if (u + C * 8 < units) {
+        load_b(u + C * 8);
+        load_base(u + C * 8);
+      }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <typename T, typename TO, int RP>
+cudaError_t lora_few_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  auto kernel = lora_few_kernel<T, TO, RP>;
+  constexpr int kBytes = ((8 + 2) * kFewRows * RP + kFewRows) * 4;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kBytes);
+  if (e != cudaSuccess) return e;
+  const int C = lora_few_cluster(max_tiles);
+  LoraLaunch l(max_tiles, C, kFewThreads, kBytes, num_sms, stream);
+  return cudaLaunchKernelEx(&l.config, kernel, a, C);
+}
 
 template <typename T, typename TO, int RP>
 cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
@@ -700,18 +935,7 @@ cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaSt
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kBytes);
   if (e != cudaSuccess) return e;
   const int C = lora_cluster(a.T);
-  // (clusters that do not fit wait; each takes every gridDim.x / C-th tile)
-  const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(max_tiles, std::max(1, 4 * num_sms / C)));
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(clusters * C);
-  lc.blockDim = dim3(kLoraThreads);
-  lc.dynamicSmemBytes = S::kBytes;
-  lc.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-  lc.attrs = at;
-  lc.numAttrs = 1;
+  LoraLaunch l(max_tiles, C, kLoraThreads, S::kBytes, num_sms, stream);
   LoraMaps maps;
   const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t K = a.K, N = a.N, r = a.r, L = a.L;
@@ -720,11 +944,17 @@ cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaSt
   if (!encode_tma(&maps.a, type, 3, a.a, da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tma(&maps.b, type, 3, a.b, db, sb, bb, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  return cudaLaunchKernelEx(&lc, kernel, maps, a, C);
+  return cudaLaunchKernelEx(&l.config, kernel, maps, a, C);
 }
 
 template <typename T, typename TO>
 cudaError_t lora_by_rank(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  if (lora_tile_rows(a.T) == kFewRows) {
+    if (a.r <= 16) return lora_few_typed<T, TO, 16>(a, max_tiles, num_sms, stream);
+    if (a.r <= 32) return lora_few_typed<T, TO, 32>(a, max_tiles, num_sms, stream);
+    if (a.r <= 64) return lora_few_typed<T, TO, 64>(a, max_tiles, num_sms, stream);
+    return lora_few_typed<T, TO, 128>(a, max_tiles, num_sms, stream);
+  }
   if (a.r <= 16) return lora_typed<T, TO, 16>(a, max_tiles, num_sms, stream);
   if (a.r <= 32) return lora_typed<T, TO, 32>(a, max_tiles, num_sms, stream);
   if (a.r <= 64) return lora_typed<T, TO, 64>(a, max_tiles, num_sms, stream);
