@@ -103,7 +103,7 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 #define MOE_LORA_MAX_RANK 128
 #define MOE_MAX_ADAPTERS 1024
 /* Bytes of the workspace that moe_balance_loss needs. */
-#define MOE_BALANCE_WS_BYTES 16384
+#define MOE_BALANCE_WS_BYTES 81920
 /* Longest row of moe_rmsnorm. */
 #define MOE_NORM_MAX_COLUMNS 32768
 

@@ -39,7 +39,7 @@ MOE_MAX_GROUPS = 32
 MOE_WS_HEADER_BYTES = 256
 MOE_LORA_MAX_RANK = 128
 MOE_MAX_ADAPTERS = 1024
-MOE_BALANCE_WS_BYTES = 16384
+MOE_BALANCE_WS_BYTES = 81920
 MOE_NORM_MAX_COLUMNS = 32768
 MOE_MAX_TOP_K = 16
 MOE_MAX_EXPERTS = 1024

@@ -8,10 +8,10 @@
 // (The usual form sums f_e times the mean of p_e: the same sum in another
 // order.)  So once the ids are counted, one pass over the logits gives both.
 //
-// One kernel: blocks zero the counts, count their tokens' ids, and pass over
-// their logits, with a barrier of the whole grid between (a cooperative launch;
-// one block for small batches).  The logits are on their way to shared memory
-// from the start, so counting costs no time of its own for large batches.
+// One kernel.  Some blocks count: a sequence each, and sixteen parts where there
+// is one sequence alone.  The others wait for them (a cooperative launch; small
+// batches take one block) while their logits come to shared memory, so counting
+// costs large batches no time of its own.  Then every warp walks over tokens.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -61,39 +61,52 @@ __device__ __forceinline__ float to_f32(T v) {
   return static_cast<float>(v);
 }
 
-constexpr int kBalThreads = 512, kBalWarps = kBalThreads / 32;
-constexpr int kBalStage = 200 * 1024;  // bytes of logits that a block fetches ahead
-constexpr int64_t kBalOneBlock = 16384, kBalPerBlock = 8192;  // logits of a batch in one block, and of a block otherwise
+constexpr int kBalStage = 196 * 1024;  // bytes of logits that a block fetches ahead
+constexpr int kBalParts = BalanceWs::kParts;
+// logits of a batch that one block takes by itself, and of a block otherwise
+constexpr int64_t kBalOneBlock = 16384, kBalPerBlock = 8192;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 
-// All blocks of the grid; false when the others did not come in time.
-__device__ __forceinline__ bool grid_barrier(BalanceWs* ws, int phase, int* s_ok) {
-  if (gridDim.x == 1) {
-    __syncthreads();
-    return true;
-  }
+constexpr int kSeqStage = 2048;
+
+// Counts the ids of tokens t0 .. t1 - 1 in shared memory (hist: zeroed here); n: tokens.
+__device__ __forceinline__ void count_tokens(const BalanceArgs& a, int t0, int t1, int32_t* hist, int32_t* n) {
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
+  if (threadIdx.x == 0) *n = a.mask == nullptr ? max(t1 - t0, 0) : 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(&ws->header.balance_arrived, 1);
-    const int all = phase * static_cast<int>(gridDim.x);
-    const uint64_t t0 = globaltimer_ns();
-    int ok = 1;
-    for (uint32_t it = 1;; ++it) {
-      int v;
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&ws->header.balance_arrived) : "memory");
-      if (v >= all) break;
-      if ((it & 255u) == 0u && globaltimer_ns() - t0 > kTimeoutNs) {
-        report_error(&ws->header.error, MOE_ERR_DEVICE_TIMEOUT, 1);
-        ok = 0;
-        break;
-      }
+  if (a.mask != nullptr) {
+    int mine = 0;
+    for (int t = t0 + static_cast<int>(threadIdx.x); t < t1; t += blockDim.x) mine += a.mask[t] != 0;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (threadIdx.x % 32 == 0 && mine != 0) atomicAdd(n, mine);
+  }
+  const int64_t end = static_cast<int64_t>(t1) * a.k;
+  constexpr int kAtOnce = 8;
+  for (int64_t i = static_cast<int64_t>(t0) * a.k + threadIdx.x; i < end; i += kAtOnce * blockDim.x) {
+    int v[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int64_t at = i + j * static_cast<int>(blockDim.x);
+      v[j] = at < end ? __ldg(a.ids + at) : -1;
+      if (a.mask != nullptr && at < end && a.mask[at / a.k] == 0) v[j] = -1;
     }
-    __threadfence();
-    *s_ok = ok;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (v[j] >= 0 && v[j] < a.E) atomicAdd(&hist[v[j]], 1);
   }
   __syncthreads();
-  return *s_ok != 0;
+}
+
+// The hardware's 2^x and 1 / x, results below fp32's normal range to 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Eight neighbouring values at p, `left` of them there; `vec`: as 16-byte pieces.
@@ -138,12 +151,14 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float (&v
 // A token lies on LPT = 2^lpt_log lanes, each with NV = 8 NC values: chunks of 8
 // neighbours, chunk i of lane l at expert 8 (l + LPT i).
 template <typename TZ, typename TG, bool SOFTMAX, int NC>
-__global__ void __launch_bounds__(kBalThreads, 1)
+__global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
     balance_kernel(const BalanceArgs a, int lpt_log, int per_block, bool z_vec, bool g_vec, bool ahead) {
   extern __shared__ __align__(128) unsigned char s_rows[];  // logits fetched ahead
-  __shared__ double s_part[kBalWarps];
-  __shared__ int s_count[MOE_MAX_EXPERTS];
-  __shared__ int s_n, s_live, s_ok;
+  constexpr int kThreads = NC == 1 ? 1024 : 512, kWarps = kThreads / 32;
+  __shared__ double s_part[kWarps];
+  __shared__ int32_t s_count[MOE_MAX_EXPERTS];  // ids of a sequence, or f of the only one
+  __shared__ int32_t s_seq[kSeqStage];          // the first tokens' sequences, -1: not counted
+  __shared__ int32_t s_n, s_ok;
   __shared__ __align__(8) uint64_t s_bar;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int t0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * per_block, static_cast<int64_t>(a.T)));
@@ -165,46 +180,77 @@ __global__ void __launch_bounds__(kBalThreads, 1)
                    "r"(smem_u32(&s_bar))
                    : "memory");
     }
-    s_n = s_live = 0;
+    s_ok = 1;
   }
 
-  // counts to zero
-  const bool one = a.offsets == nullptr;  // (one sequence: a block counts in shared memory first)
-  {
-    const int64_t n = static_cast<int64_t>(a.S) * a.E, step = static_cast<int64_t>(gridDim.x) * kBalThreads;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBalThreads + tid; i < n; i += step) a.counts[i] = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBalThreads + tid; i < a.S; i += step) a.tokens[i] = 0;
+  // ---------------------------------------------------------------- count --
+  const bool one = a.offsets == nullptr;
+  const int parts = one && gridDim.x > 1 ? min(kBalParts, static_cast<int>(gridDim.x)) : 1;
+  const int units = one ? parts : a.S;
+  int live = 0;  // sequences with tokens, of this block's
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t from = one ? static_cast<int64_t>(a.T) * u / parts : __ldg(a.offsets + u);
+    const int64_t to = one ? static_cast<int64_t>(a.T) * (u + 1) / parts : __ldg(a.offsets + u + 1);
+    const int first = static_cast<int>(max(from, int64_t(0)));
+    count_tokens(a, first, max(first, static_cast<int>(min(to, static_cast<int64_t>(a.T)))), s_count, &s_n);
+    int32_t* row = parts > 1 ? a.ws->counts[u] : a.counts + static_cast<int64_t>(u) * a.E;
+    for (int e = tid; e < a.E; e += kThreads) row[e] = s_count[e];
+    if (tid == 0) (parts > 1 ? a.ws->tokens : a.tokens)[u] = s_n;
+    live += s_n > 0;
+    __syncthreads();
   }
-  if (one)
-    for (int i = tid; i < a.E; i += kBalThreads) s_count[i] = 0;
-  bool ok = grid_barrier(a.ws, 1, &s_ok);
-
-  // count (whole numbers: the order of the additions does not show)
-  if (one) {
-    for (int t = t0 + tid; t < t1; t += kBalThreads)
-      if (counted(a, t)) atomicAdd(&s_n, 1);
-    const int64_t end = static_cast<int64_t>(t1) * a.k;
-    for (int64_t i = static_cast<int64_t>(t0) * a.k + tid; i < end; i += kBalThreads) {
-      const int e = __ldg(a.ids + i);
-      if (e >= 0 && e < a.E && (a.mask == nullptr || counted(a, static_cast<int>(i / a.k)))) atomicAdd(&s_count[e], 1);
+  for (int t = t0 + tid; t < min(t1, t0 + kSeqStage); t += kThreads) s_seq[t - t0] = counted(a, t) ? sequence_of(a, t) : -1;
+  if (gridDim.x > 1) {  // (one block: its own stores, behind its own barrier)
+    if (tid == 0) {
+      const int counting = min(units, static_cast<int>(gridDim.x));
+      if (blockIdx.x < counting) {
+        if (live > 0) atomicAdd(&a.ws->header.balance_live, live);
+        __threadfence();
+        atomicAdd(&a.ws->header.balance_arrived, 1);
+      }
+      const uint64_t since = globaltimer_ns();
+      for (uint32_t it = 1;; ++it) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(&a.ws->header.balance_arrived) : "memory");
+        if (v >= counting) break;
+        if ((it & 255u) == 0u && globaltimer_ns() - since > kTimeoutNs) {
+          report_error(&a.ws->header.error, MOE_ERR_DEVICE_TIMEOUT, 1);
+          s_ok = 0;
+          break;
+        }
+      }
+      __threadfence();
     }
     __syncthreads();
-    for (int e = tid; e < a.E; e += kBalThreads)
-      if (s_count[e] != 0) atomicAdd(a.counts + e, s_count[e]);
-    if (tid == 0 && s_n != 0) atomicAdd(a.tokens, s_n);
-  } else {
-    for (int t = t0 + tid; t < t1; t += kBalThreads) {
-      const int s = counted(a, t) ? sequence_of(a, t) : -1;
-      if (s < 0) continue;
-      atomicAdd(a.tokens + s, 1);
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __ldg(a.ids + static_cast<int64_t>(t) * a.k + j);
-        if (e >= 0 && e < a.E) atomicAdd(a.counts + static_cast<int64_t>(s) * a.E + e, 1);
-      }
-    }
+    live = __ldcg(&a.ws->header.balance_live);
   }
-  ok = grid_barrier(a.ws, 2, &s_ok) && ok;
-
+  const float ek = static_cast<float>(a.E) / static_cast<float>(a.k);
+  // f of an expert that c of n tokens chose: E c / (k n), exactly E / k where all did
+  auto share_of = [&](int c, int n, float per_token) { return c == n ? ek : static_cast<float>(c) * per_token; };
+  float* s_f = reinterpret_cast<float*>(s_count);
+  int n_one = s_n;
+  if (one) {
+    if (parts > 1) {
+      n_one = __reduce_add_sync(0xffffffffu, lane < parts ? __ldcg(&a.ws->tokens[lane]) : 0);
+      live = n_one > 0;
+    }
+    const float per_token = ek / static_cast<float>(max(n_one, 1));
+    for (int e = tid; e < a.E; e += kThreads) {
+      int c = s_count[e];
+      if (parts > 1) {
+        int32_t v[kBalParts];
+#pragma unroll
+        for (int p = 0; p < kBalParts; ++p) v[p] = p < parts ? __ldcg(&a.ws->counts[p][e]) : 0;
+        c = 0;
+#pragma unroll
+        for (int p = 0; p < kBalParts; ++p) c += v[p];
+        if (blockIdx.x == 0) a.counts[e] = c;
+      }
+      s_f[e] = share_of(c, n_one, per_token);
+    }
+    if (parts > 1 && blockIdx.x == 0 && tid == 0) a.tokens[0] = n_one;
+  }
+  bool ok = s_ok != 0;
   if (fetched > 0) {
     volatile int32_t never = 0;
     if (!mbar_wait_bounded(&s_bar, 0, &never, kTimeoutNs)) {
@@ -214,58 +260,67 @@ __global__ void __launch_bounds__(kBalThreads, 1)
   }
   ok = __syncthreads_and(ok) != 0;
 
+  // --------------------------------------------------------------- tokens --
   double part = 0.0;
   if (ok) {
-    int live = 0;
-    for (int i = tid; i < a.S; i += kBalThreads) live += __ldcg(a.tokens + i) > 0;
-    if (live) atomicAdd(&s_live, live);
-    __syncthreads();
-    const double whole = static_cast<double>(a.coef) / max(s_live, 1);
+    const float whole = a.coef / static_cast<float>(max(live, 1));
     const float up = a.up != nullptr ? *a.up : 1.f;
-    const float ek = static_cast<float>(a.E) / static_cast<float>(a.k);
     const int LPT = 1 << lpt_log, l = lane & (LPT - 1), per_warp = 32 >> lpt_log;
-    int seq = -1, seq_end = 0;  // the last token's sequence and its end; f of it
-    float f[NC][8], scale = 0.f;
-    double share = 0.0;
+    int seq = -1;  // the last token's sequence; f of it
+    float f[NC][8], share = 0.f;  // share: coef / (S' n)
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
-    for (int tb = t0 + warp * per_warp; tb < t1; tb += kBalWarps * per_warp) {
-      const int t = tb + (lane >> lpt_log);
+      for (int j = 0; j < 8; ++j) {
+        const int e = 8 * (l + (i << lpt_log)) + j;
+        f[i][j] = one && e < a.E ? s_f[e] : 0.f;
+      }
+    if (one && n_one > 0) {
+      seq = 0;
+      share = whole / static_cast<float>(n_one);
+    }
+    auto row8 = [&](int t, int e0, float (&v)[8]) {
+      if (t - t0 < fetched)
+        load8(reinterpret_cast<const TZ*>(s_rows) + (t - t0) * a.E + e0, a.E - e0, z_vec, v);
+      else
+        load8(static_cast<const TZ*>(a.logits) + t * a.stride + e0, a.E - e0, z_vec, v);
+    };
+    // a group of lanes takes tokens that follow one another: few changes of sequence
+    const int run = (t1 - t0 + kWarps * per_warp - 1) / (kWarps * per_warp);
+    const int mine = t0 + (warp * per_warp + (lane >> lpt_log)) * run;
+    const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (lane & ~(LPT - 1));
+    for (int r = 0; r < run; ++r) {
+      const int t = mine + r;
       const bool in = t < t1;
       int s = -1;
-      if (in && counted(a, t)) {
-        if (seq >= 0 && t < seq_end) {
-          s = seq;
-        } else {
-          s = sequence_of(a, t);
-          if (s >= 0) {
+      if (in) {
+        s = t - t0 < kSeqStage ? s_seq[t - t0] : counted(a, t) ? sequence_of(a, t) : -1;
+        if (s >= 0 && s != seq) {
             seq = s;
-            seq_end = one ? a.T : __ldg(a.offsets + s + 1);
-            const float n = static_cast<float>(__ldcg(a.tokens + s));
-            share = whole / n;
-            scale = static_cast<float>(share * up);
+            const int n = __ldcg(a.tokens + s);
+            int c[NC][8];
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const int e = 8 * (l + (i << lpt_log)) + j;
-                f[i][j] = e < a.E ? static_cast<float>(__ldcg(a.counts + static_cast<int64_t>(s) * a.E + e)) / n * ek : 0.f;
+                c[i][j] = e < a.E ? __ldcg(a.counts + static_cast<int64_t>(s) * a.E + e) : 0;
               }
-          }
+            const float per_token = ek / static_cast<float>(n);
+            share = whole / static_cast<float>(n);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[i][j] = share_of(c[i][j], n, per_token);
         }
       }
-      // (tokens that do not count go along with zeros: the lanes of a warp reduce together)
+      // (tokens that do not count go along: the lanes of a warp reduce together)
       float z[NC][8], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int e0 = 8 * (l + (i << lpt_log));
         if (s >= 0 && e0 < a.E) {
-          if (t - t0 < fetched)
-            load8(reinterpret_cast<const TZ*>(s_rows) + (t - t0) * a.E + e0, a.E - e0, z_vec, z[i]);
-          else
-            load8(static_cast<const TZ*>(a.logits) + t * a.stride + e0, a.E - e0, z_vec, z[i]);
+          row8(t, e0, z[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) z[i][j] = -INFINITY;
@@ -273,39 +328,64 @@ __global__ void __launch_bounds__(kBalThreads, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, z[i][j]);
       }
-      for (int o = LPT / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!SOFTMAX) top = fminf(top, 0.f);
-      // z becomes the score over exp(top) (sigmoid: finite for every row, right
-      // where all scores underflow); 1 - sigmoid(z) is kept beside it.  __expf: its
-      // argument's rounding, |z - top| 2^-24, is what its result is off by.
-      float sum = 0.f, dot = 0.f, slope[SOFTMAX ? 1 : NC][8];
+      // z becomes the score (softmax: over exp(top)), 0 for lanes without experts,
+      // and for sigmoids then score times 1 - score.  Powers of two of the hardware:
+      // the rounding of their argument, |z| 2^-24, is what they are off by.
+      constexpr float kLog2e = 1.4426950408889634f;
+      float sum = 0.f, dot = 0.f;
+      if (SOFTMAX) {
+        for (int o = LPT / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = z[i][j];
-          const bool there = s >= 0 && 8 * (l + (i << lpt_log)) + j < a.E;
-          float p;
-          if (SOFTMAX) {
-            p = __expf(v - top);
-          } else {
-            const float u = __expf(-fabsf(v)), r = __fdividef(1.f, 1.f + u);
-            slope[SOFTMAX ? 0 : i][j] = v >= 0.f ? u * r : r;
-            p = (v >= 0.f ? 1.f : top < 0.f ? __expf(v - top) : u) * r;
+          for (int j = 0; j < 8; ++j) {
+            z[i][j] = exp2_fast((z[i][j] - top) * kLog2e);
+            sum += z[i][j];
+            dot = fmaf(z[i][j], f[i][j], dot);
           }
-          p = there ? p : 0.f;
-          z[i][j] = p;
-          sum += p;
-          dot = fmaf(p, f[i][j], dot);
+      } else {
+        // (where every score is below e^-40 all are taken over the largest: they may underflow)
+        const uint32_t high = __ballot_sync(0xffffffffu, top >= -40.f);
+        const bool low = s >= 0 && (high & group) == 0u;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = z[i][j], u = exp2_fast(-fabsf(v) * kLog2e), q = rcp_fast(1.f + u), w = u * q;
+            const float p = v >= 0.f ? q : w;
+            sum += p;
+            dot = fmaf(p, f[i][j], dot);
+            z[i][j] = q * w;
+          }
+        if (__any_sync(0xffffffffu, low)) {
+          for (int o = LPT / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (low) {
+            sum = dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+              const int e0 = 8 * (l + (i << lpt_log));
+              float w[8];
+              if (e0 < a.E) {
+                row8(t, e0, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // (1 - score is 1 in fp32)
+                  z[i][j] = exp2_fast((w[j] - top) * kLog2e);
+                  sum += z[i][j];
+                  dot = fmaf(z[i][j], f[i][j], dot);
+                }
+              }
+            }
+          }
         }
+      }
       for (int o = LPT / 2; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
       }
-      const float d = dot / sum;  // (exactly 1 where every f is)
-      if (s >= 0 && l == 0) part += static_cast<double>(d) * share;
+      const float inv = 1.f / sum, d = dot == sum ? 1.f : dot * inv;  // (every f is 1: the gradient is 0)
+      if (s >= 0 && l == 0) part += static_cast<double>(d) * static_cast<double>(share);
       if (a.grad != nullptr && in) {
-        const float gs = s >= 0 ? scale / sum : 0.f;
+        const float gs = share * up * inv, dg = d * gs;
         TG* g = static_cast<TG*>(a.grad) + t * a.grad_stride;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -313,8 +393,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
           if (e0 < a.E) {
             float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              y[j] = s >= 0 ? z[i][j] * (f[i][j] - d) * (SOFTMAX ? 1.f : slope[SOFTMAX ? 0 : i][j]) * gs : 0.f;
+            for (int j = 0; j < 8; ++j) y[j] = s >= 0 ? z[i][j] * fmaf(f[i][j], gs, -dg) : 0.f;
             store8(g + e0, a.E - e0, g_vec, y);
           }
         }
@@ -330,7 +409,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     int last = 0;
     if (lane == 0) {
       double sum = 0.0;
-      for (int i = 0; i < kBalWarps; ++i) sum += s_part[i];
+      for (int i = 0; i < kWarps; ++i) sum += s_part[i];
       a.ws->part[blockIdx.x] = sum;
       __threadfence();
       last = atomicAdd(&a.ws->header.balance_done, 1) == static_cast<int>(gridDim.x) - 1;
@@ -345,6 +424,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         *a.loss = static_cast<float>(sum);
         a.ws->header.balance_done = 0;
         a.ws->header.balance_arrived = 0;
+        a.ws->header.balance_live = 0;
       }
     }
   }
@@ -366,7 +446,7 @@ cudaError_t balance_launch(const BalanceArgs& a, int lpt_log, int num_sms, cudaS
   const int64_t stage = ahead ? std::min<int64_t>(kBalStage, static_cast<int64_t>(per_block) * a.E * sizeof(TZ)) : 0;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(blocks);
-  lc.blockDim = dim3(kBalThreads);
+  lc.blockDim = dim3(NC == 1 ? 1024 : 512);
   lc.dynamicSmemBytes = static_cast<size_t>(stage);
   lc.stream = stream;
   cudaLaunchAttribute at[1];

@@ -23,10 +23,12 @@ struct WsHeader {
   // Ticket counter of the permute's count blocks: zero when a launch starts,
   // reset to zero by the block that takes the last ticket.
   int32_t perm_done;
-  // The same of the balance loss's blocks, and how many came to its barriers.
+  // The same of the balance loss's blocks; how many have counted, and how many
+  // sequences have tokens.
   int32_t balance_done;
   int32_t balance_arrived;
-  int32_t pad[51];
+  int32_t balance_live;
+  int32_t pad[50];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 // (a layer has 4-bit or FP8 experts, never both: their kernels share the slots)

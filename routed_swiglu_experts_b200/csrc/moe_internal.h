@@ -263,7 +263,10 @@ cudaError_t launch_lora(const void* x, int dtype, int64_t x_stride, const void* 
 constexpr int kBalanceBlocks = 1024;
 struct BalanceWs {
   WsHeader header;
-  double part[kBalanceBlocks];  // the blocks' shares of the loss
+  static constexpr int kParts = 16;
+  double part[kBalanceBlocks];               // the blocks' shares of the loss
+  int32_t counts[kParts][MOE_MAX_EXPERTS];   // of one sequence's parts
+  int32_t tokens[kParts];
 };
 static_assert(sizeof(BalanceWs) <= MOE_BALANCE_WS_BYTES, "MOE_BALANCE_WS_BYTES");
 cudaError_t launch_balance(const moe_config& cfg, const void* logits, int dtype, int64_t stride, const int32_t* ids,
