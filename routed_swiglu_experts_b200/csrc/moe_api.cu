@@ -616,7 +616,7 @@ moe_status moe_rmsnorm(const void* x, int32_t x_type, int64_t x_stride, const vo
   if (!aligned16(weight) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
   return from_cuda(launch_rmsnorm(x, x_type, x_stride, residual, residual_stride, residual_out, residual_out_stride,
                                   residual != nullptr ? residual_type : x_type, weight, weight_type, eps, rows, H, out,
-                                  out_stride, q, scale, stream));
+                                  out_stride, q, scale, num_sms_current_device(), stream));
 }
 
 moe_status moe_lora_plan_size(int32_t T, int32_t num_adapters, size_t* bytes) {

@@ -228,7 +228,8 @@ cudaError_t launch_fp8_ffn(const moe_config& cfg, const moe_weights& w, const vo
 // RMS norm (rmsnorm.cu): see moe_rmsnorm.
 cudaError_t launch_rmsnorm(const void* x, int x_type, int64_t x_stride, const void* res, int64_t res_stride,
                            void* res_out, int64_t res_out_stride, int res_type, const void* w, int w_type, float eps,
-                           int rows, int H, void* out, int64_t out_stride, void* q, float* scale, cudaStream_t stream);
+                           int rows, int H, void* out, int64_t out_stride, void* q, float* scale, int num_sms,
+                           cudaStream_t stream);
 
 // Adapters (lora.cu).  A plan is its head, the tokens sorted by adapter (those
 // without one last) and tiles of rows of one adapter each.

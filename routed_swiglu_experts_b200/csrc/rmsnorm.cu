@@ -3,11 +3,13 @@
 //   h = round(x + residual) in the residual's type,  r = 1 / sqrt(mean(h^2) + eps)
 //   y = h * r * w,  out = round(y),  scale, q of y as in fp8_quant.cu
 // A row is read once and held in registers between the sum and the results.
-// The mean is summed in fp64 (exact squares of 16-bit values; no overflow for
-// large fp32 ones), y is fp32.  A block whose largest |y| lies within a few
-// fp32 steps of 448 * 2^e takes its scale from fp64 values: the scale there
-// doubles with the last bit.
+// Squares are added in fp32, pairwise over a thread's values, the lanes and the
+// warps.  fp64 is for two kinds of rows: with a block whose largest |y| lies within
+// some fp32 steps of 448 * 2^e (the scale there doubles with the last bit), and
+// with a sum near fp32's ends.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "moe_internal.h"
@@ -16,88 +18,97 @@ namespace moe {
 
 namespace {
 
+// Eight values as loaded, and as numbers.
 template <typename T>
-__device__ __forceinline__ void load16f(const T* p, float (&v)[16]);
+struct Vec8 {
+  static constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes
+  uint4 v[kPieces];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  // (fp32: whole sectors of 32 bytes where the address allows it)
+  __device__ __forceinline__ void store(T* p) const {
+    if (kPieces == 2 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0].x), "r"(v[0].y), "r"(v[0].z),
+                   "r"(v[0].w), "r"(v[kPieces - 1].x), "r"(v[kPieces - 1].y), "r"(v[kPieces - 1].z), "r"(v[kPieces - 1].w)
+                   : "memory");
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const;
+  __device__ __forceinline__ void set(const float (&f)[8]);  // nearest, ties to even
+};
 template <>
-__device__ __forceinline__ void load16f<float>(const float* p, float (&v)[16]) {
+__device__ __forceinline__ void Vec8<float>::get(float (&f)[8]) const {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(v[i].x), f[4 * i + 1] = __uint_as_float(v[i].y);
+    f[4 * i + 2] = __uint_as_float(v[i].z), f[4 * i + 3] = __uint_as_float(v[i].w);
+  }
+}
+template <>
+__device__ __forceinline__ void Vec8<float>::set(const float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+}
+template <>
+__device__ __forceinline__ void Vec8<__nv_bfloat16>::get(float (&f)[8]) const {
+  const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = bf16lo(w[i]), f[2 * i + 1] = bf16hi(w[i]);
+}
+template <>
+__device__ __forceinline__ void Vec8<__nv_bfloat16>::set(const float (&f)[8]) {
+  v[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+template <>
+__device__ __forceinline__ void Vec8<__half>::get(float (&f)[8]) const {
+  const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 a = *reinterpret_cast<const float4*>(p + 4 * i);
-    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = p.x, f[2 * i + 1] = p.y;
   }
 }
 template <>
-__device__ __forceinline__ void load16f<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[16]) {
+__device__ __forceinline__ void Vec8<__half>::set(const float (&f)[8]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p + 8 * i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[8 * i + 2 * j] = bf16lo(w[j]), v[8 * i + 2 * j + 1] = bf16hi(w[j]);
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
-}
-template <>
-__device__ __forceinline__ void load16f<__half>(const __half* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p + 8 * i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      v[8 * i + 2 * j] = f.x, v[8 * i + 2 * j + 1] = f.y;
-    }
-  }
+  v[0] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Stores 16 values, nearest with ties to even, and leaves in v what was stored.
-template <typename T>
-__device__ __forceinline__ void store16f(T* p, float (&v)[16]);
-template <>
-__device__ __forceinline__ void store16f<float>(float* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+// 1 / sqrt(m): Newton steps from the hardware's value (2^-22 relative).
+__device__ __forceinline__ float inv_sqrt(float m) {
+  const float r = rsqrtf(m), h = 0.5f * r;
+  return fmaf(h, fmaf(-m * r, r, 1.f), r);
 }
-template <>
-__device__ __forceinline__ void store16f<__nv_bfloat16>(__nv_bfloat16* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float &a = v[8 * i + 2 * j], &b = v[8 * i + 2 * j + 1];
-      w[j] = pack_bf16x2(a, b);
-      a = bf16lo(w[j]), b = bf16hi(w[j]);
-    }
-    *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-template <>
-__device__ __forceinline__ void store16f<__half>(__half* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float &a = v[8 * i + 2 * j], &b = v[8 * i + 2 * j + 1];
-      const __half2 h = __floats2half2_rn(a, b);
-      w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      const float2 f = __half22float2(h);
-      a = f.x, b = f.y;
-    }
-    *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// 1 / sqrt(m): two Newton steps in fp64 from the fp32 value (2^-22 to 2^-43 to
-// the last bits of fp64), outside fp32's range the fp64 functions.
 __device__ __forceinline__ double inv_sqrt(double m) {
   if (!(m > 1e-30 && m < 1e30)) return 1.0 / sqrt(m);
   double r = static_cast<double>(rsqrtf(static_cast<float>(m)));
 #pragma unroll
   for (int i = 0; i < 2; ++i) r = r * (1.5 - 0.5 * m * r * r);
   return r;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void sts16(uint32_t a, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 struct NormArgs {
@@ -113,120 +124,329 @@ struct NormArgs {
   float eps;
 };
 
-static_assert(MOE_NORM_MAX_COLUMNS == 1024 * 2 * 16, "1024 threads of two units of 16 values");
+static_assert(MOE_NORM_MAX_COLUMNS == 1024 * 4 * 8, "1024 threads of four units of 8 values");
+constexpr int kThreadsPerSm = 1024, kBytesPerSm = 208 * 1024;  // what the ring's blocks share
+constexpr int kAhead = 2;  // rows (or groups of them) of a thread in shared memory
 
-// `warps` warps per row (rows_per_block rows per block): thread t of a row
-// holds values 16 t .. 16 t + 15 and, V == 2, those 16 * 32 * warps behind.
-template <typename TX, typename TR, int V>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int warps) {
-  __shared__ double s_sum[32];
+// The larger magnitude, NaN if one is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// Sum of the first n (<= 32) floats at p, pairwise; what follows them up to a multiple of four is zero.
+__device__ __forceinline__ float sum_pairs(const float* p, int n) {
+  float s = 0.f;
+  for (int i = 0; i < n; i += 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
+    s += ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  }
+  return s;
+}
+
+// A row lies on `warps` warps.  A thread's V units of 8 values lie in one block of
+// 128, which 16 / V lanes share, each unit's lanes side by side: the block's largest
+// value takes few shuffles and its scale is found once a thread.  One warp a row: four rows a block,
+// each warp for itself.  RING: blocks walk over rows, and every thread fetches its
+// own units of the next ones ahead by cp.async (no thread waits for another's).
+template <typename TX, typename TR, bool RES, int V, bool RING, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) rmsnorm_kernel(const NormArgs a, const int warps) {
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  __shared__ __align__(16) float s_sum[2][32];
+  __shared__ double s_exact[32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int sub = warp / warps, wr = warp % warps;  // row of the block, warp of the row
-  const int row = blockIdx.x * (blockDim.x / 32 / warps) + sub;
-  const bool live = row < a.rows;
-  float h[V][16];
-  double sum = 0.0;
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int k = 16 * (u * 32 * warps + wr * 32 + lane);
-    if (live && k < a.H) {
-      load16f(static_cast<const TX*>(a.x) + row * a.x_stride + k, h[u]);
-      if (a.res != nullptr) {
-        float g[16];
-        load16f(static_cast<const TR*>(a.res) + row * a.res_stride + k, g);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) h[u][i] += g[i];
-        store16f(static_cast<TR*>(a.res_out) + row * a.res_out_stride + k, h[u]);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const double d = h[u][i];
-        sum = fma(d, d, sum);
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (warps > 1) {
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    sum = 0.0;
-    for (int i = 0; i < warps; ++i) sum += s_sum[sub * warps + i];
-  }
-  const double rd = inv_sqrt(sum / a.H + static_cast<double>(a.eps));
-  const float r = static_cast<float>(rd);
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int k = 16 * (u * 32 * warps + wr * 32 + lane);
-    const bool mine = live && k < a.H;
-    float w[16], y[16];
-    if (mine && a.w != nullptr) {
-      if (a.w_f32)
-        load16f(static_cast<const float*>(a.w) + k, w);
-      else
-        load16f(static_cast<const TX*>(a.w) + k, w);
+  const bool alone = warps == 1;
+  const int tr = alone ? lane : static_cast<int>(threadIdx.x);  // thread of the row
+  const int per = alone ? blockDim.x / 32 : 1;
+  const int step = RING ? static_cast<int>(gridDim.x) * per : a.rows;
+  constexpr int kLanes = 16 / V, kStep = 8 * kLanes;  // lanes of a block, values between a thread's units
+  const int k0 = tr / kLanes * 128 + tr % kLanes * 8, left = a.H - k0;  // unit u is in the row when u kStep < left
+  // a stage of the ring: V units of x, then of residual, in planes of 16 bytes a thread
+  constexpr int kX = V * Vec8<TX>::kPieces, kPlanes = kX + (RES ? V * Vec8<TR>::kPieces : 0);
+  const uint32_t plane = blockDim.x * 16, stage_bytes = kPlanes * plane;
+  constexpr bool kSharedCopies = sizeof(TX) == 4 || (RES && sizeof(TR) == 4);
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+  int row = blockIdx.x * per + (alone ? warp : 0);
+  const TX* x = static_cast<const TX*>(a.x) + row * a.x_stride + k0;
+  const TR* res = static_cast<const TR*>(a.res) + (RES ? row * a.res_stride + k0 : 0);
+  const TX* x_next = x;  // the next row to be fetched
+  const TR* res_next = res;
+  // A unit of the row at p (this thread's place in it) to its slot.  fp32: the
+  // lanes of a block load 16 neighbouring bytes each, also for one another.
+  auto fetch_unit = [&](const auto* p, int u, uint32_t at) {
+    using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    if constexpr (sizeof(E) == 2) {
+      if (u * kStep < left) copy16(at, p + u * kStep);
     } else {
+      const int j = tr % kLanes;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = 1.f;
+      for (int i = 0; i < 2; ++i) {
+        const int c = j + i * kLanes, off = u * kStep + 4 * c - 8 * j;
+        if (off < left) copy16(at + (c / 2 - j) * 16 + c % 2 * plane, p + off);
+      }
     }
+  };
+  auto fetch = [&](int next, uint32_t at) {
+    if (next < a.rows) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = mine ? h[u][i] * r * w[i] : 0.f;
+      for (int u = 0; u < V; ++u) {
+        fetch_unit(x_next, u, at + u * Vec8<TX>::kPieces * plane);
+        if constexpr (RES) fetch_unit(res_next, u, at + (kX + u * Vec8<TR>::kPieces) * plane);
+      }
+      x_next += step * a.x_stride;
+      if (RES) res_next += step * a.res_stride;
+    }
+    cp_async_commit();
+  };
+  if (!alone)  // (sums of warps that are not there)
+    for (int i = threadIdx.x; i < 64; i += blockDim.x)
+      if (i % 32 >= warps) s_sum[i / 32][i % 32] = 0.f;
+  // the weight stays in shared memory as fp32, behind the ring
+  const uint32_t w_at = ring + kAhead * stage_bytes;
+  auto weight = [&](int u, float (&w)[8]) {
+    if (a.w == nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    } else if (a.w_f32) {
+      Vec8<float> v;
+      v.load(static_cast<const float*>(a.w) + k0 + u * kStep);
+      v.get(w);
+    } else {
+      Vec8<TX> v;
+      v.load(static_cast<const TX*>(a.w) + k0 + u * kStep);
+      v.get(w);
+    }
+  };
+  if (RING) {
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (u * kStep < left) {
+        float w[8];
+        weight(u, w);
+        sts16(w_at + 2 * u * plane, make_float4(w[0], w[1], w[2], w[3]));
+        sts16(w_at + (2 * u + 1) * plane, make_float4(w[4], w[5], w[6], w[7]));
+      }
+  }
+  uint32_t at = ring, next_at = ring;
+  const uint32_t ring_end = ring + kAhead * stage_bytes;
+  if (RING) {
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) {
+      fetch(row + i * step, next_at);
+      next_at += stage_bytes;
+    }
+  }
+  int turn = 0;
+  for (; row < a.rows; row += step) {
+    if (RING) {
+      if (kSharedCopies) __syncwarp();  // (the slots' last values are read)
+      fetch(row + (kAhead - 1) * step, next_at);
+      next_at = next_at + stage_bytes == ring_end ? ring : next_at + stage_bytes;
+      cp_async_wait<kAhead - 1>();
+      if (kSharedCopies) __syncwarp();
+    }
+    float y[V][8], sum = 0.f;  // h first, then y
+    TR* sum_out = RES ? static_cast<TR*>(a.res_out) + row * a.res_out_stride + k0 : nullptr;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      if (u * kStep < left) {
+        Vec8<TX> v;
+        if (RING) {
+#pragma unroll
+          for (int i = 0; i < Vec8<TX>::kPieces; ++i) v.v[i] = lds16(at + (u * Vec8<TX>::kPieces + i) * plane);
+        } else {
+          v.load(x + u * kStep);
+        }
+        v.get(y[u]);
+        if (RES) {
+          Vec8<TR> g;
+          if (RING) {
+#pragma unroll
+            for (int i = 0; i < Vec8<TR>::kPieces; ++i) g.v[i] = lds16(at + (kX + u * Vec8<TR>::kPieces + i) * plane);
+          } else {
+            g.load(res + u * kStep);
+          }
+          float f[8];
+          g.get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[u][i] += f[i];
+          g.set(y[u]);
+          g.store(sum_out + u * kStep);
+          g.get(y[u]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[u][i] = 0.f;
+      }
+      float t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = fmaf(y[u][i], y[u][i], y[u][i + 4] * y[u][i + 4]);
+      sum += (t[0] + t[1]) + (t[2] + t[3]);
+    }
+    if (RING) at = at + stage_bytes == ring_end ? ring : at + stage_bytes;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (!alone) {
+      if (lane == 0) s_sum[turn][warp] = sum;
+      __syncthreads();
+      sum = sum_pairs(s_sum[turn], warps);
+      turn ^= 1;  // (the next row's sums go elsewhere: warps may still read these)
+    }
+    float r = inv_sqrt(__fdividef(sum, static_cast<float>(a.H)) + a.eps);
+    // h again, for the rows that need fp64: the sum as it was stored, or x (which
+    // out, if it is in its place, has not overwritten yet)
+    auto again = [&](int u, float (&h)[8]) {
+      if (u * kStep >= left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = 0.f;
+      } else if (RES) {
+        Vec8<TR> g;
+        g.load(sum_out + u * kStep);
+        g.get(h);
+      } else {
+        Vec8<TX> g;
+        g.load(static_cast<const TX*>(a.x) + row * a.x_stride + k0 + u * kStep);
+        g.get(h);
+      }
+    };
+    auto exact = [&] {
+      double e = 0.0;
+#pragma unroll 1
+      for (int u = 0; u < V; ++u) {
+        float h[8];
+        again(u, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e = fma(static_cast<double>(h[i]), static_cast<double>(h[i]), e);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      if (!alone) {
+        __syncthreads();
+        if (lane == 0) s_exact[warp] = e;
+        __syncthreads();
+        e = 0.0;
+        for (int i = 0; i < warps; ++i) e += s_exact[i];
+      }
+      return inv_sqrt(e / a.H + static_cast<double>(a.eps));
+    };
+    // near fp32's ends, or no number (the same for every thread of the row)
+    const bool wild = !(sum < 1e30f) || (sum < 1e-30f && sum > 0.f);
+    if (wild) r = static_cast<float>(exact());
+    float m = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      if (u * kStep < left) {
+        float w[8];
+        if (RING) {
+          Vec8<float> v;
+          v.v[0] = lds16(w_at + 2 * u * plane), v.v[1] = lds16(w_at + (2 * u + 1) * plane);
+          v.get(w);
+        } else {
+          weight(u, w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[u][i] = y[u][i] * r * w[i];
+          m = max_abs(m, y[u][i]);
+        }
+      }
+    }
     if (a.q != nullptr) {
-      uint32_t m = 0u;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // y is within 2.5 steps of the exact value (r half a step, two products)
-      const bool close = m < 0x7F800000u && (m & 0x7FFFFFu) - 0x5FFFF8u <= 16u;
-      if (__any_sync(0xffffffffu, close)) {
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // y is within 11 half steps of the exact value (14 additions' by half, 2 of r, two products)
+      const uint32_t bits = __float_as_uint(m);
+      const bool close = bits < 0x7F800000u && (bits & 0x7FFFFFu) - 0x5FFFF4u <= 24u;
+      if (alone ? __any_sync(0xffffffffu, close) : __syncthreads_or(close)) {
+        const double rd = exact();
         double e = 0.0;
+#pragma unroll 1
+        for (int u = 0; u < V; ++u)
+          if (u * kStep < left) {
+            float h[8], w[8];
+            again(u, h);
+            weight(u, w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e = mine ? fmax(e, fabs(static_cast<double>(h[u][i]) * rd * w[i])) : 0.0;
+            for (int i = 0; i < 8; ++i) e = fmax(e, fabs(static_cast<double>(h[i]) * rd * w[i]));
+          }
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) e = fmax(e, __shfl_xor_sync(0xffffffffu, e, o));
-        if (close) m = __float_as_uint(__double2float_ru(e));
+        for (int o = kLanes / 2; o > 0; o >>= 1) e = fmax(e, __shfl_xor_sync(0xffffffffu, e, o));
+        if (close) m = __double2float_ru(e);
       }
       float sc, inv;
-      e4m3_block_scale(m, sc, inv);
-      if (mine) {
-        uint32_t c[4];
+      e4m3_block_scale(__float_as_uint(m) & 0x7FFFFFFFu, sc, inv);
+      unsigned char* q = a.q + static_cast<size_t>(row) * a.H + k0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = e4m3x4(y[4 * i] * inv, y[4 * i + 1] * inv, y[4 * i + 2] * inv, y[4 * i + 3] * inv);
-        *reinterpret_cast<uint4*>(a.q + static_cast<size_t>(row) * a.H + k) = make_uint4(c[0], c[1], c[2], c[3]);
-        if ((lane & 7) == 0) a.scale[static_cast<size_t>(k / 128) * a.rows + row] = sc;
-      }
+      for (int u = 0; u < V; ++u)
+        if (u * kStep < left) {
+          const uint32_t c0 = e4m3x4(y[u][0] * inv, y[u][1] * inv, y[u][2] * inv, y[u][3] * inv);
+          const uint32_t c1 = e4m3x4(y[u][4] * inv, y[u][5] * inv, y[u][6] * inv, y[u][7] * inv);
+          *reinterpret_cast<uint2*>(q + u * kStep) = make_uint2(c0, c1);
+        }
+      if (tr % kLanes == 0 && left > 0) a.scale[static_cast<size_t>(tr / kLanes) * a.rows + row] = sc;
     }
-    if (mine && a.out != nullptr) store16f(static_cast<TX*>(a.out) + row * a.out_stride + k, y);
+    if (a.out != nullptr) {
+      TX* out = static_cast<TX*>(a.out) + row * a.out_stride + k0;
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (u * kStep < left) {
+          Vec8<TX> o;
+          o.set(y[u]);
+          o.store(out + u * kStep);
+        }
+    }
   }
 }
 
-template <typename TX, typename TR>
-cudaError_t norm_typed(const NormArgs& a, cudaStream_t stream) {
-  const int warps_row = (a.H + 511) / 512;
-  if (warps_row > 32) {
-    const int warps = (warps_row + 1) / 2;
-    return launch_kernel(rmsnorm_kernel<TX, TR, 2>, dim3(static_cast<unsigned>(a.rows)), dim3(32 * warps), 0, stream, a,
-                         warps);
+template <typename TX, typename TR, bool RES, int V, bool RING, int THREADS>
+cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cudaStream_t stream) {
+  auto kernel = rmsnorm_kernel<TX, TR, RES, V, RING, THREADS>;
+  if (RING) {
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kBytesPerSm);
+    if (e != cudaSuccess) return e;
   }
-  const int per = std::max(1, 4 / warps_row);  // small rows: four warps a block
-  return launch_kernel(rmsnorm_kernel<TX, TR, 1>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
-                       dim3(32 * warps_row * per), 0, stream, a, warps_row);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * warps * (warps == 1 ? 4 : 1)), bytes, stream, a, warps);
+}
+
+// Many rows: blocks that walk over them with the ring, 32 values a thread (what a
+// row costs beside its values is shared by more of them).  Few rows, or rows that
+// the ring has no room for: a block each, 16 values a thread while they fit.
+template <typename TX, typename TR, bool RES>
+cudaError_t norm_typed(const NormArgs& a, int num_sms, cudaStream_t stream) {
+  const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 4 : 1;
+  const int threads = 32 * warps * per, groups = (a.rows + per - 1) / per;
+  const int bytes = V * (kAhead * (Vec8<TX>::kPieces + (RES ? Vec8<TR>::kPieces : 0)) + 2) * 16 * threads;
+  const int resident = std::min(kThreadsPerSm / threads, kBytesPerSm / bytes);
+  if (resident >= 1 && groups > 2 * resident * num_sms) {
+    const int blocks = resident * num_sms;
+    if (V == 1) return norm_launch<TX, TR, RES, 1, true, 128>(a, warps, blocks, bytes, stream);
+    if (V == 2) return norm_launch<TX, TR, RES, 2, true, 128>(a, warps, blocks, bytes, stream);
+    if (threads <= 256) return norm_launch<TX, TR, RES, 4, true, 256>(a, warps, blocks, bytes, stream);
+    return norm_launch<TX, TR, RES, 4, true, 1024>(a, warps, blocks, bytes, stream);
+  }
+  if (a.H <= 256) return norm_launch<TX, TR, RES, 1, false, 128>(a, 1, groups, 0, stream);
+  const int v = a.H <= 16384 ? 2 : 4, w = (a.H + 256 * v - 1) / (256 * v), blocks = w == 1 ? (a.rows + 3) / 4 : a.rows;
+  return v == 2 ? norm_launch<TX, TR, RES, 2, false, 1024>(a, w, blocks, 0, stream) : norm_launch<TX, TR, RES, 4, false, 1024>(a, w, blocks, 0, stream);
+}
+
+template <typename TX>
+cudaError_t by_residual(const NormArgs& a, bool wide, int num_sms, cudaStream_t stream) {
+  if (a.res == nullptr) return norm_typed<TX, TX, false>(a, num_sms, stream);
+  return wide ? norm_typed<TX, float, true>(a, num_sms, stream) : norm_typed<TX, TX, true>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const void* x, int x_type, int64_t x_stride, const void* res, int64_t res_stride,
                            void* res_out, int64_t res_out_stride, int res_type, const void* w, int w_type, float eps,
-                           int rows, int H, void* out, int64_t out_stride, void* q, float* scale, cudaStream_t stream) {
+                           int rows, int H, void* out, int64_t out_stride, void* q, float* scale, int num_sms,
+                           cudaStream_t stream) {
   const NormArgs a{x, res, res_out, w, out, static_cast<unsigned char*>(q), scale, x_stride, res_stride,
                    res_out_stride, out_stride, rows, H, w_type == MOE_F32 ? 1 : 0, eps};
-  if (x_type == MOE_F32) return norm_typed<float, float>(a, stream);
-  if (x_type == MOE_BF16)
-    return res_type == MOE_F32 ? norm_typed<__nv_bfloat16, float>(a, stream)
-                               : norm_typed<__nv_bfloat16, __nv_bfloat16>(a, stream);
-  return res_type == MOE_F32 ? norm_typed<__half, float>(a, stream) : norm_typed<__half, __half>(a, stream);
+  if (x_type == MOE_F32) return by_residual<float>(a, true, num_sms, stream);
+  if (x_type == MOE_BF16) return by_residual<__nv_bfloat16>(a, res_type == MOE_F32, num_sms, stream);
+  return by_residual<__half>(a, res_type == MOE_F32, num_sms, stream);
 }
 
 }  // namespace moe
