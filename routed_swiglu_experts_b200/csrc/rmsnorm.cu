@@ -107,8 +107,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ void sts16(uint32_t a, float4 v) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 struct NormArgs {
@@ -120,12 +120,15 @@ struct NormArgs {
   unsigned char* q;
   float* scale;
   int64_t x_stride, res_stride, res_out_stride, out_stride;
-  int rows, H, w_f32;
+  int rows, H;
   float eps;
 };
 
 static_assert(MOE_NORM_MAX_COLUMNS == 1024 * 4 * 8, "1024 threads of four units of 8 values");
-constexpr int kThreadsPerSm = 1024, kBytesPerSm = 208 * 1024;  // what the ring's blocks share
+// What the ring's blocks share of an SM.  More bytes of rows on their way at once
+// take longer, not shorter (16384 x 6144, bf16 with residual: 96 KB 145 us, 144 KB
+// 168, 48 KB 210; without: 96 KB 75, 72 KB 84, 120 KB 93).
+constexpr int kThreadsPerSm = 768, kBytesPerSm = 208 * 1024, kInFlight = 96 * 1024;
 constexpr int kAhead = 2;  // rows (or groups of them) of a thread in shared memory
 
 // The larger magnitude, NaN if one is.
@@ -150,7 +153,7 @@ __device__ __forceinline__ float sum_pairs(const float* p, int n) {
 // value takes few shuffles and its scale is found once a thread.  One warp a row: four rows a block,
 // each warp for itself.  RING: blocks walk over rows, and every thread fetches its
 // own units of the next ones ahead by cp.async (no thread waits for another's).
-template <typename TX, typename TR, bool RES, int V, bool RING, int THREADS>
+template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) rmsnorm_kernel(const NormArgs a, const int warps) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ __align__(16) float s_sum[2][32];
@@ -202,19 +205,17 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
   if (!alone)  // (sums of warps that are not there)
     for (int i = threadIdx.x; i < 64; i += blockDim.x)
       if (i % 32 >= warps) s_sum[i / 32][i % 32] = 0.f;
-  // the weight stays in shared memory as fp32, behind the ring
+  // the weight stays in shared memory behind the ring (few rows: where it is)
+  using TW = std::conditional_t<W32, float, TX>;
+  const TW* weights = static_cast<const TW*>(a.w) + k0;
   const uint32_t w_at = ring + kAhead * stage_bytes;
   auto weight = [&](int u, float (&w)[8]) {
     if (a.w == nullptr) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    } else if (a.w_f32) {
-      Vec8<float> v;
-      v.load(static_cast<const float*>(a.w) + k0 + u * kStep);
-      v.get(w);
     } else {
-      Vec8<TX> v;
-      v.load(static_cast<const TX*>(a.w) + k0 + u * kStep);
+      Vec8<TW> v;
+      v.load(weights + u * kStep);
       v.get(w);
     }
   };
@@ -224,8 +225,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
       if (u * kStep < left) {
         float w[8];
         weight(u, w);
-        sts16(w_at + 2 * u * plane, make_float4(w[0], w[1], w[2], w[3]));
-        sts16(w_at + (2 * u + 1) * plane, make_float4(w[4], w[5], w[6], w[7]));
+        Vec8<TW> v;
+        v.set(w);
+#pragma unroll
+        for (int i = 0; i < Vec8<TW>::kPieces; ++i) sts16(w_at + (u * Vec8<TW>::kPieces + i) * plane, v.v[i]);
       }
   }
   uint32_t at = ring, next_at = ring;
@@ -339,8 +342,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
       if (u * kStep < left) {
         float w[8];
         if (RING) {
-          Vec8<float> v;
-          v.v[0] = lds16(w_at + 2 * u * plane), v.v[1] = lds16(w_at + (2 * u + 1) * plane);
+          Vec8<TW> v;
+#pragma unroll
+          for (int i = 0; i < Vec8<TW>::kPieces; ++i) v.v[i] = lds16(w_at + (u * Vec8<TW>::kPieces + i) * plane);
           v.get(w);
         } else {
           weight(u, w);
@@ -399,9 +403,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
   }
 }
 
-template <typename TX, typename TR, bool RES, int V, bool RING, int THREADS>
+template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS>
 cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cudaStream_t stream) {
-  auto kernel = rmsnorm_kernel<TX, TR, RES, V, RING, THREADS>;
+  auto kernel = rmsnorm_kernel<TX, TR, RES, W32, V, RING, THREADS>;
   if (RING) {
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kBytesPerSm);
     if (e != cudaSuccess) return e;
@@ -412,28 +416,33 @@ cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cud
 // Many rows: blocks that walk over them with the ring, 32 values a thread (what a
 // row costs beside its values is shared by more of them).  Few rows, or rows that
 // the ring has no room for: a block each, 16 values a thread while they fit.
-template <typename TX, typename TR, bool RES>
+template <typename TX, typename TR, bool RES, bool W32>
 cudaError_t norm_typed(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 4 : 1;
   const int threads = 32 * warps * per, groups = (a.rows + per - 1) / per;
-  const int bytes = V * (kAhead * (Vec8<TX>::kPieces + (RES ? Vec8<TR>::kPieces : 0)) + 2) * 16 * threads;
-  const int resident = std::min(kThreadsPerSm / threads, kBytesPerSm / bytes);
+  const int rows_bytes = V * kAhead * (Vec8<TX>::kPieces + (RES ? Vec8<TR>::kPieces : 0)) * 16 * threads;
+  const int bytes = rows_bytes + V * Vec8<std::conditional_t<W32, float, TX>>::kPieces * 16 * threads;
+  const int resident = std::min(std::min(std::max(1, kThreadsPerSm / threads), std::max(1, kInFlight / rows_bytes)), kBytesPerSm / bytes);
   if (resident >= 1 && groups > 2 * resident * num_sms) {
     const int blocks = resident * num_sms;
-    if (V == 1) return norm_launch<TX, TR, RES, 1, true, 128>(a, warps, blocks, bytes, stream);
-    if (V == 2) return norm_launch<TX, TR, RES, 2, true, 128>(a, warps, blocks, bytes, stream);
-    if (threads <= 256) return norm_launch<TX, TR, RES, 4, true, 256>(a, warps, blocks, bytes, stream);
-    return norm_launch<TX, TR, RES, 4, true, 1024>(a, warps, blocks, bytes, stream);
+    if (V == 1) return norm_launch<TX, TR, RES, W32, 1, true, 128>(a, warps, blocks, bytes, stream);
+    if (V == 2) return norm_launch<TX, TR, RES, W32, 2, true, 128>(a, warps, blocks, bytes, stream);
+    if (threads <= 256) return norm_launch<TX, TR, RES, W32, 4, true, 256>(a, warps, blocks, bytes, stream);
+    return norm_launch<TX, TR, RES, W32, 4, true, 1024>(a, warps, blocks, bytes, stream);
   }
-  if (a.H <= 256) return norm_launch<TX, TR, RES, 1, false, 128>(a, 1, groups, 0, stream);
+  if (a.H <= 256) return norm_launch<TX, TR, RES, W32, 1, false, 128>(a, 1, groups, 0, stream);
   const int v = a.H <= 16384 ? 2 : 4, w = (a.H + 256 * v - 1) / (256 * v), blocks = w == 1 ? (a.rows + 3) / 4 : a.rows;
-  return v == 2 ? norm_launch<TX, TR, RES, 2, false, 1024>(a, w, blocks, 0, stream) : norm_launch<TX, TR, RES, 4, false, 1024>(a, w, blocks, 0, stream);
+  return v == 2 ? norm_launch<TX, TR, RES, W32, 2, false, 1024>(a, w, blocks, 0, stream) : norm_launch<TX, TR, RES, W32, 4, false, 1024>(a, w, blocks, 0, stream);
 }
 
-template <typename TX>
+template <typename TX, bool W32>
 cudaError_t by_residual(const NormArgs& a, bool wide, int num_sms, cudaStream_t stream) {
-  if (a.res == nullptr) return norm_typed<TX, TX, false>(a, num_sms, stream);
-  return wide ? norm_typed<TX, float, true>(a, num_sms, stream) : norm_typed<TX, TX, true>(a, num_sms, stream);
+  if (a.res == nullptr) return norm_typed<TX, TX, false, W32>(a, num_sms, stream);
+  return wide ? norm_typed<TX, float, true, W32>(a, num_sms, stream) : norm_typed<TX, TX, true, W32>(a, num_sms, stream);
+}
+template <typename TX>
+cudaError_t by_weight(const NormArgs& a, bool w32, bool wide, int num_sms, cudaStream_t stream) {
+  return w32 ? by_residual<TX, true>(a, wide, num_sms, stream) : by_residual<TX, false>(a, wide, num_sms, stream);
 }
 
 }  // namespace
@@ -443,10 +452,11 @@ cudaError_t launch_rmsnorm(const void* x, int x_type, int64_t x_stride, const vo
                            int rows, int H, void* out, int64_t out_stride, void* q, float* scale, int num_sms,
                            cudaStream_t stream) {
   const NormArgs a{x, res, res_out, w, out, static_cast<unsigned char*>(q), scale, x_stride, res_stride,
-                   res_out_stride, out_stride, rows, H, w_type == MOE_F32 ? 1 : 0, eps};
-  if (x_type == MOE_F32) return by_residual<float>(a, true, num_sms, stream);
-  if (x_type == MOE_BF16) return by_residual<__nv_bfloat16>(a, res_type == MOE_F32, num_sms, stream);
-  return by_residual<__half>(a, res_type == MOE_F32, num_sms, stream);
+                   res_out_stride, out_stride, rows, H, eps};
+  const bool w32 = w != nullptr && w_type == MOE_F32, wide = res_type == MOE_F32;
+  if (x_type == MOE_F32) return by_residual<float, true>(a, true, num_sms, stream);
+  if (x_type == MOE_BF16) return by_weight<__nv_bfloat16>(a, w32, wide, num_sms, stream);
+  return by_weight<__half>(a, w32, wide, num_sms, stream);
 }
 
 }  // namespace moe
