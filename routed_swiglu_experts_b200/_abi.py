@@ -305,6 +305,9 @@ class _Torch:
         self.i32 = (torch.int32,)
         self.u8 = (torch.uint8,)
         self.masks = (torch.bool, torch.uint8)
+        # a float type alone, and it or fp32
+        self.alone = {t: (t,) for t in self.floats}
+        self.or_f32 = {t: (t, torch.float32) for t in self.floats}
         self.halves = (torch.bfloat16, torch.float16)
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.outs = (torch.bfloat16, torch.float32)
@@ -360,6 +363,21 @@ def _row_stride(t, name, where):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rows(t, name, dtypes, shape, where, dev):
+    """A 2-D tensor argument whose rows may be strided (shape None: any): the
+    checks of _want, and the elements between its rows."""
+    if t is not None and t.dtype in dtypes and t.get_device() == dev:
+        s = t.shape
+        if s == shape or (shape is None and len(s) == 2):
+            if t.is_contiguous():
+                return s[1]
+            st = t.stride()
+            if st[1] == 1 or s[1] == 1:
+                return st[0] if s[0] > 1 else s[1]
+    _want(t, name, dtypes, shape, where, dev, contiguous=False)
+    return _row_stride(t, name, where)
 
 
 def moe_gate_topk(cfg, logits, correction_bias, topk_ids, topk_w, stream=None):
@@ -443,30 +461,30 @@ def moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, out=None, q=No
     Rows of x, residual, residual_out and out may be strided."""
     where, tt = "moe_rmsnorm", _tt()
     dev = tt.device()
-    _want(x, "x", tt.floats, None, where, dev, contiguous=False)
-    x_stride = _row_stride(x, "x", where)
-    shape = rows, H = x.shape
-    types = (x.dtype,) + tt.f32
+    x_stride = _rows(x, "x", tt.floats, None, where, dev)
+    shape, dtype = x.shape, x.dtype
+    rows, H = shape
+    same, types = tt.alone[dtype], tt.or_f32[dtype]
+    x_type = res_type = w_type = tt.types[dtype]
+    res_ptr = res_out_ptr = w_ptr = out_ptr = q_ptr = scale_ptr = None
     res_stride = res_out_stride = out_stride = H
-    res_type = tt.types[x.dtype]
     if residual is not None or residual_out is not None:
-        _want(residual, "residual", types, shape, where, dev, contiguous=False)
-        _want(residual_out, "residual_out", (residual.dtype,), shape, where, dev, contiguous=False)
-        res_stride, res_out_stride = _row_stride(residual, "residual", where), _row_stride(residual_out, "residual_out", where)
-        res_type = tt.types[residual.dtype]
-    w_type = 0
+        res_stride = _rows(residual, "residual", types, shape, where, dev)
+        res_out_stride = _rows(residual_out, "residual_out", tt.alone[residual.dtype], shape, where, dev)
+        res_type, res_ptr, res_out_ptr = tt.types[residual.dtype], residual.data_ptr(), residual_out.data_ptr()
     if weight is not None:
         _want(weight, "weight", types, (H,), where, dev)
-        w_type = tt.types[weight.dtype]
+        w_type, w_ptr = tt.types[weight.dtype], weight.data_ptr()
     if out is not None:
-        _want(out, "out", (x.dtype,), shape, where, dev, contiguous=False)
-        out_stride = _row_stride(out, "out", where)
+        out_stride = _rows(out, "out", same, shape, where, dev)
+        out_ptr = out.data_ptr()
     if q is not None or scale is not None:
         _want(q, "q", tt.codes, shape, where, dev)
         _want(scale, "scale", tt.f32, (_blocks(H), rows), where, dev)
-    _check(load_library().moe_rmsnorm(x.data_ptr(), tt.types[x.dtype], x_stride, _ptr(residual), res_stride,
-                                      _ptr(residual_out), res_out_stride, res_type, _ptr(weight), w_type, eps, rows, H,
-                                      _ptr(out), out_stride, _ptr(q), _ptr(scale), _stream(stream, dev)), where)
+        q_ptr, scale_ptr = q.data_ptr(), scale.data_ptr()
+    _check(load_library().moe_rmsnorm(x.data_ptr(), x_type, x_stride, res_ptr, res_stride, res_out_ptr, res_out_stride, res_type,
+                                      w_ptr, w_type, eps, rows, H, out_ptr, out_stride, q_ptr, scale_ptr,
+                                      _stream(stream, dev)), where)
 
 
 def moe_lora_plan_size(T: int, num_adapters: int) -> int:
@@ -494,27 +512,29 @@ def moe_lora(x, a, b, scale, plan, base, out, ws, stream=None):
     a_l^T) b_l^T by the plan's adapters; a [L, rank, K], b [L, N, rank]."""
     where, tt = "moe_lora", _tt()
     dev = tt.device()
-    _want(x, "x", tt.halves, None, where, dev, contiguous=False)
-    x_stride = _row_stride(x, "x", where)
-    same = (x.dtype,)
+    x_stride = _rows(x, "x", tt.halves, None, where, dev)
+    same = tt.alone[x.dtype]
     _want(a, "a", same, None, where, dev)
     _want(b, "b", same, None, where, dev)
-    T, K = x.shape
-    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != K or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+    (T, K), a_shape, b_shape = x.shape, a.shape, b.shape
+    if len(a_shape) != 3 or len(b_shape) != 3 or a_shape[2] != K or b_shape[0] != a_shape[0] or b_shape[2] != a_shape[1]:
         raise ValueError(f"{where}: a must be [adapters, rank, {K}] and b [adapters, N, rank]")
-    L, r, _ = a.shape
-    N = b.shape[1]
+    L, N, r = b_shape
+    scale_ptr = base_ptr = None
     if scale is not None:
         _want(scale, "scale", tt.f32, (L,), where, dev)
+        scale_ptr = scale.data_ptr()
     _want(plan, "plan", tt.u8, None, where, dev)
-    _want(out, "out", same + tt.f32, (T, N), where, dev, contiguous=False)
-    out_stride = base_stride = _row_stride(out, "out", where)
-    if base is not None and base is not out:
-        _want(base, "base", (out.dtype,), (T, N), where, dev, contiguous=False)
-        base_stride = _row_stride(base, "base", where)
+    out_stride = base_stride = _rows(out, "out", tt.or_f32[x.dtype], (T, N), where, dev)
+    out_ptr = out.data_ptr()
+    if base is out:
+        base_ptr = out_ptr
+    elif base is not None:
+        base_stride = _rows(base, "base", tt.alone[out.dtype], (T, N), where, dev)
+        base_ptr = base.data_ptr()
     _want(ws, "ws", tt.u8, None, where, dev)
-    _check(load_library().moe_lora(x.data_ptr(), tt.types[x.dtype], x_stride, a.data_ptr(), b.data_ptr(), _ptr(scale), T, K,
-                                   N, r, L, plan.data_ptr(), plan.numel(), _ptr(base), base_stride, out.data_ptr(),
+    _check(load_library().moe_lora(x.data_ptr(), tt.types[x.dtype], x_stride, a.data_ptr(), b.data_ptr(), scale_ptr, T, K,
+                                   N, r, L, plan.data_ptr(), plan.numel(), base_ptr, base_stride, out_ptr,
                                    tt.types[out.dtype], out_stride, ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
 
 
@@ -527,36 +547,40 @@ def moe_balance_loss(cfg, logits, topk_ids, counts, seq_tokens, loss, ws, grad_l
     token_mask bool or uint8 [T]: tokens to count."""
     where, tt = "moe_balance_loss", _tt()
     dev = tt.device()
-    _want(logits, "logits", tt.floats, None, where, dev, contiguous=False)
-    stride = grad_stride = _row_stride(logits, "logits", where)
-    shape = T, E = logits.shape
+    stride = grad_stride = _rows(logits, "logits", tt.floats, None, where, dev)
+    shape, dtype = logits.shape, logits.dtype
+    T, E = shape
     if E != cfg.num_experts:
         raise ValueError(f"{where}: logits has {E} columns for {cfg.num_experts} experts")
     _want(topk_ids, "topk_ids", tt.i32, (T, cfg.top_k), where, dev)
-    S = 1
+    S, offsets_ptr, mask_ptr, up_ptr, grad_ptr = 1, None, None, None, None
     if seq_offsets is not None:
         _want(seq_offsets, "seq_offsets", tt.i32, None, where, dev)
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
             raise ValueError(f"{where}: seq_offsets must be [sequences + 1]")
-        S = seq_offsets.shape[0] - 1
+        S, offsets_ptr = seq_offsets.shape[0] - 1, seq_offsets.data_ptr()
     _want(counts, "counts", tt.i32, (S, E), where, dev)
     _want(seq_tokens, "seq_tokens", tt.i32, (S,), where, dev)
     if token_mask is not None:
         _want(token_mask, "token_mask", tt.masks, (T,), where, dev)
-    for t, name in ((loss, "loss"), (grad_loss, "grad_loss")):
-        if t is not None or name == "loss":
-            _want(t, name, tt.f32, None, where, dev)
-            if t.numel() != 1:
-                raise ValueError(f"{where}: {name} has {t.numel()} elements, expected 1")
+        mask_ptr = token_mask.data_ptr()
+    _want(loss, "loss", tt.f32, None, where, dev)
+    if loss.numel() != 1:
+        raise ValueError(f"{where}: loss has {loss.numel()} elements, expected 1")
+    if grad_loss is not None:
+        _want(grad_loss, "grad_loss", tt.f32, None, where, dev)
+        if grad_loss.numel() != 1:
+            raise ValueError(f"{where}: grad_loss has {grad_loss.numel()} elements, expected 1")
+        up_ptr = grad_loss.data_ptr()
     grad_type = 0
     if grad_logits is not None:
-        _want(grad_logits, "grad_logits", (logits.dtype,) + tt.f32, shape, where, dev, contiguous=False)
-        grad_stride, grad_type = _row_stride(grad_logits, "grad_logits", where), tt.types[grad_logits.dtype]
+        grad_stride = _rows(grad_logits, "grad_logits", tt.or_f32[dtype], shape, where, dev)
+        grad_type, grad_ptr = tt.types[grad_logits.dtype], grad_logits.data_ptr()
     _want(ws, "ws", tt.u8, None, where, dev)
     _check(load_library().moe_balance_loss(
-        ctypes.byref(cfg), logits.data_ptr(), tt.types[logits.dtype], stride, topk_ids.data_ptr(), _ptr(seq_offsets), S,
-        _ptr(token_mask), T, coef, _ptr(grad_loss), counts.data_ptr(), seq_tokens.data_ptr(), loss.data_ptr(),
-        _ptr(grad_logits), grad_type, grad_stride, ws.data_ptr(), ws.numel(), _stream(stream, dev)), where)
+        ctypes.byref(cfg), logits.data_ptr(), tt.types[dtype], stride, topk_ids.data_ptr(), offsets_ptr, S, mask_ptr, T, coef,
+        up_ptr, counts.data_ptr(), seq_tokens.data_ptr(), loss.data_ptr(), grad_ptr, grad_type, grad_stride, ws.data_ptr(),
+        ws.numel(), _stream(stream, dev)), where)
 
 
 def moe_permute_no_alloc(cfg, topk_ids, topk_w, x, T, expert_offsets, row_of, src, w_perm, x_perm, stream=None):

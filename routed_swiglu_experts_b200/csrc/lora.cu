@@ -629,13 +629,22 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   }
 }
 
-// CTAs of a cluster: of tiles of up to 128 tokens, and of tiles of at most 16
-// by how many of them there may be.
+// CTAs of a cluster of tiles of up to 128 tokens: as many as let the tiles, about
+// half of the adapters' last ones among them, run at once.  A cluster lies in one
+// of eight GPCs.  (4096 tokens, 34 tiles: 7 CTAs 36 us, 8 50, 4 47; 8192 tokens, 68
+// tiles: 4 CTAs 51 us, 5 70, 3 61; 16384 tokens, 136 tiles: 2 CTAs 109 us, 3 139.)
 #ifdef LORA_EXP
-int lora_cluster(int) { return atoi(getenv("LORA_C")); }
+int lora_cluster(int, int, int, int) { return atoi(getenv("LORA_C")); }
 int lora_few_cluster(int64_t) { return atoi(getenv("LORA_C")); }
 #else
-int lora_cluster(int T) { return T <= 4096 ? 8 : T <= 8192 ? 4 : 2; }
+int lora_cluster(int T, int L, int ctas_per_sm, int num_sms) {
+  const int tiles = T / lora_tile_rows(T) + std::min(T, L + 1) / 2, slots = num_sms / 8 * ctas_per_sm;  // (of a GPC)
+  for (int C = 8; C > 2; --C)
+    if (8 * (slots / C) >= tiles) return C;
+  return 2;
+}
+// ... and of tiles of at most 16, by how many there may be (32 tokens of 32 adapters:
+// 8 CTAs 9.5 us, 4 13; 64 of 64: 8 16 us, 4 14; 512 of 512: 4 105 us, 2 79).
 int lora_few_cluster(int64_t max_tiles) { return max_tiles <= 56 ? 8 : max_tiles <= 128 ? 4 : 2; }
 #endif
 
@@ -934,7 +943,7 @@ cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaSt
   auto kernel = lora_kernel<T, TO, RP>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kBytes);
   if (e != cudaSuccess) return e;
-  const int C = lora_cluster(a.T);
+  const int C = lora_cluster(a.T, a.L, RP == 128 ? 1 : 2, num_sms);
   LoraLaunch l(max_tiles, C, kLoraThreads, S::kBytes, num_sms, stream);
   LoraMaps maps;
   const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -240,11 +240,13 @@ struct LoraTile {
   int32_t adapter, row0, rows, pad;  // adapter -1: rows without one
 };
 constexpr int32_t kLoraPlanMagic = 0x4C6F5261;
-// Rows of a tile: few tokens in tiles of 16 or 32, so that their clusters cover the device.
+// Rows of a tile.  Decode batches: 16, one row tile of their kernel's products; else
+// 128, the rows of a tcgen05 product (64 or 32 for 1024 and 2048 tokens: more
+// clusters, but no faster).
 #ifdef LORA_EXP
 inline int lora_tile_rows(int T) { return atoi(getenv("LORA_M")); }
 #else
-inline int lora_tile_rows(int T) { return T <= 512 ? 16 : T <= 1024 ? 32 : T <= 2048 ? 64 : 128; }
+inline int lora_tile_rows(int T) { return T <= 512 ? 16 : 128; }
 #endif
 // Tiles that T tokens can make: whole ones, and a partial one per adapter that occurs.
 inline int64_t lora_max_tiles(int T, int L) { return T / lora_tile_rows(T) + std::min<int64_t>(T, int64_t(L) + 1); }
