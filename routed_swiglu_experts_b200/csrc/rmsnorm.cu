@@ -166,37 +166,22 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
   constexpr int kLanes = 16 / V, kStep = 8 * kLanes;  // lanes of a block, values between a thread's units
   const int k0 = tr / kLanes * 128 + tr % kLanes * 8, left = a.H - k0;  // unit u is in the row when u kStep < left
   // a stage of the ring: V units of x, then of residual, in planes of 16 bytes a thread
-  constexpr int kX = V * Vec8<TX>::kPieces, kPlanes = kX + (RES ? V * Vec8<TR>::kPieces : 0);
-  const uint32_t plane = blockDim.x * 16, stage_bytes = kPlanes * plane;
-  constexpr bool kSharedCopies = sizeof(TX) == 4 || (RES && sizeof(TR) == 4);
+  static_assert(!RING || (sizeof(TX) == 2 && (!RES || sizeof(TR) == 2)), "a unit is 16 bytes");
+  const uint32_t plane = blockDim.x * 16, stage_bytes = V * (RES ? 2 : 1) * plane;
   const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
   int row = blockIdx.x * per + (alone ? warp : 0);
   const TX* x = static_cast<const TX*>(a.x) + row * a.x_stride + k0;
   const TR* res = static_cast<const TR*>(a.res) + (RES ? row * a.res_stride + k0 : 0);
   const TX* x_next = x;  // the next row to be fetched
   const TR* res_next = res;
-  // A unit of the row at p (this thread's place in it) to its slot.  fp32: the
-  // lanes of a block load 16 neighbouring bytes each, also for one another.
-  auto fetch_unit = [&](const auto* p, int u, uint32_t at) {
-    using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    if constexpr (sizeof(E) == 2) {
-      if (u * kStep < left) copy16(at, p + u * kStep);
-    } else {
-      const int j = tr % kLanes;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = j + i * kLanes, off = u * kStep + 4 * c - 8 * j;
-        if (off < left) copy16(at + (c / 2 - j) * 16 + c % 2 * plane, p + off);
-      }
-    }
-  };
   auto fetch = [&](int next, uint32_t at) {
     if (next < a.rows) {
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        fetch_unit(x_next, u, at + u * Vec8<TX>::kPieces * plane);
-        if constexpr (RES) fetch_unit(res_next, u, at + (kX + u * Vec8<TR>::kPieces) * plane);
-      }
+      for (int u = 0; u < V; ++u)
+        if (u * kStep < left) {
+          copy16(at + u * plane, x_next + u * kStep);
+          if constexpr (RES) copy16(at + (V + u) * plane, res_next + u * kStep);
+        }
       x_next += step * a.x_stride;
       if (RES) res_next += step * a.res_stride;
     }
@@ -243,11 +228,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
   int turn = 0;
   for (; row < a.rows; row += step) {
     if (RING) {
-      if (kSharedCopies) __syncwarp();  // (the slots' last values are read)
       fetch(row + (kAhead - 1) * step, next_at);
       next_at = next_at + stage_bytes == ring_end ? ring : next_at + stage_bytes;
       cp_async_wait<kAhead - 1>();
-      if (kSharedCopies) __syncwarp();
     }
     float y[V][8], sum = 0.f;  // h first, then y
     TR* sum_out = RES ? static_cast<TR*>(a.res_out) + row * a.res_out_stride + k0 : nullptr;
@@ -255,18 +238,16 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
     for (int u = 0; u < V; ++u) {
       if (u * kStep < left) {
         Vec8<TX> v;
-        if (RING) {
-#pragma unroll
-          for (int i = 0; i < Vec8<TX>::kPieces; ++i) v.v[i] = lds16(at + (u * Vec8<TX>::kPieces + i) * plane);
+        if constexpr (RING) {
+          v.v[0] = lds16(at + u * plane);
         } else {
           v.load(x + u * kStep);
         }
         v.get(y[u]);
         if (RES) {
           Vec8<TR> g;
-          if (RING) {
-#pragma unroll
-            for (int i = 0; i < Vec8<TR>::kPieces; ++i) g.v[i] = lds16(at + (kX + u * Vec8<TR>::kPieces + i) * plane);
+          if constexpr (RING) {
+            g.v[0] = lds16(at + (V + u) * plane);
           } else {
             g.load(res + u * kStep);
           }
@@ -413,26 +394,30 @@ cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cud
   return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * warps * (warps == 1 ? 4 : 1)), bytes, stream, a, warps);
 }
 
-// Many rows: blocks that walk over them with the ring, 32 values a thread (what a
-// row costs beside its values is shared by more of them).  Few rows, or rows that
-// the ring has no room for: a block each, 16 values a thread while they fit.
+// Many rows of 16-bit values: blocks that walk over them with the ring, 32 values a
+// thread (what a row costs beside its values is shared by more of them).  Few rows,
+// and rows of fp32 values or with an fp32 residual, whose loads alone keep enough
+// bytes on their way: a block each, 16 values a thread while they fit.  (16384 x
+// 6144 bf16 with residual: ring 146 us, blocks 222; 8192 x 4096 fp32: 123 and 90.)
 template <typename TX, typename TR, bool RES, bool W32>
 cudaError_t norm_typed(const NormArgs& a, int num_sms, cudaStream_t stream) {
-  const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 4 : 1;
-  const int threads = 32 * warps * per, groups = (a.rows + per - 1) / per;
-  const int rows_bytes = V * kAhead * (Vec8<TX>::kPieces + (RES ? Vec8<TR>::kPieces : 0)) * 16 * threads;
-  const int bytes = rows_bytes + V * Vec8<std::conditional_t<W32, float, TX>>::kPieces * 16 * threads;
-  const int resident = std::min(std::min(std::max(1, kThreadsPerSm / threads), std::max(1, kInFlight / rows_bytes)), kBytesPerSm / bytes);
-  if (resident >= 1 && groups > 2 * resident * num_sms) {
-    const int blocks = resident * num_sms;
-    if (V == 1) return norm_launch<TX, TR, RES, W32, 1, true, 128>(a, warps, blocks, bytes, stream);
-    if (V == 2) return norm_launch<TX, TR, RES, W32, 2, true, 128>(a, warps, blocks, bytes, stream);
-    if (threads <= 256) return norm_launch<TX, TR, RES, W32, 4, true, 256>(a, warps, blocks, bytes, stream);
-    return norm_launch<TX, TR, RES, W32, 4, true, 1024>(a, warps, blocks, bytes, stream);
+  if constexpr (sizeof(TX) == 2 && (!RES || sizeof(TR) == 2)) {
+    const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 4 : 1;
+    const int threads = 32 * warps * per, groups = (a.rows + per - 1) / per;
+    const int rows_bytes = V * kAhead * (RES ? 2 : 1) * 16 * threads, bytes = rows_bytes + V * (W32 ? 2 : 1) * 16 * threads;
+    const int resident = std::min(std::min(std::max(1, kThreadsPerSm / threads), std::max(1, kInFlight / rows_bytes)), kBytesPerSm / bytes);
+    if (resident >= 1 && groups > 2 * resident * num_sms) {
+      const int blocks = resident * num_sms;
+      if (V == 1) return norm_launch<TX, TR, RES, W32, 1, true, 128>(a, warps, blocks, bytes, stream);
+      if (V == 2) return norm_launch<TX, TR, RES, W32, 2, true, 128>(a, warps, blocks, bytes, stream);
+      if (threads <= 256) return norm_launch<TX, TR, RES, W32, 4, true, 256>(a, warps, blocks, bytes, stream);
+      return norm_launch<TX, TR, RES, W32, 4, true, 1024>(a, warps, blocks, bytes, stream);
+    }
   }
-  if (a.H <= 256) return norm_launch<TX, TR, RES, W32, 1, false, 128>(a, 1, groups, 0, stream);
+  if (a.H <= 256) return norm_launch<TX, TR, RES, W32, 1, false, 128>(a, 1, (a.rows + 3) / 4, 0, stream);
   const int v = a.H <= 16384 ? 2 : 4, w = (a.H + 256 * v - 1) / (256 * v), blocks = w == 1 ? (a.rows + 3) / 4 : a.rows;
-  return v == 2 ? norm_launch<TX, TR, RES, W32, 2, false, 1024>(a, w, blocks, 0, stream) : norm_launch<TX, TR, RES, W32, 4, false, 1024>(a, w, blocks, 0, stream);
+  return v == 2 ? norm_launch<TX, TR, RES, W32, 2, false, 1024>(a, w, blocks, 0, stream)
+                : norm_launch<TX, TR, RES, W32, 4, false, 1024>(a, w, blocks, 0, stream);
 }
 
 template <typename TX, bool W32>
