@@ -240,48 +240,40 @@ __device__ __forceinline__ uint4 pack16(const float (&y)[8], T) {
   return make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
 }
 
-// 16 bytes of base from `at` on, `left` values of them there (left > 0), to
-// shared memory: by cp.async where every row starts on 16 bytes (wide), else value
-// by value.  No base: zeros.
+// Value by value, for rows that do not start on 16 bytes and for their ends: 16
+// bytes (`left` values of them there, or more) to shared memory, zeros without a
+// base; and the other way.  Not inlined: kept out of the way of the wide copies.
 template <typename TO>
-__device__ __forceinline__ void base_to_shared(uint32_t dst, const TO* base, int64_t at, int left, bool wide) {
+__device__ __noinline__ void base_to_shared(uint32_t dst, const TO* base, int left) {
   constexpr int kPer = 16 / sizeof(TO);
-  if (base == nullptr) {
-    sts128(dst, make_uint4(0u, 0u, 0u, 0u));
-  } else if (wide) {
-    cp_async16_part(dst, base + at, static_cast<uint32_t>(min(left, kPer) * static_cast<int>(sizeof(TO))));
-  } else {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (base != nullptr) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (i < left) {
-        const TO v = base[at + i];
+        const TO v = base[i];
         if constexpr (sizeof(TO) == 4)
           w[i] = __float_as_uint(v);
         else
           w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v)) << (i % 2 * 16);
       }
-    sts128(dst, make_uint4(w[0], w[1], w[2], w[3]));
   }
+  sts128(dst, make_uint4(w[0], w[1], w[2], w[3]));
 }
 template <typename TO>
-__device__ __forceinline__ void shared_to_out(TO* out, int64_t at, int left, bool wide, uint4 v) {
+__device__ __noinline__ void shared_to_out(TO* out, int left, uint4 v) {
   constexpr int kPer = 16 / sizeof(TO);
-  if (wide && left >= kPer) {
-    *reinterpret_cast<uint4*>(out + at) = v;
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < left) {
-        if constexpr (sizeof(TO) == 4) {
-          out[at + i] = __uint_as_float(w[i]);
-        } else {
-          const uint16_t b = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
-          out[at + i] = *reinterpret_cast<const TO*>(&b);
-        }
+  for (int i = 0; i < kPer; ++i)
+    if (i < left) {
+      if constexpr (sizeof(TO) == 4) {
+        out[i] = __uint_as_float(w[i]);
+      } else {
+        const uint16_t b = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+        out[i] = *reinterpret_cast<const TO*>(&b);
       }
-  }
+    }
 }
 
 __device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
@@ -432,11 +424,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       for (int n = (rank * 32 + lane) * kPer; n < a.N; n += C * 32 * kPer)
         for (int row = warp; row < rows; row += kLoraWorkers / 32) {
           const int64_t t = ctl.rows[row];
-          const uint32_t at = s_stage + tid * 16;
-          base_to_shared(at, static_cast<const TO*>(a.base), t * a.base_stride + n, a.N - n, a.wide);
-          cp_async_commit();
-          cp_async_wait<0>();
-          shared_to_out(static_cast<TO*>(a.out), t * a.out_stride + n, a.N - n, a.wide, lds128(at));
+          const TO* from = static_cast<const TO*>(a.base) + t * a.base_stride + n;
+          TO* to = static_cast<TO*>(a.out) + t * a.out_stride + n;
+          if (a.wide && a.N - n >= kPer) {
+            *reinterpret_cast<uint4*>(to) = a.base != nullptr ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            for (int i = 0; i < min(kPer, a.N - n); ++i) to[i] = a.base != nullptr ? from[i] : TO(0.f);
+          }
         }
       continue;
     }
@@ -555,15 +549,34 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     const int q32 = warp % 4 * 32, half = warp / 4;
     const bool busy = q32 < rows;
     const int boxes = mine * kOfChunk;
-    auto feature = [&](int box) { return (rank + C * (box / kOfChunk)) * 128 + box % kOfChunk * kBox + half * kHalf; };
-    auto fetch = [&](int box) {
-      const int n = feature(box) + lane % 4 * kPer;
+    auto feature = [&](int box) {  // this lane's first one in a box, as it fetches and stores
+      return (rank + C * (box / kOfChunk)) * 128 + box % kOfChunk * kBox + half * kHalf + lane % 4 * kPer;
+    };
+    // a lane's rows q32 + 8 i + lane / 4, where they are, and their place in a box
+    const TO* base_at[4];
+    TO* out_at[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = q32 + 8 * i + lane / 4;
-        if (row < rows && n < a.N)
-          base_to_shared(s_box + box % kRing * 16384 + swizzled(row, half * 4 + lane % 4), static_cast<const TO*>(a.base),
-                         ctl.rows[row] * a.base_stride + n, a.N - n, a.wide);
+    for (int i = 0; i < 4; ++i) {
+      const int row = q32 + 8 * i + lane / 4;
+      const int64_t t = row < rows ? ctl.rows[row] : 0;
+      base_at[i] = static_cast<const TO*>(a.base) + t * a.base_stride;
+      out_at[i] = row < rows ? static_cast<TO*>(a.out) + t * a.out_stride : nullptr;
+    }
+    const uint32_t place = s_box + swizzled(q32 + lane / 4, half * 4 + lane % 4);  // (+ 1024 i: eight rows on)
+    const bool fast = a.wide && a.base != nullptr;
+    auto fetch = [&](int box) {
+      const int n = feature(box), left = a.N - n;
+      const uint32_t at = place + box % kRing * 16384;
+      if (left <= 0) return;
+      if (fast) {
+        const uint32_t bytes = min(left, kPer) * static_cast<int>(sizeof(TO));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (out_at[i] != nullptr) cp_async16_part(at + 1024 * i, base_at[i] + n, bytes);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (out_at[i] != nullptr) base_to_shared(at + 1024 * i, a.base != nullptr ? base_at[i] + n : nullptr, left);
       }
     };
     if (busy) {
@@ -594,23 +607,28 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         tmem_ld_wait();
         const float f = kBf16 ? 1.f : __uint_as_float(static_cast<uint32_t>(ctl.exponent[q32 + lane]) << 23);
         const uint32_t at = s_box + box % kRing * 16384;
+        if (q32 + lane < rows) {
 #pragma unroll
-        for (int c = 0; c < 4 && q32 + lane < rows; ++c) {
-          const uint32_t p = at + swizzled(q32 + lane, half * 4 + c);
-          float y[kPer];
-          unpack16(lds128(p), y, TO());
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t p = at + swizzled(q32 + lane, half * 4 + c);
+            float y[kPer];
+            unpack16(lds128(p), y, TO());
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) y[i] = fmaf(__uint_as_float(v[c * kPer + i]), f, y[i]);
-          sts128(p, pack16(y, TO()));
+            for (int i = 0; i < kPer; ++i) y[i] = fmaf(__uint_as_float(v[c * kPer + i]), f, y[i]);
+            sts128(p, pack16(y, TO()));
+          }
         }
         __syncwarp();
-        const int n = feature(box) + lane % 4 * kPer;
+        const int n = feature(box), left = a.N - n;
+        const uint32_t from = place + box % kRing * 16384;
+        if (a.wide && left >= kPer) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = q32 + 8 * i + lane / 4;
-          if (row < rows && n < a.N)
-            shared_to_out(static_cast<TO*>(a.out), ctl.rows[row] * a.out_stride + n, a.N - n, a.wide,
-                          lds128(at + swizzled(row, half * 4 + lane % 4)));
+          for (int i = 0; i < 4; ++i)
+            if (out_at[i] != nullptr) *reinterpret_cast<uint4*>(out_at[i] + n) = lds128(from + 1024 * i);
+        } else if (left > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (out_at[i] != nullptr) shared_to_out(out_at[i] + n, left, lds128(from + 1024 * i));
         }
       }
       if (box % kOfChunk == kOfChunk - 1) {
