@@ -460,13 +460,13 @@ cudaError_t balance_launch(const BalanceArgs& a, int lpt_log, int num_sms, cudaS
 template <typename TZ, typename TG>
 cudaError_t balance_typed(const BalanceArgs& a, bool softmax, int num_sms, cudaStream_t stream) {
   int lpt_log = 0;
-  while (lpt_log < 5 && (8 << lpt_log) < a.E) ++lpt_log;
+  while (lpt_log < 5 && ((a.E > 128 ? 16 : 8) << lpt_log) < a.E) ++lpt_log;  // (two tokens a warp up to 256 experts)
   auto pick = [&](auto nc) {
     constexpr int NC = decltype(nc)::value;
     return softmax ? balance_launch<TZ, TG, true, NC>(a, lpt_log, num_sms, stream)
                    : balance_launch<TZ, TG, false, NC>(a, lpt_log, num_sms, stream);
   };
-  if (a.E <= 256) return pick(std::integral_constant<int, 1>());
+  if (a.E <= 128) return pick(std::integral_constant<int, 1>());
   if (a.E <= 512) return pick(std::integral_constant<int, 2>());
   return pick(std::integral_constant<int, 4>());
 }
