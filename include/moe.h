@@ -458,7 +458,10 @@ MOE_API moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t row
  *   h[t] = round(x[t] + residual[t])     in residual_type; written to residual_out
  *   y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * weight
  *   out[t] = round(y[t]) in x_type;  q, scale of y as moe_fp8_quantize's
- * The mean is summed in fp64, y is fp32 and rounded once for each result.
+ * Sums and y are fp32 (y within 2^-20 of its exact value), rounded once for
+ * each result; rows whose sum is near fp32's ends, and blocks whose largest |y|
+ * lies so near 448 * 2^e that fp32 leaves the scale open, are taken in fp64, so
+ * the scales are those of the exact y.
  * (The norm sees the residual as it is held, so a later reader of
  * residual_out finds the values that were normalised.)  A row that holds an
  * infinity or a NaN becomes NaN.
@@ -503,7 +506,8 @@ MOE_API moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num
  *            rows: pointer and stride), else it aliases no input
  * Products are summed in fp32; A_l x is carried to B as the sum of two values
  * of x_type (an error of 2^-16 of it at most); one rounding to out_type at
- * the end.  K and rank multiples of 8 (pad a smaller rank with zeros), rank at
+ * the end, by rows alone: a token's result does not depend on the others.  K and
+ * rank multiples of 8 (pad a smaller rank with zeros), rank at
  * most MOE_LORA_MAX_RANK, num_adapters at most MOE_MAX_ADAPTERS, K and N at
  * most 2^30; x, a and b 16-byte aligned, x's rows too.  ws: an initialised
  * workspace of any size from MOE_WS_HEADER_BYTES up. */

@@ -2,9 +2,13 @@
 //   out[t] = base[t] + scale_l * B_l (A_l x_t),  l the adapter of token t
 // A plan sorts the batch's tokens by adapter and cuts each adapter's rows into
 // tiles; it serves every projection of the step.
+// One B200, graph replay: 16384 tokens, K 6144, N 4096, 16 adapters of rank 64 100
+// us (4.9 TB/s of x, base and out: both products run at the memory's rate, the sum
+// between them does not); 4096 tokens, K 2048, N 5632, rank 16 31 us (3.5 TB/s);
+// 32 tokens of 32 adapters, K 6144, N 4096, rank 16 9.6 us and one token 5.0 us,
+// chains of latencies (11 MB and 0.3 MB).
 #include <cuda_fp16.h>
 
-#include <cstdlib>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -651,10 +655,6 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 // half of the adapters' last ones among them, run at once.  A cluster lies in one
 // of eight GPCs.  (4096 tokens, 34 tiles: 7 CTAs 36 us, 8 50, 4 47; 8192 tokens, 68
 // tiles: 4 CTAs 51 us, 5 70, 3 61; 16384 tokens, 136 tiles: 2 CTAs 109 us, 3 139.)
-#ifdef LORA_EXP
-int lora_cluster(int, int, int, int) { return atoi(getenv("LORA_C")); }
-int lora_few_cluster(int64_t) { return atoi(getenv("LORA_C")); }
-#else
 int lora_cluster(int T, int L, int ctas_per_sm, int num_sms) {
   const int tiles = T / lora_tile_rows(T) + std::min(T, L + 1) / 2, slots = num_sms / 8 * ctas_per_sm;  // (of a GPC)
   for (int C = 8; C > 2; --C)
@@ -664,7 +664,6 @@ int lora_cluster(int T, int L, int ctas_per_sm, int num_sms) {
 // ... and of tiles of at most 16, by how many there may be (32 tokens of 32 adapters:
 // 8 CTAs 9.5 us, 4 13; 64 of 64: 8 16 us, 4 14; 512 of 512: 4 105 us, 2 79).
 int lora_few_cluster(int64_t max_tiles) { return max_tiles <= 56 ? 8 : max_tiles <= 128 ? 4 : 2; }
-#endif
 
 // Clusters for the tiles; those that do not fit at once wait, and each takes
 // every so-manieth tile where there are more.

@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
-#include <cstdlib>
 #include <utility>
 
 #include "device_cache.h"
@@ -243,11 +242,7 @@ constexpr int32_t kLoraPlanMagic = 0x4C6F5261;
 // Rows of a tile.  Decode batches: 16, one row tile of their kernel's products; else
 // 128, the rows of a tcgen05 product (64 or 32 for 1024 and 2048 tokens: more
 // clusters, but no faster).
-#ifdef LORA_EXP
-inline int lora_tile_rows(int T) { return atoi(getenv("LORA_M")); }
-#else
 inline int lora_tile_rows(int T) { return T <= 512 ? 16 : 128; }
-#endif
 // Tiles that T tokens can make: whole ones, and a partial one per adapter that occurs.
 inline int64_t lora_max_tiles(int T, int L) { return T / lora_tile_rows(T) + std::min<int64_t>(T, int64_t(L) + 1); }
 __host__ __device__ inline size_t lora_tiles_at(int T) {
