@@ -8,8 +8,8 @@
 // (The usual form sums f_e times the mean of p_e: the same sum in another
 // order.)  So once the ids are counted, one pass over the logits gives both.
 //
-// One kernel.  Some blocks count: a sequence each, and sixteen parts where there
-// is one sequence alone.  The others wait for them (a cooperative launch; small
+// One kernel.  Some blocks count: runs of sequences, or sixteen parts where there is
+// one alone.  The others wait for them (a cooperative launch; small
 // batches take one block) while their logits come to shared memory.  Then every warp
 // walks over tokens.  One B200, graph replay: 16384 x 256 fp32 with gradient 19.8
 // us, of which launch and counting take half and the pass 6; 4096 x 64 bf16 in 24
@@ -189,12 +189,40 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
   const bool one = a.offsets == nullptr;
   const int parts = one && gridDim.x > 1 ? min(kBalParts, static_cast<int>(gridDim.x)) : 1;
   const int units = one ? parts : a.S;
+  const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
+  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
   int live = 0;  // sequences with tokens, of this block's
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t from = one ? static_cast<int64_t>(a.T) * u / parts : __ldg(a.offsets + u);
-    const int64_t to = one ? static_cast<int64_t>(a.T) * (u + 1) / parts : __ldg(a.offsets + u + 1);
-    const int first = static_cast<int>(max(from, int64_t(0)));
-    count_tokens(a, first, max(first, static_cast<int>(min(to, static_cast<int64_t>(a.T)))), s_count, &s_n);
+  auto border = [&](int u) {  // the first token of a part or sequence, within the tokens
+    const int64_t t = one ? static_cast<int64_t>(a.T) * u / parts : __ldg(a.offsets + u);
+    return static_cast<int>(min(max(t, int64_t(0)), static_cast<int64_t>(a.T)));
+  };
+  const bool one_by_one = one || u1 - u0 < 2 || border(u1) - border(u0) >= 64 * static_cast<int64_t>(u1 - u0);
+  if (!one_by_one) {
+    // short sequences: all of the run at once, straight into their own rows
+    const int64_t n = static_cast<int64_t>(u1 - u0) * a.E;
+    for (int64_t i = tid; i < n; i += kThreads) a.counts[static_cast<int64_t>(u0) * a.E + i] = 0;
+    for (int u = u0 + tid; u < u1; u += kThreads) a.tokens[u] = 0;
+    __syncthreads();
+    for (int t = border(u0) + tid; t < border(u1); t += kThreads) {
+      const int s = counted(a, t) ? sequence_of(a, t) : -1;
+      if (s < u0 || s >= u1) continue;
+      atomicAdd(a.tokens + s, 1);
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __ldg(a.ids + static_cast<int64_t>(t) * a.k + j);
+        if (e >= 0 && e < a.E) atomicAdd(a.counts + static_cast<int64_t>(s) * a.E + e, 1);
+      }
+    }
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    int mine = 0;
+    for (int u = u0 + tid; u < u1; u += kThreads) mine += __ldcg(a.tokens + u) > 0;
+    if (mine != 0) atomicAdd(&s_n, mine);
+    __syncthreads();
+    live = s_n;
+  }
+  for (int u = u0; u < u1 && one_by_one; ++u) {
+    const int first = border(u);
+    count_tokens(a, first, max(first, border(u + 1)), s_count, &s_n);
     int32_t* row = parts > 1 ? a.ws->counts[u] : a.counts + static_cast<int64_t>(u) * a.E;
     for (int e = tid; e < a.E; e += kThreads) row[e] = s_count[e];
     if (tid == 0) (parts > 1 ? a.ws->tokens : a.tokens)[u] = s_n;
@@ -204,8 +232,8 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
   for (int t = t0 + tid; t < min(t1, t0 + kSeqStage); t += kThreads) s_seq[t - t0] = counted(a, t) ? sequence_of(a, t) : -1;
   if (gridDim.x > 1) {  // (one block: its own stores, behind its own barrier)
     if (tid == 0) {
-      const int counting = min(units, static_cast<int>(gridDim.x));
-      if (blockIdx.x < counting) {
+      const int counting = min(units, static_cast<int>(gridDim.x));  // (blocks whose run is not empty)
+      if (u1 > u0) {
         if (live > 0) atomicAdd(&a.ws->header.balance_live, live);
         __threadfence();
         atomicAdd(&a.ws->header.balance_arrived, 1);

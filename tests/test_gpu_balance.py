@@ -240,3 +240,49 @@ def test_in_a_graph_and_on_two_streams():
     torch.cuda.synchronize()
     for o in both:
         assert all(torch.equal(x, y) for x, y in zip(a, o))
+
+
+def exact_on_device(z, ids, softmax, offsets, mask, coef):
+    """fp64 with the device's own operators, for sizes that the plain loops take too long on."""
+    (T, E), k, S = z.shape, ids.shape[1], offsets.numel() - 1
+    at = torch.arange(T, device="cuda")
+    seq = torch.searchsorted(offsets[1:].long(), at, right=True)
+    keep = mask & (at >= offsets[0]) & (at < offsets[-1])
+    seq = seq.clamp(max=S - 1)
+    n = torch.zeros(S, dtype=torch.int64, device="cuda").index_add(0, seq, keep.long())
+    flat = (seq[:, None] * E + ids.long()).view(-1)
+    counts = torch.zeros(S * E, dtype=torch.int64, device="cuda").index_add(0, flat, keep[:, None].expand(T, k).reshape(-1).long()).view(S, E)
+    p = torch.softmax(z if softmax else torch.nn.functional.logsigmoid(z), dim=1)
+    per = torch.where(keep, 1 / n.clamp(min=1).double()[seq], 0.0) * (coef / max(1, int((n > 0).sum())))
+    f = counts.double()[seq] * (E / k) / n.clamp(min=1).double()[seq][:, None]
+    d = (p * f).sum(1, keepdim=True)
+    slope = 1.0 if softmax else torch.sigmoid(-z)
+    return (per * d[:, 0]).sum(), counts, n, p * (f - d) * slope * per[:, None], p * (f + d) * slope * per[:, None]
+
+
+@pytest.mark.parametrize("T,E,k,S,dtype,pad", [(700, 8, 2, 600, F32, 0), (5000, 24, 3, 4000, BF16, 0), (5000, 24, 3, 4000, F32, 3),
+                                               (9001, 40, 4, 300, F32, 0), (20000, 33, 4, 7, BF16, 5), (16384, 256, 8, 512, F32, 0),
+                                               (3000, 512, 16, 50, F16, 0), (2001, 1000, 8, 3, F32, 0), (300, 4, 1, 100000, F32, 0),
+                                               (12000, 128, 8, 1, F16, 8), (30000, 256, 8, 2, BF16, 0)])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_large_batches_in_many_and_few_sequences(T, E, k, S, dtype, pad, softmax):
+    g = torch.Generator(device="cuda").manual_seed(T + S)
+    wide = (torch.randn(T, E + pad, generator=g, device="cuda") * 1.5).to(dtype)
+    z = wide[:, pad // 2:pad // 2 + E]
+    ids = z.float().topk(k, dim=1).indices.to(torch.int32)
+    cuts = torch.randint(0, T + 1, (S - 1,), generator=g, device="cuda").sort().values
+    offsets = torch.cat([torch.tensor([5], device="cuda"), cuts.clamp(5, T - 7), torch.tensor([T - 7], device="cuda")]).to(torch.int32)
+    mask = torch.rand(T, generator=g, device="cuda") < 0.8
+    counts = torch.full((S, E), -5, dtype=torch.int32, device="cuda")
+    tokens, loss = torch.full((S,), -5, dtype=torch.int32, device="cuda"), torch.full((), -5.0, device="cuda")
+    grad = torch.full((T, E), -5.0, device="cuda")
+    ws = workspace()
+    for _ in range(2):
+        rse.moe_balance_loss(config(E, k, softmax), z, ids, counts, tokens, loss, ws, grad_logits=grad, seq_offsets=offsets,
+                             token_mask=mask, coef=0.01)
+        assert rse.moe_read_device_error(ws) == 0
+        want, c, n, exact, size = exact_on_device(z.double(), ids, softmax, offsets, mask, 0.01)
+        assert torch.equal(counts.long(), c) and torch.equal(tokens.long(), n)
+        assert abs(float(loss) - float(want)) <= 2.0 ** -17 * float(want)
+        near = ((grad.double() - exact).abs() <= size * 2.0 ** -16 + 2.0 ** -149).all()
+        assert bool(near)
