@@ -8,12 +8,12 @@
 // (The usual form sums f_e times the mean of p_e: the same sum in another
 // order.)  So once the ids are counted, one pass over the logits gives both.
 //
-// One kernel.  Some blocks count: runs of sequences, or sixteen parts where there is
-// one alone.  The others wait for them (a cooperative launch; small
+// One kernel.  Some blocks count: runs of sequences, or about sixteen parts of few
+// ones.  The others wait for them (a cooperative launch; small
 // batches take one block) while their logits come to shared memory.  Then every warp
-// walks over tokens.  One B200, graph replay: 16384 x 256 fp32 with gradient 19.8
-// us, of which launch and counting take half and the pass 6; 4096 x 64 bf16 in 24
-// sequences 12.0; 64 x 8 7.2.
+// walks over tokens.  One B200, graph replay: 16384 x 256 fp32 with gradient 19.7
+// us, of which launch and counting take half and the pass 6 (in 512 sequences 23);
+// 16384 x 64 bf16 in 1 to 16 sequences 13.5 to 14.7; 4096 x 64 in 24 13; 64 x 8 8.4.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -63,13 +63,14 @@ __device__ __forceinline__ float to_f32(T v) {
   return static_cast<float>(v);
 }
 
-constexpr int kBalStage = 196 * 1024;  // bytes of logits that a block fetches ahead
+constexpr int kBalStage = 192 * 1024;  // bytes of logits that a block fetches ahead
 constexpr int kBalParts = BalanceWs::kParts;
 // logits of a batch that one block takes by itself, and of a block otherwise
 constexpr int64_t kBalOneBlock = 16384, kBalPerBlock = 8192;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 
-constexpr int kSeqStage = 2048;
+constexpr int kSeqStage = 2048, kFew = 2048;
+static_assert(kFew >= MOE_MAX_EXPERTS, "one sequence is few");
 
 // Counts the ids of tokens t0 .. t1 - 1 in shared memory (hist: zeroed here); n: tokens.
 __device__ __forceinline__ void count_tokens(const BalanceArgs& a, int t0, int t1, int32_t* hist, int32_t* n) {
@@ -158,8 +159,10 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
   extern __shared__ __align__(128) unsigned char s_rows[];  // logits fetched ahead
   constexpr int kThreads = NC == 1 ? 1024 : 512, kWarps = kThreads / 32;
   __shared__ double s_part[kWarps];
-  __shared__ int32_t s_count[MOE_MAX_EXPERTS];  // ids of a sequence, or f of the only one
+  __shared__ int32_t s_count[MOE_MAX_EXPERTS];  // ids of a sequence
   __shared__ int32_t s_seq[kSeqStage];          // the first tokens' sequences, -1: not counted
+  __shared__ float s_f[kFew];           // f of few sequences
+  __shared__ int32_t s_tokens[kBalParts];
   __shared__ int32_t s_n, s_ok;
   __shared__ __align__(8) uint64_t s_bar;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -187,16 +190,28 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
 
   // ---------------------------------------------------------------- count --
   const bool one = a.offsets == nullptr;
-  const int parts = one && gridDim.x > 1 ? min(kBalParts, static_cast<int>(gridDim.x)) : 1;
-  const int units = one ? parts : a.S;
+  // parts of each sequence, where the counts of all fit s_f
+  const bool few = one || static_cast<int64_t>(a.S) * a.E <= kFew;
+  const int parts = gridDim.x > 1 && few ? max(1, min(kBalParts, static_cast<int>(gridDim.x)) / a.S) : 1;
+  const int units = a.S * parts;
   const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
   int live = 0;  // sequences with tokens, of this block's
-  auto border = [&](int u) {  // the first token of a part or sequence, within the tokens
-    const int64_t t = one ? static_cast<int64_t>(a.T) * u / parts : __ldg(a.offsets + u);
-    return static_cast<int>(min(max(t, int64_t(0)), static_cast<int64_t>(a.T)));
+  auto start = [&](int s) {  // a sequence's first token, within the tokens (s = S: the last one's end)
+    const int t = one ? (s == 0 ? 0 : a.T) : __ldg(a.offsets + s);
+    return min(max(t, 0), a.T);
   };
-  const bool one_by_one = one || u1 - u0 < 2 || border(u1) - border(u0) >= 64 * static_cast<int64_t>(u1 - u0);
+  auto border = [&](int u) {  // a part's first token
+    const int s = u / parts;
+    if (parts == 1 || s == a.S) return start(s);
+    const int t = start(s);
+    return t + static_cast<int>(static_cast<int64_t>(max(start(s + 1) - t, 0)) * (u % parts) / parts);
+  };
+  auto border_end = [&](int u) {
+    const int s = u / parts;
+    return u % parts == parts - 1 ? start(s + 1) : border(u + 1);
+  };
+  const bool one_by_one = parts > 1 || u1 - u0 < 2 || border(u1) - border(u0) >= 64 * static_cast<int64_t>(u1 - u0);
   if (!one_by_one) {
     // short sequences: all of the run at once, straight into their own rows
     const int64_t n = static_cast<int64_t>(u1 - u0) * a.E;
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
   }
   for (int u = u0; u < u1 && one_by_one; ++u) {
     const int first = border(u);
-    count_tokens(a, first, max(first, border(u + 1)), s_count, &s_n);
+    count_tokens(a, first, max(first, border_end(u)), s_count, &s_n);
     int32_t* row = parts > 1 ? a.ws->counts[u] : a.counts + static_cast<int64_t>(u) * a.E;
     for (int e = tid; e < a.E; e += kThreads) row[e] = s_count[e];
     if (tid == 0) (parts > 1 ? a.ws->tokens : a.tokens)[u] = s_n;
@@ -257,28 +272,37 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
   const float ek = static_cast<float>(a.E) / static_cast<float>(a.k);
   // f of an expert that c of n tokens chose: E c / (k n), exactly E / k where all did
   auto share_of = [&](int c, int n, float per_token) { return c == n ? ek : static_cast<float>(c) * per_token; };
-  float* s_f = reinterpret_cast<float*>(s_count);
-  int n_one = s_n;
-  if (one) {
+  // Few sequences: their tokens and f once a block, for all of its warps (each warp
+  // for itself would read the same lines thousands of times).
+  const bool shared_f = one || parts > 1;
+  if (shared_f) {
     if (parts > 1) {
-      n_one = __reduce_add_sync(0xffffffffu, lane < parts ? __ldcg(&a.ws->tokens[lane]) : 0);
-      live = n_one > 0;
+      if (tid < a.S) s_tokens[tid] = 0;
+      __syncthreads();
+      if (tid < units) atomicAdd(&s_tokens[tid / parts], __ldcg(&a.ws->tokens[tid]));
+      __syncthreads();
+      live = __popc(__ballot_sync(0xffffffffu, lane < a.S && s_tokens[min(lane, a.S - 1)] > 0));
+      if (blockIdx.x == 0 && tid < a.S) a.tokens[tid] = s_tokens[tid];
+    } else if (tid == 0) {
+      s_tokens[0] = s_n;
     }
-    const float per_token = ek / static_cast<float>(max(n_one, 1));
-    for (int e = tid; e < a.E; e += kThreads) {
-      int c = s_count[e];
+    __syncthreads();
+    for (int i = tid; i < a.S * a.E; i += kThreads) {
+      const int s = i / a.E, e = i - s * a.E, n = s_tokens[s];
+      int c;
       if (parts > 1) {
         int32_t v[kBalParts];
 #pragma unroll
-        for (int p = 0; p < kBalParts; ++p) v[p] = p < parts ? __ldcg(&a.ws->counts[p][e]) : 0;
+        for (int p = 0; p < kBalParts; ++p) v[p] = p < parts ? __ldcg(&a.ws->counts[s * parts + p][e]) : 0;
         c = 0;
 #pragma unroll
         for (int p = 0; p < kBalParts; ++p) c += v[p];
-        if (blockIdx.x == 0) a.counts[e] = c;
+        if (blockIdx.x == 0) a.counts[i] = c;
+      } else {
+        c = s_count[e];
       }
-      s_f[e] = share_of(c, n_one, per_token);
+      s_f[i] = share_of(c, n, ek / static_cast<float>(max(n, 1)));
     }
-    if (parts > 1 && blockIdx.x == 0 && tid == 0) a.tokens[0] = n_one;
   }
   bool ok = s_ok != 0;
   if (fetched > 0) {
@@ -305,9 +329,9 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
         const int e = 8 * (l + (i << lpt_log)) + j;
         f[i][j] = one && e < a.E ? s_f[e] : 0.f;
       }
-    if (one && n_one > 0) {
+    if (one && s_tokens[0] > 0) {
       seq = 0;
-      share = whole / static_cast<float>(n_one);
+      share = whole / static_cast<float>(s_tokens[0]);
     }
     auto row8 = [&](int t, int e0, float (&v)[8]) {
       if (t - t0 < fetched)
@@ -327,21 +351,31 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
         s = t - t0 < kSeqStage ? s_seq[t - t0] : counted(a, t) ? sequence_of(a, t) : -1;
         if (s >= 0 && s != seq) {
             seq = s;
-            const int n = __ldcg(a.tokens + s);
-            int c[NC][8];
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int e = 8 * (l + (i << lpt_log)) + j;
-                c[i][j] = e < a.E ? __ldcg(a.counts + static_cast<int64_t>(s) * a.E + e) : 0;
-              }
-            const float per_token = ek / static_cast<float>(n);
+            const int n = shared_f ? s_tokens[s] : __ldcg(a.tokens + s);
             share = whole / static_cast<float>(n);
+            if (shared_f) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
+              for (int i = 0; i < NC; ++i)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) f[i][j] = share_of(c[i][j], n, per_token);
+                for (int j = 0; j < 8; ++j) {
+                  const int e = 8 * (l + (i << lpt_log)) + j;
+                  f[i][j] = e < a.E ? s_f[s * a.E + e] : 0.f;
+                }
+            } else {
+              int c[NC][8];
+#pragma unroll
+              for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const int e = 8 * (l + (i << lpt_log)) + j;
+                  c[i][j] = e < a.E ? __ldcg(a.counts + static_cast<int64_t>(s) * a.E + e) : 0;
+                }
+              const float per_token = ek / static_cast<float>(n);
+#pragma unroll
+              for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[i][j] = share_of(c[i][j], n, per_token);
+            }
         }
       }
       // (tokens that do not count go along: the lanes of a warp reduce together)
