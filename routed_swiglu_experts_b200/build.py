@@ -16,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -54,7 +55,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     nvcc = nvcc_path()
     os.makedirs(OBJDIR, exist_ok=True)
     hdr_time = max([_mtime(h) for h in headers()] + [_mtime(__file__)])
-    objs = []
+    objs, todo = [], []
     for src in sources():
         obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -63,7 +64,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
                 print(" ".join(cmd), flush=True)
-            subprocess.run(cmd, check=True)
+            todo.append(cmd)
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:  # (a compiler a core)
+        list(pool.map(lambda cmd: subprocess.run(cmd, check=True), todo))
     if force or _mtime(LIB) < max(_mtime(o) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs]
         if verbose:
