@@ -153,26 +153,31 @@ __device__ __forceinline__ float sum_pairs(const float* p, int n) {
 
 // A row lies on `warps` warps.  A thread's V units of 8 values lie in one block of
 // 128, which 16 / V lanes share, each unit's lanes side by side: the block's largest
-// value takes few shuffles and its scale is found once a thread.  One warp a row: four rows a block,
-// each warp for itself.  RING: blocks walk over rows, and every thread fetches its
-// own units of the next ones ahead by cp.async (no thread waits for another's).
-template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS>
+// value takes few shuffles and its scale is found once a thread.  Rows on one warp:
+// each warp of the block for itself, with LANES lanes a row, 8 up to 64 values and 16
+// up to 128 (131072 x 128 bf16 to both forms: 21 us, 42 with a warp a row; LANES as an
+// argument: 25, and 15% slower at 256 values).  RING: blocks walk over rows, and every
+// thread fetches its own units of the next ones ahead by cp.async (no thread waits for
+// another's).
+template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS, int LANES = 32>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) rmsnorm_kernel(const NormArgs a, const int warps) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ __align__(16) float s_sum[2][32];
   __shared__ double s_exact[32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const bool alone = warps == 1;
-  const int tr = alone ? lane : static_cast<int>(threadIdx.x);  // thread of the row
-  const int per = alone ? blockDim.x / 32 : 1;
+  const int tr = alone ? lane % LANES : static_cast<int>(threadIdx.x);  // thread of the row
+  const int per = alone ? blockDim.x / LANES : 1;
   const int step = RING ? static_cast<int>(gridDim.x) * per : a.rows;
   constexpr int kLanes = 16 / V, kStep = 8 * kLanes;  // lanes of a block, values between a thread's units
-  const int k0 = tr / kLanes * 128 + tr % kLanes * 8, left = a.H - k0;  // unit u is in the row when u kStep < left
+  const int k0 = tr / kLanes * 128 + tr % kLanes * 8;
+  int left = a.H - k0;  // unit u is in the row when u kStep < left (no row: none is)
   // a stage of the ring: V units of x, then of residual, in planes of 16 bytes a thread
   static_assert(!RING || (sizeof(TX) == 2 && (!RES || sizeof(TR) == 2)), "a unit is 16 bytes");
   const uint32_t plane = blockDim.x * 16, stage_bytes = V * (RES ? 2 : 1) * plane;
   const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
-  int row = blockIdx.x * per + (alone ? warp : 0);
+  const int in_warp = alone ? lane / LANES : 0;  // which of a warp's rows
+  int row = blockIdx.x * per + (alone ? threadIdx.x / LANES : 0);
   const TX* x = static_cast<const TX*>(a.x) + row * a.x_stride + k0;
   const TR* res = static_cast<const TR*>(a.res) + (RES ? row * a.res_stride + k0 : 0);
   const TX* x_next = x;  // the next row to be fetched
@@ -229,7 +234,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
     }
   }
   int turn = 0;
-  for (; row < a.rows; row += step) {
+  for (; row - in_warp < a.rows; row += step) {  // (the lanes of a warp stay together)
+    if (row >= a.rows) left = 0;
     if (RING) {
       fetch(row + (kAhead - 1) * step, next_at);
       next_at = next_at + stage_bytes == ring_end ? ring : next_at + stage_bytes;
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
     }
     if (RING) at = at + stage_bytes == ring_end ? ring : at + stage_bytes;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (!alone) {
       if (lane == 0) s_sum[turn][warp] = sum;
       __syncthreads();
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
         for (int i = 0; i < 8; ++i) e = fma(static_cast<double>(h[i]), static_cast<double>(h[i]), e);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      for (int o = LANES / 2; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
       if (!alone) {
         __syncthreads();
         if (lane == 0) s_exact[warp] = e;
@@ -319,7 +325,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
     };
     // near fp32's ends, or no number (the same for every thread of the row)
     const bool wild = !(sum < 1e30f) || (sum < 1e-30f && sum > 0.f);
-    if (wild) r = static_cast<float>(exact());
+    if (alone ? __any_sync(0xffffffffu, wild) : wild) {
+      const float precise = static_cast<float>(exact());
+      if (wild) r = precise;
+    }
     float m = 0.f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
@@ -341,8 +350,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
       }
     }
     if (a.q != nullptr) {
+      constexpr int block_lanes = kLanes < LANES ? kLanes : LANES;
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = block_lanes / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
       // y is within 11 half steps of the exact value (14 additions' by half, 2 of r, two products)
       const uint32_t bits = __float_as_uint(m);
       const bool close = bits < 0x7F800000u && (bits & 0x7FFFFFu) - 0x5FFFF4u <= 24u;
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
             for (int i = 0; i < 8; ++i) e = fmax(e, fabs(static_cast<double>(h[i]) * rd * w[i]));
           }
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) e = fmax(e, __shfl_xor_sync(0xffffffffu, e, o));
+        for (int o = block_lanes / 2; o > 0; o >>= 1) e = fmax(e, __shfl_xor_sync(0xffffffffu, e, o));
         if (close) m = __double2float_ru(e);
       }
       float sc, inv;
@@ -387,9 +397,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
   }
 }
 
-template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS>
+template <typename TX, typename TR, bool RES, bool W32, int V, bool RING, int THREADS, int LANES = 32>
 cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cudaStream_t stream) {
-  auto kernel = rmsnorm_kernel<TX, TR, RES, W32, V, RING, THREADS>;
+  auto kernel = rmsnorm_kernel<TX, TR, RES, W32, V, RING, THREADS, LANES>;
   if (RING) {
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kBytesPerSm);
     if (e != cudaSuccess) return e;
@@ -404,20 +414,29 @@ cudaError_t norm_launch(const NormArgs& a, int warps, int blocks, int bytes, cud
 // 6144 bf16 with residual: ring 146 us, blocks 222; 8192 x 4096 fp32: 123 and 90.)
 template <typename TX, typename TR, bool RES, bool W32>
 cudaError_t norm_typed(const NormArgs& a, int num_sms, cudaStream_t stream) {
+  const int row_lanes = a.H <= 64 ? 8 : a.H <= 128 ? 16 : 32;
   if constexpr (sizeof(TX) == 2 && (!RES || sizeof(TR) == 2)) {
-    const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 4 : 1;
-    const int threads = 32 * warps * per, groups = (a.rows + per - 1) / per;
+    const int V = a.H <= 256 ? 1 : a.H <= 512 ? 2 : 4, warps = (a.H + 256 * V - 1) / (256 * V), per = warps == 1 ? 128 / row_lanes : 1;
+    const int threads = warps == 1 ? 128 : 32 * warps, groups = (a.rows + per - 1) / per;
     const int rows_bytes = V * kAhead * (RES ? 2 : 1) * 16 * threads, bytes = rows_bytes + V * (W32 ? 2 : 1) * 16 * threads;
     const int resident = std::min(std::min(std::max(1, kThreadsPerSm / threads), std::max(1, kInFlight / rows_bytes)), kBytesPerSm / bytes);
     if (resident >= 1 && groups > 2 * resident * num_sms) {
       const int blocks = resident * num_sms;
+      if (row_lanes == 8) return norm_launch<TX, TR, RES, W32, 1, true, 128, 8>(a, warps, blocks, bytes, stream);
+      if (row_lanes == 16) return norm_launch<TX, TR, RES, W32, 1, true, 128, 16>(a, warps, blocks, bytes, stream);
       if (V == 1) return norm_launch<TX, TR, RES, W32, 1, true, 128>(a, warps, blocks, bytes, stream);
       if (V == 2) return norm_launch<TX, TR, RES, W32, 2, true, 128>(a, warps, blocks, bytes, stream);
       if (threads <= 256) return norm_launch<TX, TR, RES, W32, 4, true, 256>(a, warps, blocks, bytes, stream);
       return norm_launch<TX, TR, RES, W32, 4, true, 1024>(a, warps, blocks, bytes, stream);
     }
   }
-  if (a.H <= 256) return norm_launch<TX, TR, RES, W32, 1, false, 128>(a, 1, (a.rows + 3) / 4, 0, stream);
+  if (a.H <= 256) {
+    const int per = 128 / row_lanes;
+    const int blocks = (a.rows + per - 1) / per;
+    if (row_lanes == 8) return norm_launch<TX, TR, RES, W32, 1, false, 128, 8>(a, 1, blocks, 0, stream);
+    if (row_lanes == 16) return norm_launch<TX, TR, RES, W32, 1, false, 128, 16>(a, 1, blocks, 0, stream);
+    return norm_launch<TX, TR, RES, W32, 1, false, 128>(a, 1, blocks, 0, stream);
+  }
   const int v = a.H <= 16384 ? 2 : 4, w = (a.H + 256 * v - 1) / (256 * v), blocks = w == 1 ? (a.rows + 3) / 4 : a.rows;
   return v == 2 ? norm_launch<TX, TR, RES, W32, 2, false, 1024>(a, w, blocks, 0, stream)
                 : norm_launch<TX, TR, RES, W32, 4, false, 1024>(a, w, blocks, 0, stream);

@@ -113,3 +113,39 @@ def test_bad_rows_stay_alone():
     _, y = exact(x[keep], None)
     check(o[keep], q[keep], s[:, keep], y)
     assert bool(torch.isnan(o[1001]).all()) and bool(torch.isnan(o[3999, 1000]))
+
+
+@pytest.mark.parametrize("H", [16, 48, 64, 80, 112, 128])
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 7, 9, 31, 1001, 30001])
+@pytest.mark.parametrize("x_dtype,res_dtype", [(BF16, None), (F16, F16), (F32, None), (BF16, F32)])
+def test_small_rows_lie_side_by_side(rows, H, x_dtype, res_dtype):
+    """Several rows to a warp: rows of nothing, of NaN, of fp32's ends and at the scale's border next to ordinary
+    ones, and a last warp that is not full."""
+    g = torch.Generator(device="cuda").manual_seed(100 * rows + H)
+    x = torch.randn(rows, H, generator=g, device="cuda")
+    kind = torch.arange(rows, device="cuda") % 6
+    x[kind == 1] = 0
+    one = torch.zeros(H, device="cuda")
+    one[H // 2] = 1
+    x[kind == 2] = one
+    if x_dtype != F16:
+        x[kind == 3] *= 2.0 ** 70
+        x[kind == 4] *= 2.0 ** -70
+    x = x.to(x_dtype)
+    x[kind == 5, 3] = float("nan")
+    res = None if res_dtype is None else torch.zeros(rows, H, dtype=res_dtype, device="cuda")
+    w = torch.full((H,), 28 / H ** 0.5, device="cuda")
+    h, y = exact(x, w, res)
+    wide = torch.full((rows + 2, H + 16), 9.0, dtype=x_dtype, device="cuda")
+    o = wide[1:rows + 1, 8:H + 8]
+    q = torch.full((rows + 2, H), 1.0, device="cuda").to(F8)
+    s = torch.full((rows + 2,), 7.0, device="cuda")
+    sums = None if res is None else torch.empty_like(res)
+    rse.moe_rmsnorm(x, w, EPS, residual=res, residual_out=sums, out=o, q=q[1:rows + 1], scale=s[1:rows + 1].view(1, rows))
+    fine = kind != 5
+    check(o[fine], q[1:rows + 1][fine], s[1:rows + 1][fine].view(1, -1), y[fine])
+    assert bool(torch.isnan(o[~fine]).all())
+    if res is not None:
+        assert torch.equal(sums[fine], h[fine])
+    assert bool((wide[[0, -1]] == 9).all()) and bool((wide[:, :8] == 9).all()) and bool((wide[:, H + 8:] == 9).all())
+    assert bool((q[[0, -1]].float() == 1).all()) and bool((s[[0, -1]] == 7).all())
