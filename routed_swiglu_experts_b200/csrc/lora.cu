@@ -689,8 +689,10 @@ struct LoraLaunch {
 // global memory: K is taken in an order in which a lane's values are neighbours
 // (both operands in the same one).  A cluster of C CTAs x 8 warps shares K, the
 // sums go through shared memory twice (warps, then CTAs), and every warp adds
-// 32 features at a time to base; the first ones' B and base are on the way
-// while A x is summed.  (tcgen05 on the same tiles: 128 rows per instruction
+// 32 features at a time to base (16 above rank 32); the first ones' B and base are
+// on the way while A x is summed.  Rank above 64: one CTA a SM, 255 registers, 8 rank
+// tiles' A in flight (one token, 6144 to 2048, rank 128: 12.4 us; two CTAs with 2 tiles
+// in flight 17.9; at rank 64 two CTAs are ahead, 40 to 55 at 256 tokens).  (tcgen05 on the same tiles: 128 rows per instruction
 // whatever the tile has, 71 clocks for each k16 of a 16-row tile.)
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -738,7 +740,7 @@ __device__ __forceinline__ void store_pair(TO* p, int left, bool pair, float x, 
 }
 
 template <typename T, typename TO, int RP>
-__global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(const LoraArgs a, const int C) {
+__global__ void __launch_bounds__(kFewThreads, RP == 128 ? 1 : 2) lora_few_kernel(const LoraArgs a, const int C) {
   constexpr int kTiles = RP / 8;
   extern __shared__ __align__(16) float few_smem[];
   float* red = few_smem;                                // [8 warps][16][RP]
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_few_kernel(const LoraArgs
           w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
         }
       };
-      constexpr int kHold = RP == 128 || kTiles < 4 ? 2 : 4;  // rank tiles held at once
+      constexpr int kHold = RP == 128 ? 8 : kTiles < 4 ? 2 : 4;  // rank tiles held at once
       uint32_t x0[8], x1[8], w[kHold][8];
 #pragma unroll
       for (int i0 = 0; i0 < kTiles; i0 += kHold) {
