@@ -83,15 +83,17 @@ __device__ __forceinline__ void count_tokens(const BalanceArgs& a, int t0, int t
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (threadIdx.x % 32 == 0 && mine != 0) atomicAdd(n, mine);
   }
-  const int64_t end = static_cast<int64_t>(t1) * a.k;
+  // (at most 2^21 tokens of 16 ids: their numbers fit 32 bits)
+  const int32_t* ids = a.ids + static_cast<int64_t>(t0) * a.k;
+  const unsigned n_ids = static_cast<unsigned>(max(t1 - t0, 0)) * a.k, k = a.k;
   constexpr int kAtOnce = 8;
-  for (int64_t i = static_cast<int64_t>(t0) * a.k + threadIdx.x; i < end; i += kAtOnce * blockDim.x) {
+  for (unsigned i = threadIdx.x; i < n_ids; i += kAtOnce * blockDim.x) {
     int v[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      const int64_t at = i + j * static_cast<int>(blockDim.x);
-      v[j] = at < end ? __ldg(a.ids + at) : -1;
-      if (a.mask != nullptr && at < end && a.mask[at / a.k] == 0) v[j] = -1;
+      const unsigned at = i + j * blockDim.x;
+      v[j] = at < n_ids ? __ldg(ids + at) : -1;
+      if (a.mask != nullptr && at < n_ids && a.mask[t0 + at / k] == 0) v[j] = -1;
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j)
