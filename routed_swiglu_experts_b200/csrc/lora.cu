@@ -662,8 +662,13 @@ int lora_cluster(int T, int L, int ctas_per_sm, int num_sms) {
   return 2;
 }
 // ... and of tiles of at most 16, by how many there may be (32 tokens of 32 adapters:
-// 8 CTAs 9.5 us, 4 13; 64 of 64: 8 16 us, 4 14; 512 of 512: 4 105 us, 2 79).
-int lora_few_cluster(int64_t max_tiles) { return max_tiles <= 56 ? 8 : max_tiles <= 128 ? 4 : 2; }
+// 8 CTAs 9.5 us, 4 13; 64 of 64: 8 16 us, 4 14; 512 of 512: 4 105 us, 2 79).  One
+// CTA a SM, rank 128, 6144 to 4096: 16 tiles 8 CTAs 20 us, 4 28; 24: 8 33, 4 29; 32: 8
+// 36, 4 29, 2 46; 64, 4096 to 4096: 4 48, 2 42.
+int lora_few_cluster(int64_t max_tiles, int ctas_per_sm) {
+  if (ctas_per_sm == 1) return max_tiles <= 18 ? 8 : max_tiles <= 36 ? 4 : 2;
+  return max_tiles <= 56 ? 8 : max_tiles <= 128 ? 4 : 2;
+}
 
 // Clusters for the tiles; those that do not fit at once wait, and each takes
 // every so-manieth tile where there are more.
@@ -951,7 +956,7 @@ cudaError_t lora_few_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cu
   constexpr int kBytes = ((8 + 2) * kFewRows * RP + kFewRows) * 4;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kBytes);
   if (e != cudaSuccess) return e;
-  const int C = lora_few_cluster(max_tiles);
+  const int C = lora_few_cluster(max_tiles, RP == 128 ? 1 : 2);
   LoraLaunch l(max_tiles, C, kFewThreads, kBytes, num_sms, stream);
   return cudaLaunchKernelEx(&l.config, kernel, a, C);
 }
