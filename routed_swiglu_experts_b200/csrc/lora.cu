@@ -697,8 +697,9 @@ struct LoraLaunch {
 // 32 features at a time to base (16 above rank 32); the first ones' B and base are
 // on the way while A x is summed.  Rank above 64: one CTA a SM, 255 registers, 8 rank
 // tiles' A in flight (one token, 6144 to 2048, rank 128: 12.4 us; two CTAs with 2 tiles
-// in flight 17.9; at rank 64 two CTAs are ahead, 40 to 55 at 256 tokens).  (tcgen05 on the same tiles: 128 rows per instruction
-// whatever the tile has, 71 clocks for each k16 of a 16-row tile.)
+// in flight 17.9; at rank 64 two CTAs are ahead, 40 to 55 at 256 tokens).  (tcgen05
+// on the same tiles: 128 rows per instruction whatever the tile has, 71 clocks for
+// each k16 of a 16-row tile.)
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
