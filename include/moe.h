@@ -505,7 +505,8 @@ MOE_API moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num
  *   out      [T, N] of out_type (x_type or MOE_F32); may be base (the same
  *            rows: pointer and stride), else it aliases no input
  * Products are summed in fp32; A_l x is carried to B as the sum of two values
- * of x_type (an error of 2^-16 of it at most); one rounding to out_type at
+ * of x_type (an error of at most 2^-16 of each rank's value, or, MOE_F16, of
+ * 2^-39 of the token's largest one where that is more); one rounding to out_type at
  * the end, by rows alone: a token's result does not depend on the others.  K and
  * rank multiples of 8 (pad a smaller rank with zeros), rank at
  * most MOE_LORA_MAX_RANK, num_adapters at most MOE_MAX_ADAPTERS, K and N at

@@ -215,6 +215,16 @@ __device__ __forceinline__ float rest_of(float v) {
   return fabsf(h) <= 3.4028234e38f ? v - h : 0.f;
 }
 
+// fp16 has 5 bits of exponent: a token's A x is multiplied by a power of two that
+// brings its largest value m to [2^14, 2^15), so that values down to 2^-24 of it keep
+// 16 bits in hi + lo (brought to [1, 2), those down to 2^-9 did).  The exponent to go
+// by (15 for all below 2^-112: the power stays in fp32's range; an infinity has one
+// too, so that finite values beside it stay finite), the power, and the exponent of its
+// inverse as fp32 holds them.
+__device__ __forceinline__ uint32_t half_exponent(float m) { return max(__float_as_uint(m) >> 23, 15u); }
+__device__ __forceinline__ float half_scale(uint32_t e) { return __uint_as_float((268u - e) << 23); }
+__device__ __forceinline__ uint32_t half_back(uint32_t e) { return e - 14u; }
+
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -516,16 +526,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         v.x *= sc, v.y *= sc, v.z *= sc, v.w *= sc;
         uint32_t exponent = 127u;
         if (!kBf16) {
-          // fp16 has 5 bits of exponent: the token's values are brought to [1, 2) by a power of two
           float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
           for (int o = LT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t e = __float_as_uint(m) >> 23;
-          if (e > 0u && e < 254u) {
-            exponent = e;
-            const float inv = __uint_as_float((254u - e) << 23);
-            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-          }
+          const uint32_t e = half_exponent(m);
+          exponent = half_back(e);
+          const float inv = half_scale(e);
+          v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
         }
         const uint32_t h0 = pack2<T>(v.x, v.y), h1 = pack2<T>(v.z, v.w);
         const uint32_t l0 = pack2<T>(rest_of<T>(v.x), rest_of<T>(v.y)), l1 = pack2<T>(rest_of<T>(v.z), rest_of<T>(v.w));
@@ -905,13 +912,12 @@ __global__ void __launch_bounds__(kFewThreads, RP == 128 ? 1 : 2) lora_few_kerne
         m = fmaxf(m, fabsf(v[p]));
       }
       float inv = 1.f;
-      if (!kBf16) {  // fp16 has 5 bits of exponent: the token's values are brought to [1, 2) by a power of two
+      if (!kBf16) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t e = __float_as_uint(m) >> 23;
-        const bool scaled = e > 0u && e < 254u;
-        inv = scaled ? __uint_as_float((254u - e) << 23) : 1.f;
-        if (lane == 0) factor[row] = scaled ? __uint_as_float(e << 23) : 1.f;
+        const uint32_t e = half_exponent(m);
+        inv = half_scale(e);
+        if (lane == 0) factor[row] = __uint_as_float(half_back(e) << 23);
       }
 #pragma unroll
       for (int p = 0; p < kPerLane; ++p)
