@@ -141,7 +141,19 @@ __device__ __forceinline__ float max_abs(float m, float v) {
   return r;
 }
 
-// Sum of the first n (<= 32) floats at p, pairwise; what follows them up to a multiple of four is zero.
+// How far y may be off, in half units 2^-24 of its value, in the longest row (V 4, 32
+// warps).  Roundings of a square on its way through the sum: product and fma 2, a
+// unit's four 2, the units 3, the lanes 5, eight warps 3, the groups of them 3.  The
+// division has 2 ulp, a unit of 2^-23 each: 4; eps added 1.  Half of these reach r,
+// which the Newton step leaves at 1.5 more; and two products.
+constexpr int kSumRoundings = 2 + 2 + 3 + 5 + 3 + 3;
+constexpr double kHalfUnits = (kSumRoundings + 4 + 1) / 2.0 + 1.5 + 2;
+// A block whose largest |y| is so near 1.75 * 2^e, in fp32 steps (2^-23 there), is taken in fp64.
+constexpr uint32_t kBorderSteps = 16;
+static_assert(kHalfUnits * 1.75 / 2 < kBorderSteps - 1, "y's error and the step that the comparison itself needs");
+static_assert(kHalfUnits < 16, "y within 2^-20 of its exact value");
+
+// Sum of the first n (<= 32) floats at p, pairwise; what follows them up to a multiple of eight is zero.
 __device__ __forceinline__ float sum_pairs(const float* p, int n) {
   float s = 0.f;
   for (int i = 0; i < n; i += 8) {
@@ -353,9 +365,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 768 / THREADS : 1) r
       constexpr int block_lanes = kLanes < LANES ? kLanes : LANES;
 #pragma unroll
       for (int o = block_lanes / 2; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // y is within 11 half steps of the exact value (14 additions' by half, 2 of r, two products)
       const uint32_t bits = __float_as_uint(m);
-      const bool close = bits < 0x7F800000u && (bits & 0x7FFFFFu) - 0x5FFFF4u <= 24u;
+      const bool close = bits < 0x7F800000u && (bits & 0x7FFFFFu) - (0x600000u - kBorderSteps) <= 2u * kBorderSteps;
       if (alone ? __any_sync(0xffffffffu, close) : __syncthreads_or(close)) {
         const double rd = exact();
         double e = 0.0;
