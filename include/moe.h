@@ -615,11 +615,15 @@ MOE_API moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_byt
  * its tile-queue words in the header to zero and frees its tensor memory,
  * and the context stays usable.  Read the result with
  * moe_read_device_error(scratch, ...).  Returns MOE_OK once the launch is
- * enqueued; MOE_ERR_INVALID_ARG for another `kernel`. */
+ * enqueued; MOE_ERR_INVALID_ARG for another `kernel`.
+ *   MOE_SELFTEST_LORA: the same of moe_lora's kernel for more than 512 tokens,
+ * on one cluster of two CTAs, whose first stage of shared memory is never given
+ * back to the copies: no tile queue, everything else as above. */
 #define MOE_SELFTEST_PAIR_BF16 0
 #define MOE_SELFTEST_PAIR_INT4 1
 #define MOE_SELFTEST_PAIR_FP8_FEW 3
 #define MOE_SELFTEST_PAIR_FP8_WIDE 4
+#define MOE_SELFTEST_LORA 5
 MOE_API moe_status moe_selftest_pair_timeout(void* scratch, size_t scratch_bytes, int32_t kernel,
                                              moe_stream_t stream);
 

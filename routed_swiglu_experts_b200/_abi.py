@@ -58,6 +58,7 @@ MOE_SELFTEST_PAIR_BF16 = 0
 MOE_SELFTEST_PAIR_INT4 = 1
 MOE_SELFTEST_PAIR_FP8_FEW = 3
 MOE_SELFTEST_PAIR_FP8_WIDE = 4
+MOE_SELFTEST_LORA = 5
 
 
 class MoEError(RuntimeError):
@@ -607,7 +608,7 @@ def moe_selftest_device_timeout(scratch, stream=None):
 
 def moe_selftest_pair_timeout(scratch, kernel, stream=None):
     """Test hook: force the timeout path of a CTA-pair grouped GEMM
-    (one of MOE_SELFTEST_PAIR_*) on a tiny tile; read the error with moe_read_device_error(scratch)."""
+    (one of MOE_SELFTEST_PAIR_*) or of the adapters (MOE_SELFTEST_LORA) on a tiny tile; read the error with moe_read_device_error(scratch)."""
     _check(load_library().moe_selftest_pair_timeout(_ptr(scratch), scratch.numel() * scratch.element_size(),
                                                     int(kernel), _stream(stream)), "moe_selftest_pair_timeout")
 

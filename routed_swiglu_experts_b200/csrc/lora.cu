@@ -132,6 +132,8 @@ struct LoraArgs {
   int T, K, N, r, L;
   bool wide;  // base's and out's rows all start on 16-byte boundaries
   int32_t* err;
+  uint64_t wait_ns;        // limit of every wait on another role
+  bool test_withhold;      // test hook: the first stage is never given back
 };
 
 constexpr int kLoraWorkers = 256, kLoraThreads = kLoraWorkers + 32;  // and a warp that issues the MMAs
@@ -139,7 +141,8 @@ constexpr uint32_t kLoraTmemCols = 256;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 
 struct LoraCtl {
-  uint64_t full[4];        // a stage's copies have landed (every worker's, and A)
+  uint64_t full[4];        // a stage's rows of x have landed (every worker's)
+  uint64_t a_full[4];      // ... and its part of A (apart: after a wait that gave up its copy alone is waited for)
   uint64_t empty[4];       // the MMAs that read a stage are done
   uint64_t b_full[2];      // 128 features of B have landed
   uint64_t acc_full[2];    // an accumulator is complete: features, or A x (the first)
@@ -318,7 +321,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&ctl.full[i], kLoraWorkers + 1);
+      mbar_init(&ctl.full[i], kLoraWorkers);
+      mbar_init(&ctl.a_full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -345,19 +349,38 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
   const int nchunks = (a.N + 127) / 128;
   const int mine = nchunks > rank ? (nchunks - rank + C - 1) / C : 0;  // chunks of features: rank, rank + C, ...
 
-  // Waits for a barrier's next phase (`phases`: one bit per barrier).
+  // Waits for a barrier's next phase (`phases`: one bit per barrier).  After a wait
+  // that gave up a thread starts no copy and no MMA and stores no result: it goes
+  // along with the barriers of the block and the cluster, and at the end waits for
+  // what it had started.
+  bool dead = false;
   auto wait = [&](uint64_t* bars, uint32_t& phases, int i) {
-    if (!mbar_wait_bounded(bars + i, (phases >> i) & 1u, abort_flag, kTimeoutNs)) {
+    if (dead) return false;
+    if (!mbar_wait_bounded(bars + i, (phases >> i) & 1u, abort_flag, a.wait_ns)) {
+      dead = true;
       *abort_flag = 1;
       report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 1);
+      return false;
     }
     phases ^= 1u << i;
+    return true;
+  };
+  // The last copy by TMA on each of n barriers (bit i of `copies`: their number, odd or
+  // even); a barrier without one is in the phase that counts as over.
+  auto drain = [&](uint64_t* bars, uint32_t copies, int n) {
+    volatile int32_t never = 0;
+    for (int i = 0; i < n; ++i)
+      if (!mbar_wait_bounded(bars + i, ((copies >> i) & 1u) ^ 1u, &never, kTimeoutNs)) report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 2);
   };
 
   if (warp == kLoraWorkers / 32) {
     // -------------------------------------------------------- MMA issuer --
-    uint32_t full_ph = 0, b_ph = 0, acc_ph = 0, empty_ph = 3;  // (both accumulators start empty)
+    uint32_t full_ph = 0, a_ph = 0, b_ph = 0, acc_ph = 0, empty_ph = 3;  // (both accumulators start empty)
+    uint32_t b_copies = 0;
+    bool withhold = a.test_withhold;
     auto load_chunk = [&](int j) {  // this CTA's j-th 128 features of B
+      if (dead) return;
+      b_copies ^= 1u << (j & 1);
       mbar_arrive_expect_tx(&ctl.b_full[j & 1], S::kB);
 #pragma unroll
       for (int c = 0; c < S::kChunks; ++c)
@@ -373,23 +396,27 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         if (mine > 1) load_chunk(1);
       }
       if (lane == 0 && nkb > 0) {
-        wait(ctl.acc_empty, empty_ph, 0);
+        bool ok = wait(ctl.acc_empty, empty_ph, 0);
         auto block = [&](uint32_t at_x, uint32_t at_a, bool first) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16(tmem, sw128_kmajor_desc(at_x + kk * 32), sw128_kmajor_desc(at_a + kk * 32), idesc_a, !first || kk > 0);
         };
         int stage = 0;
-        for (int kb = 0; kb < nkb; ++kb) {
-          wait(ctl.full, full_ph, stage);
+        for (int kb = 0; ok && kb < nkb; ++kb) {
+          ok = wait(ctl.full, full_ph, stage) && wait(ctl.a_full, a_ph, stage);
+          if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_after();
           block(s_stage + stage * S::kStage, s_stage + stage * S::kStage + S::kX, kb == 0);
-          umma_commit(&ctl.empty[stage]);
+          if (!withhold) umma_commit(&ctl.empty[stage]);
+          withhold = false;
           stage = stage + 1 == S::kStages ? 0 : stage + 1;
         }
-        umma_commit(&ctl.acc_full[0]);
-        wait(ctl.acc_full, acc_ph, 0);
+        if (ok) {
+          umma_commit(&ctl.acc_full[0]);
+          wait(ctl.acc_full, acc_ph, 0);
+        }
       }
       __syncwarp();
       cluster_sync_all();
@@ -399,11 +426,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         for (int j = 0; j < mine; ++j) {
           const uint32_t wt = s_b + (j & 1) * S::kB, d = tmem + (j & 1) * 128;
           if (j > 0) {
-            wait(ctl.acc_full, acc_ph, (j - 1) & 1);  // (its B buffer is free)
+            if (!wait(ctl.acc_full, acc_ph, (j - 1) & 1)) break;  // (its B buffer is free)
             if (j + 1 < mine) load_chunk(j + 1);
           }
-          wait(ctl.acc_empty, empty_ph, j & 1);
-          wait(ctl.b_full, b_ph, j & 1);
+          if (!wait(ctl.acc_empty, empty_ph, j & 1) || !wait(ctl.b_full, b_ph, j & 1)) break;
           asm volatile("fence.proxy.async;" ::: "memory");
           tc_fence_after();
 #pragma unroll
@@ -418,13 +444,13 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       }
       __syncwarp();
     }
-    if (lane == 0 && *abort_flag) {
-      volatile int32_t never = 0;
+    if (dead) {
+      drain(ctl.b_full, b_copies, 2);
       umma_commit(&ctl.drained);
-      if (!mbar_wait_bounded(&ctl.drained, 0, &never, kTimeoutNs)) report_error(a.err, MOE_ERR_DEVICE_TIMEOUT, 2);
+      drain(&ctl.drained, 1u, 1);
     }
   } else {
-  uint32_t empty_ph = 0xF, full_ph = 0;  // (every stage starts empty)
+  uint32_t empty_ph = 0xF, full_ph = 0, a_copies = 0;  // (every stage starts empty)
   for (int it = blockIdx.x / C; it < head.tiles; it += gridDim.x / C) {
     if (it != static_cast<int>(blockIdx.x) / C) tile = tiles[it];
     const int rows = min(tile.rows, 128);
@@ -464,19 +490,21 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       for (int i = 0; i < 4; ++i)
         if (xr[i] != nullptr) cp_async16_or_zero(at + swizzled(tid / 8 + 32 * i, tid % 8), in ? xr[i] + k : xr[i], in);
       if (tid == 0) {
-        mbar_arrive_expect_tx(&ctl.full[stage], S::kA);
-        tma_load_3d(smem + stage * S::kStage + S::kX, &maps.a, (kb0 + kb) * 64, 0, tile.adapter, &ctl.full[stage]);
+        a_copies ^= 1u << stage;
+        mbar_arrive_expect_tx(&ctl.a_full[stage], S::kA);
+        tma_load_3d(smem + stage * S::kStage + S::kX, &maps.a, (kb0 + kb) * 64, 0, tile.adapter, &ctl.a_full[stage]);
       }
     };
     int stage = 0;
     for (int kb = 0; kb < nkb; ++kb) {
-      wait(ctl.empty, empty_ph, stage);
+      if (!wait(ctl.empty, empty_ph, stage)) break;
       load_stage(kb, stage);
       cp_async_mbar_arrive(&ctl.full[stage]);
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     // (complete: every copy into the stages has been read, their place is taken over)
     if (nkb > 0) wait(ctl.acc_full, full_ph, 0);
+    __syncwarp();
     tc_fence_after();
     {
       constexpr int kCols = RP >= 32 ? RP / 2 : RP;  // columns of a warp: two warps to a quarter of the lanes
@@ -590,7 +618,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
           if (out_at[i] != nullptr) base_to_shared(at + 1024 * i, a.base != nullptr ? base_at[i] + n : nullptr, left);
       }
     };
-    if (busy) {
+    if (busy && !dead) {
 #pragma unroll
       for (int i = 0; i < kRing - 1; ++i) {
         if (i < boxes) fetch(i);
@@ -600,7 +628,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     for (int box = 0; box < boxes; ++box) {
       const int j = box / kOfChunk;
       if (box % kOfChunk == 0) {
-        wait(ctl.acc_full, full_ph, j & 1);
+        dead = !__all_sync(0xffffffffu, wait(ctl.acc_full, full_ph, j & 1));
+        if (dead) break;
         tc_fence_after();
       }
       if (busy) {
@@ -649,7 +678,12 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
       }
     }
   }
+  if (dead) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tid == 0) drain(ctl.a_full, a_copies, 4);
   }
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -969,12 +1003,11 @@ cudaError_t lora_few_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cu
 }
 
 template <typename T, typename TO, int RP>
-cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int C, int num_sms, cudaStream_t stream) {
   using S = LoraSmem<RP>;
   auto kernel = lora_kernel<T, TO, RP>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kBytes);
   if (e != cudaSuccess) return e;
-  const int C = lora_cluster(a.T, a.L, RP == 128 ? 1 : 2, num_sms);
   LoraLaunch l(max_tiles, C, kLoraThreads, S::kBytes, num_sms, stream);
   LoraMaps maps;
   const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -995,10 +1028,11 @@ cudaError_t lora_by_rank(const LoraArgs& a, int64_t max_tiles, int num_sms, cuda
     if (a.r <= 64) return lora_few_typed<T, TO, 64>(a, max_tiles, num_sms, stream);
     return lora_few_typed<T, TO, 128>(a, max_tiles, num_sms, stream);
   }
-  if (a.r <= 16) return lora_typed<T, TO, 16>(a, max_tiles, num_sms, stream);
-  if (a.r <= 32) return lora_typed<T, TO, 32>(a, max_tiles, num_sms, stream);
-  if (a.r <= 64) return lora_typed<T, TO, 64>(a, max_tiles, num_sms, stream);
-  return lora_typed<T, TO, 128>(a, max_tiles, num_sms, stream);
+  const int C = lora_cluster(a.T, a.L, a.r > 64 ? 1 : 2, num_sms);
+  if (a.r <= 16) return lora_typed<T, TO, 16>(a, max_tiles, C, num_sms, stream);
+  if (a.r <= 32) return lora_typed<T, TO, 32>(a, max_tiles, C, num_sms, stream);
+  if (a.r <= 64) return lora_typed<T, TO, 64>(a, max_tiles, C, num_sms, stream);
+  return lora_typed<T, TO, 128>(a, max_tiles, C, num_sms, stream);
 }
 
 }  // namespace
@@ -1020,13 +1054,28 @@ cudaError_t launch_lora(const void* x, int dtype, int64_t x_stride, const void* 
   };
   const bool wide = rows16(out, out_stride) && (base == nullptr || rows16(base, base_stride));
   const LoraArgs a{x, w_a, w_b, scale, static_cast<const unsigned char*>(plan), base, out,
-                   x_stride, base_stride, out_stride, T, K, N, r, L, wide, err};
+                   x_stride, base_stride, out_stride, T, K, N, r, L, wide, err, kTimeoutNs, false};
   const int64_t tiles = lora_max_tiles(T, L);
   if (dtype == MOE_BF16)
     return out_type == MOE_F32 ? lora_by_rank<__nv_bfloat16, float>(a, tiles, num_sms, stream)
                                : lora_by_rank<__nv_bfloat16, __nv_bfloat16>(a, tiles, num_sms, stream);
   return out_type == MOE_F32 ? lora_by_rank<__half, float>(a, tiles, num_sms, stream)
                              : lora_by_rank<__half, __half>(a, tiles, num_sms, stream);
+}
+
+// Test hook: 16 tokens of one adapter of rank 16, K 640, N 256 (all zeros, in
+// `scratch`, which the caller has zeroed) on one cluster of two CTAs.  Each has five
+// K blocks for three stages, and its first stage is never given back, with every wait
+// limited to 20 ms: copies stop, both CTAs leave through the cluster's barriers.
+cudaError_t launch_lora_timeout_selftest(void* scratch, int32_t* err, cudaStream_t stream) {
+  unsigned char* at = static_cast<unsigned char*>(scratch);
+  constexpr int T = 16, K = 640, N = 256, r = 16, L = 1;
+  unsigned char* plan = at + 2048;
+  const cudaError_t e = launch_lora_plan(reinterpret_cast<const int32_t*>(at + 1024), T, L, plan, stream);
+  if (e != cudaSuccess) return e;
+  const LoraArgs a{at + 4096, at + 24576, at + 45056, nullptr, plan, nullptr, at + 53248, K, N, N, T, K, N, r, L, true, err,
+                   20000000ull, true};
+  return lora_typed<__nv_bfloat16, __nv_bfloat16, 16>(a, 1, 2, 2, stream);
 }
 
 }  // namespace moe

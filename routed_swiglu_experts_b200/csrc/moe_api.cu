@@ -703,9 +703,10 @@ moe_status moe_selftest_pair_timeout(void* scratch, size_t scratch_bytes, int32_
   if (scratch == nullptr || scratch_bytes < MOE_SELFTEST_SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(scratch) & 255u) != 0) return MOE_ERR_INVALID_ARG;
   if (kernel != MOE_SELFTEST_PAIR_BF16 && kernel != MOE_SELFTEST_PAIR_INT4 && kernel != MOE_SELFTEST_PAIR_FP8_FEW &&
-      kernel != MOE_SELFTEST_PAIR_FP8_WIDE)
+      kernel != MOE_SELFTEST_PAIR_FP8_WIDE && kernel != MOE_SELFTEST_LORA)
     return MOE_ERR_INVALID_ARG;
   MOE_CUDA_TRY(cudaMemsetAsync(scratch, 0, MOE_SELFTEST_SCRATCH_BYTES, stream));
+  if (kernel == MOE_SELFTEST_LORA) return from_cuda(launch_lora_timeout_selftest(scratch, err_word(scratch), stream));
   if (kernel == MOE_SELFTEST_PAIR_BF16)
     return from_cuda(launch_pair_timeout_selftest(scratch, err_word(scratch), tile_queue(scratch, kQueueGateUp), stream));
   if (kernel == MOE_SELFTEST_PAIR_FP8_FEW)

@@ -256,6 +256,8 @@ cudaError_t launch_lora(const void* x, int dtype, int64_t x_stride, const void* 
                         const float* scale, int T, int K, int N, int r, int L, const void* plan, const void* base,
                         int64_t base_stride, void* out, int out_type, int64_t out_stride, int32_t* err, int num_sms,
                         cudaStream_t stream);
+// Test hook of lora_kernel's timeout path (see moe_selftest_pair_timeout).
+cudaError_t launch_lora_timeout_selftest(void* scratch, int32_t* err, cudaStream_t stream);
 
 // Balance loss (balance.cu): workspace and launch; see moe_balance_loss.
 constexpr int kBalanceBlocks = 1024;
