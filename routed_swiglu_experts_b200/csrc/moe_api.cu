@@ -614,6 +614,17 @@ moe_status moe_rmsnorm(const void* x, int32_t x_type, int64_t x_stride, const vo
       bad_rows(residual_out, residual_out_stride, residual_type) || bad_rows(out, out_stride, x_type))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(weight) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  // an output in an input's place has its rows, and no two outputs are one
+  auto other_rows = [&](const void* o, int32_t o_type, int64_t o_stride, const void* i, int32_t i_type, int64_t i_stride) {
+    return o != nullptr && o == i && (o_type != i_type || (rows > 1 && o_stride != i_stride));
+  };
+  if (other_rows(residual_out, residual_type, residual_out_stride, x, x_type, x_stride) ||
+      other_rows(residual_out, residual_type, residual_out_stride, residual, residual_type, residual_stride) ||
+      other_rows(out, x_type, out_stride, x, x_type, x_stride) ||
+      other_rows(out, x_type, out_stride, residual, residual_type, residual_stride))
+    return MOE_ERR_INVALID_ARG;
+  if (out != nullptr && (out == residual_out || out == q || out == weight)) return MOE_ERR_INVALID_ARG;
+  if (q != nullptr && (q == x || q == residual || q == residual_out || q == weight)) return MOE_ERR_INVALID_ARG;
   return from_cuda(launch_rmsnorm(x, x_type, x_stride, residual, residual_stride, residual_out, residual_out_stride,
                                   residual != nullptr ? residual_type : x_type, weight, weight_type, eps, rows, H, out,
                                   out_stride, q, scale, num_sms_current_device(), stream));
