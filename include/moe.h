@@ -463,8 +463,11 @@ MOE_API moe_status moe_fp8_gemm(const void* a, const float* a_scale, int32_t row
  * lies so near 448 * 2^e that fp32 leaves the scale open, are taken in fp64, so
  * the scales are those of the exact y.
  * (The norm sees the residual as it is held, so a later reader of
- * residual_out finds the values that were normalised.)  A row that holds an
- * infinity or a NaN becomes NaN.
+ * residual_out finds the values that were normalised.)  A row of h that holds a
+ * NaN becomes NaN throughout.  One with an infinity becomes NaN where the
+ * infinities are and 0 elsewhere, as the formula has it: look at all of a row, or
+ * at residual_out, to find one.  Codes and scales follow: blocks with a NaN are
+ * NaN codes with scale 1, blocks of zeros zero codes with scale 1.
  *   x            [rows, H] of x_type, rows x_stride elements apart
  *   residual     [rows, H] of residual_type (x_type or MOE_F32), or NULL
  *   residual_out [rows, H] of residual_type; given with residual alone
