@@ -510,8 +510,10 @@ MOE_API moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num
  * Products are summed in fp32; A_l x is carried to B as the sum of two values
  * of x_type (an error of at most 2^-16 of each rank's value, or, MOE_F16, of
  * 2^-39 of the token's largest one where that is more); one rounding to out_type at
- * the end, by rows alone: a token's result does not depend on the others.  K and
- * rank multiples of 8 (pad a smaller rank with zeros), rank at
+ * the end.  A token's result does not depend on the other tokens' rows, on which
+ * adapters they have or on its place among them.  T and num_adapters decide how K is
+ * split and so the order of its sums: a token may differ in its last bits between
+ * calls of other sizes.  K and rank multiples of 8 (pad a smaller rank with zeros), rank at
  * most MOE_LORA_MAX_RANK, num_adapters at most MOE_MAX_ADAPTERS, K and N at
  * most 2^30; x, a and b 16-byte aligned, x's rows too.  ws: an initialised
  * workspace of any size from MOE_WS_HEADER_BYTES up. */
