@@ -544,7 +544,9 @@ MOE_API moe_status moe_lora(const void* x, int32_t x_type, int64_t x_stride, con
  *   grad_logits   [T, E] of grad_type (logits_type or MOE_F32), rows
  *                 grad_stride elements apart, out; or NULL.  Must not alias logits.
  * Sums are fp32 within a token and fp64 over tokens, in an order that does not
- * change from call to call.  T == 0 writes zeros.  ws: an initialised
+ * change from call to call.  Scores take the hardware's 2^x and 1 / x, a few units
+ * of 2^-24 of the score, and carry the rounding of its exponent, at most 2^-22
+ * |z - max z| of the score (sigmoid: 2^-22 |z|).  T == 0 writes zeros.  ws: an initialised
  * workspace of at least MOE_BALANCE_WS_BYTES. */
 MOE_API moe_status moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, int64_t row_stride,
                                     const int32_t* topk_ids, const int32_t* seq_offsets, int32_t num_seqs,
