@@ -352,32 +352,32 @@ __global__ void __launch_bounds__(NC == 1 ? 1024 : 512, 1)
       if (in) {
         s = t - t0 < kSeqStage ? s_seq[t - t0] : counted(a, t) ? sequence_of(a, t) : -1;
         if (s >= 0 && s != seq) {
-            seq = s;
-            const int n = shared_f ? s_tokens[s] : __ldcg(a.tokens + s);
-            share = whole / static_cast<float>(n);
-            if (shared_f) {
+          seq = s;
+          const int n = shared_f ? s_tokens[s] : __ldcg(a.tokens + s);
+          share = whole / static_cast<float>(n);
+          if (shared_f) {
 #pragma unroll
-              for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const int e = 8 * (l + (i << lpt_log)) + j;
-                  f[i][j] = e < a.E ? s_f[s * a.E + e] : 0.f;
-                }
-            } else {
-              int c[NC][8];
+              for (int j = 0; j < 8; ++j) {
+                const int e = 8 * (l + (i << lpt_log)) + j;
+                f[i][j] = e < a.E ? s_f[s * a.E + e] : 0.f;
+              }
+          } else {
+            int c[NC][8];
 #pragma unroll
-              for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const int e = 8 * (l + (i << lpt_log)) + j;
-                  c[i][j] = e < a.E ? __ldcg(a.counts + static_cast<int64_t>(s) * a.E + e) : 0;
-                }
-              const float per_token = ek / static_cast<float>(n);
+              for (int j = 0; j < 8; ++j) {
+                const int e = 8 * (l + (i << lpt_log)) + j;
+                c[i][j] = e < a.E ? __ldcg(a.counts + static_cast<int64_t>(s) * a.E + e) : 0;
+              }
+            const float per_token = ek / static_cast<float>(n);
 #pragma unroll
-              for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] = share_of(c[i][j], n, per_token);
-            }
+              for (int j = 0; j < 8; ++j) f[i][j] = share_of(c[i][j], n, per_token);
+          }
         }
       }
       // (tokens that do not count go along: the lanes of a warp reduce together)

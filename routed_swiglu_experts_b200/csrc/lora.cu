@@ -24,7 +24,7 @@ namespace {
 // then each warp walks its part again and hands out places 32 tokens at a time.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restrict__ ids, int T, int L, int tile_rows,
                                                         unsigned char* plan) {
-  extern __shared__ int32_t s_count[];  // [32][L + 1], then [L + 1] tile prefix
+  extern __shared__ int32_t s_count[];  // [32][L + 1]: a warp's tokens of each adapter, then their places
   __shared__ int32_t s_scan[2][32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, bins = L + 1;
   LoraPlan* head = reinterpret_cast<LoraPlan*>(plan);

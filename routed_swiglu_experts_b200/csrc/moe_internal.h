@@ -265,7 +265,7 @@ struct BalanceWs {
   WsHeader header;
   static constexpr int kParts = 16;
   double part[kBalanceBlocks];               // the blocks' shares of the loss
-  int32_t counts[kParts][MOE_MAX_EXPERTS];   // of one sequence's parts
+  int32_t counts[kParts][MOE_MAX_EXPERTS];   // of the parts of few sequences, one sequence's side by side
   int32_t tokens[kParts];
 };
 static_assert(sizeof(BalanceWs) <= MOE_BALANCE_WS_BYTES, "MOE_BALANCE_WS_BYTES");
