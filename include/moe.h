@@ -508,9 +508,9 @@ MOE_API moe_status moe_lora_plan(const int32_t* adapters, int32_t T, int32_t num
  *   out      [T, N] of out_type (x_type or MOE_F32); may be base (the same
  *            rows: pointer and stride), else it aliases no input
  * Products are summed in fp32; A_l x is carried to B as the sum of two values
- * of x_type (an error of at most 2^-16 of each rank's value, or, MOE_F16, of
- * 2^-39 of the token's largest one where that is more); one rounding to out_type at
- * the end.  A token's result does not depend on the other tokens' rows, on which
+ * of x_type, an error of at most 2^-16 of each rank's value (MOE_F16 2^-22, or 2^-39
+ * of the token's largest one where that is more), three where x is bf16 and out fp32,
+ * 2^-24; one rounding to out_type at the end.  A token's result does not depend on the other tokens' rows, on which
  * adapters they have or on its place among them.  T and num_adapters decide how K is
  * split and so the order of its sums: a token may differ in its last bits between
  * calls of other sizes.  K and rank multiples of 8 (pad a smaller rank with zeros), rank at

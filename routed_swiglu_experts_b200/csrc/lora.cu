@@ -112,10 +112,12 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
 //   shrink  each CTA multiplies its share of K: D[token, rank] in TMEM, x as the
 //           M operand (128 rows), A as N
 //   sum     the CTAs' shares are added through distributed shared memory, scaled
-//           and split into two 16-bit values hi + lo (the second is what the
-//           rounding of the first left), so that 16 bits or more of A x count
-//   expand  each CTA takes every C-th 128 features: D[token, feature], hi and lo as
-//           M, B as N; base comes through shared memory 128 bytes of a row at a
+//           and split into 16-bit values, each what the rounding of those before
+//           left: two, which carry 16 bits or more of A x, more than a 16-bit
+//           result keeps; three of bf16, all of fp32's bits, for an fp32 result (of
+//           fp16 two carry 22)
+//   expand  each CTA takes every C-th 128 features: D[token, feature], the parts of
+//           A x as M, B as N; base comes through shared memory 128 bytes of a row at a
 //           time, is added to in place, and the rows leave from there
 // Operands lie in shared memory as K-major rows of 128 bytes, 128-byte swizzle:
 // A and B by TMA (which fills up ranks, features and K with zeros), x and base by
@@ -151,7 +153,7 @@ struct LoraCtl {
   uint32_t tmem_base;
   int32_t abort_flag;
   int32_t rows[128];       // the tile's tokens
-  uint8_t exponent[128];   // fp16: what a token's hi and lo are to be multiplied by, 2^(exponent - 127)
+  uint8_t exponent[128];   // fp16: what a token's parts are to be multiplied by, 2^(exponent - 127)
 };
 
 // Maps of A [L, r, K] and B [L, N, r], boxes of 64 along the last dimension.
@@ -159,19 +161,30 @@ struct alignas(64) LoraMaps {
   CUtensorMap a, b;
 };
 
-template <int RP>
+// 16-bit values that A x is carried in.
+template <typename T, typename TO>
+constexpr int kLoraParts = std::is_same<T, __nv_bfloat16>::value && sizeof(TO) == 4 ? 3 : 2;
+
+template <int RP, int PARTS>
 struct LoraSmem {
   static constexpr int kX = 128 * 128, kA = RP * 128, kStage = kX + kA;
   static constexpr int kStages = RP == 128 ? 4 : 3;
   static constexpr int kChunks = RP == 128 ? 2 : 1;     // K chunks of 64 of the expand operands
   static constexpr int kB = kChunks * 128 * 128;        // 128 features of B
-  // In the stages' place, once A x is summed: hi and lo (side by side in one
-  // row where both fit), and kBoxes boxes of base, 128 bytes of each token; until
+  // In the stages' place, once A x is summed: its parts (side by side in one row of
+  // 64 values where they fit), and kBoxes boxes of base, 128 bytes of each token; until
   // then this CTA's share of A x lies where the boxes will be.
-  static constexpr int kLoAt = RP <= 32 ? 2 * RP : kChunks * 128 * 128;  // lo behind hi, bytes
-  static constexpr int kV = RP <= 32 ? 128 * 128 : 2 * kChunks * 128 * 128;
-  static constexpr int kBoxes = RP == 128 ? 4 : 3;
-  static constexpr int kPart = (128 * (RP + 4) * 4 + 1023) / 1024 * 1024;
+  static constexpr int kInRow = RP < 64 ? 64 / RP : 1;
+  static constexpr int part_at(int p) { return p / kInRow * kChunks * 16384 + p % kInRow * 2 * RP; }
+  static constexpr int kV = (PARTS + kInRow - 1) / kInRow * kChunks * 16384;
+  // (rank 64 in three parts: what two CTAs an SM leave holds two boxes, and the share
+  // without padding, its 16-byte pieces in another order in every row)
+  static constexpr bool kTight = RP == 64 && PARTS == 3;
+  static constexpr int kBoxes = RP == 128 ? 4 : kTight ? 2 : 3;
+  static constexpr int kPart = (128 * (RP + (kTight ? 0 : 4)) * 4 + 1023) / 1024 * 1024;
+  __device__ static uint32_t share_at(int row, int r) {  // r a multiple of 4
+    return kTight ? row * RP * 4 + ((r / 4 ^ row % 16) << 4) : (row * (RP + 4) + r) * 4;
+  }
   static constexpr int kAfter = kV + (kPart > kBoxes * 16384 ? kPart : kBoxes * 16384);
   static constexpr int kFront = kAfter > kStages * kStage ? kAfter : kStages * kStage;
   // (two CTAs of 256 TMEM columns fit an SM, a third must not start: it would
@@ -220,7 +233,7 @@ __device__ __forceinline__ float rest_of(float v) {
 
 // fp16 has 5 bits of exponent: a token's A x is multiplied by a power of two that
 // brings its largest value m to [2^14, 2^15), so that values down to 2^-24 of it keep
-// 16 bits in hi + lo (brought to [1, 2), those down to 2^-9 did).  The exponent to go
+// 16 bits in two parts (brought to [1, 2), those down to 2^-9 did).  The exponent to go
 // by (15 for all below 2^-112: the power stays in fp32's range; an infinity has one
 // too, so that finite values beside it stay finite), the power, and the exponent of its
 // inverse as fp32 holds them.
@@ -300,7 +313,8 @@ __device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
 template <typename T, typename TO, int RP>
 __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
     lora_kernel(const __grid_constant__ LoraMaps maps, const LoraArgs a, const int C) {
-  using S = LoraSmem<RP>;
+  constexpr int kParts = kLoraParts<T, TO>;
+  using S = LoraSmem<RP, kParts>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const LoraPlan head = *reinterpret_cast<const LoraPlan*>(a.plan);
   const int32_t* src = reinterpret_cast<const int32_t*>(a.plan + sizeof(LoraPlan));
@@ -433,10 +447,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
           asm volatile("fence.proxy.async;" ::: "memory");
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 2 * (RP / 16); ++kk) {  // hi, then lo
+          for (int kk = 0; kk < kParts * (RP / 16); ++kk) {  // part after part
             const int q = kk % (RP / 16);
             const uint32_t at = q / 4 * 16384 + q % 4 * 32;
-            umma_bf16(d, sw128_kmajor_desc(s_v + (kk >= RP / 16 ? S::kLoAt : 0) + at), sw128_kmajor_desc(wt + at), idesc_b, kk > 0);
+            umma_bf16(d, sw128_kmajor_desc(s_v + S::part_at(kk / (RP / 16)) + at), sw128_kmajor_desc(wt + at), idesc_b, kk > 0);
           }
           umma_commit(&ctl.acc_full[j & 1]);
         }
@@ -521,9 +535,10 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
             for (int i = 0; i < 16; ++i) v[i] = 0u;
           }
           if (row < rows) {
-            uint4* p = reinterpret_cast<uint4*>(smem + S::kV + (row * (RP + 4) + c0 + c) * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(smem + S::kV + S::share_at(row, c0 + c + 4 * i)) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
       }
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
         const int i = i0 + tid / LT;
         const bool live = i < todo;
         const int row = live ? rank + C * i : 0;
-        const uint32_t at = s_box + (row * (RP + 4) + r0) * 4;
+        const uint32_t at = s_box + S::share_at(row, r0);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < C; ++c) {
@@ -562,16 +577,23 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
           const float inv = half_scale(e);
           v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
         }
-        const uint32_t h0 = pack2<T>(v.x, v.y), h1 = pack2<T>(v.z, v.w);
-        const uint32_t l0 = pack2<T>(rest_of<T>(v.x), rest_of<T>(v.y)), l1 = pack2<T>(rest_of<T>(v.z), rest_of<T>(v.w));
+        uint32_t w[kParts][2];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          w[p][0] = pack2<T>(v.x, v.y), w[p][1] = pack2<T>(v.z, v.w);
+          v.x = rest_of<T>(v.x), v.y = rest_of<T>(v.y), v.z = rest_of<T>(v.z), v.w = rest_of<T>(v.w);
+        }
         if (live) {
-          const uint32_t to = s_v + r0 / 64 * 16384 + swizzled(row, r0 % 64 / 8) + (r0 & 4) * 2;
-          const int k_lo = RP <= 32 ? RP + r0 : r0;  // lo's column in its row
-          const uint32_t lo = s_v + (RP <= 32 ? 0 : S::kLoAt) + k_lo / 64 * 16384 + swizzled(row, k_lo % 64 / 8) + (k_lo & 4) * 2;
+          uint32_t to[kParts];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            const int k = p % S::kInRow * RP + r0;  // the part's column in its row
+            to[p] = s_v + p / S::kInRow * S::kChunks * 16384 + k / 64 * 16384 + swizzled(row, k % 64 / 8) + (k & 4) * 2;
+          }
           const uint32_t e_at = smem_u32(&ctl.exponent[row]);
           for (int c = 0; c < C; ++c) {
-            st_cluster_v2(map_to_rank(to, c), h0, h1);
-            st_cluster_v2(map_to_rank(lo, c), l0, l1);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) st_cluster_v2(map_to_rank(to[p], c), w[p][0], w[p][1]);
             if (!kBf16 && r0 == 0) st_cluster_u8(map_to_rank(e_at, c), exponent);
           }
         }
@@ -788,7 +810,7 @@ __device__ __forceinline__ void store_pair(TO* p, int left, bool pair, float x, 
 
 template <typename T, typename TO, int RP>
 __global__ void __launch_bounds__(kFewThreads, RP == 128 ? 1 : 2) lora_few_kernel(const LoraArgs a, const int C) {
-  constexpr int kTiles = RP / 8;
+  constexpr int kTiles = RP / 8, kParts = kLoraParts<T, TO>;
   extern __shared__ __align__(16) float few_smem[];
   float* red = few_smem;                                // [8 warps][16][RP]
   float* part = red + 8 * kFewRows * RP;                // [16][RP] this CTA's share
@@ -968,18 +990,20 @@ __global__ void __launch_bounds__(kFewThreads, RP == 128 ? 1 : 2) lora_few_kerne
       for (int i = 0; i < kN; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
 #pragma unroll
       for (int s = 0; s < RP / 16; ++s) {
-        uint32_t hi[4], lo[4];
+        uint32_t v[kParts][4];  // A x in parts, as in the kernel above
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float4 f = *reinterpret_cast<const float4*>(vsum + (g + 8 * h) * RP + 16 * s + 4 * q);
-          hi[h] = pack2<T>(f.x, f.y), hi[2 + h] = pack2<T>(f.z, f.w);
-          lo[h] = pack2<T>(rest_of<T>(f.x), rest_of<T>(f.y)), lo[2 + h] = pack2<T>(rest_of<T>(f.z), rest_of<T>(f.w));
+          float4 f = *reinterpret_cast<const float4*>(vsum + (g + 8 * h) * RP + 16 * s + 4 * q);
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            v[p][h] = pack2<T>(f.x, f.y), v[p][2 + h] = pack2<T>(f.z, f.w);
+            f.x = rest_of<T>(f.x), f.y = rest_of<T>(f.y), f.z = rest_of<T>(f.z), f.w = rest_of<T>(f.w);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          mma16816<T>(y[i], lo[0], lo[1], lo[2], lo[3], bw[i][s].x, bw[i][s].y);
-          mma16816<T>(y[i], hi[0], hi[1], hi[2], hi[3], bw[i][s].x, bw[i][s].y);
-        }
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+          for (int p = kParts - 1; p >= 0; --p) mma16816<T>(y[i], v[p][0], v[p][1], v[p][2], v[p][3], bw[i][s].x, bw[i][s].y);
       }
       store_out(u, y);
       if (u + C * 8 < units) {
@@ -1004,7 +1028,7 @@ cudaError_t lora_few_typed(const LoraArgs& a, int64_t max_tiles, int num_sms, cu
 
 template <typename T, typename TO, int RP>
 cudaError_t lora_typed(const LoraArgs& a, int64_t max_tiles, int C, int num_sms, cudaStream_t stream) {
-  using S = LoraSmem<RP>;
+  using S = LoraSmem<RP, kLoraParts<T, TO>>;
   auto kernel = lora_kernel<T, TO, RP>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kBytes);
   if (e != cudaSuccess) return e;
