@@ -623,8 +623,9 @@ moe_status moe_rmsnorm(const void* x, int32_t x_type, int64_t x_stride, const vo
       other_rows(out, x_type, out_stride, x, x_type, x_stride) ||
       other_rows(out, x_type, out_stride, residual, residual_type, residual_stride))
     return MOE_ERR_INVALID_ARG;
-  if (out != nullptr && (out == residual_out || out == q || out == weight)) return MOE_ERR_INVALID_ARG;
-  if (q != nullptr && (q == x || q == residual || q == residual_out || q == weight)) return MOE_ERR_INVALID_ARG;
+  if (out != nullptr && (out == residual_out || out == weight)) return MOE_ERR_INVALID_ARG;
+  if (residual_out != nullptr && residual_out == weight) return MOE_ERR_INVALID_ARG;
+  if (q != nullptr && (q == x || q == residual || q == residual_out || q == out || q == weight)) return MOE_ERR_INVALID_ARG;
   return from_cuda(launch_rmsnorm(x, x_type, x_stride, residual, residual_stride, residual_out, residual_out_stride,
                                   residual != nullptr ? residual_type : x_type, weight, weight_type, eps, rows, H, out,
                                   out_stride, q, scale, num_sms_current_device(), stream));
@@ -667,6 +668,7 @@ moe_status moe_lora(const void* x, int32_t x_type, int64_t x_stride, const void*
   if (plan_bytes < need) return MOE_ERR_WORKSPACE;
   if (ws == nullptr || ws_bytes < MOE_WS_HEADER_BYTES) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  if (out == x || out == a || out == b) return MOE_ERR_INVALID_ARG;  // (others still read them)
   return from_cuda(launch_lora(x, x_type, x_stride, a, b, scale, T, K, N, rank, num_adapters, plan, base, base_stride, out,
                                out_type, out_stride, err_word(ws), num_sms_current_device(), stream));
 }

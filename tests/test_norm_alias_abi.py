@@ -23,7 +23,7 @@ def call(x=A, xs=256, res=None, rs=256, ro=None, ros=256, rt=BF16, w=None, rows=
     dict(res=B, ro=D, rt=F32, out=B),                            # ... of another type
     dict(res=B, ro=B, out=B),                                    # both results in one place
     dict(res=B, ro=C, out=C),
-    dict(q=C, s=D), dict(q=A, s=D), dict(res=B, ro=B, q=B, s=D, out=None), dict(w=D, q=D, s=B), dict(w=C, out=C),
+    dict(res=B, ro=D, w=D), dict(q=C, s=D), dict(q=A, s=D), dict(res=B, ro=B, q=B, s=D, out=None), dict(w=D, q=D, s=B), dict(w=C, out=C),
 ])
 def test_refused(kw):
     assert call(**kw) == BAD
