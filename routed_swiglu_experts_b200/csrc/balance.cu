@@ -11,9 +11,11 @@
 // One kernel.  Some blocks count: runs of sequences, or about sixteen parts of few
 // ones.  The others wait for them (a cooperative launch; small
 // batches take one block) while their logits come to shared memory.  Then every warp
-// walks over tokens.  One B200, graph replay: 16384 x 256 fp32 with gradient 19.7
-// us, of which launch and counting take half and the pass 6 (in 512 sequences 23);
-// 16384 x 64 bf16 in 1 to 16 sequences 13.5 to 14.7; 4096 x 64 in 24 13; 64 x 8 8.4.
+// walks over tokens.  One B200, a graph of calls on sets of inputs in turn: 16384 x 256
+// fp32 with gradient 20.0 us, of which launch and counting take half and the pass 6 (in
+// 512 sequences 25); 16384 x 64 bf16 in one sequence 13.5, in 4 to 16 16 to 19; 4096 x
+// 64 in 24 13.4; 64 x 8 8.  Many sequences of few experts, 64 tokens or more each, are
+// counted one after another by few blocks: 4096 x 4 in 64 129, 16384 x 4 in 200 56.
 #include <cuda_fp16.h>
 
 #include <type_traits>

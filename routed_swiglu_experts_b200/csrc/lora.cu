@@ -2,11 +2,12 @@
 //   out[t] = base[t] + scale_l * B_l (A_l x_t),  l the adapter of token t
 // A plan sorts the batch's tokens by adapter and cuts each adapter's rows into
 // tiles; it serves every projection of the step.
-// One B200, graph replay: 16384 tokens, K 6144, N 4096, 16 adapters of rank 64 100
-// us (4.9 TB/s of x, base and out: both products run at the memory's rate, the sum
-// between them does not); 4096 tokens, K 2048, N 5632, rank 16 31 us (3.5 TB/s);
-// 32 tokens of 32 adapters, K 6144, N 4096, rank 16 9.6 us and one token 5.0 us,
-// chains of latencies (11 MB and 0.3 MB).
+// One B200, a graph of calls on three or more sets of inputs in turn, bf16: 16384
+// tokens, K 6144, N 4096, 16 adapters of rank 64 101 us (4.8 TB/s of x, base and out:
+// both products run at the memory's rate, the sum between them does not; 114 with a
+// tenth of the tokens without an adapter); 4096 tokens, K 2048, N 5632, rank 16 32 us
+// (3.4 TB/s); 32 tokens of 32 adapters, K 6144, N 4096, rank 16 9.8 us (7.4 with its
+// inputs in L2) and one token 5.0 us, chains of latencies (11 MB and 0.3 MB).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -175,7 +176,7 @@ struct LoraSmem {
   // 64 values where they fit), and kBoxes boxes of base, 128 bytes of each token; until
   // then this CTA's share of A x lies where the boxes will be.
   static constexpr int kInRow = RP < 64 ? 64 / RP : 1;
-  static constexpr int part_at(int p) { return p / kInRow * kChunks * 16384 + p % kInRow * 2 * RP; }
+  __host__ __device__ static constexpr int part_at(int p) { return p / kInRow * kChunks * 16384 + p % kInRow * 2 * RP; }
   static constexpr int kV = (PARTS + kInRow - 1) / kInRow * kChunks * 16384;
   // (rank 64 in three parts: what two CTAs an SM leave holds two boxes, and the share
   // without padding, its 16-byte pieces in another order in every row)
