@@ -535,6 +535,12 @@ __global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0u;
           }
+          // (ranks that are not there: an infinity in x times their zeros is NaN)
+          if (c0 + c + 16 > a.r) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + c + i / 8 * 8 >= a.r) v[i] = 0u;
+          }
           if (row < rows) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -957,7 +963,7 @@ __global__ void __launch_bounds__(kFewThreads, RP == 128 ? 1 : 2) lora_few_kerne
       for (int p = 0; p < kPerLane; ++p) {
         const int j = p * 32 + lane;
         v[p] = 0.f;
-        if (j < RP) {
+        if (j < a.r) {  // (those that are not there are 0, as in the kernel above)
           const uint32_t at = smem_u32(part + row * RP + j);
           float s[kFewMaxCluster];
 #pragma unroll
