@@ -3,7 +3,7 @@
 // A plan sorts the batch's tokens by adapter and cuts each adapter's rows into
 // tiles; it serves every projection of the step.
 // One B200, a graph of calls on three or more sets of inputs in turn, bf16: 16384
-// tokens, K 6144, N 4096, 16 adapters of rank 64 101 us (4.8 TB/s of x, base and out:
+// tokens, K 6144, N 4096, 16 adapters of rank 64 102 us (4.8 TB/s of x, base and out:
 // both products run at the memory's rate, the sum between them does not; 114 with a
 // tenth of the tokens without an adapter); 4096 tokens, K 2048, N 5632, rank 16 32 us
 // (3.4 TB/s); 32 tokens of 32 adapters, K 6144, N 4096, rank 16 9.8 us (7.4 with its

@@ -9,7 +9,7 @@
 // with a sum near fp32's ends.
 // Bound by memory: 16384 x 6144 bf16 with residual, 16-bit and 8-bit results 145 us,
 // 0.96 of the copy rate (a graph of calls on three sets of inputs in turn; calls on
-// their own 148 to 160 by the box); 8192 x 4096 fp32 with residual 82 us, 0.99.  8-bit
+// their own 148 to 161 by the box); 8192 x 4096 fp32 with residual 82 us, 0.99.  8-bit
 // results alone (16384 x 6144 bf16, 74 us, 0.63) are bound by their instructions, 14 a
 // value.
 #include <cuda_fp16.h>
