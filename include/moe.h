@@ -630,7 +630,7 @@ MOE_API moe_status moe_selftest_device_timeout(void* scratch, size_t scratch_byt
 #define MOE_SELFTEST_PAIR_INT4 1
 #define MOE_SELFTEST_PAIR_FP8_FEW 3
 #define MOE_SELFTEST_PAIR_FP8_WIDE 4
-#define MOE_SELFTEST_LORA 5
+#define MOE_SELFTEST_LORA 6
 MOE_API moe_status moe_selftest_pair_timeout(void* scratch, size_t scratch_bytes, int32_t kernel,
                                              moe_stream_t stream);
 

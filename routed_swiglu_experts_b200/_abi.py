@@ -58,7 +58,7 @@ MOE_SELFTEST_PAIR_BF16 = 0
 MOE_SELFTEST_PAIR_INT4 = 1
 MOE_SELFTEST_PAIR_FP8_FEW = 3
 MOE_SELFTEST_PAIR_FP8_WIDE = 4
-MOE_SELFTEST_LORA = 5
+MOE_SELFTEST_LORA = 6
 
 
 class MoEError(RuntimeError):
